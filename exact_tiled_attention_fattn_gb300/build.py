@@ -37,7 +37,7 @@ def _sources():
 
 def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    return _sources() + hdrs + [os.path.join(INCLUDE, "fattn.h"), os.path.abspath(__file__)]
+    return _sources() + hdrs + [os.path.join(INCLUDE, h) for h in ("fattn.h", "fattn_ops.h")] + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:

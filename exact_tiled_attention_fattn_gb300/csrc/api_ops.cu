@@ -1,0 +1,83 @@
+// Entry points of include/fattn_ops.h: argument checks and dispatch.
+#include "fattn_ops.h"
+#include "fattn_internal.h"
+#include "ops_internal.h"
+
+#include <cmath>
+
+using namespace fattn;
+
+static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Checks that fattn_rope and fattn_rope_append_paged share.
+static fattn_status check_rotary(const double* inv_freq, int rows, int Hq, int Hk, int d, int rotary_dim,
+                                 float amplitude) {
+  if (rows < 0 || Hq < 0 || Hk < 0 || d <= 0 || rotary_dim < 0 || rotary_dim > d || (rotary_dim & 1))
+    return FATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return FATTN_ERR_INVALID_ARG;
+  if (rows > 0 && rotary_dim > 0 && (!inv_freq || misaligned(inv_freq, 8))) return FATTN_ERR_INVALID_ARG;
+  if (d > 1024 || (long long)Hq + Hk > 4096) return FATTN_ERR_UNSUPPORTED;
+  return FATTN_OK;
+}
+
+extern "C" fattn_status fattn_rope(const void* q, void* q_out, const void* k, void* k_out, const int32_t* positions,
+                                   int period, const double* inv_freq, int rows, int Hq, int Hk, int d,
+                                   int rotary_dim, long long q_row, long long q_head, long long qo_row,
+                                   long long qo_head, long long k_row, long long k_head, long long ko_row,
+                                   long long ko_head, int interleaved, int inverse, float amplitude, fattn_dtype dtype,
+                                   cudaStream_t stream) {
+  const fattn_status st = check_rotary(inv_freq, rows, Hq, Hk, d, rotary_dim, amplitude);
+  if (st != FATTN_OK) return st;
+  if (dtype != FATTN_BF16 && dtype != FATTN_FP32) return FATTN_ERR_INVALID_ARG;
+  if ((k == nullptr) != (k_out == nullptr) || (Hk > 0) != (k != nullptr)) {
+    if (rows > 0) return FATTN_ERR_INVALID_ARG;
+  }
+  if (q_row < 0 || q_head < 0 || qo_row < 0 || qo_head < 0 || k_row < 0 || k_head < 0 || ko_row < 0 || ko_head < 0)
+    return FATTN_ERR_INVALID_ARG;
+  if (rows == 0) return FATTN_OK;
+  const uintptr_t el = dtype == FATTN_BF16 ? 2 : 4;
+  if (Hq <= 0 || !q || !q_out || misaligned(q, el) || misaligned(q_out, el) || misaligned(k, el) ||
+      misaligned(k_out, el) || misaligned(positions, 4) || (!positions && period <= 0))
+    return FATTN_ERR_INVALID_ARG;
+  RopeParams p{};
+  p.q = {q, q_out, Hq, q_row, q_head, qo_row, qo_head};
+  p.k = {k, k_out, Hk, k_row, k_head, ko_row, ko_head};
+  p.positions = positions; p.inv_freq = inv_freq; p.period = period;
+  p.rows = rows; p.d = d; p.rot = rotary_dim; p.inverse = inverse ? 1 : 0; p.amplitude = amplitude;
+  return launch_rope(p, dtype == FATTN_BF16, interleaved != 0, false, stream) == cudaSuccess ? FATTN_OK
+                                                                                            : FATTN_ERR_CUDA;
+}
+
+extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, const void* k, const void* v, void* kcache,
+                                                void* vcache, const int32_t* block_table, const int32_t* seqlens_k,
+                                                const int32_t* cu_seqlens_q, const int32_t* positions,
+                                                const double* inv_freq, int B, int total_q, int Hq, int Hkv, int d,
+                                                int rotary_dim, int page_size, int max_pages_per_seq, int num_pages,
+                                                long long q_row, long long q_head, long long k_row, long long k_head,
+                                                long long v_row, long long v_head, int interleaved, float amplitude,
+                                                cudaStream_t stream) {
+  const fattn_status st = check_rotary(inv_freq, total_q, q ? Hq : 0, Hkv, d, rotary_dim, amplitude);
+  if (st != FATTN_OK) return st;
+  if (B < 0 || Hkv <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0) return FATTN_ERR_INVALID_ARG;
+  if (q_row < 0 || q_head < 0 || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return FATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+  if (B == 0 || total_q == 0) return FATTN_OK;
+  if ((q != nullptr) != (q_out != nullptr) || (q && Hq <= 0)) return FATTN_ERR_INVALID_ARG;
+  if (!k || !v || !kcache || !vcache || !block_table || !seqlens_k || !cu_seqlens_q) return FATTN_ERR_INVALID_ARG;
+  if (misaligned(q, 2) || misaligned(q_out, 2) || misaligned(k, 2) || misaligned(v, 2) || misaligned(kcache, 2) ||
+      misaligned(vcache, 2) || misaligned(block_table, 4) || misaligned(seqlens_k, 4) || misaligned(cu_seqlens_q, 4) ||
+      misaligned(positions, 4))
+    return FATTN_ERR_INVALID_ARG;
+  int err = 0;
+  RopeParams p{};
+  p.q = {q, q_out, q ? Hq : 0, q_row, q_head, (long long)Hq * d, d};
+  p.k = {k, kcache, Hkv, k_row, k_head, (long long)Hkv * d, d};
+  p.v = {v, vcache, Hkv, v_row, v_head, (long long)Hkv * d, d};
+  p.positions = positions; p.inv_freq = inv_freq; p.period = 1;
+  p.rows = total_q; p.d = d; p.rot = rotary_dim; p.amplitude = amplitude;
+  p.cu_seqlens = cu_seqlens_q; p.seqlens_k = seqlens_k; p.block_table = block_table;
+  p.B = B; p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  return launch_rope(p, true, interleaved != 0, true, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}

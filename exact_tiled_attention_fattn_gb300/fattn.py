@@ -50,6 +50,15 @@ SIGNATURES = {
     "fattn_debug_set_wait_limit": (None, [ctypes.c_ulonglong, _i]),
 }
 
+# Every entry point declared in include/fattn_ops.h
+_ll, _d = ctypes.c_longlong, ctypes.c_double
+SIGNATURES_OPS = {
+    "fattn_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _ll, _ll,
+                        _i, _i, _f, _i, _vp]),
+    "fattn_rope_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                                     _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _i, _f, _vp]),
+}
+
 _lib = None
 
 
@@ -68,7 +77,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"libfattn.so not found at {path}: build it with __graft_entry__.build() "
                            "or python -m exact_tiled_attention_fattn_gb300.build")
     lib = ctypes.CDLL(path)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **SIGNATURES_OPS}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -105,17 +114,17 @@ def _dtype_code(dt) -> int:
     raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
 
 
-def _need_cuda(*ts):
+def _need_cuda(*ts, contiguous: bool = True):
     """All given tensors are contiguous CUDA tensors on one device, the current one
     (the library launches on the current device, so a tensor elsewhere would be an
-    invalid address there)."""
+    invalid address there). ``contiguous=False``: for calls that take strides."""
     dev = None
     for t in ts:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors")
-        if not t.is_contiguous():
+        if contiguous and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
         if dev is None:
             dev = t.device
@@ -503,3 +512,184 @@ def debug_set_wait_limit(limit_ns: int = 0, stall: bool = False) -> None:
     barrier nothing arrives on, so each launch times out (FATTN_ERR_TIMEOUT) and
     returns without writing its outputs. Reset with debug_set_wait_limit(0, False)."""
     load_library().fattn_debug_set_wait_limit(int(limit_ns), 1 if stall else 0)
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(inv_freq float64 [rotary_dim / 2], amplitude) for ``rope``: angle per position of
+    pair i is base^(-2i / rotary_dim), then, for contexts ``factor`` times longer than trained,
+
+    * ``scaling="linear"``: every frequency divided by ``factor``;
+    * ``scaling="base"``: the base raised so that the lowest frequency is divided by ``factor``
+      and the highest stays;
+    * ``scaling="bands"``: pairs that turn more than ``beta_fast`` times over ``original_length``
+      keep their frequency, pairs that turn less than ``beta_slow`` times have it divided by
+      ``factor``, a linear ramp over the pair index between; the amplitude is 0.1 ln(factor) + 1.
+    """
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be positive and even")
+    if not (base > 0 and factor >= 1.0):
+        raise ValueError("base must be positive and factor at least 1")
+    half = rotary_dim // 2
+    i = torch.arange(half, dtype=torch.float64)
+    if scaling == "base" and half > 1:
+        base = base * factor ** (half / (half - 1))
+    f = float(base) ** (-i / half)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        def pair(turns):  # index (real) of the pair that turns `turns` times over the original length
+            return half * math.log(original_length / (2.0 * math.pi * turns)) / math.log(base)
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), half - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - ramp) + f / factor * ramp
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'base' or 'bands'")
+    return f.to(device) if device is not None else f, amplitude
+
+
+def _row_strides(t, name):
+    """(row stride, head stride) of [..., H, d] whose leading dimensions are one uniform run of rows."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [T, H, d] or [B, N, H, d]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    row = t.stride(-3)
+    if t.dim() == 4 and t.shape[0] > 1:
+        if t.shape[1] == 1:
+            row = t.stride(0)
+        elif t.stride(0) != t.shape[1] * row:
+            raise ValueError(f"{name}: the batch stride must be N row strides")
+    return row, t.stride(-2)
+
+
+def _no_overlap(t, name):
+    """An output: distinct elements have distinct addresses."""
+    row, head = _row_strides(t, name)
+    extent = t.shape[-1]
+    for stride, n in sorted([(row, t.shape[:-2].numel()), (head, t.shape[-2])]):
+        if n > 1:
+            if stride < extent:
+                raise ValueError(f"{name}: rows or heads overlap")
+            extent += (n - 1) * stride
+
+
+def _check_freq(inv_freq, d):
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float64 vector of rotary_dim / 2 frequencies")
+    rot = 2 * inv_freq.numel()
+    if rot > d:
+        raise ValueError(f"inv_freq has {inv_freq.numel()} frequencies for heads of {d} elements")
+    return rot
+
+
+def rope(q, k=None, inv_freq=None, positions=None, interleaved: bool = False, amplitude: float = 1.0,
+         inverse: bool = False, out_q=None, out_k=None, stream=None):
+    """Rotary positions on q [T,Hq,d] or [B,N,Hq,d] (bf16 or fp32; any row and head strides, so
+    slices of a packed projection serve as they are) and, in the same launch, k with the same
+    leading dimensions. ``inv_freq`` float64 [rotary_dim / 2] on the device (``rope_frequencies``);
+    pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) if ``interleaved``; the rest of the head is
+    copied. ``positions`` int32, [T] or [B,N]; None: the index along T (N). ``inverse=True`` with the
+    other arguments unchanged is the gradient: it maps (dq', dk') to (dq, dk). ``out_q`` / ``out_k``
+    may be q / k themselves. Returns q', or (q', k')."""
+    lib = load_library()
+    if inv_freq is None:
+        raise ValueError("inv_freq must be given (rope_frequencies)")
+    _need_cuda(q, k, inv_freq, positions, out_q, out_k, contiguous=False)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [T, H, d] or [B, N, H, d]")
+    code, d, lead = _dtype_code(q.dtype), q.shape[-1], tuple(q.shape[:-2])
+    rot = _check_freq(inv_freq, d)
+    if k is not None:
+        if k.dtype != q.dtype:
+            raise TypeError("q and k must share a dtype")
+        if k.dim() != q.dim() or tuple(k.shape[:-2]) != lead or k.shape[-1] != d:
+            raise ValueError("k must have q's leading dimensions and head size")
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    if positions is not None:
+        _expect(positions, lead, "positions", torch.int32)
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+    _expect(out_q, q.shape, "out_q", q.dtype)
+    if k is not None:
+        _expect(out_k, k.shape, "out_k", q.dtype)
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and out_k is None:
+        out_k = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    rows = math.prod(lead)
+    strides = []
+    for x, y, name in ((q, out_q, "q"), (k, out_k, "k")):
+        if x is None:
+            strides += [0, 0, 0, 0]
+            continue
+        _no_overlap(y, "out_" + name)
+        strides += [*_row_strides(x, name), *_row_strides(y, "out_" + name)]
+    st = lib.fattn_rope(_ptr(q), _ptr(out_q), _ptr(k), _ptr(out_k), _ptr(positions), lead[-1] if rows else 1,
+                        _ptr(inv_freq), rows, q.shape[-2], 0 if k is None else k.shape[-2], d, rot, *strides,
+                        1 if interleaved else 0, 1 if inverse else 0, float(amplitude), code,
+                        ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_rope", st)
+    return out_q if k is None else (out_q, out_k)
+
+
+def _check_paged_cache(kcache, vcache, block_table, B):
+    if kcache.dim() != 4:
+        raise ValueError("kcache must be [pages, page_size, Hkv, d]")
+    if vcache is not None:
+        _expect(vcache, kcache.shape, "vcache", kcache.dtype)
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages_per_seq]")
+
+
+def rope_append_paged(q, k, v, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, inv_freq, positions=None,
+                      interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """One serving step before the attention: q [Tq,Hq,d] (or None) and k [Tq,Hkv,d] of new tokens
+    rotated, k and v [Tq,Hkv,d] written into their slots of the paged cache, one launch. bf16; q, k and v
+    may have any row and head strides. Chunks are packed as in ``fwd_paged`` (one token each for
+    decoding): chunk b holds the last tokens of the ``seqlens_k[b]`` context tokens, the new ones
+    included. ``positions`` int32 [Tq]; None: each token's index in its sequence. Rows past the last
+    chunk are left alone. Returns the rotated q [Tq,Hq,d], packed (None without q)."""
+    lib = load_library()
+    _need_cuda(q, k, v, inv_freq, contiguous=False)
+    _need_cuda(kcache, vcache, block_table, seqlens_k, cu_seqlens_q, positions, out)
+    if not (k.dtype == v.dtype == kcache.dtype == vcache.dtype == torch.bfloat16) or (
+            q is not None and q.dtype != torch.bfloat16):
+        raise TypeError("rope_append_paged takes bf16 q, k, v and caches")
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [Tq, Hkv, d]")
+    Tq, Hkv, d = k.shape
+    rot = _check_freq(inv_freq, d)
+    if seqlens_k.dtype != torch.int32 or cu_seqlens_q.dtype != torch.int32:
+        raise TypeError("seqlens_k and cu_seqlens_q must be int32")
+    B = cu_seqlens_q.numel() - 1
+    _expect(seqlens_k, (B,), "seqlens_k")
+    _check_paged_cache(kcache, vcache, block_table, B)
+    _expect(kcache, (*kcache.shape[:2], Hkv, d), "kcache")
+    if positions is not None:
+        _expect(positions, (Tq,), "positions", torch.int32)
+    Hq = 0
+    qs = (0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != Tq or q.shape[2] != d:
+            raise ValueError(f"q must be [{Tq}, Hq, {d}]")
+        Hq = q.shape[1]
+        qs = _row_strides(q, "q")
+        _expect(out, q.shape, "out", q.dtype)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out is not None:
+        raise ValueError("out without q")
+    st = lib.fattn_rope_append_paged(_ptr(q), _ptr(out), _ptr(k), _ptr(v), _ptr(kcache), _ptr(vcache),
+                                     _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q), _ptr(positions),
+                                     _ptr(inv_freq), B, Tq, Hq, Hkv, d, rot, kcache.shape[1], block_table.shape[1],
+                                     kcache.shape[0], *qs, *_row_strides(k, "k"), *_row_strides(v, "v"),
+                                     1 if interleaved else 0, float(amplitude), ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_rope_append_paged", st)
+    return out

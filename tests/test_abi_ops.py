@@ -1,0 +1,89 @@
+"""include/fattn_ops.h without a GPU: every declared entry point is exported and bound, and bad
+arguments are refused on the host before CUDA is touched."""
+import os
+import re
+
+import pytest
+import torch
+
+from exact_tiled_attention_fattn_gb300 import build as fbuild
+from exact_tiled_attention_fattn_gb300 import fattn as F
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 0x100000  # an aligned fake device address: never dereferenced, the calls fail validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fbuild.build()
+    return F.load_library()
+
+
+def test_header_and_binding_agree(lib):
+    text = open(os.path.join(ROOT, "include", "fattn_ops.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(fattn_\w+)\s*\(", text))
+    assert names == set(F.SIGNATURES_OPS)
+    for n in names:
+        assert hasattr(lib, n)
+
+
+def _rope(lib, **kw):
+    g = lambda n, x: kw.get(n, x)
+    return lib.fattn_rope(g("q", A), g("qo", A), g("k", A), g("ko", A), g("pos", A), g("period", 1), g("f", A),
+                          g("rows", 4), g("Hq", 4), g("Hk", 2), g("d", 128), g("rot", 64), g("qr", 512), 128, 512, 128,
+                          256, g("kh", 128), 256, 128, 0, 0, g("amp", 1.0), g("dt", F.FATTN_BF16), None)
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(qo=None), dict(q=A + 1), dict(ko=None), dict(k=None), dict(f=None),
+                                 dict(f=A + 4), dict(rot=63), dict(rot=130), dict(rot=-2), dict(rows=-1), dict(Hq=0),
+                                 dict(pos=None, period=0), dict(pos=A + 2), dict(amp=float("nan")), dict(dt=9),
+                                 dict(qr=-1), dict(kh=-1), dict(d=0), dict(dt=F.FATTN_FP32, q=A + 2)])
+def test_rope_refuses(lib, bad):
+    assert _rope(lib, **bad) == F.FATTN_ERR_INVALID_ARG
+
+
+def test_rope_limits_and_empty(lib):
+    assert _rope(lib, d=1026) == F.FATTN_ERR_UNSUPPORTED
+    assert _rope(lib, Hq=4095) == F.FATTN_ERR_UNSUPPORTED
+    assert _rope(lib, rows=0, q=None, qo=None, k=None, ko=None, Hk=0, pos=None, f=None) == F.FATTN_OK
+
+
+def _append(lib, **kw):
+    g = lambda n, x: kw.get(n, x)
+    return lib.fattn_rope_append_paged(g("q", A), g("qo", A), g("k", A), g("v", A), g("kc", A), A, g("bt", A), g("sl", A),
+                                       g("cu", A), None, g("f", A), g("B", 2), g("T", 3), g("Hq", 4), g("Hkv", 2), 64,
+                                       g("rot", 64), g("ps", 16), g("maxp", 4), g("np", 8), 256, 64, 128, 64, 128, 64, 0,
+                                       g("amp", 1.0), None)
+
+
+@pytest.mark.parametrize("bad", [dict(qo=None), dict(q=None), dict(k=None), dict(v=None), dict(kc=None), dict(bt=None),
+                                 dict(sl=None), dict(cu=None), dict(f=None), dict(ps=0), dict(maxp=0), dict(np=0),
+                                 dict(B=-1), dict(Hkv=0), dict(rot=66), dict(bt=A + 2), dict(kc=A + 1),
+                                 dict(amp=float("inf"))])
+def test_append_refuses(lib, bad):
+    assert _append(lib, **bad) == F.FATTN_ERR_INVALID_ARG
+
+
+def test_append_limits_and_empty(lib):
+    assert _append(lib, maxp=1 << 28) == F.FATTN_ERR_UNSUPPORTED
+    assert _append(lib, T=0, k=None, v=None, kc=None) == F.FATTN_OK
+    assert _append(lib, B=0, k=None) == F.FATTN_OK
+
+
+def test_rope_frequencies():
+    f, a = F.rope_frequencies(8)
+    assert a == 1.0 and f.dtype == torch.float64
+    assert torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64), rtol=1e-14)
+    g, _ = F.rope_frequencies(8, scaling="linear", factor=4.0)
+    assert torch.equal(g, f / 4)
+    g, _ = F.rope_frequencies(8, scaling="base", factor=4.0)
+    assert g[0] == 1.0 and abs(g[3].item() * 4 / f[3].item() - 1) < 1e-12
+    f, _ = F.rope_frequencies(128)
+    g, a = F.rope_frequencies(128, scaling="bands", factor=8.0, original_length=4096)
+    assert g[0] == f[0] and g[-1] == f[-1] / 8 and abs(a - 1.2079441541679836) < 1e-15
+    assert bool(((g <= f) & (g >= f / 8)).all())
+    for bad in (dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=8, scaling="other"),
+                dict(rotary_dim=8, factor=0.5), dict(rotary_dim=8, base=0.0)):
+        with pytest.raises(ValueError):
+            F.rope_frequencies(**bad)
