@@ -3,6 +3,7 @@
 // contract of every entry point.
 #include "fattn.h"
 #include "fattn_internal.h"
+#include "ops_internal.h"
 
 #include <cudaTypedefs.h>
 
@@ -22,11 +23,15 @@ static std::atomic<int*> g_status_ptr[128];
 static std::atomic<unsigned long long> g_wait_limit_ns{0};
 static std::atomic<int> g_debug_stall{0};
 
+void current_waits(unsigned long long* wait_ns, int* debug_stall) {
+  const unsigned long long w = g_wait_limit_ns.load(std::memory_order_relaxed);
+  *wait_ns = w ? w : kDefaultWaitNs;
+  *debug_stall = g_debug_stall.load(std::memory_order_relaxed);
+}
+
 template <typename Params>
 void set_waits(Params& p) {
-  const unsigned long long w = g_wait_limit_ns.load(std::memory_order_relaxed);
-  p.wait_ns = w ? w : kDefaultWaitNs;
-  p.debug_stall = g_debug_stall.load(std::memory_order_relaxed);
+  current_waits(&p.wait_ns, &p.debug_stall);
 }
 
 int* status_ptr(int* err) {
@@ -234,11 +239,12 @@ extern "C" fattn_status fattn_fwd_masked(const void* q, const void* k, const voi
   return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const void* vcache,
-                                        const int32_t* block_table, const int32_t* seqlens_k,
-                                        const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
-                                        int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
-                                        int max_seqlen_q, int causal, float scale, cudaStream_t stream) {
+// fattn_fwd_paged, and with a shape fattn_fwd_paged_shaped.
+fattn_status fattn::fwd_paged_impl(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
+                                   const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B,
+                                   int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
+                                   int total_q, int max_seqlen_q, int causal, float scale, const ScoreShape* shape,
+                                   cudaStream_t stream) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || total_q < 0 || max_seqlen_q < 0 || page_size <= 0 ||
       max_pages_per_seq <= 0 || num_pages <= 0)
     return FATTN_ERR_INVALID_ARG;
@@ -264,6 +270,10 @@ extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const
   p.mask_heads = 1;
   p.block_table = block_table; p.seqlens_k = seqlens_k;
   p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  if (shape) {
+    p.shaped = 1;
+    p.shape = *shape;
+  }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
   set_waits(p);
@@ -275,6 +285,15 @@ extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const
   const int sms = num_sms_current();
   if (sms <= 0) return FATTN_ERR_CUDA;
   return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const void* vcache,
+                                        const int32_t* block_table, const int32_t* seqlens_k,
+                                        const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
+                                        int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
+                                        int max_seqlen_q, int causal, float scale, cudaStream_t stream) {
+  return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
+                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, nullptr, stream);
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -324,10 +343,11 @@ extern "C" size_t fattn_bwd_workspace_size(int B, int Hq, int N) {
   return 2 * align256((size_t)B * Hq * npad * sizeof(float));
 }
 
-extern "C" fattn_status fattn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                                  const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
-                                  int d, int causal, float scale, void* workspace, size_t workspace_bytes,
-                                  cudaStream_t stream) {
+// fattn_bwd, and with a shape fattn_bwd_shaped.
+fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
+                             int causal, float scale, const ScoreShape* shape, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
   if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FATTN_ERR_INVALID_ARG;
   if (B == 0 || N == 0) return FATTN_OK;
   if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FATTN_ERR_INVALID_ARG;
@@ -351,6 +371,10 @@ extern "C" fattn_status fattn_bwd(const void* q, const void* k, const void* v, c
   p.ws_d = reinterpret_cast<float*>(static_cast<char*>(workspace) + need / 2);
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.N = N; p.d = d; p.Npad = (int)npad;
   p.causal = causal ? 1 : 0; p.scale = scale;
+  if (shape) {
+    p.shaped = 1;
+    p.shape = *shape;
+  }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
   set_waits(p);
@@ -364,6 +388,14 @@ extern "C" fattn_status fattn_bwd(const void* q, const void* k, const void* v, c
   return launch_backward(p, tq, tk, tv, tdo, tdk, tdv, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
+extern "C" fattn_status fattn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
+                                  int d, int causal, float scale, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, nullptr, workspace,
+                  workspace_bytes, stream);
+}
+
 extern "C" size_t fattn_decode_workspace_size(int B, int Hq, int d, int num_splits) {
   if (B <= 0 || Hq <= 0 || d <= 0 || num_splits <= 0) return 0;
   size_t rows = (size_t)B * Hq * num_splits;
@@ -371,11 +403,12 @@ extern "C" size_t fattn_decode_workspace_size(int B, int Hq, int d, int num_spli
          align256((size_t)(1 + B * Hq) * sizeof(int));
 }
 
-extern "C" fattn_status fattn_decode_paged(const void* q, const void* kcache, const void* vcache,
-                                           const int32_t* block_table, const int32_t* seqlens, int num_splits,
-                                           void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
-                                           int max_pages_per_seq, int num_pages, float scale, void* workspace,
-                                           size_t workspace_bytes, cudaStream_t stream) {
+// fattn_decode_paged, and with a shape fattn_decode_paged_shaped.
+fattn_status fattn::decode_paged_impl(const void* q, const void* kcache, const void* vcache,
+                                      const int32_t* block_table, const int32_t* seqlens, int num_splits, void* o,
+                                      float* lse, int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
+                                      int num_pages, float scale, const ScoreShape* shape, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
   if (!q || !kcache || !vcache || !block_table || !seqlens || !o) return FATTN_ERR_INVALID_ARG;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 ||
       num_splits <= 0)
@@ -395,7 +428,7 @@ extern "C" fattn_status fattn_decode_paged(const void* q, const void* kcache, co
     return FATTN_ERR_WORKSPACE;
 
   int err = 0;
-  DecodeParams p;
+  DecodeParams p{};
   p.q = q; p.kcache = kcache; p.vcache = vcache; p.block_table = block_table; p.seqlens = seqlens;
   const size_t rows = (size_t)B * Hq * num_splits;
   p.lse_part = static_cast<float*>(workspace);
@@ -406,9 +439,22 @@ extern "C" fattn_status fattn_decode_paged(const void* q, const void* kcache, co
   p.lse = lse;
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages_per_seq = max_pages_per_seq;
   p.num_pages = num_pages; p.num_splits = num_splits; p.scale = scale;
+  if (shape) {
+    p.shaped = 1;
+    p.shape = *shape;
+  }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
   return launch_decode(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+extern "C" fattn_status fattn_decode_paged(const void* q, const void* kcache, const void* vcache,
+                                           const int32_t* block_table, const int32_t* seqlens, int num_splits,
+                                           void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                           int max_pages_per_seq, int num_pages, float scale, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream) {
+  return decode_paged_impl(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
+                           max_pages_per_seq, num_pages, scale, nullptr, workspace, workspace_bytes, stream);
 }
 
 extern "C" fattn_status fattn_merge_partials(const float* o_part, const float* lse_part, void* o, float* lse, int B,

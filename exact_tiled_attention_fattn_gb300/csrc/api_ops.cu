@@ -81,3 +81,87 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
   if (err) return FATTN_ERR_CUDA;
   return launch_rope(p, true, interleaved != 0, true, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
+
+// A score shape's own checks; fills *out. `scale` is the call's.
+static fattn_status check_shape(float scale, float softcap, const float* slopes, int window, const int32_t* key_begin,
+                                const int32_t* key_end, ScoreShape* out) {
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return FATTN_ERR_INVALID_ARG;
+  // the cap's argument 2 log2(e) scale / softcap must be a number
+  if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
+  if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
+  *out = {softcap, slopes, window, key_begin, key_end};
+  return FATTN_OK;
+}
+
+extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                                         int Hkv, int N, int d, int causal, float scale, float softcap,
+                                         const float* slopes, int window, const int32_t* key_begin,
+                                         const int32_t* key_end, cudaStream_t stream) {
+  if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FATTN_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return FATTN_OK;
+  if (!q || !k || !v || !o || Hq % Hkv != 0) return FATTN_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(lse, 4))
+    return FATTN_ERR_INVALID_ARG;
+  PrefillParams p{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &p.shape);
+  if (st != FATTN_OK) return st;
+  if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+  const long long rows = (long long)B * N;
+  const long long pairs = ((long long)N + 255) / 256;  // work items per (sequence, head)
+  if (rows > 0x7fffffffLL || (long long)B * Hq > 0x7fffffffLL / pairs) return FATTN_ERR_UNSUPPORTED;
+  int err = 0;
+  p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.N = N; p.d = d; p.total_rows = (int)rows;
+  p.causal = causal ? 1 : 0; p.scale = scale;
+  p.mask_heads = 1;
+  p.shaped = 1;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  current_waits(&p.wait_ns, &p.debug_stall);
+  CUtensorMap tq, tk, tv, to;
+  if (!encode_rows_map(&tq, q, p.total_rows, Hq, d, 128) || !encode_rows_map(&tk, k, p.total_rows, Hkv, d, 128) ||
+      !encode_rows_map(&tv, v, p.total_rows, Hkv, d, 128) || !encode_rows_map(&to, o, p.total_rows, Hq, d, 32))
+    return FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache, const void* vcache,
+                                               const int32_t* block_table, const int32_t* seqlens_k,
+                                               const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
+                                               int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
+                                               int max_seqlen_q, int causal, float scale, float softcap,
+                                               const float* slopes, int window, const int32_t* key_begin,
+                                               const int32_t* key_end, cudaStream_t stream) {
+  ScoreShape shape{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &shape);
+  if (st != FATTN_OK) return st;
+  return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
+                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, &shape, stream);
+}
+
+extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                         const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
+                                         int d, int causal, float scale, float softcap, const float* slopes, int window,
+                                         const int32_t* key_begin, const int32_t* key_end, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream) {
+  ScoreShape shape{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &shape);
+  if (st != FATTN_OK) return st;
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, &shape, workspace,
+                  workspace_bytes, stream);
+}
+
+extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const void* vcache,
+                                                  const int32_t* block_table, const int32_t* seqlens, int num_splits,
+                                                  void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                                  int max_pages_per_seq, int num_pages, float scale, float softcap,
+                                                  const float* slopes, int window, void* workspace,
+                                                  size_t workspace_bytes, cudaStream_t stream) {
+  ScoreShape shape{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, nullptr, nullptr, &shape);
+  if (st != FATTN_OK) return st;
+  return decode_paged_impl(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
+                           max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
+}

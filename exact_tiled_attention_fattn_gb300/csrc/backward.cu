@@ -49,6 +49,7 @@
 // drained and TMEM is freed.
 #include "device_common.cuh"
 #include "fattn_internal.h"
+#include "score_shape.cuh"
 #include "sm100_primitives.cuh"
 
 #include <math_constants.h>
@@ -292,6 +293,77 @@ __device__ __forceinline__ void write_ds(uint32_t dp_col, const float (&pv)[64],
   }
 }
 
+// ------------------------------------------------------------------ shaped scores
+// Key tiles [top - n, top) that the rows of query tile i see, n >= 1: a tile whose rows see no
+// key visits one tile with everything masked (its dQ is the zero that this gives).
+__device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n) {
+  const int first = i * BT, last = min(first + BT, p.N) - 1;
+  const int lo = shape_lo(p.shape, (long long)b * p.N + first, first);
+  const int hi = shape_hi(p.shape, (long long)b * p.N + last, last, p.N, p.causal);
+  const int t0 = min(lo / BT, nt - 1);
+  top = lo < hi ? (hi + BT - 1) / BT : t0 + 1;
+  n = max(top - t0, 1);
+}
+// First of the query tiles [from, nt) that reaches past key `key` (its last row's end is above
+// it), or with kBegin first that starts past it (its first row's begin is above it). The
+// bounds are monotone, so both are bisections.
+template <bool kBegin>
+__device__ __forceinline__ int shaped_tile_search(const BwdParams& p, int b, int from, int nt, int key) {
+  int a = from, e = nt;
+  while (a < e) {
+    const int m = (a + e) >> 1;
+    const int row = kBegin ? m * BT : min((m + 1) * BT, p.N) - 1;
+    const long long gr = (long long)b * p.N + row;
+    const bool past = kBegin ? shape_lo(p.shape, gr, row) > key : shape_hi(p.shape, gr, row, p.N, p.causal) > key;
+    if (past)
+      e = m;
+    else
+      a = m + 1;
+  }
+  return a;
+}
+// Query tiles [i0, i0 + n) that see a key of key tile j, n >= 1 (a key tile that no row sees
+// visits one with everything masked: its dK and dV are the zeros that this gives).
+__device__ __forceinline__ void shaped_query_tiles(const BwdParams& p, int b, int j, int nt, int& i0, int& n) {
+  i0 = min(shaped_tile_search<false>(p, b, p.causal ? j : 0, nt, j * BT), nt - 1);
+  n = max(shaped_tile_search<true>(p, b, i0, nt, min((j + 1) * BT, p.N) - 1) - i0, 1);
+}
+// First row of [from, to) whose end (kBegin: begin) is above `key`, or `to`.
+template <bool kBegin>
+__device__ __forceinline__ int shaped_row_search(const BwdParams& p, int b, int from, int to, int key) {
+  while (from < to) {
+    const int m = (from + to) >> 1;
+    const long long gr = (long long)b * p.N + m;
+    const bool past = kBegin ? shape_lo(p.shape, gr, m) > key : shape_hi(p.shape, gr, m, p.N, p.causal) > key;
+    if (past)
+      to = m;
+    else
+      from = m + 1;
+  }
+  return from;
+}
+// Constants of a head's scores in log2 units.
+struct ShapeConsts {
+  float sl2, cap2, capk, slope2;
+  __device__ __forceinline__ ShapeConsts(const BwdParams& p, int h)
+      : sl2(p.scale * kLog2e), cap2(p.shape.cap * kLog2e), capk(p.shape.cap > 0.f ? 2.f * p.scale * kLog2e / p.shape.cap : 0.f),
+        slope2(p.shape.slopes ? -__ldg(p.shape.slopes + h) * kLog2e : 0.f) {}
+};
+// P = 2^(score + nl2) of one raw product s at signed distance `dist`, and f, the factor that the
+// cap puts on dS (1 - tanh^2).
+__device__ __forceinline__ float shaped_p(const ShapeConsts& k, bool cap, float s, float dist, float nl2, float& f) {
+  float y;
+  if (cap) {
+    const float r = tanh_r(s * k.capk);
+    y = fmaf(-2.f * k.cap2, r, k.cap2);
+    f = 4.f * r * (1.f - r);
+  } else {
+    y = s * k.sl2;
+    f = 1.f;
+  }
+  return ex2(fmaf(k.slope2, fabsf(dist), y) + nl2);
+}
+
 // 64 consecutive fp32 TMEM columns of this lane.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   uint32_t (&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
@@ -335,7 +407,7 @@ enum : int {
   kAccFull = 10, kAccEmpty = 11, kMmaDone = 12, kDvFull = 13
 };
 
-template <int D>
+template <int D, bool kShaped>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -387,6 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = head / p.Hkv;
     hkv = head - b * p.Hkv;
   };
+  // query tiles [i0, i0 + ni) of an item
+  auto tiles = [&](int b, int j, int& i0, int& ni) {
+    if constexpr (kShaped) {
+      shaped_query_tiles(p, b, j, nt, i0, ni);
+    } else {
+      i0 = p.causal ? j : 0;
+      ni = nt - i0;
+    }
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -402,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tile<D>(sb + Lay::kOffK, &tk, bar(kKvFull), hkv, b * p.N + j * BT, pol_kv);
         load_tile<D>(sb + Lay::kOffV, &tv, bar(kKvFull), hkv, b * p.N + j * BT, pol_kv);
         ++nkv;
-        const int i0 = p.causal ? j : 0, ni = nt - i0;
+        int i0, ni;
+        tiles(b, j, i0, ni);
         for (int t = 0; t < G * ni; ++t) {
           const int h = hkv * G + t / ni, i = i0 + t % ni;
           const uint32_t st = nqd & 1, base = sb + Lay::kOffRing + st * Lay::kStage;
@@ -436,7 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
         int b, hkv, j;
         item(it, b, hkv, j);
-        const int i0 = p.causal ? j : 0, steps = G * (nt - i0);
+        int i0, ni;
+        tiles(b, j, i0, ni);
+        const int steps = G * ni;
         if (!mbar_wait(bar(kKvFull), nkv & 1, abort, p.status, p.wait_ns)) break;
         ++nkv;
         tc_fence_after();
@@ -552,7 +636,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
       int b, hkv, j;
       item(it, b, hkv, j);
-      const int i0 = p.causal ? j : 0, ni = nt - i0;
+      int i0, ni;
+      tiles(b, j, i0, ni);
+      // shaped: the queries [qa, qb) that see this thread's key (none for a key past the sequence)
+      int qa = 0, qb = 0;
+      if constexpr (kShaped) {
+        const int key = j * BT + r, end = min((i0 + ni) * BT, p.N);
+        if (key < p.N) {
+          qa = shaped_row_search<false>(p, b, i0 * BT, end, key);
+          qb = shaped_row_search<true>(p, b, qa, end, key);
+        }
+      }
       for (int t = 0; t < G * ni; ++t) {
         const int i = i0 + t % ni;
         const uint32_t st = nqd & 1;
@@ -566,7 +660,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_try_wait(bar(kQdFull + st), (nqd >> 1) & 1);
         tc_fence_after();
         float pv[64];
-        {
+        if constexpr (kShaped) {
+          uint32_t u[64];
+          tmem_ld64(s_col, u);
+          const float* nl = vec + cb;
+          const ShapeConsts k(p, hkv * G + t / ni);
+          const bool cap = p.shape.cap > 0.f;
+          const float dist = (float)(i * BT + cb - (j * BT + r));  // query of column 0 minus the key
+          const int va = qa - i * BT - cb, vb = qb - i * BT - cb;  // visible columns [va, vb)
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float f0, f1;
+            float p0 = shaped_p(k, cap, __uint_as_float(u[c]), dist + (float)c, nl[c], f0);
+            float p1 = shaped_p(k, cap, __uint_as_float(u[c + 1]), dist + (float)(c + 1), nl[c + 1], f1);
+            p0 = c >= va && c < vb ? p0 : 0.f;
+            p1 = c + 1 >= va && c + 1 < vb ? p1 : 0.f;
+            pk[c / 2] = pack_bf16x2(p0, p1);
+            pv[c] = p0 * f0;  // dS = (P f) o (dP - D)
+            pv[c + 1] = p1 * f1;
+          }
+          tmem_st32(s_col, pk);
+        } else {
           uint32_t u[64];
           tmem_ld64(s_col, u);
           const bool diag = p.causal && i == j;       // queries before this key are masked
@@ -586,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pv[c + 3] = (diag && cb + c + 3 < r) ? 0.f : ex2(x3);
           }
         }
-        {
+        if constexpr (!kShaped) {
           uint32_t pk[32];  // P^T in bf16 over the first 32 of this warpgroup's S^T columns
 #pragma unroll
           for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
@@ -682,7 +797,7 @@ enum : int {
 // written while dS of this one still feeds dQ += dS K.
 constexpr uint32_t kColDs = 384;
 
-template <int D>
+template <int D, bool kShaped>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -733,6 +848,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = head / p.Hq;
     h = head - b * p.Hq;
   };
+  // key tiles [top - jn, top) of an item, from the highest down
+  auto tiles = [&](int b, int i, int& top, int& jn) {
+    if constexpr (kShaped)
+      shaped_key_tiles(p, b, i, nt, top, jn);
+    else
+      top = jn = p.causal ? i + 1 : nt;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -748,7 +870,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tile<D>(sb + Lay::kOffQ, &tq, bar(kQFull), h, b * p.N + i * BT, pol_q);
         load_tile<D>(sb + Lay::kOffDO, &tdo, bar(kQFull), h, b * p.N + i * BT, pol_q);
         ++nq;
-        const int jn = p.causal ? i + 1 : nt, hkv = h / G;
+        int top, jn;
+        tiles(b, i, top, jn);
+        const int hkv = h / G;
         for (int j = 0; j < jn; ++j) {
           // K_j (stage j mod 3) and V_j (stage j mod 2) land on one barrier, QKvFull j mod 2:
           // the MMA issuer waits once for both (S_j comes before dP_j). Two slots suffice:
@@ -761,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(bar(kQKvFull + vs), 2 * Lay::kTile);
-          const int kt = jn - 1 - j;  // key tiles from the diagonal down
+          const int kt = top - 1 - j;  // key tiles from the diagonal down
           load_tile<D>(sb + Lay::kOffK + ks * Lay::kTile, &tk, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           load_tile<D>(sb + Lay::kOffV + vs * Lay::kTile, &tv, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           ++nk;
@@ -810,7 +934,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
         int b, h, i;
         item(it, b, h, i);
-        const int jn = p.causal ? i + 1 : nt;
+        int top, jn;
+        tiles(b, i, top, jn);
         if (!mbar_wait(bar(kQFull), nq & 1, abort, p.status, p.wait_ns)) break;
         ++nq;
         if (!issue_s(n) || !issue_dp(n)) break;
@@ -901,8 +1026,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
       int b, h, i;
       item(it, b, h, i);
-      const int jn = p.causal ? i + 1 : nt;
+      int top, jn;
+      tiles(b, i, top, jn);
       const int qrow = i * BT + r;
+      // shaped: the keys [klo, khi) that this thread's query sees
+      int klo = 0, khi = 0;
+      if constexpr (kShaped) {
+        if (qrow < p.N) {
+          klo = shape_lo(p.shape, (long long)b * p.N + qrow, qrow);
+          khi = shape_hi(p.shape, (long long)b * p.N + qrow, qrow, p.N, p.causal);
+          // ranges that are not monotone: the row's keys are not all among its tile's
+          if (klo < khi && (klo < (top - jn) * BT || khi > top * BT)) record_status(p.status, kStatusDeviceCheck);
+        }
+      }
       const size_t vrow = (size_t)(b * p.Hq + h) * p.Npad + qrow;
       if (warp == 4 && lane == 0) atomicAdd(const_cast<int*>(items_started), 1);
       // the item's four 32-row blocks of vectors are in the workspace
@@ -918,11 +1054,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         tc_fence_after();
         float pv[64];
-        {
+        if constexpr (kShaped) {
+          uint32_t u[64];
+          tmem_ld64(s_col, u);
+          const ShapeConsts k(p, h);
+          const bool cap = p.shape.cap > 0.f;
+          const int kb = (top - 1 - j) * BT + cb;       // key of column 0
+          const float dist = (float)(qrow - kb);
+          const int va = klo - kb, vb = khi - kb;       // visible columns [va, vb)
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float f;
+            const float pc = shaped_p(k, cap, __uint_as_float(u[c]), dist - (float)c, nl2, f);
+            pv[c] = c >= va && c < vb ? pc * f : 0.f;
+          }
+        } else {
           uint32_t u[64];
           tmem_ld64(s_col, u);
           // visible keys of this tile: column c < lim
-          const int lim = min(p.causal ? qrow + 1 : p.N, p.N) - (jn - 1 - j) * BT - cb;  // key tile jn - 1 - j
+          const int lim = min(p.causal ? qrow + 1 : p.N, p.N) - (top - 1 - j) * BT - cb;  // key tile top - 1 - j
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
             float x0, x1;
@@ -979,14 +1129,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kShaped>
 cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
                          cudaStream_t stream) {
   const int nt = (p.N + BT - 1) / BT;
   cudaError_t e;
   {  // dQ, and the two per-row vectors the dK/dV pass reads
-    auto kern = bwd_dq_kernel<D>;
+    auto kern = bwd_dq_kernel<D, kShaped>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<D>::kBytes);
     if (e != cudaSuccess) return e;
     const long long items = (long long)p.B * p.Hq * nt;
@@ -996,7 +1146,7 @@ cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtens
     if (e != cudaSuccess) return e;
   }
   {
-    auto kern = bwd_dkdv_kernel<D>;
+    auto kern = bwd_dkdv_kernel<D, kShaped>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
     if (e != cudaSuccess) return e;
     const long long items = (long long)p.B * p.Hkv * nt;
@@ -1012,8 +1162,11 @@ cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtens
 cudaError_t launch_backward(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
                             cudaStream_t stream) {
-  if (p.d == 128) return launch_bwd_t<128>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
-  return launch_bwd_t<64>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  if (p.shaped)
+    return p.d == 128 ? launch_bwd_t<128, true>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream)
+                      : launch_bwd_t<64, true>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  if (p.d == 128) return launch_bwd_t<128, false>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  return launch_bwd_t<64, false>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
 }
 
 }  // namespace fattn

@@ -19,6 +19,7 @@
 // separate merge launch is needed.
 #include "device_common.cuh"
 #include "fattn_internal.h"
+#include "score_shape.cuh"
 
 #include <math_constants.h>
 
@@ -80,9 +81,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // Partial (lse_s, O_s / l_s) of one non-empty split [t0, t1) of sequence b
 // for the query heads h0 .. h0 + rows_valid - 1 of KV head hkv.
-template <int D, bool kPage16>
+// Shaped: the scores get p.shape's cap and distance bias; the query sits at position `qpos`.
+template <int D, bool kPage16, bool kShaped>
 __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* smem, int split, int b, int hkv, int h0,
-                                             int rows_valid, int t0, int t1) {
+                                             int rows_valid, int t0, int t1, int qpos) {
   using Lay = DecodeLayout<D>;
   constexpr int U = D / 8;
   const uint32_t sbase = smem_u32(smem);
@@ -149,6 +151,15 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
   };
 
   const float sl2 = p.scale * kLog2e;
+  // shaped: constants in log2 units, and the slopes of this thread's rows g and g + 8
+  const float cap2 = kShaped ? p.shape.cap * kLog2e : 0.f;
+  const float capk = kShaped && p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
+  float slope0 = 0.f, slope1 = 0.f;
+  if (kShaped && p.shape.slopes) {
+    const int g = lane >> 2;
+    if (g < rows_valid) slope0 = -__ldg(p.shape.slopes + h0 + g) * kLog2e;
+    if (g + 8 < rows_valid) slope1 = -__ldg(p.shape.slopes + h0 + g + 8) * kLog2e;
+  }
   float o[D / 8][4];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -195,7 +206,14 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
       for (int j = 0; j < 4; ++j) {
         const int tok = nt * 8 + 2 * (lane & 3) + (j & 1);
         const bool ok = (vm >> tok) & 1u;
-        s[nt][j] = ok ? s[nt][j] * sl2 : -CUDART_INF_F;
+        float y;
+        if constexpr (kShaped) {
+          y = p.shape.cap > 0.f ? fmaf(-2.f * cap2, tanh_r(s[nt][j] * capk), cap2) : s[nt][j] * sl2;
+          y = fmaf(j < 2 ? slope0 : slope1, (float)(qpos - (t0 + (warp + i * kWarps) * kChunk + tok)), y);
+        } else {
+          y = s[nt][j] * sl2;
+        }
+        s[nt][j] = ok ? y : -CUDART_INF_F;
       }
       mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
       mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
@@ -326,7 +344,7 @@ __device__ __forceinline__ void merge_group(const DecodeParams& p, int b, int h0
   }
 }
 
-template <int D, bool kPage16>
+template <int D, bool kPage16, bool kShaped>
 __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_item, s_last;
@@ -336,7 +354,12 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams 
   const int groups = p.B * groups_per_seq;
   const int total = p.num_splits * groups;
   const int cap = p.max_pages_per_seq * p.page_size;
-  const int chunk_pages = (p.max_pages_per_seq + p.num_splits - 1) / p.num_splits;
+  // the splits share the pages that a query can see: all of them, or with a window W the
+  // most that W consecutive tokens touch, counted from the page of the first visible token
+  int seen_pages = p.max_pages_per_seq;
+  if (kShaped && p.shape.window > 0 && p.shape.window <= cap - p.page_size)
+    seen_pages = min(seen_pages, (p.shape.window + p.page_size - 2) / p.page_size + 1);
+  const int chunk_pages = (seen_pages + p.num_splits - 1) / p.num_splits;
   const long long span = (long long)chunk_pages * p.page_size;
   for (;;) {
     if (threadIdx.x == 0) s_item = atomicAdd(p.counters, 1);
@@ -357,15 +380,21 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams 
       if (threadIdx.x == 0 && split == 0) record_status(p.status, kStatusDeviceCheck);
       L = L < 0 ? 0 : cap;
     }
-    const int nvalid = (int)((L + span - 1) / span);   // non-empty splits of this sequence
-    const long long t0 = (long long)split * span;
+    int lo = 0, first = 0;                             // first visible token, first token of its page
+    if (kShaped && p.shape.window > 0 && L > p.shape.window) {
+      lo = L - p.shape.window;
+      first = lo / p.page_size * p.page_size;
+    }
+    const int nvalid = (int)((L - first + span - 1) / span);   // non-empty splits of this sequence
+    const long long t0 = first + (long long)split * span;
     if (t0 >= L) {  // empty split: mark it, and a sequence with no key at all gets O = 0, lse = -inf
       if (threadIdx.x < rows_valid)
         p.lse_part[((size_t)b * p.Hq + h0 + threadIdx.x) * p.num_splits + split] = -CUDART_INF_F;
       if (split == 0) merge_group<D>(p, b, h0, rows_valid, 0);
       continue;
     }
-    decode_split<D, kPage16>(p, smem, split, b, hkv, h0, rows_valid, (int)t0, (int)min((long long)L, t0 + span));
+    decode_split<D, kPage16, kShaped>(p, smem, split, b, hkv, h0, rows_valid, max((int)t0, lo),
+                                      (int)min((long long)L, t0 + span), L - 1);
     // publish the partial, count it, and let the last split of the group merge
     __threadfence();
     __syncthreads();
@@ -452,10 +481,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
   }
 }
 
-template <int D, bool kPage16>
+template <int D, bool kPage16, bool kShaped>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   using Lay = DecodeLayout<D>;
-  auto kern = decode_kernel<D, kPage16>;
+  auto kern = decode_kernel<D, kPage16, kShaped>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kBytes);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
@@ -476,10 +505,14 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+template <int D, bool kShaped>
+static cudaError_t launch_decode_d(const DecodeParams& p, cudaStream_t stream) {
+  return p.page_size == 16 ? launch_decode_t<D, true, kShaped>(p, stream) : launch_decode_t<D, false, kShaped>(p, stream);
+}
+
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-  const bool p16 = p.page_size == 16;
-  if (p.d == 128) return p16 ? launch_decode_t<128, true>(p, stream) : launch_decode_t<128, false>(p, stream);
-  return p16 ? launch_decode_t<64, true>(p, stream) : launch_decode_t<64, false>(p, stream);
+  if (p.shaped) return p.d == 128 ? launch_decode_d<128, true>(p, stream) : launch_decode_d<64, true>(p, stream);
+  return p.d == 128 ? launch_decode_d<128, false>(p, stream) : launch_decode_d<64, false>(p, stream);
 }
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {

@@ -15,6 +15,15 @@ enum : int { kStatusOk = 0, kStatusTimeout = 5, kStatusDeviceCheck = 6 };
 // Limit of one pipeline wait unless a test sets another (fattn_debug_set_wait_limit).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 
+// Shape of the scores (all off when zero): tanh cap, distance bias, window and key ranges.
+struct ScoreShape {
+  float cap;                // s = cap tanh(s / cap); 0: none
+  const float* slopes;      // device [Hq]: s -= slope_h |pos - j|; nullptr: none
+  int window;               // |pos - j| < window; 0: none
+  const int32_t* key_begin; // device, one per query row, non-decreasing in a sequence: keys
+  const int32_t* key_end;   // [begin, end) are visible; nullptr: no bound
+};
+
 // Problem description shared by both prefill kernels.
 struct PrefillParams {
   const void* q;
@@ -48,6 +57,9 @@ struct PrefillParams {
   // scale * q_descale * k_descale
   int fp8;
   float v_descale;
+  // shaped variant only (dense, or paged with a block table)
+  int shaped;
+  ScoreShape shape;
   // bounded pipeline waits: each mbarrier wait gives up after wait_ns; debug_stall != 0
   // (test hook) makes the softmax / element-wise warps first wait on a barrier that no
   // role arrives on, so that the wait runs out and every role takes the abort exit
@@ -81,6 +93,8 @@ struct DecodeParams {
   int B, Hq, Hkv, d, page_size, max_pages_per_seq, num_pages, num_splits;
   float scale;
   int* status;
+  int shaped;       // shaped variant: scores formed with `shape` (no key ranges)
+  ScoreShape shape;
 };
 
 // Split-KV decode with the merge fused in (one launch, after a memset of the counters).
@@ -116,6 +130,8 @@ struct BwdParams {
   int causal;
   float scale;
   int* status;
+  int shaped;                 // shaped variant: scores formed with `shape`
+  ScoreShape shape;
   // bounded pipeline waits: each mbarrier wait gives up after wait_ns; debug_stall != 0
   // (test hook) makes the softmax / element-wise warps first wait on a barrier that no
   // role arrives on, so that the wait runs out and every role takes the abort exit

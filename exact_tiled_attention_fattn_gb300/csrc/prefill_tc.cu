@@ -62,6 +62,7 @@
 // copies and MMAs are drained, TMEM is freed and the kernel returns.
 #include "device_common.cuh"
 #include "fattn_internal.h"
+#include "score_shape.cuh"
 #include "sm100_primitives.cuh"
 
 #include <cuda_fp8.h>
@@ -120,16 +121,18 @@ enum : int {
   kBarSFree = kBarMaskFull + 2 * kMaskSlotsMax, kBarPvDone = kBarSFree + 2, kBarCount = kBarPvDone + 2
 };
 
-enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4 };
+enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4, kModeShaped = 5,
+       kModeShapedPaged = 6 };
+__host__ __device__ constexpr bool mode_shaped(int m) { return m == kModeShaped || m == kModeShapedPaged; }
 
 template <int D, int kMode>
 struct TcLayout {
   static constexpr bool kFp8 = kMode == kModeFp8;
   // S_t(j + 1) issued as soon as the softmax has read S_t(j), not after P_t(j) V, where P
-  // does not overwrite S: the dense, paged and masked variants at d = 64 (S_A, S_B, O_A and O_B take 384 TMEM
+  // does not overwrite S: the dense, paged, masked and shaped variants at d = 64 (S_A, S_B, O_A and O_B take 384 TMEM
   // columns, so P_A and P_B get buffers of their own in the other 128, bf16 pairs, 64
   // columns each) and the FP8 variant (P in shared memory).
-  static constexpr bool kPTmem = (kMode == kModeDense || kMode == kModePaged || kMode == kModeMasked) && D == 64;
+  static constexpr bool kPTmem = (kMode == kModeDense || kMode == kModePaged || kMode == kModeMasked || mode_shaped(kMode)) && D == 64;
   static constexpr bool kEarly = kPTmem || kFp8;
   static constexpr int kElem = kFp8 ? 1 : 2;      // bytes per Q/K/V element (E4M3 or bf16)
   static constexpr int kQBytes = BM * D * kElem;  // one Q tile
@@ -171,6 +174,9 @@ struct Item {
   int b, h, base, row0, L;  // L: query rows of the sequence (its length, or the chunk's)
   int Lk, off;              // keys of the sequence; query i sees keys j <= i + off if causal
   int n[2];   // K/V tiles tile A / tile B must visit (0: tile B has no row of the sequence)
+  // shaped variant: tile t visits K/V tiles [top[t] - n[t], top[t]); the item's steps run from
+  // tile jtop - 1 down to jbot, over both tiles' ranges (n = 0 as well where no row sees a key)
+  int top[2], jtop, jbot;
   bool valid;
 };
 
@@ -212,8 +218,10 @@ __device__ __forceinline__ int item_index(const Schedule& s, int k) {
   return idx < s.total ? idx : -1;
 }
 
+template <bool kShaped>
 __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedule& s, int it) {
   Item x;
+  x.top[0] = x.top[1] = x.jtop = x.jbot = 0;
   const int per_group = s.group * s.pairs;
   const int g = it / per_group;
   const int rem = it - g * per_group;
@@ -247,6 +255,27 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
   x.valid = x.base < x.L;
   const int kv_tiles = (x.Lk + BN - 1) / BN;
   const bool has_b = x.base + BM < x.L;
+  if constexpr (kShaped) {
+    // the bounds are monotone: a tile's first row has its lowest key, its last row its highest
+    x.n[0] = x.n[1] = 0;
+    x.jbot = 1 << 30;
+    if (x.valid) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t && !has_b) continue;
+        const int first = x.base + t * BM, last = min(first + BM, x.L) - 1;
+        const int lo = shape_lo(p.shape, (long long)x.row0 + first, first + x.off);
+        const int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
+        if (lo < hi) {
+          x.top[t] = (hi + BN - 1) / BN;
+          x.n[t] = x.top[t] - lo / BN;
+          x.jtop = max(x.jtop, x.top[t]);
+          x.jbot = min(x.jbot, lo / BN);
+        }
+      }
+    }
+    return x;
+  }
   if (p.causal) {  // up to the key the tile's last row sees
     x.n[0] = min((min(x.base + BM, x.L) - 1 + x.off) / BN + 1, kv_tiles);
     x.n[1] = has_b ? min((min(x.base + 2 * BM, x.L) - 1 + x.off) / BN + 1, kv_tiles) : 0;
@@ -308,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                       const PrefillParams p) {
   constexpr bool kSparse = kMode == kModeSparse;  // fixed block mask, zero blocks skipped
-  constexpr bool kPaged = kMode == kModePaged;    // K/V through a block table
+  constexpr bool kPaged = kMode == kModePaged || kMode == kModeShapedPaged;  // K/V through a block table
+  constexpr bool kShaped = mode_shaped(kMode);    // tanh cap, distance bias, window, key ranges
   constexpr bool kMasked = kMode == kModeMasked;  // additive bf16 mask M on the scores
   constexpr bool kFp8 = kMode == kModeFp8;        // E4M3 Q, K, V; P in E4M3 through shared memory
   // key tiles visited from the last (the diagonal under the causal rule) down to 0, so that the
@@ -371,10 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0;; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item(p, sch, it);
+        const Item x = decode_item<kShaped>(p, sch, it);
         if (!x.valid) continue;
         const int hkv = x.h / G;
-        const int n = max(x.n[0], x.n[1]);
+        const int n = kShaped ? x.jtop - x.jbot : max(x.n[0], x.n[1]);
+        const int kv_top = kShaped ? x.jtop : n;  // the steps' K/V tiles: kv_top - 1 down
+        if (kShaped && n <= 0) continue;          // no row of the item sees a key
         const uint32_t* mw = nullptr;
         if constexpr (kSparse) {
           if (!mbar_wait(bar(kBarMaskFull + nm % kMaskSlots), (nm / kMaskSlots) & 1, abort, p.status, p.wait_ns))
@@ -463,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             if (leader) mbar_arrive_expect_tx(bar(kBarKvFull + st), ((s < n) + (s > 0)) * Lay::kKVBytes);
-            if (s < n) issue_kv(&tk, sb + Lay::kOffK + st * Lay::kKVBytes, bar(kBarKvFull + st), kReverse ? n - 1 - s : s, false);
-            if (s > 0) issue_kv(&tv, sb + Lay::kOffV + st * Lay::kKVBytes, bar(kBarKvFull + st), kReverse ? n - s : s - 1, true);
+            if (s < n) issue_kv(&tk, sb + Lay::kOffK + st * Lay::kKVBytes, bar(kBarKvFull + st), kReverse ? kv_top - 1 - s : s, false);
+            if (s > 0) issue_kv(&tv, sb + Lay::kOffV + st * Lay::kKVBytes, bar(kBarKvFull + st), kReverse ? kv_top - s : s - 1, true);
             ++nk;
           }
         }
@@ -551,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item(p, sch, it);
+        const Item x = decode_item<kShaped>(p, sch, it);
         if (!x.valid) continue;
         if constexpr (kSparse) {
           // walk the blocks either tile keeps: per block j, O_t += P_t(prev) V_prev for each tile
@@ -616,9 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int nA = x.n[0], nB = x.n[1];
-        const int n = max(nA, nB);
-        // tile t takes part in steps [f_t, f_t + n_t) (reverse order: the last n_t steps)
-        const int fA = kReverse ? n - nA : 0, fB = kReverse ? n - nB : 0;
+        const int n = kShaped ? x.jtop - x.jbot : max(nA, nB);
+        if (kShaped && n <= 0) continue;
+        // tile t takes part in steps [f_t, f_t + n_t) (reverse order: the last n_t steps; shaped:
+        // from the step of its highest K/V tile)
+        const int fA = kShaped ? x.jtop - x.top[0] : kReverse ? n - nA : 0;
+        const int fB = kShaped ? x.jtop - x.top[1] : kReverse ? n - nB : 0;
         auto in_a = [&](int s) { return s >= fA && s < fA + nA; };
         auto in_b = [&](int s) { return s >= fB && s < fB + nB; };
         if (!mbar_wait(bar(kBarQFull), nq & 1, abort, p.status, p.wait_ns)) break;
@@ -725,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0;; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item(p, sch, it);
+      const Item x = decode_item<kShaped>(p, sch, it);
       if (!x.valid) continue;
       if (!warp_wait(bar(kBarMaskEmpty + nm % kMaskSlots), ((nm / kMaskSlots) & 1) ^ 1, abort, p.status, p.wait_ns)) break;
       uint32_t* w = reinterpret_cast<uint32_t*>(smem + Lay::kOffMask + (nm % kMaskSlots) * kMaskSlotBytes);
@@ -779,6 +814,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool neg = sl2 < 0.f;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint64_t scale2 = f2_pack(p.scale, p.scale);
+    // shaped variant: capped, biased or negatively scaled scores are brought to log2 units
+    // before the row maximum, others stay as the product left them (shape_mul = sl2)
+    const bool log2_units = kShaped && (p.shape.cap > 0.f || p.shape.slopes != nullptr || !(sl2 > 0.f));
+    const float shape_mul = log2_units ? 1.f : sl2;
+    const float cap2 = kShaped ? p.shape.cap * kLog2e : 0.f;
+    const float capk = kShaped && p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
     uint32_t ns = 0, no = 0;                 // S_t and O_t completions seen
     uint32_t npv = 0;                        // O_t += P_t V completions seen (dense d = 64)
     const uint32_t p_col = tmem + lane_off + (Lay::kPTmem ? Lay::col_p(t) : Lay::col_s(t));
@@ -794,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item(p, sch, it);
+      const Item x = decode_item<kShaped>(p, sch, it);
       if (!x.valid) continue;
       const uint32_t* mw = nullptr;
       // this tile's K/V tile count, selected rather than indexed (a run-time index into the
@@ -816,12 +857,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nm;
         }
       };
+      const int row = x.base + t * BM + r;
       if (nt == 0) {
         release_mask();
+        if constexpr (kShaped) {  // no row of the tile sees a key: O = 0, lse = -inf
+          if (row < x.L) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
+                                                  ((size_t)(x.row0 + row) * p.Hq + x.h) * D);
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+              p.lse[p.cu_seqlens ? (size_t)x.h * p.total_rows + x.row0 + row
+                                 : ((size_t)x.b * p.Hq + x.h) * p.N + row] = -CUDART_INF_F;
+          }
+        }
         continue;
       }
-      const int row = x.base + t * BM + r;
-      const int lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;  // keys < lim are visible
+      int lo = 0;  // keys lo <= j < lim are visible (lo > 0: shaped variant only)
+      int lim;
+      const int kv_hi = kShaped ? (t ? x.top[1] : x.top[0]) : nt;
+      const int pos = row + x.off;
+      float slope2 = 0.f;  // distance bias: -slope_h log2(e) per key of distance
+      if constexpr (kShaped) {
+        // (rows past the sequence take its last row's range: they are not written)
+        const int rc = min(row, x.L - 1);
+        lo = shape_lo(p.shape, (long long)x.row0 + rc, rc + x.off);
+        lim = shape_hi(p.shape, (long long)x.row0 + rc, rc + x.off, x.Lk, p.causal);
+        // ranges that are not monotone: the row's keys are not all among its tile's
+        if (lo < lim && (lo < (kv_hi - nt) * BN || lim > kv_hi * BN)) record_status(p.status, kStatusDeviceCheck);
+        if (p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
+      } else {
+        lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;
+      }
       if constexpr (kSparse) {  // a tile that keeps no block: O = 0, lse = -inf
         if (kept_blocks == 0) {
           release_mask();
@@ -843,7 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mrow = static_cast<const __nv_bfloat16*>(p.mask) + (size_t)x.b * p.mask_sb + (size_t)x.h * p.mask_sh +
                (size_t)min(row, x.L - 1) * p.mask_ld;
       BitWalk walk(mw, 1 << t, nt);
-      for (int j = kSparse ? walk.next() : (kReverse ? nt - 1 : 0); kSparse || kReverse ? j >= 0 : j < nt;
+      const int kv_lo = kShaped ? kv_hi - nt : 0;
+      for (int j = kSparse ? walk.next() : (kReverse ? kv_hi - 1 : 0); kSparse || kReverse ? j >= kv_lo : j < nt;
            j = kSparse ? walk.next() : (kReverse ? j - 1 : j + 1)) {
         // the tile's 128 mask entries, requested before waiting for S (16-byte loads
         // of whole 8-key groups; groups at or past the visible limit are not read)
@@ -952,7 +1020,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarSFree + t));
           }
         }
-        if (!kMasked && masked) {
+        if constexpr (kShaped) {
+          if (p.shape.cap > 0.f) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = fmaf(-2.f * cap2, tanh_r(s[c] * capk), cap2);
+          } else if (log2_units) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] *= sl2;
+          }
+          if (p.shape.slopes) {
+            const float dist = (float)(pos - kbase);
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = fmaf(slope2, fabsf(dist - (float)c), s[c]);
+          }
+          if (masked || kbase < lo) {
+            const uint32_t span = (uint32_t)max(lim - lo, 0), first_key = (uint32_t)(lo - kbase);
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if ((uint32_t)c - first_key >= span) s[c] = -CUDART_INF_F;
+          }
+          masked = false;
+        }
+        if (!kMasked && !kShaped && masked) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (kbase + c >= lim) s[c] = neg ? CUDART_INF_F : -CUDART_INF_F;
@@ -963,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] = s[i];
-          if (kMasked || !neg) {
+          if (kMasked || kShaped || !neg) {
 #pragma unroll
             for (int c = 8; c < BN; c += 16)
 #pragma unroll
@@ -977,13 +1066,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmin3(fmin3(a[0], a[1], a[2]), fmin3(a[3], a[4], a[5]), fminf(a[6], a[7]));
           }
         }
-        const float m_cand = fmaxf(m, mx * (kMasked ? kLog2e : sl2));  // the masked scores carry the scale
+        // (the masked scores carry the scale, the shaped ones the scale and log2(e) unless they
+        // are as the product left them)
+        const float m_cand = fmaxf(m, mx * (kMasked ? kLog2e : kShaped ? shape_mul : sl2));
         const bool need = m_cand > m + kLazyRescaleLog2;          // always true on the first tile
         const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
         const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
         const float alpha = ex2(m - base);                        // 1 when m is kept
         const uint64_t nbase2 = f2_pack(-base, -base);
-        const uint64_t mul2 = kMasked ? f2_pack(kLog2e, kLog2e) : sl2x2;
+        const uint64_t mul2 = kMasked ? f2_pack(kLog2e, kLog2e) : kShaped ? f2_pack(shape_mul, shape_mul) : sl2x2;
         constexpr int kAcc = kMasked ? 2 : 8;  // packed row-sum partials (fewer registers when masked)
         uint64_t acc2[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};  // row-sum partials, packed pairs
         // a column pair of P: bf16x2, or (FP8 variant) E4M3x2 in the low 16 bits
@@ -1083,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool live = row < x.L;
       // a row the mask left with no key: O = 0, lse = -inf
-      const float inv = (kMasked && l == 0.f) ? 0.f : (kFp8 ? p.v_descale : 1.f) / l;
+      const float inv = ((kMasked || kShaped) && l == 0.f) ? 0.f : (kFp8 ? p.v_descale : 1.f) / l;
       const int wrow0 = x.base + t * BM + q4 * 32;  // this warp's first row
       if (wrow0 + 32 <= x.L) {
         // all 32 rows of the warp lie in the sequence: stage each 64-column half in the
@@ -1134,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (live && p.lse) {
-        const float lse = (kMasked && l == 0.f) ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+        const float lse = ((kMasked || kShaped) && l == 0.f) ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
         if (p.cu_seqlens)
           p.lse[(size_t)x.h * p.total_rows + x.row0 + row] = lse;
         else
@@ -1175,6 +1266,13 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, con
   if (p.block_mask) {
     if (p.d == 128) return launch_t<128, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
     return launch_t<64, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
+  }
+  if (p.shaped) {
+    if (p.block_table)
+      return p.d == 128 ? launch_t<128, kModeShapedPaged>(p, tq, tk, tv, to, num_sms, stream)
+                        : launch_t<64, kModeShapedPaged>(p, tq, tk, tv, to, num_sms, stream);
+    return p.d == 128 ? launch_t<128, kModeShaped>(p, tq, tk, tv, to, num_sms, stream)
+                      : launch_t<64, kModeShaped>(p, tq, tk, tv, to, num_sms, stream);
   }
   if (p.block_table) {
     if (p.d == 128) return launch_t<128, kModePaged>(p, tq, tk, tv, to, num_sms, stream);

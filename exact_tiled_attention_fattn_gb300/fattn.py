@@ -57,6 +57,13 @@ SIGNATURES_OPS = {
                         _i, _i, _f, _i, _vp]),
     "fattn_rope_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                      _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _i, _f, _vp]),
+    "fattn_fwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _vp, _vp, _vp]),
+    "fattn_fwd_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                    _f, _vp, _i, _vp, _vp, _vp]),
+    "fattn_bwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i,
+                              _vp, _vp, _vp, _sz, _vp]),
+    "fattn_decode_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
+                                       _i, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -693,3 +700,180 @@ def rope_append_paged(q, k, v, kcache, vcache, block_table, seqlens_k, cu_seqlen
                                      1 if interleaved else 0, float(amplitude), ctypes.c_void_p(_stream_handle(stream)))
     _check("fattn_rope_append_paged", st)
     return out
+
+
+# ------------------------------------------------------------------ shaped scores
+def document_ranges(doc_ids, prefix_len=None):
+    """Key ranges (key_begin, key_end), int32 [B, N], of packed documents: ``doc_ids`` [B, N] names
+    each row's document, equal ids are contiguous; an id < 0 is padding, which sees nothing and is seen by
+    nobody. Every row sees its document; with ``prefix_len`` (tokens of every document that all of
+    it sees, an int) row i sees max(i + 1, document start + prefix_len), and without
+    ``causal`` in the call. Made once per batch, for every layer."""
+    if doc_ids.dim() != 2:
+        raise ValueError("doc_ids must be [B, N]")
+    B, N = doc_ids.shape
+    i = torch.arange(N, device=doc_ids.device).expand(B, N)
+    edge = torch.ones(B, N, dtype=torch.bool, device=doc_ids.device)
+    edge[:, 1:] = doc_ids[:, 1:] != doc_ids[:, :-1]
+    begin = torch.where(edge, i, 0).cummax(1)[0]
+    last = torch.ones_like(edge)
+    last[:, :-1] = edge[:, 1:]
+    end = torch.where(last, i + 1, N).flip(1).cummin(1)[0].flip(1)
+    if prefix_len is not None:
+        end = torch.minimum(end, torch.maximum(i + 1, begin + int(prefix_len)))
+    end = torch.where(doc_ids < 0, begin, end)
+    return begin.to(torch.int32).contiguous(), end.to(torch.int32).contiguous()
+
+
+def _check_shape(slopes, Hq, key_begin, key_end, range_shape):
+    _need_cuda(slopes, key_begin, key_end)
+    _expect(slopes, (Hq,), "slopes", torch.float32)
+    _expect(key_begin, range_shape, "key_begin", torch.int32)
+    _expect(key_end, range_shape, "key_end", torch.int32)
+
+
+def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softcap: float = 0.0, slopes=None,
+               window: int = 0, key_begin=None, key_end=None, out=None, lse=None, want_lse: bool = True, stream=None):
+    """Prefill with shaped scores: s = scale q.k, then s = softcap tanh(s / softcap) (softcap > 0), then
+    s -= slopes[h] |i - j| (slopes fp32 [Hq]); key j is visible iff j <= i (causal), |i - j| < window
+    (window > 0) and key_begin[b, i] <= j < key_end[b, i] (int32 [B, N], non-decreasing along N:
+    ``document_ranges``). q [B,N,Hq,d], k, v [B,N,Hkv,d] bf16, d 64 or 128. Returns (O, lse [B,Hq,N]); a row that
+    sees no key gets O = 0, lse = -inf."""
+    lib = load_library()
+    _need_cuda(q, k, v, out, lse)
+    if not (q.dtype == k.dtype == v.dtype == torch.bfloat16):
+        raise TypeError("shaped prefill takes bf16 q, k, v")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [B,N,Hq,d] and k [B,N,Hkv,d] expected")
+    B, N, Hq, d = q.shape
+    _expect(k, (B, N, k.shape[2], d), "k")
+    _expect(v, k.shape, "v")
+    _expect(out, q.shape, "out", q.dtype)
+    _expect(lse, (B, Hq, N), "lse", torch.float32)
+    _check_shape(slopes, Hq, key_begin, key_end, (B, N))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
+    st = lib.fattn_fwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
+                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
+                              _ptr(key_begin), _ptr(key_end), ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_fwd_shaped", st)
+    return out, lse
+
+
+def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int, causal: bool = True,
+                     scale: float | None = None, softcap: float = 0.0, slopes=None, window: int = 0, key_begin=None,
+                     key_end=None, out=None, lse=None, want_lse: bool = True, stream=None):
+    """``fwd_paged`` with the shaped scores of ``fwd_shaped``; a chunk's queries sit at the last positions
+    of their sequence's context. key_begin / key_end int32 [Tq], keys of the row's sequence.
+    Returns (O [Tq,Hq,d], lse [Hq,Tq])."""
+    lib = load_library()
+    _need_cuda(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, out, lse)
+    if not (q.dtype == kcache.dtype == vcache.dtype == torch.bfloat16):
+        raise TypeError("paged prefill takes bf16 q and caches")
+    if seqlens_k.dtype != torch.int32 or cu_seqlens_q.dtype != torch.int32:
+        raise TypeError("seqlens_k and cu_seqlens_q must be int32")
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, d]")
+    Tq, Hq, d = q.shape
+    B = cu_seqlens_q.numel() - 1
+    _check_paged_cache(kcache, vcache, block_table, B)
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _expect(kcache, (num_pages, page_size, Hkv, d), "kcache")
+    _expect(seqlens_k, (B,), "seqlens_k")
+    _expect(out, q.shape, "out", q.dtype)
+    _expect(lse, (Hq, Tq), "lse", torch.float32)
+    _check_shape(slopes, Hq, key_begin, key_end, (Tq,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
+                                    _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
+                                    block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
+                                    float(scale), float(softcap), _ptr(slopes), int(window), _ptr(key_begin),
+                                    _ptr(key_end), ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_fwd_paged_shaped", st)
+    return out, lse
+
+
+def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
+               slopes=None, window: int = 0, key_begin=None, key_end=None, dq=None, dk=None, dv=None, workspace=None,
+               stream=None):
+    """Gradients of ``fwd_shaped`` (same arguments; o and lse are its outputs) with respect to q, k and v;
+    the slopes are constants. Returns (dq, dk, dv), bf16 in the input layouts."""
+    lib = load_library()
+    _need_cuda(q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    if not (q.dtype == k.dtype == v.dtype == o.dtype == dout.dtype == torch.bfloat16):
+        raise TypeError("backward takes bf16 q, k, v, o and dout")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, d] and k [B, N, Hkv, d]")
+    B, N, Hq, d = q.shape
+    Hkv = k.shape[2]
+    _expect(k, (B, N, Hkv, d), "k")
+    _expect(v, k.shape, "v")
+    _expect(o, q.shape, "o")
+    _expect(dout, q.shape, "dout")
+    _expect(lse, (B, Hq, N), "lse", torch.float32)
+    _expect(dq, q.shape, "dq", q.dtype)
+    _expect(dk, k.shape, "dk", q.dtype)
+    _expect(dv, k.shape, "dv", q.dtype)
+    _check_shape(slopes, Hq, key_begin, key_end, (B, N))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if workspace is None:
+        workspace = torch.empty(max(bwd_workspace_size(B, Hq, N), 1), dtype=torch.uint8, device=q.device)
+    st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+                              B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
+                              int(window), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_bwd_shaped", st)
+    return dq, dk, dv
+
+
+def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int, scale: float | None = None,
+                        softcap: float = 0.0, slopes=None, window: int = 0, out=None, lse=None, workspace=None,
+                        want_lse: bool = True, stream=None):
+    """``decode_paged`` with the cap, distance bias and window of ``fwd_shaped`` (the query is the
+    sequence's last token). With a window, num_splits cuts the pages that it touches: pass
+    choose_num_splits their count, min(max_pages, (window + page_size - 2) // page_size + 1).
+    Returns (O [B,Hq,d], lse [B,Hq])."""
+    lib = load_library()
+    _need_cuda(q, kcache, vcache, block_table, seqlens, out, lse, workspace)
+    if not (q.dtype == kcache.dtype == vcache.dtype == torch.bfloat16):
+        raise TypeError("q, kcache and vcache must be bfloat16 (the decode kernels read bf16 only)")
+    if seqlens.dtype != torch.int32:
+        raise TypeError("block_table and seqlens must be int32")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _check_paged_cache(kcache, vcache, block_table, B)
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _expect(kcache, (num_pages, page_size, Hkv, d), "kcache")
+    _expect(seqlens, (B,), "seqlens")
+    _expect(out, q.shape, "out", q.dtype)
+    _expect(lse, (B, Hq), "lse", torch.float32)
+    _check_shape(slopes, Hq, None, None, None)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(decode_workspace_size(B, Hq, d, num_splits), 1), dtype=torch.uint8, device=q.device)
+    st = lib.fattn_decode_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
+                                       num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
+                                       block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
+                                       int(window), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_decode_paged_shaped", st)
+    return out, lse

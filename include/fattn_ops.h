@@ -4,7 +4,12 @@
  *
  *   - rotary positions on q and k (fattn_rope), and their serving form, which
  *     also puts the new tokens' k and v into the paged cache
- *     (fattn_rope_append_paged).
+ *     (fattn_rope_append_paged);
+ *   - shaped scores: attention whose scores are capped by a tanh, carry a bias
+ *     that depends on the distance, and see a window, a document or a prefix
+ *     (fattn_fwd_shaped, its gradient fattn_bwd_shaped, query chunks and single
+ *     tokens over the paged cache: fattn_fwd_paged_shaped,
+ *     fattn_decode_paged_shaped).
  *
  * The conventions of fattn.h hold: DEVICE pointers owned by the caller, host
  * checks before anything is launched, work enqueued on `stream`, no
@@ -80,6 +85,82 @@ fattn_status fattn_rope_append_paged(const void* q, void* q_out, const void* k, 
                                      int max_pages_per_seq, int num_pages, long long q_row, long long q_head,
                                      long long k_row, long long k_head, long long v_row, long long v_head,
                                      int interleaved, float amplitude, cudaStream_t stream);
+
+/*
+ * Shaped scores. For the query at position i (in key coordinates: the row's
+ * index, for chunks plus the context before the chunk) and key j,
+ *   s = scale q.k
+ *   s = softcap tanh(s / softcap)            if softcap > 0
+ *   s = s - slopes[h] |i - j|                if slopes != NULL
+ * and key j is visible iff
+ *   j <= i                                   if causal != 0,
+ *   |i - j| < window                         if window > 0,
+ *   key_begin[row] <= j < key_end[row]       where given (either may be NULL).
+ * O = softmax(s) V over the visible keys, lse the logsumexp; a row that sees no
+ * key gets O = 0, lse = -inf.
+ *
+ * slopes: DEVICE fp32 [Hq], any sign. key_begin, key_end: DEVICE int32, one per
+ * query row ([B, N]; [total_q] for chunks), keys of the row's own sequence; they
+ * must not decrease from a row to the next of its sequence (rows that see
+ * nothing repeat their neighbour's begin as end). Packed documents (begin = the
+ * document's first row, end = one past its last), prefixes (end = max(i + 1,
+ * prefix end)) and padding are such ranges; so are their unions with causal and
+ * window. Ranges that decrease make the rows concerned wrong and are recorded as
+ * FATTN_ERR_DEVICE_CHECK where a row's keys are outside its tile's.
+ * Work goes by 128 x 128 tiles: a tile in which no row sees a key is not computed,
+ * and keys before the lowest one that 256 consecutive rows see, rounded down to a
+ * multiple of 128, are not read for them. Within the computed tiles hidden keys
+ * get weight 0, so every row of the inputs must be finite.
+ *
+ * fattn_fwd_shaped — dense prefill: bf16, layouts of fattn_fwd (q, o [B, N, Hq,
+ *   d]; k, v [B, N, Hkv, d]; lse [B, Hq, N], may be NULL).
+ * Errors (all four): those of the plain call; INVALID_ARG also for a softcap that
+ *   is negative or not finite (or so small that scale / softcap is not), a negative
+ *   window, misaligned slopes or ranges.
+ */
+fattn_status fattn_fwd_shaped(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                              int N, int d, int causal, float scale, float softcap, const float* slopes, int window,
+                              const int32_t* key_begin, const int32_t* key_end, cudaStream_t stream);
+
+/*
+ * fattn_fwd_paged_shaped — query chunks over the paged cache: fattn_fwd_paged with
+ * shaped scores; the position of a chunk's query i is i + seqlens_k[b] - Lq_b.
+ * Pages before token 128 floor(t / 128), t the first token that any row of the
+ * chunk sees, are not read, nor are their table entries.
+ */
+fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
+                                    const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B,
+                                    int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
+                                    int total_q, int max_seqlen_q, int causal, float scale, float softcap,
+                                    const float* slopes, int window, const int32_t* key_begin, const int32_t* key_end,
+                                    cudaStream_t stream);
+
+/*
+ * fattn_bwd_shaped — gradients of fattn_fwd_shaped with respect to q, k and v:
+ * fattn_bwd with P rebuilt from the shaped scores and dS multiplied by the cap's
+ * derivative 1 - tanh^2. o and lse are fattn_fwd_shaped's for the same arguments;
+ * the slopes are constants (no gradient). Rows that see no key and keys that no row
+ * sees get gradient 0. workspace: as fattn_bwd (fattn_bwd_workspace_size).
+ */
+fattn_status fattn_bwd_shaped(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                              const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
+                              int causal, float scale, float softcap, const float* slopes, int window,
+                              const int32_t* key_begin, const int32_t* key_end, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fattn_decode_paged_shaped — one query token per sequence, at position
+ * seqlens[b] - 1: fattn_decode_paged with a cap, a distance bias and a window. With
+ * a window the splits share the pages that it touches: a sequence's visible pages,
+ * counted from the page of its first visible token, are cut into S chunks of
+ * C = ceil(n / S) pages, n = min(max_pages_per_seq, (window + page_size - 2) /
+ * page_size + 1); pages before are not read. Workspace as fattn_decode_paged.
+ */
+fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const void* vcache,
+                                       const int32_t* block_table, const int32_t* seqlens, int num_splits, void* o,
+                                       float* lse, int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
+                                       int num_pages, float scale, float softcap, const float* slopes, int window,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -87,3 +87,52 @@ def test_rope_frequencies():
                 dict(rotary_dim=8, factor=0.5), dict(rotary_dim=8, base=0.0)):
         with pytest.raises(ValueError):
             F.rope_frequencies(**bad)
+
+
+SHAPE_BAD = [dict(cap=-1.0), dict(cap=float("nan")), dict(cap=1e-44), dict(win=-1), dict(sl=A + 2), dict(kb=A + 1),
+             dict(ke=A + 3), dict(scale=float("nan"))]
+
+
+def _shape(kw):
+    return kw.get("cap", 0.0), kw.get("sl"), kw.get("win", 0), kw.get("kb"), kw.get("ke")
+
+
+def _calls(lib, kw):
+    g = lambda n, x: kw.get(n, x)
+    cap, sl, win, kb, ke = _shape(kw)
+    sc = g("scale", 0.1)
+    yield lib.fattn_fwd_shaped(g("q", A), A, A, A, None, g("B", 2), g("Hq", 4), 2, g("N", 300), g("d", 128), 1, sc, cap,
+                               sl, win, kb, ke, None)
+    yield lib.fattn_fwd_paged_shaped(g("q", A), A, A, A, A, A, A, None, g("B", 2), g("Hq", 4), 2, g("d", 128), 16, 8, 64,
+                                     100, g("N", 300), 1, sc, cap, sl, win, kb, ke, None)
+    yield lib.fattn_bwd_shaped(g("q", A), A, A, A, A, A, A, A, A, g("B", 2), g("Hq", 4), 2, g("N", 300), g("d", 128), 1,
+                               sc, cap, sl, win, kb, ke, A, 1 << 20, None)
+    if "kb" not in kw and "ke" not in kw and "N" not in kw and "B" not in kw:
+        yield lib.fattn_decode_paged_shaped(g("q", A), A, A, A, A, 4, A, None, 2, g("Hq", 4), 2, g("d", 128), 16, 8, 64,
+                                            sc, cap, sl, win, A, 1 << 20, None)
+
+
+@pytest.mark.parametrize("bad", SHAPE_BAD + [dict(q=None), dict(q=A + 8), dict(Hq=3), dict(Hq=0), dict(N=-1), dict(B=-1)])
+def test_shaped_calls_refuse(lib, bad):
+    assert set(_calls(lib, bad)) == {F.FATTN_ERR_INVALID_ARG}
+
+
+def test_shaped_calls_limits_and_empty(lib):
+    assert set(_calls(lib, dict(d=96))) == {F.FATTN_ERR_UNSUPPORTED}
+    assert set(_calls(lib, dict(B=0, q=None))) == {F.FATTN_OK}
+    assert set(_calls(lib, dict(N=0, q=None))) == {F.FATTN_OK}
+    assert lib.fattn_bwd_shaped(A, A, A, A, A, A, A, A, A, 2, 4, 2, 300, 128, 1, 0.1, 0.0, None, 0, None, None, A, 100,
+                                None) == F.FATTN_ERR_WORKSPACE
+    assert lib.fattn_fwd_shaped(A, A, A, A, None, 1 << 15, 1 << 10, 1, 1 << 15, 64, 1, 0.1, 0.0, None, 0, None, None,
+                                None) == F.FATTN_ERR_UNSUPPORTED
+
+
+def test_document_ranges():
+    ids = torch.tensor([[0, 0, 0, 4, 4, -1, -1], [2, 2, 2, 2, 2, 2, 2]])
+    b, e = F.document_ranges(ids)
+    assert b.tolist() == [[0, 0, 0, 3, 3, 5, 5], [0] * 7] and e.tolist() == [[3, 3, 3, 5, 5, 5, 5], [7] * 7]
+    b, e = F.document_ranges(ids, prefix_len=2)
+    assert e.tolist() == [[2, 2, 3, 5, 5, 5, 5], [2, 2, 3, 4, 5, 6, 7]]
+    assert bool((b[:, 1:] >= b[:, :-1]).all() and (e[:, 1:] >= e[:, :-1]).all())
+    with pytest.raises(ValueError):
+        F.document_ranges(ids[0])

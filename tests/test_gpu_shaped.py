@@ -1,0 +1,318 @@
+"""Shaped attention (tanh cap, distance bias, window, key ranges): forward, gradient, chunks over pages.
+
+Tolerances. Forward: P is rounded to bf16 (half a step, 2^-8 of it, as l sums the unrounded P) and so is O:
+2^-8 (sum p |v| + |O|). fp32: a score is off by at most 1e-6 of the magnitude M behind it plus 5e-5 (128
+products summed in fp32; the cap's 1 - 2r, log2 units), and so is lse; P is off by twice that, relatively.
+Gradients, from the same o and lse: P and dS rounded to bf16, the result as well: 2^-8 (sum of magnitudes + |g|);
+fp32 errors as above on P, dP and D.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import shaped_ref as R
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+H = 2.0 ** -8  # half a step of bf16
+f64 = lambda t: t.detach().cpu().double().numpy()
+
+
+def score_err(M):
+    return 5e-5 + 1e-6 * M
+
+
+def check_fwd(o, lse, ref, what=""):
+    O, L, A, M = ref
+    g, gl = f64(o), f64(lse)
+    assert np.isfinite(g).all(), what
+    dead = ~np.isfinite(L)
+    assert np.array_equal(np.isneginf(gl), dead), what
+    assert (np.abs(gl - L)[~dead] <= score_err(M)[~dead] + 2.0 ** -23 * np.abs(L[~dead])).all(), \
+        (what, np.abs(gl - L)[~dead].max())
+    tol = H * (A + np.abs(O)) * 1.01 + 2 * score_err(M).T[:, :, None] * A
+    assert (np.abs(g - O) <= tol).all(), (what, np.abs(g - O).max(), (np.abs(g - O) / np.maximum(tol, 1e-30)).max())
+
+
+def make(seed, B, N, Hq, Hkv, d, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda h, s=1.0: (torch.randn(B, N, h, d, generator=g) * s).to(torch.bfloat16)
+    return r(Hq, std), r(Hkv, std), r(Hkv), r(Hq)
+
+
+def alibi(Hq):
+    return (2.0 ** (-8.0 * torch.arange(1, Hq + 1) / Hq)).float()
+
+
+def docs(fa, lens, N, prefix=None, B=1):
+    ids = torch.full((B, N), -1, dtype=torch.int64)
+    o = 0
+    for i, n in enumerate(lens):
+        ids[:, o:o + n], o = i, o + n
+    return fa.document_ranges(ids, prefix)
+
+
+# name: B, N, Hq, Hkv, d, causal, cap, slopes, window, documents, prefix
+CASES = {
+    "one": (1, 1, 1, 1, 64, True, 30.0, True, 1, None, None),
+    "three": (2, 3, 2, 1, 128, True, 0.0, True, 2, None, None),
+    "plain": (1, 200, 2, 2, 128, False, 0.0, False, 0, None, None),
+    "cap128": (2, 300, 4, 2, 128, True, 20.0, False, 0, None, None),
+    "cap64": (1, 513, 4, 1, 64, True, 5.0, False, 0, None, None),
+    "cap_full": (1, 257, 2, 2, 128, False, 50.0, False, 0, None, None),
+    "bias": (1, 700, 8, 2, 128, True, 0.0, True, 0, None, None),
+    "bias_both": (1, 385, 4, 4, 64, False, 0.0, True, 0, None, None),
+    "window": (1, 900, 2, 1, 128, True, 0.0, False, 100, None, None),
+    "window_both": (1, 640, 2, 2, 64, False, 0.0, False, 130, None, None),
+    "window1": (1, 129, 1, 1, 128, True, 0.0, False, 1, None, None),
+    "window_huge": (1, 300, 1, 1, 64, False, 0.0, False, 2 ** 31 - 1, None, None),
+    "docs": (2, 777, 2, 1, 128, True, 0.0, False, 0, [1, 130, 2, 255, 389], None),
+    "docs64": (1, 1000, 2, 2, 64, True, 0.0, False, 0, [300, 700], None),
+    "docs_both": (1, 600, 2, 2, 128, False, 0.0, False, 0, [128, 128, 1, 300, 43], None),
+    "padded": (2, 700, 2, 1, 128, True, 0.0, False, 0, [100, 33], None),       # most rows see nothing
+    "padded64": (1, 515, 1, 1, 64, False, 0.0, False, 0, [5], None),
+    "prefix": (1, 500, 4, 2, 64, False, 0.0, False, 0, [200, 300], 77),
+    "prefix128": (1, 400, 2, 2, 128, False, 0.0, False, 0, [400], 150),
+    "all": (2, 650, 4, 2, 128, True, 30.0, True, 90, [123, 27, 400], None),
+    "all64": (1, 650, 8, 1, 64, False, 15.0, True, 200, [300, 250], 40),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_forward_and_gradient(name):
+    fa = need_gpu()
+    B, N, Hq, Hkv, d, causal, cap, sl, window, dl, prefix = CASES[name]
+    q, k, v, do = make(len(name) * 31 + N, B, N, Hq, Hkv, d, 2.0 if cap else 1.0)
+    slopes = alibi(Hq) if sl else None
+    begin, end = docs(fa, dl, N, prefix, B) if dl else (None, None)
+    scale = 1 / math.sqrt(d)
+    dev = lambda t: None if t is None else t.cuda()
+    kw = dict(causal=causal, scale=scale, softcap=cap, slopes=dev(slopes), window=window, key_begin=dev(begin), key_end=dev(end))
+    o = torch.full((B, N, Hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, Hq, N), float("nan"), device="cuda")
+    fa.fwd_shaped(dev(q), dev(k), dev(v), out=o, lse=lse, **kw)
+    assert fa.debug_read_status() == 0
+    nan = lambda t: torch.full(t.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    grads = dict(dq=nan(q), dk=nan(k), dv=nan(v))
+    fa.bwd_shaped(dev(q), dev(k), dev(v), o, lse, dev(do), **kw, **grads)
+    assert fa.debug_read_status() == 0
+    for b in range(B):
+        lo, hi = R.ranges(N, N, 0, causal, window, None if begin is None else begin[b].numpy(),
+                          None if end is None else end[b].numpy())
+        s = None if slopes is None else f64(slopes)
+        ref = R.forward(f64(q[b]), f64(k[b]), f64(v[b]), scale, cap, s, lo, hi)
+        check_fwd(o[b], lse[b], ref, f"{name} sequence {b}")
+        g, a, e = R.backward(f64(q[b]), f64(k[b]), f64(v[b]), f64(o[b]), f64(lse[b]), f64(do[b]), scale, cap, s, lo, hi)
+        es = 2 * score_err(ref[3].max())
+        for n in grads:
+            got = f64(grads[n][b])
+            assert np.isfinite(got).all(), n
+            tol = H * 1.02 * (a[n] + np.abs(g[n])) + es * e[n] + 1e-30
+            assert (np.abs(got - g[n]) <= tol).all(), (name, n, (np.abs(got - g[n]) / tol).max())
+
+
+def test_gradient_against_differences():
+    """Directional derivative of the 64-bit forward; the bound adds o's rounding (2^-8 |o| in D) to the gradient's own."""
+    fa = need_gpu()
+    N, Hq, Hkv, d, cap, scale = 150, 2, 1, 64, 10.0, 0.2
+    q, k, v, do = make(5, 1, N, Hq, Hkv, d, 1.5)
+    slopes = alibi(Hq)
+    begin, end = docs(fa, [90, 60], N)
+    kw = dict(causal=True, scale=scale, softcap=cap, slopes=slopes.cuda(), window=70, key_begin=begin.cuda(), key_end=end.cuda())
+    o, lse = fa.fwd_shaped(q.cuda(), k.cuda(), v.cuda(), **kw)
+    got = dict(zip(("dq", "dk", "dv"), fa.bwd_shaped(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), **kw)))
+    lo, hi = R.ranges(N, N, 0, True, 70, begin[0].numpy(), end[0].numpy())
+    x = dict(dq=f64(q[0]), dk=f64(k[0]), dv=f64(v[0]))
+    _, a, e = R.backward(x["dq"], x["dk"], x["dv"], f64(o[0]), f64(lse[0]), f64(do[0]), scale, cap, f64(slopes), lo, hi)
+    rng = np.random.default_rng(0)
+    for n in got:
+        dirn = rng.standard_normal(x[n].shape)
+        f = lambda h: (R.forward(*[x[m] + (h * dirn if m == n else 0) for m in ("dq", "dk", "dv")], scale, cap,
+                                 f64(slopes), lo, hi)[0] * f64(do[0])).sum()
+        num = (f(1e-5) - f(-1e-5)) / 2e-5
+        tol = ((H * 1.02 * (a[n] + np.abs(f64(got[n][0]))) + (2e-4 + H) * e[n]) * np.abs(dirn)).sum()
+        err = abs((f64(got[n][0]) * dirn).sum() - num)
+        assert err <= tol and tol < 0.2 * np.abs(f64(got[n][0]) * dirn).sum(), (n, err, tol, num)
+
+
+def test_hidden_keys_do_not_leak():
+    """Huge and non-finite keys outside the visible range: of no effect on the scores that count."""
+    fa = need_gpu()
+    q, k, v, _ = make(9, 1, 400, 2, 2, 128)
+    begin, end = docs(fa, [150, 250], 400)
+    kw = dict(causal=True, key_begin=begin.cuda(), key_end=end.cuda(), softcap=20.0)
+    o, lse = fa.fwd_shaped(q.cuda(), k.cuda(), v.cuda(), **kw)
+    for bad in (1e30, float("inf"), float("nan")):
+        k2 = k.clone()
+        k2[:, :150] = bad
+        o2, lse2 = fa.fwd_shaped(q.cuda(), k2.cuda(), v.cuda(), **kw)
+        assert torch.equal(o2[:, 150:], o[:, 150:]) and torch.equal(lse2[..., 150:], lse[..., 150:])
+    assert fa.debug_read_status() == 0
+
+
+def test_scales_caps_and_slopes_of_any_sign():
+    fa = need_gpu()
+    q, k, v, _ = make(11, 1, 260, 2, 1, 128)
+    lo, hi = R.ranges(260, 260, 0, True, 0)
+    for scale, cap, sl in ((-0.2, 0.0, None), (-0.3, 7.0, None), (0.0, 0.0, None), (0.1, 0.0, [-0.01, 0.3]), (-0.1, 0.0, [0.5, 0.0]),
+                           (3.0, 25.0, None), (0.088, 1e4, None)):
+        s = None if sl is None else torch.tensor(sl)
+        o, lse = fa.fwd_shaped(q.cuda(), k.cuda(), v.cuda(), causal=True, scale=scale, softcap=cap, slopes=None if s is None else s.cuda())
+        assert fa.debug_read_status() == 0
+        O, L, A, M = R.forward(f64(q[0]), f64(k[0]), f64(v[0]), scale, cap, None if s is None else f64(s), lo, hi)
+        # the cap's 1 - 2r is off by 2^-22 of the cap, and the raw product by 1e-6 of itself
+        check_fwd(o[0], lse[0], (O, L, A, M + cap), f"scale {scale} cap {cap}")
+
+
+def test_ranges_that_decrease_are_recorded():
+    fa = need_gpu()
+    q, k, v, _ = make(3, 1, 512, 1, 1, 64)
+    end = torch.full((1, 512), 512, dtype=torch.int32)
+    end[0, 127] = 60                       # the tile's last row ends below the others
+    fa.fwd_shaped(q.cuda(), k.cuda(), v.cuda(), key_end=end.cuda())
+    assert fa.debug_read_status() == fa.FATTN_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("P,Hq,Hkv,d,lk,lq,causal,cap,sl,window,ranged", [
+    (16, 4, 2, 128, [700, 257, 1, 130], [300, 257, 1, 1], True, 20.0, False, 0, False),
+    (32, 8, 1, 64, [513, 40, 900], [130, 40, 256], True, 0.0, True, 200, False),
+    (64, 2, 2, 128, [1000, 129], [129, 128], False, 0.0, True, 300, False),
+    (128, 5, 1, 64, [384, 1023], [1, 200], True, 0.0, False, 1, False),
+    (16, 2, 1, 64, [600, 300], [500, 300], True, 10.0, True, 170, True)])
+def test_paged_chunks(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window, ranged):
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(P + Hq)
+    B, T, pad = len(lk), sum(lq), 5
+    per = [-(-n // P) for n in lk]
+    pages, maxp = sum(per) + 2, max(per) + 1
+    perm, table, used = torch.randperm(pages, generator=g), torch.full((B, maxp), -1, dtype=torch.int32), 0
+    kc, vc = (torch.randn(pages, P, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T + pad, Hq, d, generator=g).to(torch.bfloat16)
+    cu = np.concatenate([[0], np.cumsum(lq)])
+    slopes = alibi(Hq) if sl else None
+    begin = end = None
+    if ranged:   # two documents per sequence, cut at half its context
+        begin, end = torch.zeros(T + pad, dtype=torch.int32), torch.zeros(T + pad, dtype=torch.int32)
+    want = []
+    for b in range(B):
+        table[b, :per[b]], used = perm[used:used + per[b]].int(), used + per[b]
+        full = [c[table[b, :per[b]].long()].reshape(-1, Hkv, d)[:lk[b]] for c in (kc, vc)]
+        i = np.arange(lq[b]) + lk[b] - lq[b]
+        bb, ee = (np.where(i < lk[b] // 2, 0, lk[b] // 2), np.where(i < lk[b] // 2, lk[b] // 2, lk[b])) if ranged else (None, None)
+        if ranged:
+            begin[cu[b]:cu[b + 1]], end[cu[b]:cu[b + 1]] = torch.from_numpy(bb), torch.from_numpy(ee)
+        lo, hi = R.ranges(lq[b], lk[b], lk[b] - lq[b], causal, window, bb, ee)
+        want.append(R.forward(f64(q[cu[b]:cu[b + 1]]), f64(full[0]), f64(full[1]), 0.15, cap,
+                              None if slopes is None else f64(slopes), lo, hi, off=lk[b] - lq[b]))
+        # pages before the first visible tile of 128 are not read: their entries may be anything
+        table[b, :(max(int(lo.min()), 0) // 128) * 128 // P] = -5
+    dev = lambda t: None if t is None else t.cuda()
+    o = torch.full((T + pad, Hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Hq, T + pad), 3.0, device="cuda")
+    fa.fwd_paged_shaped(dev(q), dev(kc), dev(vc), dev(table), torch.tensor(lk, dtype=torch.int32).cuda(),
+                        torch.from_numpy(cu).int().cuda(), max(lq), causal=causal, scale=0.15, softcap=cap, slopes=dev(slopes),
+                        window=window, key_begin=dev(begin), key_end=dev(end), out=o, lse=lse)
+    assert fa.debug_read_status() == 0
+    for b in range(B):
+        check_fwd(o[cu[b]:cu[b + 1]], lse[:, cu[b]:cu[b + 1]], want[b], f"chunk {b}")
+    assert bool((o[T:] == 3).all()) and bool((lse[:, T:] == 3).all())  # rows behind the last chunk
+
+
+@pytest.mark.parametrize("P,Hq,Hkv,d,lens,S,cap,sl,window", [
+    (16, 8, 2, 128, [700, 1, 0, 33], 4, 20.0, False, 0),
+    (32, 4, 4, 64, [513, 40, 900], 7, 0.0, True, 200),
+    (16, 16, 1, 64, [1500, 20], 3, 0.0, True, 1),
+    (64, 20, 1, 128, [1000, 129], 5, 30.0, True, 65),
+    (3, 2, 1, 64, [50, 7], 2, 0.0, False, 10),
+    (16, 2, 2, 128, [600], 1, 0.0, False, 10 ** 9)])
+def test_decode(P, Hq, Hkv, d, lens, S, cap, sl, window):
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(P + Hq + d)
+    B = len(lens)
+    per = [-(-n // P) for n in lens]
+    pages, maxp = sum(per) + 2, max(per) + 1
+    perm, table, used = torch.randperm(pages, generator=g), torch.full((B, maxp), -1, dtype=torch.int32), 0
+    kc, vc = (torch.randn(pages, P, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = (torch.randn(B, Hq, d, generator=g) * 2).to(torch.bfloat16)
+    slopes = alibi(Hq) if sl else None
+    want = []
+    for b, n in enumerate(lens):
+        table[b, :per[b]], used = perm[used:used + per[b]].int(), used + per[b]
+        if n:
+            full = [c[table[b, :per[b]].long()].reshape(-1, Hkv, d)[:n] for c in (kc, vc)]
+            lo, hi = R.ranges(1, n, n - 1, True, window)
+            want.append(R.forward(f64(q[b:b + 1]), f64(full[0]), f64(full[1]), 0.1, cap, None if slopes is None else f64(slopes),
+                                  lo, hi, off=n - 1))
+            table[b, :max(int(lo[0]), 0) // P] = -5   # pages before the window are not read
+        else:
+            want.append((np.zeros((1, Hq, d)), np.full((Hq, 1), -np.inf), np.zeros((1, Hq, d)), np.zeros((Hq, 1))))
+    dev = lambda t: None if t is None else t.cuda()
+    o, lse = fa.decode_paged_shaped(dev(q), dev(kc), dev(vc), dev(table), torch.tensor(lens, dtype=torch.int32).cuda(), S, scale=0.1,
+                                    softcap=cap, slopes=dev(slopes), window=window)
+    assert fa.debug_read_status() == 0
+    for b in range(B):
+        check_fwd(o[b:b + 1], lse[b][:, None], want[b], f"sequence {b}")
+
+
+def test_unshaped_calls_agree_with_the_plain_ones():
+    """With every shape off the shaped kernels compute what the plain ones do, in the same order."""
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(21, 2, 333, 4, 2, 128))
+    o, lse = fa.fwd(q, k, v, causal=True)
+    o2, lse2 = fa.fwd_shaped(q, k, v, causal=True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for x, y in zip(fa.bwd(q, k, v, o, lse, do, causal=True), fa.bwd_shaped(q, k, v, o, lse, do, causal=True)):
+        # S scale and the addition of lse round separately in one of them: P differs by 2^-22 |S|, a bf16 step at most
+        assert (x.float() - y.float()).abs().max() <= 2.0 ** -7 * x.float().abs().max()
+
+
+def test_streams_graphs_and_timeouts():
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(31, 1, 600, 2, 1, 128))
+    kw = dict(causal=True, softcap=20.0, window=200, slopes=alibi(2).cuda())
+    o, lse = fa.fwd_shaped(q, k, v, **kw)
+    ref = fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    bufs = [torch.zeros_like(t) for t in (o, lse, *ref)]
+    ws = torch.empty(fa.bwd_workspace_size(1, 2, 600), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        fa.fwd_shaped(q, k, v, out=bufs[0], lse=bufs[1], stream=s, **kw)
+        fa.bwd_shaped(q, k, v, bufs[0], bufs[1], do, dq=bufs[2], dk=bufs[3], dv=bufs[4], workspace=ws, stream=s, **kw)
+    for _ in range(2):
+        for b in bufs:
+            b.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((o, lse, *ref), bufs))
+    # the bounded waits run out as in the plain calls, and the next call is right
+    assert fa.debug_read_status() == 0
+    fa.debug_set_wait_limit(1_000_000, True)
+    try:
+        fa.fwd_shaped(q, k, v, **kw)
+        st = fa.debug_read_status()
+        fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+        torch.cuda.synchronize()
+    finally:
+        fa.debug_set_wait_limit(0, False)
+    assert st == fa.FATTN_ERR_TIMEOUT and fa.debug_read_status() == fa.FATTN_ERR_TIMEOUT
+    assert torch.equal(fa.fwd_shaped(q, k, v, **kw)[0], o) and fa.debug_read_status() == 0
+
+
+def test_refusals():
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(1, 1, 40, 4, 2, 64))
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    for bad in (dict(slopes=torch.zeros(3, device="cuda")), dict(slopes=torch.zeros(4, device="cuda", dtype=torch.float64)),
+                dict(key_begin=z(1, 39)), dict(key_end=z(1, 40).long()), dict(softcap=-1.0), dict(softcap=float("nan")),
+                dict(softcap=1e-45), dict(window=-1), dict(scale=float("inf")), dict(slopes=torch.zeros(4))):
+        with pytest.raises((ValueError, TypeError, fa.FattnError)):
+            fa.fwd_shaped(q, k, v, **bad)
+        with pytest.raises((ValueError, TypeError, fa.FattnError)):
+            fa.bwd_shaped(q, k, v, q, torch.zeros(1, 4, 40, device="cuda"), do, **bad)
+    with pytest.raises(fa.FattnError):
+        fa.fwd_shaped(torch.zeros(1, 4, 2, 96, device="cuda", dtype=torch.bfloat16), *(torch.zeros(1, 4, 2, 96, device="cuda", dtype=torch.bfloat16),) * 2)
