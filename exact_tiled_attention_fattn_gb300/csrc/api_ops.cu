@@ -165,3 +165,75 @@ extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kca
   return decode_paged_impl(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
                            max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
 }
+
+extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const int32_t* block_table,
+                                                const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const float* lse,
+                                                long long lse_head, long long lse_row, const float* weights_in,
+                                                float* weights_out, int B, int Hq, int Hkv, int d, int page_size,
+                                                int max_pages_per_seq, int num_pages, int total_q, int max_seqlen_q,
+                                                int causal, float scale, float softcap, const float* slopes, int window,
+                                                float decay, cudaStream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || total_q < 0 || max_seqlen_q < 0 || page_size <= 0 ||
+      max_pages_per_seq <= 0 || num_pages <= 0 || lse_head < 0 || lse_row < 0)
+    return FATTN_ERR_INVALID_ARG;
+  KeyWeightsParams p{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, nullptr, nullptr, &p.shape);
+  if (st != FATTN_OK) return st;
+  if (Hq % Hkv != 0 || !std::isfinite(decay)) return FATTN_ERR_INVALID_ARG;
+  if (B == 0) return FATTN_OK;
+  if (!kcache || !block_table || !seqlens_k || !cu_seqlens_q || !weights_out) return FATTN_ERR_INVALID_ARG;
+  if (total_q > 0 && (!q || !lse)) return FATTN_ERR_INVALID_ARG;  // no queries: the weights decay
+  if (misaligned(q, 16) || misaligned(kcache, 16) || misaligned(block_table, 4) || misaligned(seqlens_k, 4) ||
+      misaligned(cu_seqlens_q, 4) || misaligned(lse, 4) || misaligned(weights_in, 4) || misaligned(weights_out, 4))
+    return FATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL - 256 || B > 65535 || Hkv > 65535)
+    return FATTN_ERR_UNSUPPORTED;
+  int err = 0;
+  p.q = q; p.kcache = kcache; p.block_table = block_table; p.seqlens_k = seqlens_k; p.cu_seqlens = cu_seqlens_q;
+  p.lse = lse; p.lse_head = lse_head; p.lse_row = lse_row; p.w_in = weights_in; p.w_out = weights_out;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages = max_pages_per_seq;
+  p.num_pages = num_pages; p.total_q = total_q;
+  p.causal = causal ? 1 : 0; p.scale = scale; p.decay = decay;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  return launch_key_weights(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+extern "C" fattn_status fattn_evict_paged(void* kcache, void* vcache, const int32_t* block_table,
+                                          const int32_t* seqlens, const float* weights_in, const int32_t* dst_table,
+                                          int32_t* seqlens_out, float* weights_out, int32_t* kept, int B, int Hkv, int d,
+                                          int page_size, int max_pages_per_seq, int num_pages, int dst_max_pages,
+                                          int keep, int recent, int first, cudaStream_t stream) {
+  if (B < 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 || dst_max_pages <= 0 ||
+      keep <= 0 || recent < 0 || first < 0 || (long long)first + recent > keep)
+    return FATTN_ERR_INVALID_ARG;
+  if (!dst_table && dst_max_pages != max_pages_per_seq) return FATTN_ERR_INVALID_ARG;
+  const long long cap = (long long)max_pages_per_seq * page_size, dst_cap = (long long)dst_max_pages * page_size;
+  if (dst_cap < (keep < cap ? keep : cap)) return FATTN_ERR_INVALID_ARG;  // the kept tokens would not fit
+  if (B == 0) return FATTN_OK;
+  if (!kcache || !vcache || !block_table || !seqlens || !weights_in || !seqlens_out || !weights_out || !kept)
+    return FATTN_ERR_INVALID_ARG;
+  if (misaligned(kcache, 16) || misaligned(vcache, 16) || misaligned(block_table, 4) || misaligned(seqlens, 4) ||
+      misaligned(weights_in, 4) || misaligned(dst_table, 4) || misaligned(seqlens_out, 4) ||
+      misaligned(weights_out, 4) || misaligned(kept, 4))
+    return FATTN_ERR_INVALID_ARG;
+  // every block of a sequence reads its old length; weights in place keep their row length
+  if (seqlens_out == seqlens || (weights_out == weights_in && dst_max_pages != max_pages_per_seq))
+    return FATTN_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 1024) return FATTN_ERR_UNSUPPORTED;
+  if (cap > 0x7fffffffLL - 4096 || dst_cap > 0x7fffffffLL - 4096 || keep > 0x7fffffff - 4096 ||
+      (long long)B * Hkv > 65535)
+    return FATTN_ERR_UNSUPPORTED;
+  int err = 0;
+  EvictParams p{};
+  p.kcache = kcache; p.vcache = vcache; p.block_table = block_table; p.seqlens = seqlens; p.w_in = weights_in;
+  p.dst_table = dst_table; p.seqlens_out = seqlens_out; p.w_out = weights_out; p.kept = kept;
+  p.B = B; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.dst_max_pages = dst_max_pages; p.keep = keep; p.first = first; p.recent = recent;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_evict(p, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}

@@ -1,0 +1,230 @@
+// Attention weight that the tokens of a paged cache received:
+//   w_out[b, hkv, t] = decay w_in[b, hkv, t] + sum over the group's heads and the chunk's queries of e^{s - lse}
+// (s the shaped score, lse the row's logsumexp from the attention call), the statistic by
+// which fattn_evict_paged picks the tokens to keep.
+//
+// The softmax's statistics are known, so one product per pair of tiles is enough and nothing
+// is kept per query: S^T = K Q^T with the keys as rows, summed over its columns in fp32
+// registers. A block owns 128 keys of one (sequence, KV head) and no other block writes their
+// sums: no atomics, the same order of additions every time. Each of the 4 warps holds its 32
+// keys as A fragments in registers for the whole walk over the queries, whose rows (all heads
+// of the group of a query are contiguous) stream through a two-stage ring in shared memory.
+// For one query per sequence the walk is a single step and the kernel streams K.
+#include "device_common.cuh"
+#include "ops_internal.h"
+#include "score_shape.cuh"
+
+#include <math_constants.h>
+
+namespace fattn {
+namespace {
+
+constexpr int kKeys = 128;   // keys per block
+constexpr int kQRows = 32;   // query rows (query x head of the group) per step
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// C (16 x 8, fp32) += A (16 x 16, bf16, row) B (16 x 8, bf16, col)
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16-byte unit u of row r at u ^ (r & 7): the 8 rows that ldmatrix reads hit 8 bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t unit_at(int r, int u) {
+  return (uint32_t)((r * (D / 8) + (u ^ (r & 7))) * 16);
+}
+
+template <int D>
+struct KwLayout {
+  static constexpr int kK = kKeys * D * 2;
+  static constexpr int kQ = kQRows * D * 2;
+  static constexpr int kVec = kQRows * 16;   // per query row: -lse log2(e), slope, position, (unused)
+  static constexpr int kOffQ = kK;
+  static constexpr int kOffVec = kOffQ + 2 * kQ;
+  static constexpr int kBytes = kOffVec + 2 * kVec;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeightsParams p) {
+  using Lay = KwLayout<D>;
+  constexpr int U = D / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_row[kKeys];  // each key's first element in the cache, -1: none
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, hkv = blockIdx.y;
+  const int n = __ldg(p.seqlens_k + b);
+  const int key0 = blockIdx.x * kKeys;
+  const int cap = p.max_pages * p.page_size;
+  const int q0 = __ldg(p.cu_seqlens + b), q1 = __ldg(p.cu_seqlens + b + 1), m = q1 - q0;
+  if (n < 0 || n > cap || q0 < 0 || m < 0 || q1 > p.total_q || m > n) {
+    if (key0 == 0 && hkv == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
+    return;  // the sequence is skipped
+  }
+  if (key0 >= n) return;
+  const int nkeys = min(kKeys, n - key0), off = n - m;
+  const int G = p.Hq / p.Hkv;
+
+  // queries [i0, i1) that can see one of the block's keys, and their rows i * G + head
+  int i0 = 0, i1 = m;
+  if (p.causal) i0 = max(0, key0 - off);
+  if (p.shape.window > 0) {
+    i1 = (int)min((long long)m, (long long)key0 + nkeys - 1 + p.shape.window - off);
+    if (!p.causal) i0 = max(0, key0 - off - p.shape.window + 1);
+  }
+  const long long u0 = (long long)i0 * G, u1 = (long long)max(i0, i1) * G;
+  const int steps = (int)((u1 - u0 + kQRows - 1) / kQRows);
+
+  // ---- K rows of the block
+  if (threadIdx.x < kKeys) {
+    long long row = -1;
+    if ((int)threadIdx.x < nkeys && steps > 0) {
+      const int t = key0 + threadIdx.x;
+      const int page = __ldg(p.block_table + (size_t)b * p.max_pages + t / p.page_size);
+      if (page >= 0 && page < p.num_pages)
+        row = (((long long)page * p.page_size + t % p.page_size) * p.Hkv + hkv) * D;
+      else
+        record_status(p.status, kStatusDeviceCheck);
+    }
+    s_row[threadIdx.x] = row;
+  }
+  __syncthreads();
+  const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(p.kcache);
+  const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q);
+  for (int idx = threadIdx.x; idx < kKeys * U; idx += kWarps * 32) {
+    const int r = idx / U, u = idx % U;
+    const long long row = s_row[r];
+    cp16(sb + unit_at<D>(r, u), kc + (row < 0 ? 0 : row + u * 8), row < 0 ? 0 : 16);
+  }
+  auto load_q = [&](int s) {
+    const uint32_t dst = sb + Lay::kOffQ + (s & 1) * Lay::kQ;
+    for (int idx = threadIdx.x; idx < kQRows * U; idx += kWarps * 32) {
+      const int r = idx / U, u = idx % U;
+      const long long w = u0 + (long long)s * kQRows + r;
+      const bool ok = w < u1;
+      const long long i = ok ? w / G : 0, h = ok ? w - i * G : 0;
+      cp16(dst + unit_at<D>(r, u), qg + ((q0 + i) * p.Hq + (long long)hkv * G + h) * D + u * 8, ok ? 16 : 0);
+    }
+    if (threadIdx.x < kQRows) {
+      const long long w = u0 + (long long)s * kQRows + threadIdx.x;
+      float4 v = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+      if (w < u1) {
+        const long long i = w / G;
+        const int h = hkv * G + (int)(w - i * G);
+        const float lse = __ldg(p.lse + h * p.lse_head + (q0 + i) * p.lse_row);
+        // a row that saw no key (lse = -inf) gives no weight
+        if (lse > -CUDART_INF_F) v.x = -lse * kLog2e;
+        if (p.shape.slopes) v.y = -__ldg(p.shape.slopes + h) * kLog2e;
+        v.z = __int_as_float((int)i + off);
+      }
+      *reinterpret_cast<float4*>(smem + Lay::kOffVec + (s & 1) * Lay::kVec + threadIdx.x * 16) = v;
+    }
+  };
+  if (steps > 0) load_q(0);
+  cp_commit();
+  cp_wait<0>();
+  __syncthreads();
+
+  // ---- this warp's 32 keys as A fragments
+  uint32_t ka[2][D / 16][4];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldsm4(sb + unit_at<D>(warp * 32 + mt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, kk * 2 + (lane >> 4)), ka[mt][kk]);
+
+  const float sl2 = p.scale * kLog2e;
+  const float cap2 = p.shape.cap * kLog2e;
+  const float capk = p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
+  const int g = lane >> 2;
+  const int kg = key0 + warp * 32 + g;        // this thread's keys: kg, + 8, + 16, + 24
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < steps; ++s) {
+    if (s + 1 < steps) load_q(s + 1);
+    cp_commit();
+    const uint32_t qb = sb + Lay::kOffQ + (s & 1) * Lay::kQ;
+    const float4* vec = reinterpret_cast<const float4*>(smem + Lay::kOffVec + (s & 1) * Lay::kVec);
+#pragma unroll
+    for (int nt = 0; nt < kQRows / 16; ++nt) {
+      float c[2][2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bq[4];
+        ldsm4(qb + unit_at<D>(nt * 16 + (lane & 7) + (lane >> 4) * 8, kk * 2 + ((lane >> 3) & 1)), bq);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          mma(c[mt][0], ka[mt][kk], bq[0], bq[1]);
+          mma(c[mt][1], ka[mt][kk], bq[2], bq[3]);
+        }
+      }
+#pragma unroll
+      for (int n8 = 0; n8 < 2; ++n8)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 v = vec[nt * 16 + n8 * 8 + (lane & 3) * 2 + e];
+          const int pos = __float_as_int(v.z);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int dist = pos - (kg + mt * 16 + hf * 8);
+              const float x = c[mt][n8][hf * 2 + e];
+              float y = p.shape.cap > 0.f ? fmaf(-2.f * cap2, tanh_r(x * capk), cap2) : x * sl2;
+              y = fmaf(v.y, fabsf((float)dist), y);
+              bool see = !p.causal || dist >= 0;
+              if (p.shape.window > 0) see = see && abs(dist) < p.shape.window;
+              const float w = ex2(y + v.x);
+              acc[mt * 2 + hf] += see ? w : 0.f;
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();  // the next stage has landed, this one is read
+  }
+  // the four lanes of a key hold different queries
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 1);
+    acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
+    const int r = warp * 32 + g + (i >> 1) * 16 + (i & 1) * 8;
+    if ((lane & 3) == 0 && r < nkeys) {
+      const size_t at = ((size_t)b * p.Hkv + hkv) * cap + key0 + r;
+      const float sum = s_row[r] >= 0 ? acc[i] : 0.f;
+      p.w_out[at] = p.w_in ? fmaf(p.decay, p.w_in[at], sum) : sum;
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_kw(const KeyWeightsParams& p, cudaStream_t stream) {
+  auto kern = key_weights_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KwLayout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.max_pages * p.page_size + kKeys - 1) / kKeys, p.Hkv, p.B);
+  kern<<<grid, kWarps * 32, KwLayout<D>::kBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
+  return p.d == 128 ? launch_kw<128>(p, stream) : launch_kw<64>(p, stream);
+}
+
+}  // namespace fattn

@@ -33,6 +33,42 @@ struct RopeParams {
 
 cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool append, cudaStream_t stream);
 
+struct KeyWeightsParams {
+  const void* q;              // [total_q, Hq, d] bf16
+  const void* kcache;
+  const int32_t* block_table;
+  const int32_t* seqlens_k;
+  const int32_t* cu_seqlens;
+  const float* lse;           // of head h, row r at lse[h * lse_head + r * lse_row]
+  long long lse_head, lse_row;
+  const float* w_in;          // [B, Hkv, max_pages * page_size] or nullptr
+  float* w_out;               // likewise; may be w_in
+  int B, Hq, Hkv, d, page_size, max_pages, num_pages, total_q;
+  int causal;
+  float scale, decay;
+  ScoreShape shape;           // no key ranges
+  int* status;
+};
+
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+
+struct EvictParams {
+  void* kcache;
+  void* vcache;
+  const int32_t* block_table;
+  const int32_t* seqlens;
+  const float* w_in;          // [B, Hkv, max_pages * page_size]
+  const int32_t* dst_table;   // nullptr: in place
+  int32_t* seqlens_out;
+  float* w_out;               // [B, Hkv, dst_max_pages * page_size]
+  int32_t* kept;              // [B, Hkv, keep]
+  int B, Hkv, d, page_size, max_pages, num_pages, dst_max_pages;
+  int keep, first, recent;
+  int* status;
+};
+
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
+
 // From api.cu: the device status word of the current device (nullptr and *err != 0 on
 // failure), the pipeline waits' limit and stall flag, a bf16 [rows, H, d] tensor map, and the
 // calls whose plain and shaped forms differ in `shape` alone (nullptr: plain).

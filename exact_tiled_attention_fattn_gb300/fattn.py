@@ -64,6 +64,10 @@ SIGNATURES_OPS = {
                               _vp, _vp, _vp, _sz, _vp]),
     "fattn_decode_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
                                        _i, _vp, _sz, _vp]),
+    "fattn_key_weights_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                     _i, _i, _f, _f, _vp, _i, _f, _vp]),
+    "fattn_evict_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                               _vp]),
 }
 
 _lib = None
@@ -877,3 +881,87 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
                                        ctypes.c_void_p(_stream_handle(stream)))
     _check("fattn_decode_paged_shaped", st)
     return out, lse
+
+
+# ------------------------------------------------------------------ a budget for the cache
+def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int, lse, weights=None,
+                      decay: float = 1.0, causal: bool = True, scale: float | None = None, softcap: float = 0.0,
+                      slopes=None, window: int = 0, out=None, stream=None):
+    """Attention weight that cached tokens received: out[b, hkv, t] = decay * weights[b, hkv, t] + the sum over
+    the heads of the group and the queries of chunk b of exp(s - lse), fp32 [B, Hkv, max_pages * page_size].
+    q [Tq,Hq,d] and the chunk arguments as in ``fwd_paged``; ``lse`` [Hq,Tq] from the attention call, any strides
+    (``lse.t()`` of ``decode_paged``). ``weights`` None starts from zero; ``out`` may be ``weights``. Slots past a
+    sequence's length are left as they are (zero in a new ``out``)."""
+    lib = load_library()
+    _need_cuda(q, kcache, block_table, seqlens_k, cu_seqlens_q, weights, out)
+    _need_cuda(lse, contiguous=False)
+    if not (q.dtype == kcache.dtype == torch.bfloat16):
+        raise TypeError("key_weights_paged takes bf16 q and cache")
+    if seqlens_k.dtype != torch.int32 or cu_seqlens_q.dtype != torch.int32:
+        raise TypeError("seqlens_k and cu_seqlens_q must be int32")
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, d]")
+    Tq, Hq, d = q.shape
+    B = cu_seqlens_q.numel() - 1
+    _check_paged_cache(kcache, None, block_table, B)
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _expect(kcache, (num_pages, page_size, Hkv, d), "kcache")
+    _expect(seqlens_k, (B,), "seqlens_k")
+    _expect(lse, (Hq, Tq), "lse", torch.float32)
+    shape = (B, Hkv, block_table.shape[1] * page_size)
+    _expect(weights, shape, "weights", torch.float32)
+    _expect(out, shape, "out", torch.float32)
+    _check_shape(slopes, Hq, None, None, None)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.zeros(shape, dtype=torch.float32, device=q.device)
+    st = lib.fattn_key_weights_paged(_ptr(q), _ptr(kcache), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q),
+                                     _ptr(lse), lse.stride(0), lse.stride(1), _ptr(weights), _ptr(out), B, Hq, Hkv, d,
+                                     page_size, block_table.shape[1], num_pages, Tq, int(max_seqlen_q),
+                                     1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
+                                     float(decay), ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_key_weights_paged", st)
+    return out
+
+
+def evict_paged(kcache, vcache, block_table, seqlens, weights, keep: int, recent: int = 0, first: int = 0,
+                dst_table=None, out_weights=None, out_seqlens=None, kept=None, stream=None):
+    """Cuts every KV head of every sequence down to ``keep`` tokens: the first ``first``, the last ``recent`` and the
+    heaviest of the others by ``weights`` fp32 [B,Hkv,max_pages*page_size] (``key_weights_paged``; ties to the lowest
+    index). The kept tokens move, in order, to slots 0, 1, ... of the sequence's own pages, or of the unused pages
+    ``dst_table`` int32 [B, dst_pages] of the same pool. Shared pages must not be evicted in place.
+    Returns (seqlens [B], weights [B,Hkv,dst_pages*page_size], kept indices int32 [B,Hkv,keep], -1 past the end)."""
+    lib = load_library()
+    _need_cuda(kcache, vcache, block_table, seqlens, weights, dst_table, out_weights, out_seqlens, kept)
+    if not (kcache.dtype == vcache.dtype == torch.bfloat16):
+        raise TypeError("evict_paged takes bf16 caches")
+    if seqlens.dtype != torch.int32:
+        raise TypeError("seqlens must be int32")
+    B = seqlens.numel()
+    _expect(seqlens, (B,), "seqlens")
+    _check_paged_cache(kcache, vcache, block_table, B)
+    num_pages, page_size, Hkv, d = kcache.shape
+    if dst_table is not None:
+        if dst_table.dtype != torch.int32:
+            raise TypeError("dst_table must be int32")
+        if dst_table.dim() != 2 or dst_table.shape[0] != B:
+            raise ValueError(f"dst_table must be [{B}, dst_pages]")
+    maxp = block_table.shape[1]
+    dst_pages = maxp if dst_table is None else dst_table.shape[1]
+    _expect(weights, (B, Hkv, maxp * page_size), "weights", torch.float32)
+    _expect(out_weights, (B, Hkv, dst_pages * page_size), "out_weights", torch.float32)
+    _expect(out_seqlens, (B,), "out_seqlens", torch.int32)
+    _expect(kept, (B, Hkv, int(keep)), "kept", torch.int32)
+    if out_weights is None:
+        out_weights = torch.empty((B, Hkv, dst_pages * page_size), dtype=torch.float32, device=kcache.device)
+    if out_seqlens is None:
+        out_seqlens = torch.empty_like(seqlens)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(int(keep), 0)), dtype=torch.int32, device=kcache.device)
+    st = lib.fattn_evict_paged(_ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), _ptr(weights),
+                               _ptr(dst_table), _ptr(out_seqlens), _ptr(out_weights), _ptr(kept), B, Hkv, d, page_size,
+                               maxp, num_pages, dst_pages, int(keep), int(recent), int(first),
+                               ctypes.c_void_p(_stream_handle(stream)))
+    _check("fattn_evict_paged", st)
+    return out_seqlens, out_weights, kept

@@ -9,7 +9,10 @@
  *     that depends on the distance, and see a window, a document or a prefix
  *     (fattn_fwd_shaped, its gradient fattn_bwd_shaped, query chunks and single
  *     tokens over the paged cache: fattn_fwd_paged_shaped,
- *     fattn_decode_paged_shaped).
+ *     fattn_decode_paged_shaped);
+ *   - a budget for the cache: the attention weight that its tokens receive
+ *     (fattn_key_weights_paged), and the eviction of all but the heaviest
+ *     (fattn_evict_paged).
  *
  * The conventions of fattn.h hold: DEVICE pointers owned by the caller, host
  * checks before anything is launched, work enqueued on `stream`, no
@@ -161,6 +164,61 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
                                        float* lse, int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
                                        int num_pages, float scale, float softcap, const float* slopes, int window,
                                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fattn_key_weights_paged — the attention weight that the tokens of a paged cache
+ * receive from query chunks:
+ *   weights_out[b, hkv, t] = decay weights_in[b, hkv, t]
+ *                            + sum over the heads of group hkv and the queries of chunk b of e^{s - lse}
+ * for t < seqlens_k[b]; slots from seqlens_k[b] on are left as they are. s is the
+ * shaped score (softcap, slopes, window as above; causal as in fattn_fwd_paged), lse the
+ * logsumexp that the attention call with the same arguments wrote. Sums are fp32, in a fixed order.
+ *
+ * q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: as fattn_fwd_paged (for single
+ *   tokens q is [B, Hq, d] and cu_seqlens_q = 0, 1, ..., B); any page_size >= 1.
+ * lse: DEVICE fp32, head h and row r at lse[h * lse_head + r * lse_row]: fattn_fwd_paged's [Hq,
+ *   total_q] (total_q, 1) and fattn_decode_paged's [B, Hq] (1, Hq) both serve. A row of -inf gives nothing.
+ * weights_in (NULL: zeros; then decay is not used), weights_out: DEVICE fp32
+ *   [B, Hkv, max_pages_per_seq * page_size]; they may be the same array.
+ * A sequence whose lengths are inconsistent is skipped, a table entry outside the pool gives its tokens
+ *   nothing; both record FATTN_ERR_DEVICE_CHECK.
+ * Errors: as fattn_fwd_paged and the shaped calls; INVALID_ARG also for a decay that is not finite,
+ *   negative lse strides; UNSUPPORTED for d not in {64, 128}, B or Hkv > 65535.
+ */
+fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const int32_t* block_table,
+                                     const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const float* lse,
+                                     long long lse_head, long long lse_row, const float* weights_in, float* weights_out,
+                                     int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
+                                     int total_q, int max_seqlen_q, int causal, float scale, float softcap,
+                                     const float* slopes, int window, float decay, cudaStream_t stream);
+
+/*
+ * fattn_evict_paged — every KV head of every sequence cut down to `keep` tokens.
+ *
+ * Of a sequence's n = seqlens[b] tokens, every head keeps on its own m = min(n, keep): all of them if
+ * n <= keep, else the first `first`, the last `recent` and, of the others, the heaviest by
+ * weights_in[b, hkv, t] (of equal weights the lowest index; NaN is below every number). The kept
+ * tokens, in their order, become tokens 0 .. m - 1: K and V rows move to those slots (bit for bit),
+ * and seqlens_out[b] = m, weights_out[b, hkv, :m] their weights (0 in the rest of the row),
+ * kept[b, hkv, :m] their old indices (-1 in the rest). Keys carry their rotary positions with them;
+ * distances measured by slot (a window, a distance bias) no longer are those of the text.
+ *
+ * dst_table: DEVICE int32 [B, dst_max_pages], the pages (of the same pool) the kept tokens go to, not
+ *   in use by any sequence of the call; or NULL: in place, in the sequence's own first pages
+ *   (dst_max_pages = max_pages_per_seq), which then no other sequence may share.
+ * weights_in [B, Hkv, max_pages_per_seq * page_size], weights_out [B, Hkv, dst_max_pages * page_size]
+ *   (may be weights_in if the sizes agree), kept [B, Hkv, keep]; seqlens_out [B] is not seqlens.
+ * A seqlens entry outside its table counts as an empty sequence; a row whose page is outside the pool
+ *   is not moved; both record FATTN_ERR_DEVICE_CHECK. bf16 caches, any page_size >= 1.
+ * Errors: INVALID_ARG (NULL or misaligned pointers, non-positive sizes, first + recent > keep, kept tokens
+ *   that do not fit dst_max_pages, seqlens_out == seqlens); UNSUPPORTED (d not a multiple of 8 up to
+ *   1024, B * Hkv > 65535).
+ */
+fattn_status fattn_evict_paged(void* kcache, void* vcache, const int32_t* block_table, const int32_t* seqlens,
+                               const float* weights_in, const int32_t* dst_table, int32_t* seqlens_out,
+                               float* weights_out, int32_t* kept, int B, int Hkv, int d, int page_size,
+                               int max_pages_per_seq, int num_pages, int dst_max_pages, int keep, int recent, int first,
+                               cudaStream_t stream);
 
 #ifdef __cplusplus
 }

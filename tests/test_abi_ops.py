@@ -136,3 +136,47 @@ def test_document_ranges():
     assert bool((b[:, 1:] >= b[:, :-1]).all() and (e[:, 1:] >= e[:, :-1]).all())
     with pytest.raises(ValueError):
         F.document_ranges(ids[0])
+
+
+def _weights(lib, **kw):
+    g = lambda n, x: kw.get(n, x)
+    return lib.fattn_key_weights_paged(g("q", A), g("kc", A), g("bt", A), g("sl", A), g("cu", A), g("lse", A), g("lh", 1), 4,
+                                       g("wi", None), g("wo", A), g("B", 2), g("Hq", 4), 2, g("d", 64), g("ps", 16),
+                                       g("maxp", 4), 8, g("T", 2), 1, 1, g("scale", 0.1), g("cap", 0.0), g("slopes", None),
+                                       g("win", 0), g("decay", 1.0), None)
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(kc=None), dict(bt=None), dict(sl=None), dict(cu=None), dict(lse=None),
+                                 dict(wo=None), dict(q=A + 8), dict(wi=A + 2), dict(lh=-1), dict(Hq=3), dict(B=-1),
+                                 dict(ps=0), dict(T=-1), dict(decay=float("inf")), dict(cap=-2.0), dict(win=-1),
+                                 dict(scale=float("nan")), dict(slopes=A + 2)])
+def test_key_weights_refuse(lib, bad):
+    assert _weights(lib, **bad) == F.FATTN_ERR_INVALID_ARG
+
+
+def test_key_weights_limits_and_empty(lib):
+    assert _weights(lib, d=96) == F.FATTN_ERR_UNSUPPORTED
+    assert _weights(lib, maxp=1 << 28) == F.FATTN_ERR_UNSUPPORTED
+    assert _weights(lib, B=70000) == F.FATTN_ERR_UNSUPPORTED
+    assert _weights(lib, B=0, q=None, kc=None) == F.FATTN_OK
+
+
+def _evict(lib, **kw):
+    g = lambda n, x: kw.get(n, x)
+    return lib.fattn_evict_paged(g("kc", A), g("vc", A), g("bt", A), g("sl", A), g("wi", A), g("dt", None), g("so", A + 64),
+                                 g("wo", A), g("kept", A), g("B", 2), g("Hkv", 2), g("d", 64), g("ps", 16), g("maxp", 4), 8,
+                                 g("dmaxp", 4), g("keep", 20), g("recent", 2), g("first", 1), None)
+
+
+@pytest.mark.parametrize("bad", [dict(kc=None), dict(vc=None), dict(bt=None), dict(sl=None), dict(wi=None), dict(so=None),
+                                 dict(wo=None), dict(kept=None), dict(kc=A + 8), dict(so=A), dict(keep=0), dict(recent=-1),
+                                 dict(recent=20), dict(first=-1), dict(dmaxp=3), dict(dt=A, dmaxp=1, wo=A + 64),
+                                 dict(dt=A, dmaxp=3), dict(B=-1), dict(Hkv=0), dict(ps=0)])
+def test_evict_refuses(lib, bad):
+    assert _evict(lib, **bad) == F.FATTN_ERR_INVALID_ARG
+
+
+def test_evict_limits_and_empty(lib):
+    assert _evict(lib, d=60) == F.FATTN_ERR_UNSUPPORTED
+    assert _evict(lib, B=40000) == F.FATTN_ERR_UNSUPPORTED
+    assert _evict(lib, B=0, kc=None) == F.FATTN_OK
