@@ -775,7 +775,7 @@ struct DqLayout {
   static constexpr int kOffK = 2 * kTile;
   static constexpr int kOffV = kOffK + kKStages * kTile;
   static constexpr int kOffBar = kOffV + kVStages * kTile;
-  static constexpr int kNumBars = 20;
+  static constexpr int kNumBars = 21;
   static constexpr int kBarStall = kNumBars;      // test hook: a barrier no role arrives on
   static constexpr int kOffHolder = kOffBar + (kNumBars + 1) * 8;
   static constexpr int kOffAbort = kOffHolder + 8;
@@ -790,7 +790,7 @@ struct DqLayout {
 };
 enum : int {
   kQFull = 0, kQEmpty = 1, kQKvFull = 2, kKEmpty = 5, kVEmpty = 10, kQSFull = 12,
-  kQDpFull = 14, kQDpFree = 15, kQDsFull = 16, kQAccFull = 17, kQAccEmpty = 18, kQMmaDone = 19
+  kQDpFull = 14, kQDpFree = 15, kQDsFull = 16, kQAccFull = 18, kQAccEmpty = 19, kQMmaDone = 20
 };
 // dQ pass: dS of key tile n goes to TMEM columns [kColDs + 64 (n & 1), +64) (bf16 pairs;
 // warpgroup g writes the 32 columns of its keys at + 32 g), so dP of the next tile can be
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* items_started = blocks_done + 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::kNumBars; ++i)
-      mbar_init(bar(i), (i == kQDpFree || i == kQDsFull || i == kQAccEmpty) ? kEwArrivals : 1);
+      mbar_init(bar(i), (i == kQDpFree || i == kQDsFull || i == kQDsFull + 1 || i == kQAccEmpty) ? kEwArrivals : 1);
     mbar_init(bar(Lay::kBarStall), 1);
     *abort = 0;
     *blocks_done = 0;
@@ -956,7 +956,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (!mbar_wait(bar(kQDsFull), n & 1, abort, p.status, p.wait_ns)) {
+          // dS alternates between two barriers as between its buffers: S and dP of tile n + 1 are
+          // issued before this wait, so the element-wise warps may finish dS_{n+1} before a
+          // late issuer looks at dS_n; on one barrier that phase would be gone (a wait by
+          // parity cannot tell two completed phases from none) and the pass would stop
+          if (!mbar_wait(bar(kQDsFull + (n & 1)), (n >> 1) & 1, abort, p.status, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -1102,11 +1106,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                pv[2 * e + 1] * (__uint_as_float(a[2 * e + 1]) - dval));
           tmem_st32(ds_col + 64 * (ndp & 1), w);
         }
-        ++ndp;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQDsFull));
+        if (lane == 0) mbar_arrive(bar(kQDsFull + (ndp & 1)));
+        ++ndp;
         // the previous item's dQ: its accumulator is free for this item's first dQ product
         if (j == 0 && pend >= 0 && !epilogue()) {
           ok = false;
