@@ -779,12 +779,12 @@ struct DqLayout {
   static constexpr int kBarStall = kNumBars;      // test hook: a barrier no role arrives on
   static constexpr int kOffHolder = kOffBar + (kNumBars + 1) * 8;
   static constexpr int kOffAbort = kOffHolder + 8;
-  // two counters: 32-row blocks whose per-row vectors are in the workspace (warps 2-3),
-  // and items the element-wise warps have started
+  // three counters: items whose per-row vectors warp 2 (rows 0-63) and warp 3 (rows 64-127)
+  // have put into the workspace, and items the element-wise warps have started
   static constexpr int kOffCounts = kOffAbort + 8;
   // + slack to align the base to 1024 B; at least 117 KB so that a second CTA
   // (which would wait in tcgen05.alloc for all 512 columns) never shares the SM
-  static constexpr int kUsed = kOffCounts + 8 + 1024;
+  static constexpr int kUsed = kOffCounts + 16 + 1024;
   static constexpr int kBytes = kUsed > 117 * 1024 ? kUsed : 117 * 1024;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -810,15 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + Lay::kOffAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // warps 2-3: 32-row blocks whose vectors are in the workspace; element-wise warps: items started
-  volatile int* blocks_done = reinterpret_cast<volatile int*>(smem + Lay::kOffCounts);
-  volatile int* items_started = blocks_done + 1;
+  // warps 2 and 3: items whose vectors of their rows are in the workspace (one count each, as one
+  // warp may be an item ahead of the other); element-wise warps: items started
+  volatile int* halves_done = reinterpret_cast<volatile int*>(smem + Lay::kOffCounts);
+  volatile int* items_started = halves_done + 2;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::kNumBars; ++i)
       mbar_init(bar(i), (i == kQDpFree || i == kQDsFull || i == kQDsFull + 1 || i == kQAccEmpty) ? kEwArrivals : 1);
     mbar_init(bar(Lay::kBarStall), 1);
     *abort = 0;
-    *blocks_done = 0;
+    halves_done[0] = halves_done[1] = 0;
     *items_started = 0;
     fence_mbar_init();
   }
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int blk = 0; blk < 2; ++blk) row_vectors<D>(p, b, h, i * BT + 64 * (warp - 2) + 32 * blk, lane);
       __threadfence_block();  // the stores above before the count that announces them
       __syncwarp();
-      if (lane == 0) atomicAdd(const_cast<int*>(blocks_done), 2);
+      if (lane == 0) halves_done[warp - 2] = kk + 1;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ element-wise (one query row per thread)
@@ -1045,8 +1046,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const size_t vrow = (size_t)(b * p.Hq + h) * p.Npad + qrow;
       if (warp == 4 && lane == 0) atomicAdd(const_cast<int*>(items_started), 1);
-      // the item's four 32-row blocks of vectors are in the workspace
-      if (!count_wait(blocks_done, 4 * (kk + 1), abort, p.status, p.wait_ns)) break;
+      // the vectors of this warp's rows are in the workspace
+      if (!count_wait(halves_done + (q4 >> 1), kk + 1, abort, p.status, p.wait_ns)) break;
       __threadfence_block();
       const float nl2 = p.ws_nl2[vrow], dval = p.ws_d[vrow];
       const uint64_t nl2x2 = f2_pack(nl2, nl2);
