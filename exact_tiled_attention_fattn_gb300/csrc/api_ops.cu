@@ -89,7 +89,22 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
   // the cap's argument 2 log2(e) scale / softcap must be a number
   if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
   if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
-  *out = {softcap, slopes, window, key_begin, key_end};
+  *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, 0};
+  out->sl2 = scale * 1.4426950408889634f;
+  out->cap2 = softcap * 1.4426950408889634f;
+  out->capk = softcap > 0.f ? 2.f * out->sl2 / softcap : 0.f;
+  out->nicap2 = softcap > 0.f ? -1.f / (out->cap2 * out->cap2) : 0.f;
+  // tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) with an absolute error below 2.5e-7 on |z| <= 0.75 (minimax,
+  // by linear programming), folded into powers of u = z softcap / scale. Outside the range of
+  // scale / softcap where every folded coefficient is an ordinary float the kernels do without.
+  const double k = (double)scale / (softcap > 0.f ? softcap : 1.0);
+  if (softcap > 0.f && std::fabs(k) >= 5e-4 && std::fabs(k) <= 1e2 && softcap < 1e6f) {
+    const double c[5] = {0.9999966, -0.33322031, 0.13220438, -0.04915907, 0.012229};
+    double pw = k * softcap * 1.4426950408889634;
+    for (int i = 0; i < 5; ++i, pw *= k * k) out->poly[i] = make_float2((float)(c[i] * pw), (float)(c[i] * pw));
+    out->poly_limit = (float)(0.75 / std::fabs(k));
+    out->poly_bound = 2.0 * 0.6352 * softcap * 1.4426950408889634 <= 96.0;  // exponents down to -96: normal floats
+  }
   return FATTN_OK;
 }
 

@@ -342,26 +342,85 @@ __device__ __forceinline__ int shaped_row_search(const BwdParams& p, int b, int 
   }
   return from;
 }
-// Constants of a head's scores in log2 units.
-struct ShapeConsts {
-  float sl2, cap2, capk, slope2;
-  __device__ __forceinline__ ShapeConsts(const BwdParams& p, int h)
-      : sl2(p.scale * kLog2e), cap2(p.shape.cap * kLog2e), capk(p.shape.cap > 0.f ? 2.f * p.scale * kLog2e / p.shape.cap : 0.f),
-        slope2(p.shape.slopes ? -__ldg(p.shape.slopes + h) * kLog2e : 0.f) {}
-};
-// P = 2^(score + nl2) of one raw product s at signed distance `dist`, and f, the factor that the
-// cap puts on dS (1 - tanh^2).
-__device__ __forceinline__ float shaped_p(const ShapeConsts& k, bool cap, float s, float dist, float nl2, float& f) {
-  float y;
+// One thread's 32 columns of raw products u: pv = P o f with P = 2^(score + nl) and f the factor that
+// the cap puts on dS (1 - tanh^2), and P itself as bf16 pairs into pk (kPack). Column c lies at
+// distance |dist + step c| and is visible iff va <= c < vb; nl is its row's -lse log2(e), per column
+// (kCols, nlv) or one for all.
+template <bool kCols, bool kPack>
+__device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uint32_t (&u)[32], float dist, float step,
+                                           int va, int vb, const float* nlv, float nl, float* pv, uint32_t* pk) {
+  const ScoreShape& sh = p.shape;
+  const bool edge = !__all_sync(0xffffffffu, va <= 0 && vb >= 32);
+  const uint32_t vis = vb <= 0 || va >= 32 || va >= vb
+                           ? 0u
+                           : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)));
+  float y[32], f[32];
+  const bool cap = sh.cap > 0.f;
   if (cap) {
-    const float r = tanh_r(s * k.capk);
-    y = fmaf(-2.f * k.cap2, r, k.cap2);
-    f = 4.f * r * (1.f - r);
+    if (edge) {  // hidden keys must not decide between the two forms of the cap
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (!((vis >> c) & 1u)) u[c] = 0u;
+    }
+    float hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hi[i] = lo[i] = __uint_as_float(u[i]);
+#pragma unroll
+    for (int c = 4; c < 32; c += 4)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = fmaxf(hi[i], __uint_as_float(u[c + i]));
+        lo[i] = fminf(lo[i], __uint_as_float(u[c + i]));
+      }
+    const float amax = fmaxf(fmax3(fmaxf(hi[0], hi[1]), hi[2], hi[3]), -fmin3(fminf(lo[0], lo[1]), lo[2], lo[3]));
+    if (amax <= sh.poly_limit) {  // by row of the tile; the cap as a polynomial (fattn_internal.h)
+      const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]),
+                     c2 = f2_bits(sh.poly[2]), c3 = f2_bits(sh.poly[3]),
+                     c4 = f2_bits(sh.poly[4]), one = f2_pack(1.f, 1.f), nic2 = f2_pack(sh.nicap2, sh.nicap2);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const uint64_t x = f2_pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), v = f2_mul(x, x);
+        const uint64_t t = f2_mul(x, f2_fma(f2_fma(f2_fma(f2_fma(c4, v, c3), v, c2), v, c1), v, c0));
+        f2_unpack(t, y[c], y[c + 1]);
+        f2_unpack(f2_fma(f2_mul(t, t), nic2, one), f[c], f[c + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float r = tanh_r(__uint_as_float(u[c]) * sh.capk);
+        y[c] = fmaf(-2.f * sh.cap2, r, sh.cap2);
+        f[c] = 4.f * r * (1.f - r);
+      }
+    }
   } else {
-    y = s * k.sl2;
-    f = 1.f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]) * sh.sl2;
   }
-  return ex2(fmaf(k.slope2, fabsf(dist), y) + nl2);
+  if (sh.slopes) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) y[c] = fmaf(slope2, fabsf(fmaf(step, (float)c, dist)), y[c]);
+  }
+#pragma unroll
+  for (int c4 = 0; c4 < 32; c4 += 4) {
+    const float4 l = kCols ? *reinterpret_cast<const float4*>(nlv + c4) : make_float4(nl, nl, nl, nl);
+    f2_unpack(f2_add(f2_pack(y[c4], y[c4 + 1]), f2_pack(l.x, l.y)), y[c4], y[c4 + 1]);
+    f2_unpack(f2_add(f2_pack(y[c4 + 2], y[c4 + 3]), f2_pack(l.z, l.w)), y[c4 + 2], y[c4 + 3]);
+  }
+  if (edge) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((vis >> c) & 1u)) y[c] = -CUDART_INF_F;
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) pv[c] = ex2(y[c]);
+  if constexpr (kPack) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
+  }
+  if (cap) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) pv[c] *= f[c];
+  }
 }
 
 // 64 consecutive fp32 TMEM columns of this lane.
@@ -661,26 +720,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float pv[64];
         if constexpr (kShaped) {
-          uint32_t u[64];
-          tmem_ld64(s_col, u);
-          const float* nl = vec + cb;
-          const ShapeConsts k(p, hkv * G + t / ni);
-          const bool cap = p.shape.cap > 0.f;
-          const float dist = (float)(i * BT + cb - (j * BT + r));  // query of column 0 minus the key
-          const int va = qa - i * BT - cb, vb = qb - i * BT - cb;  // visible columns [va, vb)
-          uint32_t pk[32];
+          const float slope2 = p.shape.slopes ? -__ldg(p.shape.slopes + hkv * G + t / ni) * kLog2e : 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            float f0, f1;
-            float p0 = shaped_p(k, cap, __uint_as_float(u[c]), dist + (float)c, nl[c], f0);
-            float p1 = shaped_p(k, cap, __uint_as_float(u[c + 1]), dist + (float)(c + 1), nl[c + 1], f1);
-            p0 = c >= va && c < vb ? p0 : 0.f;
-            p1 = c + 1 >= va && c + 1 < vb ? p1 : 0.f;
-            pk[c / 2] = pack_bf16x2(p0, p1);
-            pv[c] = p0 * f0;  // dS = (P f) o (dP - D)
-            pv[c + 1] = p1 * f1;
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];  // P^T in bf16 over the first 32 of this warpgroup's S^T columns, 16 at a time
+            uint32_t u[32];
+            tmem_ld32(s_col + 32 * q, u);
+            const int i32 = i * BT + cb + 32 * q;  // query of the first column
+            shaped_p32<true, true>(p, slope2, u, (float)(i32 - (j * BT + r)), 1.f, qa - i32, qb - i32,
+                                   vec + cb + 32 * q, 0.f, pv + 32 * q, pk);
+            tmem_st16(s_col + 16 * q, pk);
           }
-          tmem_st32(s_col, pk);
         } else {
           uint32_t u[64];
           tmem_ld64(s_col, u);
@@ -1060,18 +1110,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float pv[64];
         if constexpr (kShaped) {
-          uint32_t u[64];
-          tmem_ld64(s_col, u);
-          const ShapeConsts k(p, h);
-          const bool cap = p.shape.cap > 0.f;
-          const int kb = (top - 1 - j) * BT + cb;       // key of column 0
-          const float dist = (float)(qrow - kb);
-          const int va = klo - kb, vb = khi - kb;       // visible columns [va, vb)
+          const float slope2 = p.shape.slopes ? -__ldg(p.shape.slopes + h) * kLog2e : 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float f;
-            const float pc = shaped_p(k, cap, __uint_as_float(u[c]), dist - (float)c, nl2, f);
-            pv[c] = c >= va && c < vb ? pc * f : 0.f;
+          for (int q = 0; q < 2; ++q) {
+            uint32_t u[32];
+            tmem_ld32(s_col + 32 * q, u);
+            const int kb = (top - 1 - j) * BT + cb + 32 * q;  // key of the first column
+            shaped_p32<false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, nullptr, nl2, pv + 32 * q,
+                                     nullptr);
           }
         } else {
           uint32_t u[64];

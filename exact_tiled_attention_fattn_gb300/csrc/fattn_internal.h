@@ -22,6 +22,14 @@ struct ScoreShape {
   int window;               // |pos - j| < window; 0: none
   const int32_t* key_begin; // device, one per query row, non-decreasing in a sequence: keys
   const int32_t* key_end;   // [begin, end) are visible; nullptr: no bound
+  // the scores' constants in log2 units: scale log2(e), cap log2(e), 2 scale log2(e) / cap, and
+  // -1 / (cap log2(e))^2
+  float sl2, cap2, capk, nicap2;
+  // The cap as a polynomial of the raw product u = q.k, for |u| <= poly_limit (below 0: never):
+  // log2(e) cap tanh(scale u / cap) = u P(u^2), P's coefficients from the lowest power up.
+  float2 poly[5];           // (each twice: the packed FMAs read them as pairs)
+  float poly_limit;
+  int poly_bound;           // the cap is small enough for the row bound of the fused form (prefill_tc.cu)
 };
 
 // Problem description shared by both prefill kernels.

@@ -121,9 +121,13 @@ enum : int {
   kBarSFree = kBarMaskFull + 2 * kMaskSlotsMax, kBarPvDone = kBarSFree + 2, kBarCount = kBarPvDone + 2
 };
 
-enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4, kModeShaped = 5,
-       kModeShapedPaged = 6 };
-__host__ __device__ constexpr bool mode_shaped(int m) { return m == kModeShaped || m == kModeShapedPaged; }
+enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4 };
+// Shaped variants: kModeShaped plus what the scores get (key ranges and the window always) and
+// whether K/V come through a block table. One kernel for each, as the softmax loop of the one
+// with everything under run-time switches is 6 % slower without a cap or bias: its unrolled
+// forms no longer stay in the instruction cache.
+enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4 };
+__host__ __device__ constexpr bool mode_shaped(int m) { return m >= kModeShaped; }
 
 template <int D, int kMode>
 struct TcLayout {
@@ -337,8 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                       const PrefillParams p) {
   constexpr bool kSparse = kMode == kModeSparse;  // fixed block mask, zero blocks skipped
-  constexpr bool kPaged = kMode == kModePaged || kMode == kModeShapedPaged;  // K/V through a block table
-  constexpr bool kShaped = mode_shaped(kMode);    // tanh cap, distance bias, window, key ranges
+  constexpr bool kPaged = kMode == kModePaged || (mode_shaped(kMode) && (kMode & kShapePaged));  // K/V through a block table
+  constexpr bool kShaped = mode_shaped(kMode);    // window and key ranges
+  constexpr bool kCap = kShaped && (kMode & kShapeCap);    // and the scores' tanh cap
+  constexpr bool kBias = kShaped && (kMode & kShapeBias);  // and distance bias
+  // scores in log2 units before the row maximum (else as the product left them)
+  constexpr bool kUnits = kCap || kBias;
   constexpr bool kMasked = kMode == kModeMasked;  // additive bf16 mask M on the scores
   constexpr bool kFp8 = kMode == kModeFp8;        // E4M3 Q, K, V; P in E4M3 through shared memory
   // key tiles visited from the last (the diagonal under the causal rule) down to 0, so that the
@@ -814,12 +822,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool neg = sl2 < 0.f;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint64_t scale2 = f2_pack(p.scale, p.scale);
-    // shaped variant: capped, biased or negatively scaled scores are brought to log2 units
-    // before the row maximum, others stay as the product left them (shape_mul = sl2)
-    const bool log2_units = kShaped && (p.shape.cap > 0.f || p.shape.slopes != nullptr || !(sl2 > 0.f));
-    const float shape_mul = log2_units ? 1.f : sl2;
-    const float cap2 = kShaped ? p.shape.cap * kLog2e : 0.f;
-    const float capk = kShaped && p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
     uint32_t ns = 0, no = 0;                 // S_t and O_t completions seen
     uint32_t npv = 0;                        // O_t += P_t V completions seen (dense d = 64)
     const uint32_t p_col = tmem + lane_off + (Lay::kPTmem ? Lay::col_p(t) : Lay::col_s(t));
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim = shape_hi(p.shape, (long long)x.row0 + rc, rc + x.off, x.Lk, p.causal);
         // ranges that are not monotone: the row's keys are not all among its tile's
         if (lo < lim && (lo < (kv_hi - nt) * BN || lim > kv_hi * BN)) record_status(p.status, kStatusDeviceCheck);
-        if (p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
+        if (kBias && p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
       } else {
         lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;
       }
@@ -1020,24 +1022,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarSFree + t));
           }
         }
-        if constexpr (kShaped) {
-          if (p.shape.cap > 0.f) {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) s[c] = fmaf(-2.f * cap2, tanh_r(s[c] * capk), cap2);
-          } else if (log2_units) {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) s[c] *= sl2;
-          }
-          if (p.shape.slopes) {
-            const float dist = (float)(pos - kbase);
-#pragma unroll
-            for (int c = 0; c < BN; ++c) s[c] = fmaf(slope2, fabsf(dist - (float)c), s[c]);
-          }
-          if (masked || kbase < lo) {
-            const uint32_t span = (uint32_t)max(lim - lo, 0), first_key = (uint32_t)(lo - kbase);
+        bool fused = false;      // this row's cap is taken with its exponentials below
+        float fused_max = 0.f;   // and this bounds its capped scores
+        const bool edge = kShaped && (masked || kbase < lo);
+        const uint32_t span = kShaped ? (uint32_t)max(lim - lo, 0) : 0u, first_key = (uint32_t)(lo - kbase);
+        if constexpr (kCap) {
+          if (edge) {  // hidden keys must not decide between the forms of the cap
 #pragma unroll
             for (int c = 0; c < BN; ++c)
-              if ((uint32_t)c - first_key >= span) s[c] = -CUDART_INF_F;
+              if ((uint32_t)c - first_key >= span) s[c] = 0.f;
+          }
+          float a[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = fabsf(s[i]);
+#pragma unroll
+          for (int c = 8; c < BN; c += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              a[i] = fmax3(a[i], fabsf(s[c + i]), fabsf(s[c + 8 + i < BN ? c + 8 + i : c + i]));
+          const float amax = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+          // By row, so that a row does not depend on its neighbours. Where the polynomial holds, no key is
+          // hidden and nothing is added to the capped score, the row takes its capped scores together with
+          // their exponentials, against the cap of its largest |u| in place of their maximum: a bound
+          // that is at most 2 tanh(0.75) cap above it, which poly_bound admits where the exponentials stay
+          // normal numbers.
+          if (!kBias && amax <= p.shape.poly_limit && !edge && p.shape.poly_bound) {
+            fused = true;
+            const float v = amax * amax;
+            fused_max = amax * fabsf(fmaf(fmaf(fmaf(fmaf(p.shape.poly[4].x, v, p.shape.poly[3].x), v, p.shape.poly[2].x), v,
+                                               p.shape.poly[1].x), v, p.shape.poly[0].x));
+          } else if (amax <= p.shape.poly_limit) {
+            // the polynomial: six packed FMAs a pair on a pipe with room, where the exponential and the
+            // reciprocal would go to the one that every score's own exponential needs
+            const uint64_t c0 = f2_bits(p.shape.poly[0]), c1 = f2_bits(p.shape.poly[1]),
+                           c2 = f2_bits(p.shape.poly[2]), c3 = f2_bits(p.shape.poly[3]),
+                           c4 = f2_bits(p.shape.poly[4]);
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+              const uint64_t u2 = f2_pack(s[c], s[c + 1]), v2 = f2_mul(u2, u2);
+              f2_unpack(f2_mul(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, v2, c3), v2, c2), v2, c1), v2, c0)), s[c], s[c + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = fmaf(-2.f * p.shape.cap2, tanh_r(s[c] * p.shape.capk), p.shape.cap2);
+          }
+        }
+        if constexpr (kBias) {
+          const float dist = (float)(pos - kbase);
+          const float mul = kCap ? 1.f : p.shape.sl2;
+          if (x.base + t * BM + q4 * 32 + x.off >= kbase + BN - 1) {
+            // no key of the tile lies past a row of the warp: |pos - j| = dist - c, linear in c
+            const uint64_t mulx2 = f2_pack(mul, mul);
+            const float b0 = slope2 * dist;
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+              const uint64_t bias = f2_pack(fmaf(-slope2, (float)c, b0), fmaf(-slope2, (float)(c + 1), b0));
+              const uint64_t u2 = f2_pack(s[c], s[c + 1]);
+              f2_unpack(kCap ? f2_add(u2, bias) : f2_fma(u2, mulx2, bias), s[c], s[c + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], mul, slope2 * fabsf(dist - (float)c));
+          }
+        }
+        if constexpr (kShaped) {
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if ((uint32_t)c - first_key >= span) s[c] = !kUnits && neg ? CUDART_INF_F : -CUDART_INF_F;
           }
           masked = false;
         }
@@ -1047,12 +1099,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kbase + c >= lim) s[c] = neg ? CUDART_INF_F : -CUDART_INF_F;
         }
         // row max (min for a negative scale): 8 independent chains of 3-input max
-        float mx;
-        {
+        float mx = fused_max;
+        if (!(kCap && !kBias && fused)) {
           float a[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] = s[i];
-          if (kMasked || kShaped || !neg) {
+          if (kMasked || kUnits || !neg) {
 #pragma unroll
             for (int c = 8; c < BN; c += 16)
 #pragma unroll
@@ -1066,15 +1118,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmin3(fmin3(a[0], a[1], a[2]), fmin3(a[3], a[4], a[5]), fminf(a[6], a[7]));
           }
         }
-        // (the masked scores carry the scale, the shaped ones the scale and log2(e) unless they
-        // are as the product left them)
-        const float m_cand = fmaxf(m, mx * (kMasked ? kLog2e : kShaped ? shape_mul : sl2));
+        // (the masked scores carry the scale, the capped and biased ones the scale and log2(e))
+        const float m_cand = fmaxf(m, kUnits ? mx : mx * (kMasked ? kLog2e : sl2));
         const bool need = m_cand > m + kLazyRescaleLog2;          // always true on the first tile
         const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
         const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
         const float alpha = ex2(m - base);                        // 1 when m is kept
         const uint64_t nbase2 = f2_pack(-base, -base);
-        const uint64_t mul2 = kMasked ? f2_pack(kLog2e, kLog2e) : kShaped ? f2_pack(shape_mul, shape_mul) : sl2x2;
+        const uint64_t mul2 = kMasked ? f2_pack(kLog2e, kLog2e) : sl2x2;
         constexpr int kAcc = kMasked ? 2 : 8;  // packed row-sum partials (fewer registers when masked)
         uint64_t acc2[8] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};  // row-sum partials, packed pairs
         // a column pair of P: bf16x2, or (FP8 variant) E4M3x2 in the low 16 bits
@@ -1085,11 +1136,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             return pack_bf16x2(p0, p1);
         };
         uint32_t pk[BN / 2];
-        if (!masked) {
+        if (kCap && !kBias && fused) {  // 2^(u P(u^2) - base)
+          const uint64_t c0 = f2_bits(p.shape.poly[0]), c1 = f2_bits(p.shape.poly[1]),
+                         c2 = f2_bits(p.shape.poly[2]), c3 = f2_bits(p.shape.poly[3]),
+                         c4 = f2_bits(p.shape.poly[4]);
+#pragma unroll
+          for (int c = 0; c < BN; c += 2) {
+            const uint64_t u2 = f2_pack(s[c], s[c + 1]), v2 = f2_mul(u2, u2);
+            float a0, a1;
+            f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, v2, c3), v2, c2), v2, c1), v2, c0), nbase2), a0, a1);
+            const float p0 = ex2(a0), p1 = ex2(a1);
+            acc2[(c >> 1) & (kAcc - 1)] = f2_add(acc2[(c >> 1) & (kAcc - 1)], f2_pack(p0, p1));
+            pk[c / 2] = pack_p(p0, p1);
+          }
+        } else if (!masked) {
 #pragma unroll
           for (int c = 0; c < BN; c += 2) {
             float a0, a1;
-            f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), mul2, nbase2), a0, a1);
+            f2_unpack(kUnits ? f2_add(f2_pack(s[c], s[c + 1]), nbase2) : f2_fma(f2_pack(s[c], s[c + 1]), mul2, nbase2), a0, a1);
             const float p0 = ex2(a0), p1 = ex2(a1);
             acc2[(c >> 1) & (kAcc - 1)] = f2_add(acc2[(c >> 1) & (kAcc - 1)], f2_pack(p0, p1));
             pk[c / 2] = pack_p(p0, p1);
@@ -1259,6 +1323,24 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtens
   return cudaGetLastError();
 }
 
+template <int D, int kShape>
+cudaError_t launch_shaped_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const CUtensorMap& to, int num_sms, cudaStream_t stream) {
+  return p.block_table ? launch_t<D, kModeShaped + kShape + kShapePaged>(p, tq, tk, tv, to, num_sms, stream)
+                       : launch_t<D, kModeShaped + kShape>(p, tq, tk, tv, to, num_sms, stream);
+}
+
+template <int D>
+cudaError_t launch_shaped(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const CUtensorMap& to, int num_sms, cudaStream_t stream) {
+  // (a scale of 0 goes with the bias: -inf marks hidden keys, and raw products would carry it to 0 * inf)
+  const bool cap = p.shape.cap > 0.f, bias = p.shape.slopes != nullptr || p.scale == 0.f;
+  if (cap && bias) return launch_shaped_t<D, kShapeCap + kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
+  if (cap) return launch_shaped_t<D, kShapeCap>(p, tq, tk, tv, to, num_sms, stream);
+  if (bias) return launch_shaped_t<D, kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
+  return launch_shaped_t<D, 0>(p, tq, tk, tv, to, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -1267,13 +1349,9 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, con
     if (p.d == 128) return launch_t<128, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
     return launch_t<64, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
   }
-  if (p.shaped) {
-    if (p.block_table)
-      return p.d == 128 ? launch_t<128, kModeShapedPaged>(p, tq, tk, tv, to, num_sms, stream)
-                        : launch_t<64, kModeShapedPaged>(p, tq, tk, tv, to, num_sms, stream);
-    return p.d == 128 ? launch_t<128, kModeShaped>(p, tq, tk, tv, to, num_sms, stream)
-                      : launch_t<64, kModeShaped>(p, tq, tk, tv, to, num_sms, stream);
-  }
+  if (p.shaped)
+    return p.d == 128 ? launch_shaped<128>(p, tq, tk, tv, to, num_sms, stream)
+                      : launch_shaped<64>(p, tq, tk, tv, to, num_sms, stream);
   if (p.block_table) {
     if (p.d == 128) return launch_t<128, kModePaged>(p, tq, tk, tv, to, num_sms, stream);
     return launch_t<64, kModePaged>(p, tq, tk, tv, to, num_sms, stream);
