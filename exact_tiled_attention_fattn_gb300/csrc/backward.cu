@@ -294,6 +294,8 @@ __device__ __forceinline__ void write_ds(uint32_t dp_col, const float (&pv)[64],
 }
 
 // ------------------------------------------------------------------ shaped scores
+// Variants of both kernels: kPlain, or what the shaped scores get (key ranges and the window always).
+enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2 };
 // Key tiles [top - n, top) that the rows of query tile i see, n >= 1: a tile whose rows see no
 // key visits one tile with everything masked (its dQ is the zero that this gives).
 __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n) {
@@ -346,7 +348,7 @@ __device__ __forceinline__ int shaped_row_search(const BwdParams& p, int b, int 
 // the cap puts on dS (1 - tanh^2), and P itself as bf16 pairs into pk (kPack). Column c lies at
 // distance |dist + step c| and is visible iff va <= c < vb; nl is its row's -lse log2(e), per column
 // (kCols, nlv) or one for all.
-template <bool kCols, bool kPack>
+template <int kShape, bool kCols, bool kPack>
 __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uint32_t (&u)[32], float dist, float step,
                                            int va, int vb, const float* nlv, float nl, float* pv, uint32_t* pk) {
   const ScoreShape& sh = p.shape;
@@ -354,25 +356,25 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
   const uint32_t vis = vb <= 0 || va >= 32 || va >= vb
                            ? 0u
                            : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)));
+  constexpr bool cap = kShape & kShapeCap, bias = kShape & kShapeBias;
   float y[32], f[32];
-  const bool cap = sh.cap > 0.f;
-  if (cap) {
+  if constexpr (cap) {
     if (edge) {  // hidden keys must not decide between the two forms of the cap
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         if (!((vis >> c) & 1u)) u[c] = 0u;
     }
-    float hi[4], lo[4];
+    float a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hi[i] = lo[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < 4; ++i)
+      a[i] = fmax3(fabsf(__uint_as_float(u[i])), fabsf(__uint_as_float(u[i + 4])), fabsf(__uint_as_float(u[i + 8])));
 #pragma unroll
-    for (int c = 4; c < 32; c += 4)
+    for (int c = 12; c < 28; c += 8)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi[i] = fmaxf(hi[i], __uint_as_float(u[c + i]));
-        lo[i] = fminf(lo[i], __uint_as_float(u[c + i]));
-      }
-    const float amax = fmaxf(fmax3(fmaxf(hi[0], hi[1]), hi[2], hi[3]), -fmin3(fminf(lo[0], lo[1]), lo[2], lo[3]));
+      for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], fabsf(__uint_as_float(u[c + i])), fabsf(__uint_as_float(u[c + 4 + i])));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], fabsf(__uint_as_float(u[28 + i])));
+    const float amax = fmax3(fmaxf(a[0], a[1]), a[2], a[3]);
     if (amax <= sh.poly_limit) {  // by row of the tile; the cap as a polynomial (fattn_internal.h)
       const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]),
                      c2 = f2_bits(sh.poly[2]), c3 = f2_bits(sh.poly[3]),
@@ -394,17 +396,23 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]) * sh.sl2;
+    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]);
   }
-  if (sh.slopes) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) y[c] = fmaf(slope2, fabsf(fmaf(step, (float)c, dist)), y[c]);
-  }
+  // y (times the scale without a cap) + bias + nl
+  const uint64_t mul = f2_pack(sh.sl2, sh.sl2);
 #pragma unroll
   for (int c4 = 0; c4 < 32; c4 += 4) {
-    const float4 l = kCols ? *reinterpret_cast<const float4*>(nlv + c4) : make_float4(nl, nl, nl, nl);
-    f2_unpack(f2_add(f2_pack(y[c4], y[c4 + 1]), f2_pack(l.x, l.y)), y[c4], y[c4 + 1]);
-    f2_unpack(f2_add(f2_pack(y[c4 + 2], y[c4 + 3]), f2_pack(l.z, l.w)), y[c4 + 2], y[c4 + 3]);
+    float4 l = kCols ? *reinterpret_cast<const float4*>(nlv + c4) : make_float4(nl, nl, nl, nl);
+    if constexpr (bias) {
+      l.x = fmaf(slope2, fabsf(fmaf(step, (float)c4, dist)), l.x);
+      l.y = fmaf(slope2, fabsf(fmaf(step, (float)(c4 + 1), dist)), l.y);
+      l.z = fmaf(slope2, fabsf(fmaf(step, (float)(c4 + 2), dist)), l.z);
+      l.w = fmaf(slope2, fabsf(fmaf(step, (float)(c4 + 3), dist)), l.w);
+    }
+    const uint64_t y0 = f2_pack(y[c4], y[c4 + 1]), y1 = f2_pack(y[c4 + 2], y[c4 + 3]);
+    const uint64_t l0 = f2_pack(l.x, l.y), l1 = f2_pack(l.z, l.w);
+    f2_unpack(cap ? f2_add(y0, l0) : f2_fma(y0, mul, l0), y[c4], y[c4 + 1]);
+    f2_unpack(cap ? f2_add(y1, l1) : f2_fma(y1, mul, l1), y[c4 + 2], y[c4 + 3]);
   }
   if (edge) {
 #pragma unroll
@@ -417,9 +425,10 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
 #pragma unroll
     for (int c = 0; c < 32; c += 2) pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
   }
-  if (cap) {
+  if constexpr (cap) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) pv[c] *= f[c];
+    for (int c = 0; c < 32; c += 2)
+      f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(f[c], f[c + 1])), pv[c], pv[c + 1]);
   }
 }
 
@@ -466,13 +475,14 @@ enum : int {
   kAccFull = 10, kAccEmpty = 11, kMmaDone = 12, kDvFull = 13
 };
 
-template <int D, bool kShaped>
+template <int D, int kShape>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                     const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
                     const BwdParams p) {
   using Lay = DkdvLayout<D>;
+  constexpr bool kShaped = kShape != kPlain;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -720,14 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float pv[64];
         if constexpr (kShaped) {
-          const float slope2 = p.shape.slopes ? -__ldg(p.shape.slopes + hkv * G + t / ni) * kLog2e : 0.f;
+          const float slope2 = (kShape & kShapeBias) ? -__ldg(p.shape.slopes + hkv * G + t / ni) * kLog2e : 0.f;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t pk[16];  // P^T in bf16 over the first 32 of this warpgroup's S^T columns, 16 at a time
             uint32_t u[32];
             tmem_ld32(s_col + 32 * q, u);
             const int i32 = i * BT + cb + 32 * q;  // query of the first column
-            shaped_p32<true, true>(p, slope2, u, (float)(i32 - (j * BT + r)), 1.f, qa - i32, qb - i32,
+            shaped_p32<kShape, true, true>(p, slope2, u, (float)(i32 - (j * BT + r)), 1.f, qa - i32, qb - i32,
                                    vec + cb + 32 * q, 0.f, pv + 32 * q, pk);
             tmem_st16(s_col + 16 * q, pk);
           }
@@ -847,12 +857,13 @@ enum : int {
 // written while dS of this one still feeds dQ += dS K.
 constexpr uint32_t kColDs = 384;
 
-template <int D, bool kShaped>
+template <int D, int kShape>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const BwdParams p) {
   using Lay = DqLayout<D>;
+  constexpr bool kShaped = kShape != kPlain;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -1110,13 +1121,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float pv[64];
         if constexpr (kShaped) {
-          const float slope2 = p.shape.slopes ? -__ldg(p.shape.slopes + h) * kLog2e : 0.f;
+          const float slope2 = (kShape & kShapeBias) ? -__ldg(p.shape.slopes + h) * kLog2e : 0.f;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t u[32];
             tmem_ld32(s_col + 32 * q, u);
             const int kb = (top - 1 - j) * BT + cb + 32 * q;  // key of the first column
-            shaped_p32<false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, nullptr, nl2, pv + 32 * q,
+            shaped_p32<kShape, false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, nullptr, nl2, pv + 32 * q,
                                      nullptr);
           }
         } else {
@@ -1180,14 +1191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kShaped>
+template <int D, int kShape>
 cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
                          cudaStream_t stream) {
   const int nt = (p.N + BT - 1) / BT;
   cudaError_t e;
   {  // dQ, and the two per-row vectors the dK/dV pass reads
-    auto kern = bwd_dq_kernel<D, kShaped>;
+    auto kern = bwd_dq_kernel<D, kShape>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<D>::kBytes);
     if (e != cudaSuccess) return e;
     const long long items = (long long)p.B * p.Hq * nt;
@@ -1197,7 +1208,7 @@ cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtens
     if (e != cudaSuccess) return e;
   }
   {
-    auto kern = bwd_dkdv_kernel<D, kShaped>;
+    auto kern = bwd_dkdv_kernel<D, kShape>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
     if (e != cudaSuccess) return e;
     const long long items = (long long)p.B * p.Hkv * nt;
@@ -1208,16 +1219,25 @@ cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtens
   return e;
 }
 
+template <int D>
+cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
+                         cudaStream_t stream) {
+  if (!p.shaped) return launch_bwd_t<D, kPlain>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  const bool cap = p.shape.cap > 0.f, bias = p.shape.slopes != nullptr;
+  if (cap && bias) return launch_bwd_t<D, kShapeCap + kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  if (cap) return launch_bwd_t<D, kShapeCap>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  if (bias) return launch_bwd_t<D, kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  return launch_bwd_t<D, 0>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_backward(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
                             cudaStream_t stream) {
-  if (p.shaped)
-    return p.d == 128 ? launch_bwd_t<128, true>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream)
-                      : launch_bwd_t<64, true>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
-  if (p.d == 128) return launch_bwd_t<128, false>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
-  return launch_bwd_t<64, false>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  return p.d == 128 ? launch_bwd_d<128>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream)
+                    : launch_bwd_d<64>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
 }
 
 }  // namespace fattn
