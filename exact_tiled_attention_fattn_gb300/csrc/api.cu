@@ -2,6 +2,7 @@
 // descriptor encoding and kernel dispatch. See include/fattn.h for the
 // contract of every entry point.
 #include "fattn.h"
+#include "fattn_ops.h"
 #include "fattn_internal.h"
 #include "ops_internal.h"
 
@@ -359,7 +360,8 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   const long long rows = (long long)B * N;
   const long long npad = ((long long)N + 127) / 128 * 128;
   if (rows > 0x7fffffffLL || (long long)B * Hq * npad > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
-  const size_t need = fattn_bwd_workspace_size(B, Hq, N);
+  const size_t vectors = fattn_bwd_workspace_size(B, Hq, N);
+  const size_t need = shape ? fattn_bwd_shaped_workspace_size(B, Hq, N) : vectors;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FATTN_ERR_WORKSPACE;
 
@@ -368,12 +370,13 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   p.q = q; p.k = k; p.v = v; p.o = o; p.dout = dout; p.lse = lse;
   p.dq = dq; p.dk = dk; p.dv = dv;
   p.ws_nl2 = static_cast<float*>(workspace);
-  p.ws_d = reinterpret_cast<float*>(static_cast<char*>(workspace) + need / 2);
+  p.ws_d = reinterpret_cast<float*>(static_cast<char*>(workspace) + vectors / 2);
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.N = N; p.d = d; p.Npad = (int)npad;
   p.causal = causal ? 1 : 0; p.scale = scale;
   if (shape) {
     p.shaped = 1;
     p.shape = *shape;
+    p.ws_keys = reinterpret_cast<int2*>(static_cast<char*>(workspace) + vectors);
   }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;

@@ -156,6 +156,13 @@ extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache
                         max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, &shape, stream);
 }
 
+extern "C" size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int N) {
+  const size_t vectors = fattn_bwd_workspace_size(B, Hq, N);
+  if (vectors == 0) return 0;
+  const size_t npad = ((size_t)N + 127) / 128 * 128;
+  return vectors + ((size_t)B * npad * 8 + 255) / 256 * 256;
+}
+
 extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                          const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
                                          int d, int causal, float scale, float softcap, const float* slopes, int window,

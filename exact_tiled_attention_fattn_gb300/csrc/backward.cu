@@ -306,44 +306,48 @@ __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int 
   top = lo < hi ? (hi + BT - 1) / BT : t0 + 1;
   n = max(top - t0, 1);
 }
-// First of the query tiles [from, nt) that reaches past key `key` (its last row's end is above
-// it), or with kBegin first that starts past it (its first row's begin is above it). The
-// bounds are monotone, so both are bisections.
-template <bool kBegin>
-__device__ __forceinline__ int shaped_tile_search(const BwdParams& p, int b, int from, int nt, int key) {
-  int a = from, e = nt;
-  while (a < e) {
-    const int m = (a + e) >> 1;
-    const int row = kBegin ? m * BT : min((m + 1) * BT, p.N) - 1;
-    const long long gr = (long long)b * p.N + row;
-    const bool past = kBegin ? shape_lo(p.shape, gr, row) > key : shape_hi(p.shape, gr, row, p.N, p.causal) > key;
-    if (past)
-      e = m;
-    else
-      a = m + 1;
+// The ranges seen from the keys: the queries that see key j are [qa_j, qb_j), as the bounds are
+// monotone: qa_j the first row whose end is above j, qb_j the first whose begin is. The dQ pass's
+// warps 2-3 write them for the dK/dV pass, 32 rows a warp at a time: row i is qa of the keys
+// [end_{i-1}, end_i) and qb of the keys [begin_{i-1}, begin_i), row N that of the rest, and the
+// whole warp writes each row's keys. (Searching them per key and item in the dK/dV pass took 2 to 3 us
+// at the start of every item: packed documents, B=4 H=32 N=4096, 966 us for the whole call.)
+__device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker, int workers, int lane) {
+  const int blocks = (p.N + 1 + 31) / 32;  // rows 0 .. N of a sequence
+  for (int w = worker; w < p.B * blocks; w += workers) {
+    const int b = w / blocks, i = (w - b * blocks) * 32 + lane;
+    const long long row0 = (long long)b * p.N;
+    auto begin = [&](int r) { return r < 0 ? 0 : r >= p.N ? p.Npad : min(shape_lo(p.shape, row0 + r, r), p.N); };
+    auto end = [&](int r) {
+      return r < 0 ? 0 : r >= p.N ? p.Npad : max(shape_hi(p.shape, row0 + r, r, p.N, p.causal), 0);
+    };
+    int a0 = 0, a1 = 0, b0 = 0, b1 = 0;      // this lane's keys: qa = i for [a0, a1), qb = i for [b0, b1)
+    if (i <= p.N) {
+      a0 = end(i - 1);
+      a1 = end(i);
+      b0 = begin(i - 1);
+      b1 = begin(i);
+    }
+    int2* out = p.ws_keys + (size_t)b * p.Npad;
+    for (int l = 0; l < 32; ++l) {
+      const int r = (w - b * blocks) * 32 + l;
+      const int x0 = __shfl_sync(0xffffffffu, a0, l), x1 = __shfl_sync(0xffffffffu, a1, l);
+      const int y0 = __shfl_sync(0xffffffffu, b0, l), y1 = __shfl_sync(0xffffffffu, b1, l);
+      for (int k = x0 + lane; k < x1; k += 32) out[k].x = r;
+      for (int k = y0 + lane; k < y1; k += 32) out[k].y = r;
+    }
   }
-  return a;
 }
 // Query tiles [i0, i0 + n) that see a key of key tile j, n >= 1 (a key tile that no row sees
 // visits one with everything masked: its dK and dV are the zeros that this gives).
 __device__ __forceinline__ void shaped_query_tiles(const BwdParams& p, int b, int j, int nt, int& i0, int& n) {
-  i0 = min(shaped_tile_search<false>(p, b, p.causal ? j : 0, nt, j * BT), nt - 1);
-  n = max(shaped_tile_search<true>(p, b, i0, nt, min((j + 1) * BT, p.N) - 1) - i0, 1);
+  const int2* keys = p.ws_keys + (size_t)b * p.Npad;
+  const int first = __ldg(&keys[j * BT].x), last = __ldg(&keys[min((j + 1) * BT, p.N) - 1].y);
+  // (clamped, so that even a workspace the dQ pass did not finish keeps the tiles inside the sequence)
+  i0 = max(min(first / BT, nt - 1), 0);
+  n = max(min(last / BT + (last % BT != 0), nt) - i0, 1);
 }
-// First row of [from, to) whose end (kBegin: begin) is above `key`, or `to`.
-template <bool kBegin>
-__device__ __forceinline__ int shaped_row_search(const BwdParams& p, int b, int from, int to, int key) {
-  while (from < to) {
-    const int m = (from + to) >> 1;
-    const long long gr = (long long)b * p.N + m;
-    const bool past = kBegin ? shape_lo(p.shape, gr, m) > key : shape_hi(p.shape, gr, m, p.N, p.causal) > key;
-    if (past)
-      to = m;
-    else
-      from = m + 1;
-  }
-  return from;
-}
+
 // One thread's 32 columns of raw products u: pv = P o f with P = 2^(score + nl) and f the factor that
 // the cap puts on dS (1 - tanh^2), and P itself as bf16 pairs into pk (kPack). Column c lies at
 // distance |dist + step c| and is visible iff va <= c < vb; nl is its row's -lse log2(e), per column
@@ -710,10 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // shaped: the queries [qa, qb) that see this thread's key (none for a key past the sequence)
       int qa = 0, qb = 0;
       if constexpr (kShaped) {
-        const int key = j * BT + r, end = min((i0 + ni) * BT, p.N);
+        const int key = j * BT + r;
         if (key < p.N) {
-          qa = shaped_row_search<false>(p, b, i0 * BT, end, key);
-          qb = shaped_row_search<true>(p, b, qa, end, key);
+          const int2 q = __ldg(p.ws_keys + (size_t)b * p.Npad + key);
+          qa = q.x;
+          qb = q.y;
         }
       }
       for (int t = 0; t < G * ni; ++t) {
@@ -1046,6 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // workspace (warp 2 rows 0-63, warp 3 rows 64-127), at most two items ahead of the
     // element-wise warps; they read the vectors back once the block count shows them
     // written, and the dK/dV pass (launched after this one) reads them all.
+    if constexpr (kShaped) {
+      if (warp == 3) write_key_ranges(p, blockIdx.x, gridDim.x, lane);
+    }
     for (int kk = 0, it; (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
       if (!count_wait(items_started, kk - 1, abort, p.status, p.wait_ns)) break;
       int b, h, i;

@@ -134,6 +134,7 @@ struct BwdParams {
   void* dv;
   float* ws_nl2;              // [B * Hq, Npad]: -lse * log2(e), -inf past N
   float* ws_d;                // [B * Hq, Npad]: rowsum(dO o O), 0 past N
+  int2* ws_keys;              // shaped: [B, Npad], the query rows [x, y) that see each key
   int B, Hq, Hkv, N, d, Npad; // Npad = N rounded up to 128
   int causal;
   float scale;

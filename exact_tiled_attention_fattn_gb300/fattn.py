@@ -60,6 +60,7 @@ SIGNATURES_OPS = {
     "fattn_fwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _vp, _vp, _vp]),
     "fattn_fwd_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                     _f, _vp, _i, _vp, _vp, _vp]),
+    "fattn_bwd_shaped_workspace_size": (_sz, [_i, _i, _i]),
     "fattn_bwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i,
                               _vp, _vp, _vp, _sz, _vp]),
     "fattn_decode_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
@@ -806,6 +807,10 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
     return out, lse
 
 
+def bwd_shaped_workspace_size(B: int, Hq: int, N: int) -> int:
+    return int(load_library().fattn_bwd_shaped_workspace_size(B, Hq, N))
+
+
 def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
                slopes=None, window: int = 0, key_begin=None, key_end=None, dq=None, dk=None, dv=None, workspace=None,
                stream=None):
@@ -834,7 +839,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(max(bwd_workspace_size(B, Hq, N), 1), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(bwd_shaped_workspace_size(B, Hq, N), 1), dtype=torch.uint8, device=q.device)
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
                               int(window), _ptr(key_begin), _ptr(key_end), _ptr(workspace),

@@ -277,7 +277,7 @@ def test_streams_graphs_and_timeouts():
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     bufs = [torch.zeros_like(t) for t in (o, lse, *ref)]
-    ws = torch.empty(fa.bwd_workspace_size(1, 2, 600), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.bwd_shaped_workspace_size(1, 2, 600), dtype=torch.uint8, device="cuda")
     g = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(g, stream=s):
