@@ -89,7 +89,7 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
   // the cap's argument 2 log2(e) scale / softcap must be a number
   if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
   if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
-  *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, 0};
+  *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, -1.f};
   out->sl2 = scale * 1.4426950408889634f;
   out->cap2 = softcap * 1.4426950408889634f;
   out->capk = softcap > 0.f ? 2.f * out->sl2 / softcap : 0.f;
@@ -103,8 +103,11 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
     double pw = k * softcap * 1.4426950408889634;
     for (int i = 0; i < 5; ++i, pw *= k * k) out->poly[i] = make_float2((float)(c[i] * pw), (float)(c[i] * pw));
     out->poly_limit = (float)(0.75 / std::fabs(k));
-    out->poly_bound = 2.0 * 0.6352 * softcap * 1.4426950408889634 <= 96.0;  // exponents down to -96: normal floats
   }
+  // 2 log2(e) softcap tanh(k u) <= 96
+  const double ratio = 48.0 / (1.4426950408889634 * softcap);
+  if (softcap > 0.f && std::fabs(k) > 0.0)
+    out->bound_limit = ratio >= 1.0 ? INFINITY : (float)(std::atanh(ratio) / std::fabs(k));
   return FATTN_OK;
 }
 

@@ -29,7 +29,9 @@ struct ScoreShape {
   // log2(e) cap tanh(scale u / cap) = u P(u^2), P's coefficients from the lowest power up.
   float2 poly[5];           // (each twice: the packed FMAs read them as pairs)
   float poly_limit;
-  int poly_bound;           // the cap is small enough for the row bound of the fused form (prefill_tc.cu)
+  // largest |u| whose cap, taken as a bound of capped scores of either sign, is at most 96 (log2
+  // units) above them: exponents against it are those of normal floats
+  float bound_limit;
 };
 
 // Problem description shared by both prefill kernels.

@@ -345,8 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kShaped = mode_shaped(kMode);    // window and key ranges
   constexpr bool kCap = kShaped && (kMode & kShapeCap);    // and the scores' tanh cap
   constexpr bool kBias = kShaped && (kMode & kShapeBias);  // and distance bias
-  // scores in log2 units before the row maximum (else as the product left them)
-  constexpr bool kUnits = kCap || kBias;
   constexpr bool kMasked = kMode == kModeMasked;  // additive bf16 mask M on the scores
   constexpr bool kFp8 = kMode == kModeFp8;        // E4M3 Q, K, V; P in E4M3 through shared memory
   // key tiles visited from the last (the diagonal under the causal rule) down to 0, so that the
@@ -965,6 +963,211 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++ns;
         tc_fence_after();
+        if constexpr (kCap) {
+          // ---- capped scores: two rolled walks over the tile's 128 columns, 32 at a time from TMEM. The
+          // cap triples the instructions of a column; unrolled over 128 of them (12 KB and more, two
+          // forms) the eight warps starved for instructions (1.2 of 5 cycles an issue), rolled they stay
+          // in the instruction cache.
+          const ScoreShape& sh = p.shape;
+          const int v0 = lo - j * BN, v1 = lim - j * BN;  // visible columns [v0, v1)
+          const bool edge = __any_sync(0xffffffffu, v0 > 0 || v1 < BN);
+          // columns [32 c, 32 c + 32) that are visible, as bits
+          auto visible = [&](int c) -> uint32_t {
+            const int a = max(v0 - 32 * c, 0), e = min(v1 - 32 * c, 32);
+            return a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u;
+          };
+          // Walk 1: the row's maximum, or a bound. By row and 32 columns, so that a row does not depend on
+          // its neighbours: while no |u| exceeds bound_limit, the cap of the largest |u| bounds the row's
+          // capped scores and lies so close to the largest of them that the exponentials against it stay
+          // normal numbers; else (and with a bias) the scores are formed here and put back into TMEM.
+          float mx = -CUDART_INF_F;
+          uint32_t formed = kBias ? 15u : 0u, small = 0;  // bit c: columns 32 c .. hold scores / take the polynomial
+          auto amax32 = [](const uint32_t* u) -> float {
+            float a[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              a[i] = fmax3(fabsf(__uint_as_float(u[i])), fabsf(__uint_as_float(u[i + 4])), fabsf(__uint_as_float(u[i + 8])));
+#pragma unroll
+            for (int e = 12; e < 28; e += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                a[i] = fmax3(a[i], fabsf(__uint_as_float(u[e + i])), fabsf(__uint_as_float(u[e + 4 + i])));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], fabsf(__uint_as_float(u[28 + i])));
+            return fmax3(fmaxf(a[0], a[1]), a[2], a[3]);
+          };
+          uint32_t u[kBias ? 1 : BN];
+          bool hot = false;   // every row of the warp takes the polynomial against its bound, nothing is hidden
+          if constexpr (!kBias) {
+            tmem_ld128(s_col, u);
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t vis = 0xffffffffu;
+              if (edge) {  // hidden keys must not decide between the forms
+                vis = visible(c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((vis >> e) & 1u)) u[32 * c + e] = 0u;
+              }
+              const float amax = amax32(u + 32 * c);
+              if (amax <= sh.poly_limit) small |= 1u << c;
+              if (!(amax <= sh.bound_limit)) formed |= 1u << c;
+              // (a formed one's bound is replaced by its scores' maximum below)
+              else if (vis) mx = fmaxf(mx, amax);
+            }
+            if (mx >= 0.f) mx = fmaf(-2.f * sh.cap2, tanh_r(mx * fabsf(sh.capk)), sh.cap2);
+            hot = !edge && __all_sync(0xffffffffu, small == 15u && formed == 0u);
+          }
+          if (kBias || __any_sync(0xffffffffu, formed != 0u)) {
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t u[32];
+              tmem_ld32(s_col + 32 * c, u);
+              const uint32_t vis = edge ? visible(c) : 0xffffffffu;
+              if constexpr (kBias) {
+                if (edge) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!((vis >> e) & 1u)) u[e] = 0u;
+                }
+                if (amax32(u) <= sh.poly_limit) small |= 1u << c;
+              }
+              if ((formed >> c) & 1u) {
+                if ((small >> c) & 1u) {
+                  const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
+                                 c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2) {
+                    const uint64_t u2 = f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), w2 = f2_mul(u2, u2);
+                    float y0, y1;
+                    f2_unpack(f2_mul(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0)), y0, y1);
+                    u[e] = __float_as_uint(y0);
+                    u[e + 1] = __float_as_uint(y1);
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    u[e] = __float_as_uint(fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), sh.cap2));
+                }
+                if constexpr (kBias) {
+                  const float dist = (float)(pos - j * BN - 32 * c);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    u[e] = __float_as_uint(fmaf(slope2, fabsf(dist - (float)e), __uint_as_float(u[e])));
+                }
+                if (edge) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!((vis >> e) & 1u)) u[e] = __float_as_uint(-CUDART_INF_F);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+              }
+              __syncwarp();
+              tmem_st32(s_col + 32 * c, u);
+              tmem_st_wait();
+            }
+          }
+          const float m_cand = fmaxf(m, mx);
+          const bool need = m_cand > m + kLazyRescaleLog2;
+          const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
+          const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
+          const float alpha = ex2(m - base);
+          if constexpr (kEarly) {  // O_t += P_t(j-1) V has completed: O_t and P_t's buffer may be rewritten
+            if (!first) {
+              if (!warp_wait(bar(kBarPvDone + t), npv & 1, abort, p.status, p.wait_ns)) {
+                ok = false;
+                break;
+              }
+              ++npv;
+              tc_fence_after();
+            }
+          }
+          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t u[32];
+              tmem_ld32(o_col + 32 * c, u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+              tmem_st32(o_col + 32 * c, u);
+            }
+          }
+          m = m_new;
+          first = false;
+          // Walk 2: P = 2^(score - base), its sum, and bf16 pairs over S's first columns (columns [16 c, 16 c + 16):
+          // all of them read by then)
+          const uint64_t nbase2 = f2_pack(-base, -base);
+          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+          auto p32 = [&](int c, const uint32_t (&u)[32]) {
+            float e2[32];
+            if (kBias || ((formed >> c) & 1u)) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                f2_unpack(f2_add(f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nbase2), e2[e], e2[e + 1]);
+            } else if ((small >> c) & 1u) {
+              const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
+                             c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t u2 = f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), w2 = f2_mul(u2, u2);
+                f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0), nbase2), e2[e],
+                          e2[e + 1]);
+              }
+            } else {
+              const float top = sh.cap2 - base;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) e2[e] = fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), top);
+            }
+            if (edge) {
+              const uint32_t vis = visible(c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) e2[e] = -CUDART_INF_F;
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = ex2(e2[e]), p1 = ex2(e2[e + 1]);
+              acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
+              w[e / 2] = pack_bf16x2(p0, p1);
+            }
+            __syncwarp();
+            tmem_st16(p_col + 16 * c, w);
+          };
+          if (!kBias && hot) {
+            // the usual tile: straight through, from the registers of walk 1 (the same operations on a row)
+            const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
+                           c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
+            uint32_t w[BN / 2];
+#pragma unroll
+            for (int e = 0; e < BN; e += 2) {
+              const uint64_t u2 = f2_pack(__uint_as_float(u[kBias ? 0 : e]), __uint_as_float(u[kBias ? 0 : e + 1]));
+              const uint64_t w2 = f2_mul(u2, u2);
+              float a0, a1;
+              f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0), nbase2), a0, a1);
+              const float p0 = ex2(a0), p1 = ex2(a1);
+              acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
+              w[e / 2] = pack_bf16x2(p0, p1);
+            }
+            tmem_st64(p_col, w);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(s_col + 32 * c, v);
+              p32(c, v);
+            }
+          }
+          float sum0, sum1;
+          f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), sum0, sum1);
+          l = l * alpha + (sum0 + sum1);
+          if constexpr (kEarly) {  // S_t(j) is read: the next product may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarSFree + t));
+          }
+        } else {
         float s[BN];
         const int kbase = j * BN;
         bool masked = kbase + BN > lim;  // causal diagonal tile or sequence end
@@ -1022,54 +1225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarSFree + t));
           }
         }
-        bool fused = false;      // this row's cap is taken with its exponentials below
-        float fused_max = 0.f;   // and this bounds its capped scores
         const bool edge = kShaped && (masked || kbase < lo);
         const uint32_t span = kShaped ? (uint32_t)max(lim - lo, 0) : 0u, first_key = (uint32_t)(lo - kbase);
-        if constexpr (kCap) {
-          if (edge) {  // hidden keys must not decide between the forms of the cap
-#pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if ((uint32_t)c - first_key >= span) s[c] = 0.f;
-          }
-          float a[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = fabsf(s[i]);
-#pragma unroll
-          for (int c = 8; c < BN; c += 16)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              a[i] = fmax3(a[i], fabsf(s[c + i]), fabsf(s[c + 8 + i < BN ? c + 8 + i : c + i]));
-          const float amax = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-          // By row, so that a row does not depend on its neighbours. Where the polynomial holds, no key is
-          // hidden and nothing is added to the capped score, the row takes its capped scores together with
-          // their exponentials, against the cap of its largest |u| in place of their maximum: a bound
-          // that is at most 2 tanh(0.75) cap above it, which poly_bound admits where the exponentials stay
-          // normal numbers.
-          if (!kBias && amax <= p.shape.poly_limit && !edge && p.shape.poly_bound) {
-            fused = true;
-            const float v = amax * amax;
-            fused_max = amax * fabsf(fmaf(fmaf(fmaf(fmaf(p.shape.poly[4].x, v, p.shape.poly[3].x), v, p.shape.poly[2].x), v,
-                                               p.shape.poly[1].x), v, p.shape.poly[0].x));
-          } else if (amax <= p.shape.poly_limit) {
-            // the polynomial: six packed FMAs a pair on a pipe with room, where the exponential and the
-            // reciprocal would go to the one that every score's own exponential needs
-            const uint64_t c0 = f2_bits(p.shape.poly[0]), c1 = f2_bits(p.shape.poly[1]),
-                           c2 = f2_bits(p.shape.poly[2]), c3 = f2_bits(p.shape.poly[3]),
-                           c4 = f2_bits(p.shape.poly[4]);
-#pragma unroll
-            for (int c = 0; c < BN; c += 2) {
-              const uint64_t u2 = f2_pack(s[c], s[c + 1]), v2 = f2_mul(u2, u2);
-              f2_unpack(f2_mul(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, v2, c3), v2, c2), v2, c1), v2, c0)), s[c], s[c + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) s[c] = fmaf(-2.f * p.shape.cap2, tanh_r(s[c] * p.shape.capk), p.shape.cap2);
-          }
-        }
         if constexpr (kBias) {
           const float dist = (float)(pos - kbase);
-          const float mul = kCap ? 1.f : p.shape.sl2;
+          const float mul = p.shape.sl2;
           if (x.base + t * BM + q4 * 32 + x.off >= kbase + BN - 1) {
             // no key of the tile lies past a row of the warp: |pos - j| = dist - c, linear in c
             const uint64_t mulx2 = f2_pack(mul, mul);
@@ -1078,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < BN; c += 2) {
               const uint64_t bias = f2_pack(fmaf(-slope2, (float)c, b0), fmaf(-slope2, (float)(c + 1), b0));
               const uint64_t u2 = f2_pack(s[c], s[c + 1]);
-              f2_unpack(kCap ? f2_add(u2, bias) : f2_fma(u2, mulx2, bias), s[c], s[c + 1]);
+              f2_unpack(f2_fma(u2, mulx2, bias), s[c], s[c + 1]);
             }
           } else {
 #pragma unroll
@@ -1089,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (edge) {
 #pragma unroll
             for (int c = 0; c < BN; ++c)
-              if ((uint32_t)c - first_key >= span) s[c] = !kUnits && neg ? CUDART_INF_F : -CUDART_INF_F;
+              if ((uint32_t)c - first_key >= span) s[c] = !kBias && neg ? CUDART_INF_F : -CUDART_INF_F;
           }
           masked = false;
         }
@@ -1099,12 +1259,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kbase + c >= lim) s[c] = neg ? CUDART_INF_F : -CUDART_INF_F;
         }
         // row max (min for a negative scale): 8 independent chains of 3-input max
-        float mx = fused_max;
-        if (!(kCap && !kBias && fused)) {
+        float mx;
+        {
           float a[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] = s[i];
-          if (kMasked || kUnits || !neg) {
+          if (kMasked || kBias || !neg) {
 #pragma unroll
             for (int c = 8; c < BN; c += 16)
 #pragma unroll
@@ -1118,8 +1278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmin3(fmin3(a[0], a[1], a[2]), fmin3(a[3], a[4], a[5]), fminf(a[6], a[7]));
           }
         }
-        // (the masked scores carry the scale, the capped and biased ones the scale and log2(e))
-        const float m_cand = fmaxf(m, kUnits ? mx : mx * (kMasked ? kLog2e : sl2));
+        // (the masked scores carry the scale, the biased ones the scale and log2(e))
+        const float m_cand = fmaxf(m, kBias ? mx : mx * (kMasked ? kLog2e : sl2));
         const bool need = m_cand > m + kLazyRescaleLog2;          // always true on the first tile
         const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
         const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
@@ -1136,24 +1296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             return pack_bf16x2(p0, p1);
         };
         uint32_t pk[BN / 2];
-        if (kCap && !kBias && fused) {  // 2^(u P(u^2) - base)
-          const uint64_t c0 = f2_bits(p.shape.poly[0]), c1 = f2_bits(p.shape.poly[1]),
-                         c2 = f2_bits(p.shape.poly[2]), c3 = f2_bits(p.shape.poly[3]),
-                         c4 = f2_bits(p.shape.poly[4]);
-#pragma unroll
-          for (int c = 0; c < BN; c += 2) {
-            const uint64_t u2 = f2_pack(s[c], s[c + 1]), v2 = f2_mul(u2, u2);
-            float a0, a1;
-            f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, v2, c3), v2, c2), v2, c1), v2, c0), nbase2), a0, a1);
-            const float p0 = ex2(a0), p1 = ex2(a1);
-            acc2[(c >> 1) & (kAcc - 1)] = f2_add(acc2[(c >> 1) & (kAcc - 1)], f2_pack(p0, p1));
-            pk[c / 2] = pack_p(p0, p1);
-          }
-        } else if (!masked) {
+        if (!masked) {
 #pragma unroll
           for (int c = 0; c < BN; c += 2) {
             float a0, a1;
-            f2_unpack(kUnits ? f2_add(f2_pack(s[c], s[c + 1]), nbase2) : f2_fma(f2_pack(s[c], s[c + 1]), mul2, nbase2), a0, a1);
+            f2_unpack(kBias ? f2_add(f2_pack(s[c], s[c + 1]), nbase2) : f2_fma(f2_pack(s[c], s[c + 1]), mul2, nbase2), a0, a1);
             const float p0 = ex2(a0), p1 = ex2(a1);
             acc2[(c >> 1) & (kAcc - 1)] = f2_add(acc2[(c >> 1) & (kAcc - 1)], f2_pack(p0, p1));
             pk[c / 2] = pack_p(p0, p1);
@@ -1218,6 +1365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         } else {
           tmem_st64(p_col, pk);
+        }
         }
         tmem_st_wait();
         tc_fence_before();
