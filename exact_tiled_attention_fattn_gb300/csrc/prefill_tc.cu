@@ -976,12 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int a = max(v0 - 32 * c, 0), e = min(v1 - 32 * c, 32);
             return a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u;
           };
-          // Walk 1: the row's maximum, or a bound. By row and 32 columns, so that a row does not depend on
-          // its neighbours: while no |u| exceeds bound_limit, the cap of the largest |u| bounds the row's
-          // capped scores and lies so close to the largest of them that the exponentials against it stay
-          // normal numbers; else (and with a bias) the scores are formed here and put back into TMEM.
-          float mx = -CUDART_INF_F;
-          uint32_t formed = kBias ? 15u : 0u, small = 0;  // bit c: columns 32 c .. hold scores / take the polynomial
+          // Against what a row's exponentials are taken, by row, so that a row does not depend on its
+          // neighbours: while no |u| of 32 columns exceeds bound_limit, the cap of the largest |u| bounds
+          // their capped scores and lies so close to the largest of them that the exponentials against
+          // it stay normal numbers; else (and with a bias) the scores' own maximum.
+          float base = 0.f, alpha = 0.f;
           auto amax32 = [](const uint32_t* u) -> float {
             float a[4];
 #pragma unroll
@@ -996,167 +995,164 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], fabsf(__uint_as_float(u[28 + i])));
             return fmax3(fmaxf(a[0], a[1]), a[2], a[3]);
           };
-          uint32_t u[kBias ? 1 : BN];
-          bool hot = false;   // every row of the warp takes the polynomial against its bound, nothing is hidden
-          if constexpr (!kBias) {
-            tmem_ld128(s_col, u);
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-              uint32_t vis = 0xffffffffu;
-              if (edge) {  // hidden keys must not decide between the forms
-                vis = visible(c);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((vis >> e) & 1u)) u[32 * c + e] = 0u;
+          auto bound = [&](float amax) -> float { return fmaf(-2.f * sh.cap2, tanh_r(amax * fabsf(sh.capk)), sh.cap2); };
+          // 2^(u P(u^2) - base) arguments of a pair
+          auto poly_arg = [&](uint32_t x0, uint32_t x1, uint64_t add) -> uint64_t {
+            const uint64_t u2 = f2_pack(__uint_as_float(x0), __uint_as_float(x1)), w2 = f2_mul(u2, u2);
+            const uint64_t q = f2_fma(f2_fma(f2_fma(f2_fma(f2_bits(sh.poly[4]), w2, f2_bits(sh.poly[3])), w2, f2_bits(sh.poly[2])),
+                                             w2, f2_bits(sh.poly[1])), w2, f2_bits(sh.poly[0]));
+            return f2_fma(u2, q, add);
+          };
+          // the running maximum raised to m or above mx, O rescaled if it moved
+          auto raise = [&](float mx) -> bool {
+            const float m_cand = fmaxf(m, mx);
+            const bool need = m_cand > m + kLazyRescaleLog2;
+            const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
+            base = m_new == -CUDART_INF_F ? 0.f : m_new;
+            alpha = ex2(m - base);
+            if constexpr (kEarly) {  // O_t += P_t(j-1) V has completed: O_t and P_t's buffer may be rewritten
+              if (!first) {
+                if (!warp_wait(bar(kBarPvDone + t), npv & 1, abort, p.status, p.wait_ns)) return false;
+                ++npv;
+                tc_fence_after();
               }
-              const float amax = amax32(u + 32 * c);
-              if (amax <= sh.poly_limit) small |= 1u << c;
-              if (!(amax <= sh.bound_limit)) formed |= 1u << c;
-              // (a formed one's bound is replaced by its scores' maximum below)
-              else if (vis) mx = fmaxf(mx, amax);
             }
-            if (mx >= 0.f) mx = fmaf(-2.f * sh.cap2, tanh_r(mx * fabsf(sh.capk)), sh.cap2);
-            hot = !edge && __all_sync(0xffffffffu, small == 15u && formed == 0u);
+            if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(o_col + 32 * c, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                tmem_st32(o_col + 32 * c, v);
+              }
+            }
+            m = m_new;
+            first = false;
+            return true;
+          };
+          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};  // row-sum partials, packed pairs
+          bool done = false;
+          if constexpr (!kBias) {
+            if (!edge) {
+              // the usual tile, straight through: nothing hidden, every row of the warp takes the polynomial
+              // against its bound (the operations on a row are those of the walks below)
+              uint32_t u[BN];
+              tmem_ld128(s_col, u);
+              const float amax = fmax3(fmaxf(amax32(u), amax32(u + 32)), amax32(u + 64), amax32(u + 96));
+              if (__all_sync(0xffffffffu, amax <= fminf(sh.poly_limit, sh.bound_limit))) {
+                if (!raise(bound(amax))) {
+                  ok = false;
+                  break;
+                }
+                const uint64_t nbase2 = f2_pack(-base, -base);
+                uint32_t w[BN / 2];
+#pragma unroll
+                for (int e = 0; e < BN; e += 2) {
+                  float a0, a1;
+                  f2_unpack(poly_arg(u[e], u[e + 1], nbase2), a0, a1);
+                  const float p0 = ex2(a0), p1 = ex2(a1);
+                  acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
+                  w[e / 2] = pack_bf16x2(p0, p1);
+                }
+                tmem_st64(p_col, w);
+                done = true;
+              }
+            }
           }
-          if (kBias || __any_sync(0xffffffffu, formed != 0u)) {
+          if (!done) {
+            // Walk 1: the row's maximum or bound; scores that need their own maximum are formed and put
+            // back into TMEM.
+            float mx = -CUDART_INF_F;
+            uint32_t formed = 0, small = 0;  // bit c: columns 32 c .. hold scores / take the polynomial
 #pragma unroll 1
             for (int c = 0; c < BN / 32; ++c) {
               uint32_t u[32];
               tmem_ld32(s_col + 32 * c, u);
-              const uint32_t vis = edge ? visible(c) : 0xffffffffu;
-              if constexpr (kBias) {
-                if (edge) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((vis >> e) & 1u)) u[e] = 0u;
-                }
-                if (amax32(u) <= sh.poly_limit) small |= 1u << c;
-              }
-              if ((formed >> c) & 1u) {
-                if ((small >> c) & 1u) {
-                  const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
-                                 c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
-#pragma unroll
-                  for (int e = 0; e < 32; e += 2) {
-                    const uint64_t u2 = f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), w2 = f2_mul(u2, u2);
-                    float y0, y1;
-                    f2_unpack(f2_mul(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0)), y0, y1);
-                    u[e] = __float_as_uint(y0);
-                    u[e + 1] = __float_as_uint(y1);
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    u[e] = __float_as_uint(fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), sh.cap2));
-                }
-                if constexpr (kBias) {
-                  const float dist = (float)(pos - j * BN - 32 * c);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    u[e] = __float_as_uint(fmaf(slope2, fabsf(dist - (float)e), __uint_as_float(u[e])));
-                }
-                if (edge) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((vis >> e) & 1u)) u[e] = __float_as_uint(-CUDART_INF_F);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
-              }
-              __syncwarp();
-              tmem_st32(s_col + 32 * c, u);
-              tmem_st_wait();
-            }
-          }
-          const float m_cand = fmaxf(m, mx);
-          const bool need = m_cand > m + kLazyRescaleLog2;
-          const float m_new = __any_sync(0xffffffffu, need) ? m_cand : m;
-          const float base = m_new == -CUDART_INF_F ? 0.f : m_new;
-          const float alpha = ex2(m - base);
-          if constexpr (kEarly) {  // O_t += P_t(j-1) V has completed: O_t and P_t's buffer may be rewritten
-            if (!first) {
-              if (!warp_wait(bar(kBarPvDone + t), npv & 1, abort, p.status, p.wait_ns)) {
-                ok = false;
-                break;
-              }
-              ++npv;
-              tc_fence_after();
-            }
-          }
-          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t u[32];
-              tmem_ld32(o_col + 32 * c, u);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-              tmem_st32(o_col + 32 * c, u);
-            }
-          }
-          m = m_new;
-          first = false;
-          // Walk 2: P = 2^(score - base), its sum, and bf16 pairs over S's first columns (columns [16 c, 16 c + 16):
-          // all of them read by then)
-          const uint64_t nbase2 = f2_pack(-base, -base);
-          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-          auto p32 = [&](int c, const uint32_t (&u)[32]) {
-            float e2[32];
-            if (kBias || ((formed >> c) & 1u)) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                f2_unpack(f2_add(f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nbase2), e2[e], e2[e + 1]);
-            } else if ((small >> c) & 1u) {
-              const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
-                             c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const uint64_t u2 = f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), w2 = f2_mul(u2, u2);
-                f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0), nbase2), e2[e],
-                          e2[e + 1]);
-              }
-            } else {
-              const float top = sh.cap2 - base;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) e2[e] = fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), top);
-            }
-            if (edge) {
               const uint32_t vis = visible(c);
+              if (edge) {  // hidden keys must not decide between the forms
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((vis >> e) & 1u)) e2[e] = -CUDART_INF_F;
-            }
-            uint32_t w[16];
+                for (int e = 0; e < 32; ++e)
+                  if (!((vis >> e) & 1u)) u[e] = 0u;
+              }
+              const float amax = amax32(u);
+              if (amax <= sh.poly_limit) small |= 1u << c;
+              const bool form = kBias || !(amax <= sh.bound_limit);
+              if (!form && vis) mx = fmaxf(mx, bound(amax));
+              if (kBias || __any_sync(0xffffffffu, form)) {
+                if (form) {
+                  if ((small >> c) & 1u) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float p0 = ex2(e2[e]), p1 = ex2(e2[e + 1]);
-              acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
-              w[e / 2] = pack_bf16x2(p0, p1);
-            }
-            __syncwarp();
-            tmem_st16(p_col + 16 * c, w);
-          };
-          if (!kBias && hot) {
-            // the usual tile: straight through, from the registers of walk 1 (the same operations on a row)
-            const uint64_t c0 = f2_bits(sh.poly[0]), c1 = f2_bits(sh.poly[1]), c2 = f2_bits(sh.poly[2]),
-                           c3 = f2_bits(sh.poly[3]), c4 = f2_bits(sh.poly[4]);
-            uint32_t w[BN / 2];
+                    for (int e = 0; e < 32; e += 2) {
+                      float y0, y1;
+                      f2_unpack(poly_arg(u[e], u[e + 1], 0ull), y0, y1);
+                      u[e] = __float_as_uint(y0);
+                      u[e + 1] = __float_as_uint(y1);
+                    }
+                  } else {
 #pragma unroll
-            for (int e = 0; e < BN; e += 2) {
-              const uint64_t u2 = f2_pack(__uint_as_float(u[kBias ? 0 : e]), __uint_as_float(u[kBias ? 0 : e + 1]));
-              const uint64_t w2 = f2_mul(u2, u2);
-              float a0, a1;
-              f2_unpack(f2_fma(u2, f2_fma(f2_fma(f2_fma(f2_fma(c4, w2, c3), w2, c2), w2, c1), w2, c0), nbase2), a0, a1);
-              const float p0 = ex2(a0), p1 = ex2(a1);
-              acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
-              w[e / 2] = pack_bf16x2(p0, p1);
+                    for (int e = 0; e < 32; ++e)
+                      u[e] = __float_as_uint(fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), sh.cap2));
+                  }
+                  if constexpr (kBias) {
+                    const float dist = (float)(pos - j * BN - 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                      u[e] = __float_as_uint(fmaf(slope2, fabsf(dist - (float)e), __uint_as_float(u[e])));
+                  }
+                  if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                      if (!((vis >> e) & 1u)) u[e] = __float_as_uint(-CUDART_INF_F);
+                  }
+                  formed |= 1u << c;
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+                }
+                __syncwarp();
+                tmem_st32(s_col + 32 * c, u);
+                tmem_st_wait();
+              }
             }
-            tmem_st64(p_col, w);
-          } else {
+            if (!raise(mx)) {
+              ok = false;
+              break;
+            }
+            // Walk 2: P = 2^(score - base), its sum, and bf16 pairs over S's first columns (columns [16 c, 16 c + 16):
+            // all of them read by then)
+            const uint64_t nbase2 = f2_pack(-base, -base);
 #pragma unroll 1
             for (int c = 0; c < BN / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(s_col + 32 * c, v);
-              p32(c, v);
+              uint32_t u[32];
+              tmem_ld32(s_col + 32 * c, u);
+              float e2[32];
+              if (kBias || ((formed >> c) & 1u)) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                  f2_unpack(f2_add(f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nbase2), e2[e], e2[e + 1]);
+              } else if ((small >> c) & 1u) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) f2_unpack(poly_arg(u[e], u[e + 1], nbase2), e2[e], e2[e + 1]);
+              } else {
+                const float top = sh.cap2 - base;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) e2[e] = fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), top);
+              }
+              if (edge) {
+                const uint32_t vis = visible(c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((vis >> e) & 1u)) e2[e] = -CUDART_INF_F;
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float p0 = ex2(e2[e]), p1 = ex2(e2[e + 1]);
+                acc2[(e >> 1) & 3] = f2_add(acc2[(e >> 1) & 3], f2_pack(p0, p1));
+                w[e / 2] = pack_bf16x2(p0, p1);
+              }
+              __syncwarp();
+              tmem_st16(p_col + 16 * c, w);
             }
           }
           float sum0, sum1;
