@@ -191,6 +191,9 @@ extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kca
                            max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
 }
 
+// Query rows (queries x heads of a group) of the longest chunk from which the tensor-core kernel is used.
+constexpr int kTcRows = 64;
+
 extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const int32_t* block_table,
                                                 const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const float* lse,
                                                 long long lse_head, long long lse_row, const float* weights_in,
@@ -222,7 +225,20 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
   p.causal = causal ? 1 : 0; p.scale = scale; p.decay = decay;
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
-  return launch_key_weights(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  current_waits(&p.wait_ns, &p.debug_stall);
+  const int G = Hq / Hkv;
+  const bool tc = (long long)max_seqlen_q * G >= kTcRows && total_q > 0 && G <= 128 &&
+                  (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
+                  (long long)(num_pages + 1) * page_size <= 0x7fffffffLL &&
+                  ((long long)max_pages_per_seq * page_size + 127) / 128 * B * Hkv <= 0x7fffffffLL;
+  if (!tc) return launch_key_weights(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  CUtensorMap tq, tk;
+  if (!encode_rows_map(&tq, q, total_q, Hq, d, 128 / G, G) ||
+      !encode_rows_map(&tk, kcache, num_pages * page_size, Hkv, d, page_size))
+    return FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_key_weights_tc(p, tq, tk, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 extern "C" fattn_status fattn_evict_paged(void* kcache, void* vcache, const int32_t* block_table,

@@ -77,6 +77,10 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
     if (key0 == 0 && hkv == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
     return;  // the sequence is skipped
   }
+  const size_t w_row = ((size_t)b * p.Hkv + hkv) * cap;
+  if (p.w_out != p.w_in) {  // slots past the sequence
+    for (int t = max(key0, n) + threadIdx.x; t < min(key0 + kKeys, cap); t += kWarps * 32) p.w_out[w_row + t] = 0.f;
+  }
   if (key0 >= n) return;
   const int nkeys = min(kKeys, n - key0), off = n - m;
   const int G = p.Hq / p.Hkv;
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
     acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
     const int r = warp * 32 + g + (i >> 1) * 16 + (i & 1) * 8;
     if ((lane & 3) == 0 && r < nkeys) {
-      const size_t at = ((size_t)b * p.Hkv + hkv) * cap + key0 + r;
+      const size_t at = w_row + key0 + r;
       const float sum = s_row[r] >= 0 ? acc[i] : 0.f;
       p.w_out[at] = p.w_in ? fmaf(p.decay, p.w_in[at], sum) : sum;
     }

@@ -48,9 +48,15 @@ struct KeyWeightsParams {
   float scale, decay;
   ScoreShape shape;           // no key ranges
   int* status;
+  unsigned long long wait_ns; // tensor-core kernel: limit of a pipeline wait, and the stall flag
+  int debug_stall;
 };
 
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+// Tensor-core kernel: tensor maps over q (boxes of G heads x 128 / G rows) and the key pool (boxes
+// of one page), G = Hq / Hkv <= 128, page_size 16, 32, 64 or 128.
+cudaError_t launch_key_weights_tc(const KeyWeightsParams& p, const CUtensorMap& tq, const CUtensorMap& tk, int num_sms,
+                                  cudaStream_t stream);
 
 struct EvictParams {
   void* kcache;
@@ -74,7 +80,7 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
 // calls whose plain and shaped forms differ in `shape` alone (nullptr: plain).
 int* status_ptr(int* err);
 void current_waits(unsigned long long* wait_ns, int* debug_stall);
-bool encode_rows_map(CUtensorMap* map, const void* base, int rows, int H, int d, int box_rows);
+bool encode_rows_map(CUtensorMap* map, const void* base, int rows, int H, int d, int box_rows, int box_heads = 1);
 fattn_status fwd_paged_impl(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
                             const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq,
                             int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,

@@ -896,7 +896,7 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
     the heads of the group and the queries of chunk b of exp(s - lse), fp32 [B, Hkv, max_pages * page_size].
     q [Tq,Hq,d] and the chunk arguments as in ``fwd_paged``; ``lse`` [Hq,Tq] from the attention call, any strides
     (``lse.t()`` of ``decode_paged``). ``weights`` None starts from zero; ``out`` may be ``weights``. Slots past a
-    sequence's length are left as they are (zero in a new ``out``)."""
+    sequence's length are 0, or, with ``out`` the same tensor as ``weights``, left as they are."""
     lib = load_library()
     _need_cuda(q, kcache, block_table, seqlens_k, cu_seqlens_q, weights, out)
     _need_cuda(lse, contiguous=False)
@@ -920,7 +920,7 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.zeros(shape, dtype=torch.float32, device=q.device)
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
     st = lib.fattn_key_weights_paged(_ptr(q), _ptr(kcache), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q),
                                      _ptr(lse), lse.stride(0), lse.stride(1), _ptr(weights), _ptr(out), B, Hq, Hkv, d,
                                      page_size, block_table.shape[1], num_pages, Tq, int(max_seqlen_q),

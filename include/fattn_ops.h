@@ -178,8 +178,8 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
  * receive from query chunks:
  *   weights_out[b, hkv, t] = decay weights_in[b, hkv, t]
  *                            + sum over the heads of group hkv and the queries of chunk b of e^{s - lse}
- * for t < seqlens_k[b]; slots from seqlens_k[b] on are left as they are. s is the
- * shaped score (softcap, slopes, window as above; causal as in fattn_fwd_paged), lse the
+ * for t < seqlens_k[b]; slots from seqlens_k[b] on are set to 0, or in place (weights_out ==
+ * weights_in) left as they are. s is the shaped score (softcap, slopes, window as above; causal as in fattn_fwd_paged), lse the
  * logsumexp that the attention call with the same arguments wrote. Sums are fp32, in a fixed order.
  *
  * q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: as fattn_fwd_paged (for single
@@ -188,7 +188,9 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
  *   total_q] (total_q, 1) and fattn_decode_paged's [B, Hq] (1, Hq) both serve. A row of -inf gives nothing.
  * weights_in (NULL: zeros; then decay is not used), weights_out: DEVICE fp32
  *   [B, Hkv, max_pages_per_seq * page_size]; they may be the same array.
- * A sequence whose lengths are inconsistent is skipped, a table entry outside the pool gives its tokens
+ * max_seqlen_q: host upper bound on the chunks' queries; it chooses between the streaming kernel (few
+ *   query rows) and the tensor-core kernel, whose pipeline waits are bounded as the other calls' are.
+ * A sequence whose lengths are inconsistent is skipped (its weights are left as they are), a table entry outside the pool gives its tokens
  *   nothing; both record FATTN_ERR_DEVICE_CHECK.
  * Errors: as fattn_fwd_paged and the shaped calls; INVALID_ARG also for a decay that is not finite,
  *   negative lse strides; UNSUPPORTED for d not in {64, 128}, B or Hkv > 65535.

@@ -53,7 +53,11 @@ def weights_ref(q, k, lse, scale, cap, slopes, lo, hi, off):
     (64, 2, 2, 128, [1000, 129], [129, 128], False, 0.0, True, 300),
     (128, 5, 1, 64, [384, 1023], [1, 200], True, 0.0, False, 1),
     (3, 20, 1, 64, [50, 7, 300], [3, 0, 33], True, 0.0, False, 40),
-    (16, 16, 2, 128, [400, 0], [400, 0], True, 30.0, True, 0)])
+    (16, 16, 2, 128, [400, 0], [400, 0], True, 30.0, True, 0),
+    (32, 6, 2, 64, [2100, 700], [900, 650], True, 0.0, False, 0),      # many steps a tile, rows of 126
+    (64, 7, 1, 128, [333], [40], False, 0.0, True, 0),
+    (16, 130, 1, 64, [90], [60], True, 0.0, False, 0),                 # a group of more than 128 heads
+    (128, 128, 1, 64, [300], [3], True, 0.0, False, 0)])               # one query a step
 def test_key_weights(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window):
     fa = need_gpu()
     kc, vc, table, _, g = pool(P + Hq, lk, P, Hkv, d)
@@ -293,6 +297,25 @@ def test_serving_path(captured):
         # cache rows: within a bf16 step of 64 bits (k), equal (v)
         assert np.abs(f64(rows(kc.cpu(), table, b, n)) - K[b]).max() <= 2.0 ** -7 * np.abs(K[b]).max()
         assert np.array_equal(f64(rows(vc.cpu(), table, b, n)), V[b])
+
+
+def test_key_weights_wait_runs_out():
+    """The tensor-core kernel's bounded waits, as in the attention kernels; the next call is right."""
+    fa = need_gpu()
+    kc, _, table, _, g = pool(6, [500], 16, 1, 64)
+    q, lse = torch.randn(100, 2, 64, generator=g).to(torch.bfloat16).cuda(), torch.zeros(2, 100, device="cuda")
+    args = (q, kc.cuda(), table.cuda(), i32([500]), i32([0, 100]), 100, lse)
+    want = fa.key_weights_paged(*args)
+    assert fa.debug_read_status() == 0
+    out = torch.full_like(want, -1.0)
+    fa.debug_set_wait_limit(1_000_000, True)
+    try:
+        fa.key_weights_paged(*args, out=out)
+        st = fa.debug_read_status()
+    finally:
+        fa.debug_set_wait_limit(0, False)
+    assert st == fa.FATTN_ERR_TIMEOUT and bool((out == -1).all())
+    assert torch.equal(fa.key_weights_paged(*args), want) and fa.debug_read_status() == 0
 
 
 def test_key_weights_refusals():
