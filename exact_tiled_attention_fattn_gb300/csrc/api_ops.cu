@@ -191,8 +191,6 @@ extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kca
                            max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
 }
 
-// Query rows (queries x heads of a group) of the longest chunk from which the tensor-core kernel is used.
-constexpr int kTcRows = 64;
 
 extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const int32_t* block_table,
                                                 const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const float* lse,
@@ -215,7 +213,8 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
       misaligned(cu_seqlens_q, 4) || misaligned(lse, 4) || misaligned(weights_in, 4) || misaligned(weights_out, 4))
     return FATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
-  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL - 256 || B > 65535 || Hkv > 65535)
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL - 1024 || B > 65535 || Hkv > 65535 ||
+      ((long long)max_pages_per_seq * page_size / 128 + 1) * Hkv > 0x7fffffffLL)
     return FATTN_ERR_UNSUPPORTED;
   int err = 0;
   p.q = q; p.kcache = kcache; p.block_table = block_table; p.seqlens_k = seqlens_k; p.cu_seqlens = cu_seqlens_q;
@@ -227,17 +226,26 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
   if (err) return FATTN_ERR_CUDA;
   current_waits(&p.wait_ns, &p.debug_stall);
   const int G = Hq / Hkv;
-  const bool tc = (long long)max_seqlen_q * G >= kTcRows && total_q > 0 && G <= 128 &&
+  const long long rows = (long long)max_seqlen_q * G;
+  // up to 32 query rows K's bytes bound the sums (stream kernel); above, the tensor-core kernel, and the
+  // mma.sync one for page sizes and groups that TMA boxes do not take (d = 128, 128 rows over 8k tokens: 13 and
+  // 15 us; 64 rows over 4 sequences of 2k: 19 and 17 us; 128 rows: 18 and 23 us; 2048-query prompts: 130
+  // and 697 us)
+  const bool tc = rows > 32 && total_q > 0 && G <= 128 &&
                   (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
                   (long long)(num_pages + 1) * page_size <= 0x7fffffffLL &&
                   ((long long)max_pages_per_seq * page_size + 127) / 128 * B * Hkv <= 0x7fffffffLL;
-  if (!tc) return launch_key_weights(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
   CUtensorMap tq, tk;
+  if (rows <= 32 && page_size % 16 == 0 && (long long)num_pages * page_size <= 0x7fffffffLL) {
+    if (!encode_rows_map(&tk, kcache, num_pages * page_size, Hkv, d, 16)) return FATTN_ERR_CUDA;
+    return launch_key_weights_stream(p, tk, (int)rows, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  }
+  if (!tc) return launch_key_weights(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
   if (!encode_rows_map(&tq, q, total_q, Hq, d, 128 / G, G) ||
       !encode_rows_map(&tk, kcache, num_pages * page_size, Hkv, d, page_size))
     return FATTN_ERR_CUDA;
-  const int sms = num_sms_current();
-  if (sms <= 0) return FATTN_ERR_CUDA;
   return launch_key_weights_tc(p, tq, tk, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 

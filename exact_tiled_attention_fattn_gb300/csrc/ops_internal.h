@@ -48,11 +48,17 @@ struct KeyWeightsParams {
   float scale, decay;
   ScoreShape shape;           // no key ranges
   int* status;
+  int tiles;                  // tensor-core kernel: 128-key tiles per item, set by its launch
   unsigned long long wait_ns; // tensor-core kernel: limit of a pipeline wait, and the stall flag
   int debug_stall;
 };
 
+// mma.sync, any number of queries, page size and group.
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+// At most max_rows <= 32 query rows (queries x heads of a group) per sequence, page_size a multiple of 16;
+// tensor map over the key pool with boxes of 16 rows.
+cudaError_t launch_key_weights_stream(const KeyWeightsParams& p, const CUtensorMap& tk, int max_rows, int num_sms,
+                                      cudaStream_t stream);
 // Tensor-core kernel: tensor maps over q (boxes of G heads x 128 / G rows) and the key pool (boxes
 // of one page), G = Hq / Hkv <= 128, page_size 16, 32, 64 or 128.
 cudaError_t launch_key_weights_tc(const KeyWeightsParams& p, const CUtensorMap& tq, const CUtensorMap& tk, int num_sms,

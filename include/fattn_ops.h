@@ -190,7 +190,7 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
  *   [B, Hkv, max_pages_per_seq * page_size]; they may be the same array.
  * max_seqlen_q: host upper bound on the chunks' queries; it chooses between the streaming kernel (few
  *   query rows) and the tensor-core kernel, whose pipeline waits are bounded as the other calls' are.
- * A sequence whose lengths are inconsistent is skipped (its weights are left as they are), a table entry outside the pool gives its tokens
+ * A sequence whose lengths are inconsistent, or with more queries than max_seqlen_q, is skipped (its weights are left as they are), a table entry outside the pool gives its tokens
  *   nothing; both record FATTN_ERR_DEVICE_CHECK.
  * Errors: as fattn_fwd_paged and the shaped calls; INVALID_ARG also for a decay that is not finite,
  *   negative lse strides; UNSUPPORTED for d not in {64, 128}, B or Hkv > 65535.
