@@ -44,8 +44,10 @@ extern "C" fattn_status fattn_rope(const void* q, void* q_out, const void* k, vo
   p.k = {k, k_out, Hk, k_row, k_head, ko_row, ko_head};
   p.positions = positions; p.inv_freq = inv_freq; p.period = period;
   p.rows = rows; p.d = d; p.rot = rotary_dim; p.inverse = inverse ? 1 : 0; p.amplitude = amplitude;
-  return launch_rope(p, dtype == FATTN_BF16, interleaved != 0, false, stream) == cudaSuccess ? FATTN_OK
-                                                                                            : FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_rope(p, dtype == FATTN_BF16, interleaved != 0, false, sms, stream) == cudaSuccess ? FATTN_OK
+                                                                                                 : FATTN_ERR_CUDA;
 }
 
 extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, const void* k, const void* v, void* kcache,
@@ -79,7 +81,9 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
   p.B = B; p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
-  return launch_rope(p, true, interleaved != 0, true, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_rope(p, true, interleaved != 0, true, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 // A score shape's own checks; fills *out. `scale` is the call's.

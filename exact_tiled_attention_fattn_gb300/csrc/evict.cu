@@ -3,11 +3,11 @@
 //
 // select_kernel, one block per (sequence, KV head): the weights of the middle tokens as
 // order-preserving 32-bit integers, the threshold by four passes of an 8-bit histogram from the top
-// digit down, then one walk in index order that counts what is kept and the ties already taken
-// (ties go to the lowest index) and writes the kept indices and their weights.
+// digit down, then a scan in index order that counts what is kept and the ties already taken
+// (ties go to the lowest index) and places the kept indices and their weights.
 // move_kernel copies the kept K and V rows by that list. Into other pages every row is
 // independent. In place a row moves to a slot at or below its own, which may hold a row that has
-// yet to move: there a block owns one 16-byte column slice of one head's K or V and walks its
+// yet to move: there a block owns one 32-byte column slice of one head's K or V and walks its
 // rows in order, a batch in registers at a time, so a slot is read before it is written.
 #include "device_common.cuh"
 #include "ops_internal.h"
@@ -27,11 +27,15 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+constexpr int kPer = 16;                        // weights per thread and tile
+constexpr int kTile = kSelThreads * kPer;       // 16384 tokens
+
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
   __shared__ int s_hist[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  __shared__ int s_warp[32];
+  __shared__ int s_cnt[kPer * 32];   // per 32 consecutive tokens of a tile: kept above the threshold | ties << 16
+  __shared__ int s_tile[2];          // of the tile
   const int b = blockIdx.y, h = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages * p.page_size;
@@ -47,6 +51,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   float* wo = p.w_out + ((size_t)b * p.Hkv + h) * out_cap;
   int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.keep;
 
+  // A tile's weights in registers (token tile + 1024 i + tid in x[i]): the loads are on their way together,
+  // and with a single tile (16384 tokens) they are read once for all the passes.
+  float x[kPer];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + i * kSelThreads + tid;
+      x[i] = t < n ? w[t] : 0.f;
+    }
+  };
+  if (n <= kTile) load(0);
+
   // middle tokens [lo, hi): `need` of them are kept
   const int lo = m < n ? p.first : 0, hi = m < n ? n - p.recent : 0;
   const int need = m < n ? m - p.first - p.recent : 0;
@@ -54,15 +70,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     s_prefix = 0;
     s_need = need;
   }
-  __syncthreads();
   if (need > 0) {
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) s_hist[tid] = 0;
       __syncthreads();
       const uint32_t prefix = s_prefix;
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t k = order_key(w[t]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+      for (int t0 = 0; t0 < n; t0 += kTile) {
+        if (n > kTile) load(t0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int t = t0 + i * kSelThreads + tid;
+          if (t >= lo && t < hi) {
+            const uint32_t k = order_key(x[i]);
+            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+          }
+        }
       }
       __syncthreads();
       if (warp == 0) {  // digits from the highest down: lane l holds digits 255 - 8l ... 248 - 8l
@@ -89,39 +111,74 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       }
       __syncthreads();
     }
+  } else {
+    __syncthreads();
   }
   const uint32_t thr = s_prefix;
   const int ties = s_need;   // tokens equal to the threshold that are kept, the lowest indices
 
-  // walk in index order; `done` and `tied` count over the tokens before the batch
+  // In index order, tile by tile: counts per 32 tokens, their scan, then every kept token's place.
+  // `done` and `tied` count over the tiles before. In place a weight moves to or below its own place,
+  // and a tile's are all in registers before any is written.
   int done = 0, tied = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-    const int t = t0 + tid;
-    const bool in = t < n, mid = in && t >= lo && t < hi;
-    const float x = in ? w[t] : 0.f;
-    const uint32_t k = order_key(x);
-    const bool gt = in && (!mid || (need > 0 && k > thr)), eq = mid && need > 0 && k == thr;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_warp[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();   // also: every weight of the batch is read before any is written (in place)
-    int v = s_warp[lane];
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += a;
+  for (int t0 = 0; t0 < n; t0 += kTile) {
+    if (n > kTile) load(t0);
+    const int batches = min(kPer, (n - t0 + kSelThreads - 1) / kSelThreads);
+    uint32_t gts = 0, eqs = 0;   // bit i: this thread's token of batch i
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + i * kSelThreads + tid;
+      const bool in = t < n, mid = in && t >= lo && t < hi;
+      const uint32_t k = order_key(x[i]);
+      const bool gt = in && (!mid || (need > 0 && k > thr)), eq = mid && need > 0 && k == thr;
+      gts |= (uint32_t)gt << i;
+      eqs |= (uint32_t)eq << i;
+      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+      if (lane == 0) s_cnt[i * 32 + warp] = __popc(bg) | (__popc(be) << 16);
     }
-    const int all = __shfl_sync(0xffffffffu, v, 31);
-    const int prev = warp ? __shfl_sync(0xffffffffu, v, warp - 1) : 0;
-    const uint32_t below = (1u << lane) - 1u;
-    const int g_before = done + (prev & 0xffff) + __popc(bg & below);
-    const int e_before = tied + (prev >> 16) + __popc(be & below);
-    if (gt || (eq && e_before < ties)) {
-      const int at = g_before + min(e_before, ties);
-      kept[at] = t;
-      wo[at] = x;
-    }
-    done += all & 0xffff;
-    tied += all >> 16;
     __syncthreads();
+    if (warp == 0) {   // exclusive scan of the 512 counts (the sums stay below 2^15 and 2^16: 16384 tokens)
+      int c[kPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        c[i] = s_cnt[lane * kPer + i];
+        sum += c[i];
+      }
+      int v = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += a;
+      }
+      if (lane == 31) {
+        s_tile[0] = v & 0xffff;
+        s_tile[1] = v >> 16;
+      }
+      v -= sum;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        s_cnt[lane * kPer + i] = v;
+        v += c[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i >= batches) break;
+      const bool gt = (gts >> i) & 1u, eq = (eqs >> i) & 1u;
+      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+      const int before = s_cnt[i * 32 + warp];
+      const uint32_t below = (1u << lane) - 1u;
+      const int g_before = done + (before & 0xffff) + __popc(bg & below);
+      const int e_before = tied + (before >> 16) + __popc(be & below);
+      if (gt || (eq && e_before < ties)) {
+        const int at = g_before + min(e_before, ties);
+        kept[at] = t0 + i * kSelThreads + tid;
+        wo[at] = x[i];
+      }
+    }
+    done += s_tile[0];
+    tied += s_tile[1];
+    __syncthreads();   // (the counts are read; in place, a tile is written before the next is loaded below it)
   }
   for (int t = m + tid; t < p.keep; t += kSelThreads) kept[t] = -1;
   for (int t = m + tid; t < out_cap; t += kSelThreads) wo[t] = 0.f;
@@ -162,17 +219,18 @@ constexpr int kBatch = 8;  // rows per thread of an in-place step
 __global__ void __launch_bounds__(kMoveThreads) move_in_place_kernel(const EvictParams p) {
   const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int m = __ldg(p.seqlens_out + b);
-  const int u = blockIdx.x >> 1;               // this block's 16-byte unit of the row
+  const int u = (blockIdx.x >> 1) * 2 + (threadIdx.x & 1);   // this thread's 16-byte unit of the row
+  const bool live = u < p.d / 8;               // (an odd number of units leaves half a slice)
   uint4* c = static_cast<uint4*>(blockIdx.x & 1 ? p.vcache : p.kcache);
   const int* kept = p.kept + (size_t)bh * p.keep;
-  for (int s0 = 0; s0 < m; s0 += kMoveThreads * kBatch) {
+  for (int s0 = 0; s0 < m; s0 += kMoveThreads / 2 * kBatch) {
     uint4 x[kBatch];
     long long d[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int s = s0 + i * kMoveThreads + threadIdx.x;
+      const int s = s0 + i * (kMoveThreads / 2) + (threadIdx.x >> 1);
       d[i] = -1;
-      if (s < m) {
+      if (live && s < m) {
         const int t = __ldg(kept + s);
         if (t != s) {
           const long long a = slot_unit(p, p.block_table, p.max_pages, b, h, t);
@@ -202,7 +260,7 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   const int heads = p.B * p.Hkv;
   if (p.dst_table == nullptr) {
-    move_in_place_kernel<<<dim3(2 * (p.d / 8), heads), kMoveThreads, 0, stream>>>(p);
+    move_in_place_kernel<<<dim3(2 * ((p.d / 8 + 1) / 2), heads), kMoveThreads, 0, stream>>>(p);
   } else {
     const int rows = kMoveThreads / (p.d / 8);
     const int steps = (p.keep + rows - 1) / rows;

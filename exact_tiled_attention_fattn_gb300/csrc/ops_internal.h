@@ -31,7 +31,8 @@ struct RopeParams {
   int* status;
 };
 
-cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool append, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool append, int num_sms,
+                        cudaStream_t stream);
 
 struct KeyWeightsParams {
   const void* q;              // [total_q, Hq, d] bf16

@@ -107,15 +107,16 @@ def _check(fn: str, status: int):
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device.index != torch.cuda.current_device():
+    if stream is None:  # the handle without a Stream object around it (0.3 us against 2.9)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {stream.device} but the current CUDA device is cuda:{torch.cuda.current_device()}")
     return int(stream.cuda_stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """Address for a c_void_p argument (an int: ctypes converts it without an object of its own)."""
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_code(dt) -> int:
@@ -130,28 +131,29 @@ def _need_cuda(*ts, contiguous: bool = True):
     """All given tensors are contiguous CUDA tensors on one device, the current one
     (the library launches on the current device, so a tensor elsewhere would be an
     invalid address there). ``contiguous=False``: for calls that take strides."""
-    dev = None
+    dev = -1
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("all tensors must be CUDA tensors")
         if contiguous and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"all tensors must be on one device (got {dev} and {t.device})")
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev} but the current CUDA device is cuda:{torch.cuda.current_device()}; "
-                         f"call under torch.cuda.device({dev.index})")
+        if d != dev:
+            if dev >= 0:
+                raise ValueError(f"all tensors must be on one device (got cuda:{dev} and {t.device})")
+            dev = d
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev} but the current CUDA device is cuda:{torch.cuda.current_device()}; "
+                         f"call under torch.cuda.device({dev})")
 
 
 def _expect(t, shape, name, dtype=None):
     """Shape (and dtype) check of an argument the library will read or write in full."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -203,7 +205,7 @@ def fwd(q, k, v, causal: bool = False, scale: float | None = None, cu_seqlens=No
         lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
     st = lib.fattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, N, d, 1 if causal else 0,
                        float(scale), _ptr(cu_seqlens), T if cu_seqlens is not None else 0, _dtype_code(q.dtype),
-                       ctypes.c_void_p(_stream_handle(stream)))
+                       _stream_handle(stream))
     _check("fattn_fwd", st)
     return out, lse
 
@@ -240,7 +242,7 @@ def fwd_block_sparse(q, k, v, block_mask, causal: bool = False, scale: float | N
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     st = lib.fattn_fwd_block_sparse(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
                                     1 if causal else 0, float(scale), _ptr(block_mask), block_mask.shape[0],
-                                    ctypes.c_void_p(_stream_handle(stream)))
+                                    _stream_handle(stream))
     _check("fattn_fwd_block_sparse", st)
     return out, lse
 
@@ -276,7 +278,7 @@ def fwd_masked(q, k, v, mask, causal: bool = False, scale: float | None = None, 
     sh = 0 if Hm == 1 else N * L
     st = lib.fattn_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
                               1 if causal else 0, float(scale), _ptr(mask), sb, sh, L,
-                              ctypes.c_void_p(_stream_handle(stream)))
+                              _stream_handle(stream))
     _check("fattn_fwd_masked", st)
     return out, lse
 
@@ -305,7 +307,7 @@ def fwd_fp8(q8, k8, v8, q_descale: float, k_descale: float, v_descale: float, ca
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q8.device)
     st = lib.fattn_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(v8), _ptr(out), _ptr(lse), B, Hq, k8.shape[2], N, d,
                            1 if causal else 0, float(scale), float(q_descale), float(k_descale), float(v_descale),
-                           ctypes.c_void_p(_stream_handle(stream)))
+                           _stream_handle(stream))
     _check("fattn_fwd_fp8", st)
     return out, lse
 
@@ -343,7 +345,7 @@ def fwd_paged(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
     st = lib.fattn_fwd_paged(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
                              _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                              block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
-                             float(scale), ctypes.c_void_p(_stream_handle(stream)))
+                             float(scale), _stream_handle(stream))
     _check("fattn_fwd_paged", st)
     return out, lse
 
@@ -382,7 +384,7 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     st = lib.fattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                        B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), _ptr(workspace),
-                       workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream_handle(stream)))
+                       workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check("fattn_bwd", st)
     return dq, dk, dv
 
@@ -438,7 +440,7 @@ def decode_paged(q, kcache, vcache, block_table, seqlens, num_splits: int, scale
     ws_bytes = workspace.numel() * workspace.element_size()
     st = lib.fattn_decode_paged(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), num_splits,
                                 _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size, maxp, num_pages, float(scale),
-                                _ptr(workspace), ws_bytes, ctypes.c_void_p(_stream_handle(stream)))
+                                _ptr(workspace), ws_bytes, _stream_handle(stream))
     _check("fattn_decode_paged", st)
     return out, lse
 
@@ -477,7 +479,7 @@ def decode_paged_static(q, kcache, vcache, block_table, seqlens, num_splits: int
     st = lib.fattn_decode_paged_static(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
                                        num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                        block_table.shape[1], num_pages, float(scale),
-                                       ctypes.c_void_p(_stream_handle(stream)))
+                                       _stream_handle(stream))
     _check("fattn_decode_paged_static", st)
     return out, lse
 
@@ -508,14 +510,14 @@ def merge_partials(o_part, lse_part, out_dtype=torch.bfloat16, out=None, lse=Non
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=o_part.device)
     st = lib.fattn_merge_partials(_ptr(o_part), _ptr(lse_part), _ptr(out), _ptr(lse), B, Hq, S, d,
-                                  _dtype_code(out.dtype), ctypes.c_void_p(_stream_handle(stream)))
+                                  _dtype_code(out.dtype), _stream_handle(stream))
     _check("fattn_merge_partials", st)
     return out, lse
 
 
 def debug_read_status(stream=None) -> int:
     """Synchronise the stream, then read and clear the device status word."""
-    return int(load_library().fattn_debug_read_status(ctypes.c_void_p(_stream_handle(stream))))
+    return int(load_library().fattn_debug_read_status(_stream_handle(stream)))
 
 
 def debug_set_wait_limit(limit_ns: int = 0, stall: bool = False) -> None:
@@ -567,15 +569,16 @@ def _row_strides(t, name):
     """(row stride, head stride) of [..., H, d] whose leading dimensions are one uniform run of rows."""
     if t.dim() not in (3, 4):
         raise ValueError(f"{name} must be [T, H, d] or [B, N, H, d]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    stride = t.stride()
+    if stride[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    row = t.stride(-3)
-    if t.dim() == 4 and t.shape[0] > 1:
+    row = stride[-3]
+    if len(stride) == 4 and t.shape[0] > 1:
         if t.shape[1] == 1:
-            row = t.stride(0)
-        elif t.stride(0) != t.shape[1] * row:
+            row = stride[0]
+        elif stride[0] != t.shape[1] * row:
             raise ValueError(f"{name}: the batch stride must be N row strides")
-    return row, t.stride(-2)
+    return row, stride[-2]
 
 
 def _no_overlap(t, name):
@@ -626,25 +629,31 @@ def rope(q, k=None, inv_freq=None, positions=None, interleaved: bool = False, am
         _expect(positions, lead, "positions", torch.int32)
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
-    _expect(out_q, q.shape, "out_q", q.dtype)
-    if k is not None:
-        _expect(out_k, k.shape, "out_k", q.dtype)
+    rows = math.prod(lead)
+    Hq, Hk = q.shape[-2], 0 if k is None else k.shape[-2]
+    strides = [*_row_strides(q, "q")]
     if out_q is None:
         out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and out_k is None:
-        out_k = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    rows = math.prod(lead)
-    strides = []
-    for x, y, name in ((q, out_q, "q"), (k, out_k, "k")):
-        if x is None:
-            strides += [0, 0, 0, 0]
-            continue
-        _no_overlap(y, "out_" + name)
-        strides += [*_row_strides(x, name), *_row_strides(y, "out_" + name)]
+        strides += [Hq * d, d]
+    else:
+        _expect(out_q, q.shape, "out_q", q.dtype)
+        _no_overlap(out_q, "out_q")
+        strides += _row_strides(out_q, "out_q")
+    if k is None:
+        strides += [0, 0, 0, 0]
+    else:
+        strides += _row_strides(k, "k")
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            strides += [Hk * d, d]
+        else:
+            _expect(out_k, k.shape, "out_k", q.dtype)
+            _no_overlap(out_k, "out_k")
+            strides += _row_strides(out_k, "out_k")
     st = lib.fattn_rope(_ptr(q), _ptr(out_q), _ptr(k), _ptr(out_k), _ptr(positions), lead[-1] if rows else 1,
-                        _ptr(inv_freq), rows, q.shape[-2], 0 if k is None else k.shape[-2], d, rot, *strides,
+                        _ptr(inv_freq), rows, Hq, Hk, d, rot, *strides,
                         1 if interleaved else 0, 1 if inverse else 0, float(amplitude), code,
-                        ctypes.c_void_p(_stream_handle(stream)))
+                        _stream_handle(stream))
     _check("fattn_rope", st)
     return out_q if k is None else (out_q, out_k)
 
@@ -702,7 +711,7 @@ def rope_append_paged(q, k, v, kcache, vcache, block_table, seqlens_k, cu_seqlen
                                      _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q), _ptr(positions),
                                      _ptr(inv_freq), B, Tq, Hq, Hkv, d, rot, kcache.shape[1], block_table.shape[1],
                                      kcache.shape[0], *qs, *_row_strides(k, "k"), *_row_strides(v, "v"),
-                                     1 if interleaved else 0, float(amplitude), ctypes.c_void_p(_stream_handle(stream)))
+                                     1 if interleaved else 0, float(amplitude), _stream_handle(stream))
     _check("fattn_rope_append_paged", st)
     return out
 
@@ -764,7 +773,7 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     st = lib.fattn_fwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
                               1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
-                              _ptr(key_begin), _ptr(key_end), ctypes.c_void_p(_stream_handle(stream)))
+                              _ptr(key_begin), _ptr(key_end), _stream_handle(stream))
     _check("fattn_fwd_shaped", st)
     return out, lse
 
@@ -802,7 +811,7 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
                                     _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                     block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
                                     float(scale), float(softcap), _ptr(slopes), int(window), _ptr(key_begin),
-                                    _ptr(key_end), ctypes.c_void_p(_stream_handle(stream)))
+                                    _ptr(key_end), _stream_handle(stream))
     _check("fattn_fwd_paged_shaped", st)
     return out, lse
 
@@ -843,7 +852,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
                               int(window), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream_handle(stream)))
+                              workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check("fattn_bwd_shaped", st)
     return dq, dk, dv
 
@@ -883,7 +892,7 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
                                        num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                        block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
                                        int(window), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       ctypes.c_void_p(_stream_handle(stream)))
+                                       _stream_handle(stream))
     _check("fattn_decode_paged_shaped", st)
     return out, lse
 
@@ -925,7 +934,7 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
                                      _ptr(lse), lse.stride(0), lse.stride(1), _ptr(weights), _ptr(out), B, Hq, Hkv, d,
                                      page_size, block_table.shape[1], num_pages, Tq, int(max_seqlen_q),
                                      1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
-                                     float(decay), ctypes.c_void_p(_stream_handle(stream)))
+                                     float(decay), _stream_handle(stream))
     _check("fattn_key_weights_paged", st)
     return out
 
@@ -967,6 +976,6 @@ def evict_paged(kcache, vcache, block_table, seqlens, weights, keep: int, recent
     st = lib.fattn_evict_paged(_ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), _ptr(weights),
                                _ptr(dst_table), _ptr(out_seqlens), _ptr(out_weights), _ptr(kept), B, Hkv, d, page_size,
                                maxp, num_pages, dst_pages, int(keep), int(recent), int(first),
-                               ctypes.c_void_p(_stream_handle(stream)))
+                               _stream_handle(stream))
     _check("fattn_evict_paged", st)
     return out_seqlens, out_weights, kept
