@@ -2,8 +2,9 @@
 // last `recent` and the heaviest of the others — compacted in order.
 //
 // select_kernel, one block per (sequence, KV head): the weights of the middle tokens as
-// order-preserving 32-bit integers, the threshold by four passes of an 8-bit histogram from the top
-// digit down, then a scan in index order that counts what is kept and the ties already taken
+// order-preserving 32-bit integers, the threshold by three passes of an 11-bit histogram from the top
+// digit down (its first digit tells quarter octaves apart: few lanes of a warp meet in a bin, where the
+// 8-bit digit of an exponent brought most of them together), then a scan in index order that counts what is kept and the ties already taken
 // (ties go to the lowest index) and places the kept indices and their weights.
 // move_kernel copies the kept K and V rows by that list. Into other pages every row is
 // independent. In place a row moves to a slot at or below its own, which may hold a row that has
@@ -29,11 +30,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 constexpr int kPer = 16;                        // weights per thread and tile
 constexpr int kTile = kSelThreads * kPer;       // 16384 tokens
+constexpr int kBins = 2048;
+static_assert(kBins == 2 * kSelThreads, "two bins per thread");
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
-  __shared__ int s_hist[256];
+  __shared__ int s_hist[kBins];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
+  __shared__ int s_warp[32];
   __shared__ int s_cnt[kPer * 32];   // per 32 consecutive tokens of a tile: kept above the threshold | ties << 16
   __shared__ int s_tile[2];          // of the tile
   const int b = blockIdx.y, h = blockIdx.x;
@@ -71,43 +75,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     s_need = need;
   }
   if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) s_hist[tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {   // digits of 11, 11 and 10 bits
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      s_hist[tid] = s_hist[tid + kSelThreads] = 0;
       __syncthreads();
       const uint32_t prefix = s_prefix;
+      const int want = s_need;
       for (int t0 = 0; t0 < n; t0 += kTile) {
         if (n > kTile) load(t0);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int t = t0 + i * kSelThreads + tid;
+          if (t0 + i * kSelThreads >= n) break;
           if (t >= lo && t < hi) {
             const uint32_t k = order_key(x[i]);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+            if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&s_hist[(k >> shift) & digits], 1);
           }
         }
       }
       __syncthreads();
-      if (warp == 0) {  // digits from the highest down: lane l holds digits 255 - 8l ... 248 - 8l
-        int c[8], sum = 0;
-        for (int i = 0; i < 8; ++i) {
-          c[i] = s_hist[255 - 8 * lane - i];
-          sum += c[i];
-        }
-        int before = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += v;
-        }
-        before -= sum;  // tokens with a higher digit than this lane's
-        const int want = s_need;
-        __syncwarp();
-        for (int i = 0; i < 8; ++i) {
-          if (before < want && want <= before + c[i]) {  // one (lane, i): the threshold's digit
-            s_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-            s_need = want - before;
-          }
-          before += c[i];
-        }
+      // the threshold's digit: thread i counts bins 2047 - 2 i and 2046 - 2 i, after all that are higher
+      const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
+      int v = c0 + c1;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += a;
+      }
+      if (lane == 31) s_warp[warp] = v;
+      __syncthreads();
+      int u = lane < warp ? s_warp[lane] : 0;
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      const int before = u + v - c0 - c1;
+      if (before < want && want <= before + c0 + c1) {  // one thread
+        const bool first_bin = want <= before + c0;
+        s_prefix = prefix | ((uint32_t)(kBins - (first_bin ? 1 : 2) - 2 * tid) << shift);
+        s_need = want - before - (first_bin ? 0 : c0);
       }
       __syncthreads();
     }
@@ -127,6 +130,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     uint32_t gts = 0, eqs = 0;   // bit i: this thread's token of batch i
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      if (i >= batches) {
+        if (lane == 0) s_cnt[i * 32 + warp] = 0;
+        continue;
+      }
       const int t = t0 + i * kSelThreads + tid;
       const bool in = t < n, mid = in && t >= lo && t < hi;
       const uint32_t k = order_key(x[i]);
