@@ -8,7 +8,7 @@
 // heads of that KV head's GQA group (up to 16), so each K/V byte is read once,
 // and an empty split costs one atomic instead of a thread block. Each of the
 // 4 warps streams its own 16-token chunks through a 2-stage cp.async pipeline
-// (16-byte copies, L1 bypassed; two CTAs per SM at d = 128, set by registers), finds each token's page
+// (16-byte copies, L1 bypassed; three CTAs per SM at d = 128), finds each token's page
 // through the block table, and runs the two small products on the tensor
 // cores with mma.sync (S = Q K^T with the group's heads as the 16 rows,
 // O += P V with P kept in registers). Each warp keeps its own running (m, l, O)
@@ -151,9 +151,9 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
   };
 
   const float sl2 = p.scale * kLog2e;
-  // shaped: constants in log2 units, and the slopes of this thread's rows g and g + 8
-  const float cap2 = kShaped ? p.shape.cap * kLog2e : 0.f;
-  const float capk = kShaped && p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
+  // shaped: the slopes of this thread's rows g and g + 8 (rows from 8 on need no scores in groups of up
+  // to 8 heads)
+  const bool high_rows = !kShaped || rows_valid > 8;
   float slope0 = 0.f, slope1 = 0.f;
   if (kShaped && p.shape.slopes) {
     const int g = lane >> 2;
@@ -200,6 +200,8 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
     }
     // scale into the log2 domain, mask missing tokens, running max per row
     float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+    // shaped: distance of this thread's first token
+    const float dist = kShaped ? (float)(qpos - (t0 + (warp + i * kWarps) * kChunk + 2 * (lane & 3))) : 0.f;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
@@ -208,8 +210,12 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
         const bool ok = (vm >> tok) & 1u;
         float y;
         if constexpr (kShaped) {
-          y = p.shape.cap > 0.f ? fmaf(-2.f * cap2, tanh_r(s[nt][j] * capk), cap2) : s[nt][j] * sl2;
-          y = fmaf(j < 2 ? slope0 : slope1, (float)(qpos - (t0 + (warp + i * kWarps) * kChunk + tok)), y);
+          if (j >= 2 && !high_rows) {
+            s[nt][j] = -CUDART_INF_F;
+            continue;
+          }
+          y = p.shape.cap > 0.f ? fmaf(-2.f * p.shape.cap2, tanh_r(s[nt][j] * p.shape.capk), p.shape.cap2) : s[nt][j] * sl2;
+          if (p.shape.slopes) y = fmaf(j < 2 ? slope0 : slope1, dist - (float)(nt * 8 + (j & 1)), y);
         } else {
           y = s[nt][j] * sl2;
         }
@@ -344,8 +350,11 @@ __device__ __forceinline__ void merge_group(const DecodeParams& p, int b, int h0
   }
 }
 
+// (Held to the registers of three CTAs per SM, which is what shared memory admits at d = 128: left alone the
+// compiler takes up to 246, two CTAs, and 199k context tokens of 8 KV heads take 184 us in 8 splits instead of
+// 152, with a cap 195 instead of 150.)
 template <int D, bool kPage16, bool kShaped>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_item, s_last;
   const int G = p.Hq / p.Hkv;
