@@ -137,6 +137,57 @@ __device__ __forceinline__ void row_vectors(const BwdParams& p, int b, int h, in
   p.ws_d[(size_t)bh * p.Npad + i] = i < p.N ? mine : 0.f;
 }
 
+// The same for the shaped passes, whose items may be short (a document's few key tiles leave the two
+// warps 15k cycles for their 128 rows, where 8 rows at a time with five shuffles each took 20k): 16-byte
+// loads, D / 8 lanes a row, half of the 32 rows on their way together, and the lanes' partial sums of all
+// rows reduced by exchanging halves (D / 8 - 1 shuffles for D / 8 sums).
+template <int D>
+__device__ __forceinline__ void row_vectors_wide(const BwdParams& p, int b, int h, int i0, int lane) {
+  constexpr int L = D / 8, R = 32 / L;            // lanes per row, rows per load; L loads cover the block
+  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o);
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout);
+  const int bh = b * p.Hq + h;
+  const int mine = i0 + (lane % L) * R + lane / L;  // the row whose sum this lane ends with
+  const float lse = mine < p.N ? __ldg(p.lse + (size_t)bh * p.N + mine) : -CUDART_INF_F;
+  float sum[L];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint4 a[L / 2], d[L / 2];
+#pragma unroll
+    for (int t = 0; t < L / 2; ++t) {
+      const int i = i0 + (half * (L / 2) + t) * R + lane / L;
+      a[t] = d[t] = make_uint4(0, 0, 0, 0);
+      if (i < p.N) {
+        const size_t off = (((size_t)b * p.N + i) * p.Hq + h) * D + (lane % L) * 8;
+        a[t] = __ldg(reinterpret_cast<const uint4*>(o + off));
+        d[t] = __ldg(reinterpret_cast<const uint4*>(g + off));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < L / 2; ++t) {
+      float s0 = bf16_lo(a[t].x) * bf16_lo(d[t].x), s1 = bf16_hi(a[t].x) * bf16_hi(d[t].x);
+      s0 = fmaf(bf16_lo(a[t].y), bf16_lo(d[t].y), s0);
+      s1 = fmaf(bf16_hi(a[t].y), bf16_hi(d[t].y), s1);
+      s0 = fmaf(bf16_lo(a[t].z), bf16_lo(d[t].z), s0);
+      s1 = fmaf(bf16_hi(a[t].z), bf16_hi(d[t].z), s1);
+      s0 = fmaf(bf16_lo(a[t].w), bf16_lo(d[t].w), s0);
+      s1 = fmaf(bf16_hi(a[t].w), bf16_hi(d[t].w), s1);
+      sum[half * (L / 2) + t] = s0 + s1;
+    }
+  }
+#pragma unroll
+  for (int step = L / 2; step > 0; step /= 2) {   // lanes with bit `step` keep the upper half of the sums
+    const bool up = lane & step;
+#pragma unroll
+    for (int t = 0; t < step; ++t) {
+      const float keep = up ? sum[t + step] : sum[t], send = up ? sum[t] : sum[t + step];
+      sum[t] = keep + __shfl_xor_sync(0xffffffffu, send, step);
+    }
+  }
+  p.ws_nl2[(size_t)bh * p.Npad + mine] = (lse > -CUDART_INF_F && lse < CUDART_INF_F) ? -lse * kLog2e : -CUDART_INF_F;
+  p.ws_d[(size_t)bh * p.Npad + mine] = mine < p.N ? sum[0] : 0.f;
+}
+
 // Bounded wait until a shared-memory counter reaches `target` (abort and time limit as
 // in the mbarrier waits).
 __device__ __forceinline__ bool count_wait(volatile int* c, int target, volatile int* abort, int* status,
@@ -932,11 +983,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
         int b, h, i;
         item(it, b, h, i);
-        if (!mbar_wait(bar(kQEmpty), (nq & 1) ^ 1, abort, p.status, p.wait_ns)) break;
-        mbar_arrive_expect_tx(bar(kQFull), 2 * Lay::kTile);
-        load_tile<D>(sb + Lay::kOffQ, &tq, bar(kQFull), h, b * p.N + i * BT, pol_q);
-        load_tile<D>(sb + Lay::kOffDO, &tdo, bar(kQFull), h, b * p.N + i * BT, pol_q);
-        ++nq;
         int top, jn;
         tiles(b, i, top, jn);
         const int hkv = h / G;
@@ -957,6 +1003,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_tile<D>(sb + Lay::kOffV + vs * Lay::kTile, &tv, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           ++nk;
           ++nv;
+          if (j == 0) {  // Q and dO after the first K and V, whose stages are free a tile earlier
+            if (!mbar_wait(bar(kQEmpty), (nq & 1) ^ 1, abort, p.status, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar(kQFull), 2 * Lay::kTile);
+            load_tile<D>(sb + Lay::kOffQ, &tq, bar(kQFull), h, b * p.N + i * BT, pol_q);
+            load_tile<D>(sb + Lay::kOffDO, &tdo, bar(kQFull), h, b * p.N + i * BT, pol_q);
+            ++nq;
+          }
         }
       }
       // wait for the last load into each buffer before the CTA may exit
@@ -1055,11 +1111,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 3) write_key_ranges(p, blockIdx.x, gridDim.x, lane);
     }
     for (int kk = 0, it; (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
-      if (!count_wait(items_started, kk - 1, abort, p.status, p.wait_ns)) break;
+      if (!count_wait(items_started, kk - 2, abort, p.status, p.wait_ns)) break;
       int b, h, i;
       item(it, b, h, i);
 #pragma unroll 1
-      for (int blk = 0; blk < 2; ++blk) row_vectors<D>(p, b, h, i * BT + 64 * (warp - 2) + 32 * blk, lane);
+      for (int blk = 0; blk < 2; ++blk) {
+        const int r0 = i * BT + 64 * (warp - 2) + 32 * blk;
+        if constexpr (kShaped)
+          row_vectors_wide<D>(p, b, h, r0, lane);
+        else
+          row_vectors<D>(p, b, h, r0, lane);
+      }
       __threadfence_block();  // the stores above before the count that announces them
       __syncwarp();
       if (lane == 0) halves_done[warp - 2] = kk + 1;
