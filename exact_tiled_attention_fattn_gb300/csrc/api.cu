@@ -109,6 +109,8 @@ int num_sms_current() {  // declared in fattn_internal.h
 
 using namespace fattn;
 
+static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 extern "C" const char* fattn_status_string(fattn_status s) {
@@ -245,7 +247,7 @@ fattn_status fattn::fwd_paged_impl(const void* q, const void* kcache, const void
                                    const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B,
                                    int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
                                    int total_q, int max_seqlen_q, int causal, float scale, const ScoreShape* shape,
-                                   cudaStream_t stream) {
+                                   int num_splits, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || total_q < 0 || max_seqlen_q < 0 || page_size <= 0 ||
       max_pages_per_seq <= 0 || num_pages <= 0)
     return FATTN_ERR_INVALID_ARG;
@@ -262,6 +264,15 @@ fattn_status fattn::fwd_paged_impl(const void* q, const void* kcache, const void
   if ((long long)(num_pages + 1) * page_size > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
   if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL || (long long)B * max_pages_per_seq > 0x7fffffffLL)
     return FATTN_ERR_UNSUPPORTED;
+  if (num_splits > 1) {
+    const long long pairs = ((long long)max_seqlen_q + 255) / 256;  // items per (sequence, head) and split
+    if (B > 65535 || (long long)B * Hq > 0x7fffffffLL / pairs / num_splits ||
+        (long long)max_seqlen_q * Hq > 0x7fffffffLL)  // the joining launch's grid
+      return FATTN_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < fattn_fwd_paged_shaped_workspace_size(total_q, Hq, d, num_splits) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return FATTN_ERR_WORKSPACE;
+  }
 
   int err = 0;
   PrefillParams p{};
@@ -274,6 +285,10 @@ fattn_status fattn::fwd_paged_impl(const void* q, const void* kcache, const void
   if (shape) {
     p.shaped = 1;
     p.shape = *shape;
+    p.splits = num_splits;
+    p.lse_part = static_cast<float*>(workspace);
+    p.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align256((size_t)total_q * Hq * num_splits * sizeof(float)));
   }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
@@ -285,7 +300,8 @@ fattn_status fattn::fwd_paged_impl(const void* q, const void* kcache, const void
     return FATTN_ERR_CUDA;
   const int sms = num_sms_current();
   if (sms <= 0) return FATTN_ERR_CUDA;
-  return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  if (launch_prefill_tc(p, tq, tk, tv, to, sms, stream) != cudaSuccess) return FATTN_ERR_CUDA;
+  return num_splits <= 1 || launch_prefill_merge(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const void* vcache,
@@ -294,10 +310,9 @@ extern "C" fattn_status fattn_fwd_paged(const void* q, const void* kcache, const
                                         int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
                                         int max_seqlen_q, int causal, float scale, cudaStream_t stream) {
   return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
-                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, nullptr, stream);
+                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, nullptr, 1, nullptr, 0,
+                        stream);
 }
-
-static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 extern "C" fattn_status fattn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                                       int Hkv, int N, int d, int causal, float scale, float q_descale,

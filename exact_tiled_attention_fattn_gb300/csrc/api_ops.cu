@@ -137,6 +137,7 @@ extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const voi
   p.causal = causal ? 1 : 0; p.scale = scale;
   p.mask_heads = 1;
   p.shaped = 1;
+  p.splits = 1;
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;
   current_waits(&p.wait_ns, &p.debug_stall);
@@ -149,18 +150,27 @@ extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const voi
   return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
+extern "C" size_t fattn_fwd_paged_shaped_workspace_size(int total_q, int Hq, int d, int num_splits) {
+  if (total_q <= 0 || Hq <= 0 || d <= 0 || num_splits <= 1) return 0;
+  const size_t rows = (size_t)total_q * Hq * num_splits;
+  return (rows * 4 + 255) / 256 * 256 + (rows * d * 4 + 255) / 256 * 256;
+}
+
 extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache, const void* vcache,
                                                const int32_t* block_table, const int32_t* seqlens_k,
                                                const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
                                                int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
                                                int max_seqlen_q, int causal, float scale, float softcap,
                                                const float* slopes, int window, const int32_t* key_begin,
-                                               const int32_t* key_end, cudaStream_t stream) {
+                                               const int32_t* key_end, int num_splits, void* workspace,
+                                               size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
   const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &shape);
   if (st != FATTN_OK) return st;
+  if (num_splits < 1) return FATTN_ERR_INVALID_ARG;
   return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
-                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, &shape, stream);
+                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, &shape, num_splits, workspace,
+                        workspace_bytes, stream);
 }
 
 extern "C" size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int N) {

@@ -70,6 +70,11 @@ struct PrefillParams {
   // shaped variant only (dense, or paged with a block table)
   int shaped;
   ScoreShape shape;
+  // paged shaped: every query tile's key tiles cut into `splits` runs, each an item of its own; with more than
+  // one the partials go to o_part [total_rows, Hq, splits, d] and lse_part [total_rows, Hq, splits]
+  int splits;
+  float* o_part;
+  float* lse_part;
   // bounded pipeline waits: each mbarrier wait gives up after wait_ns; debug_stall != 0
   // (test hook) makes the softmax / element-wise warps first wait on a barrier that no
   // role arrives on, so that the wait runs out and every role takes the abort exit
@@ -85,6 +90,9 @@ constexpr int kSparseMaxBlocks = 2048;
 // boxes) and of o (bf16, 32-row boxes: the epilogue's stores).
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& to, int num_sms, cudaStream_t stream);
+
+// Joins the partials of a split paged prefill into p.o and p.lse.
+cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream);
 
 // CUDA-core fp32 prefill.
 cudaError_t launch_prefill_f32(const PrefillParams& p, cudaStream_t stream);

@@ -91,7 +91,8 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int rows, int H, int d,
 fattn_status fwd_paged_impl(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
                             const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq,
                             int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
-                            int max_seqlen_q, int causal, float scale, const ScoreShape* shape, cudaStream_t stream);
+                            int max_seqlen_q, int causal, float scale, const ScoreShape* shape, int num_splits,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 fattn_status bwd_impl(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                       void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d, int causal, float scale,
                       const ScoreShape* shape, void* workspace, size_t workspace_bytes, cudaStream_t stream);

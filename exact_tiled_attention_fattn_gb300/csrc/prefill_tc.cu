@@ -181,6 +181,7 @@ struct Item {
   // shaped variant: tile t visits K/V tiles [top[t] - n[t], top[t]); the item's steps run from
   // tile jtop - 1 down to jbot, over both tiles' ranges (n = 0 as well where no row sees a key)
   int top[2], jtop, jbot;
+  int split, all_lo[2], all_top[2];  // the run of key tiles that the item takes, and tile t's whole range
   bool valid;
 };
 
@@ -201,9 +202,11 @@ struct Schedule {
   int pairs, heads, group, total;
 };
 
+template <bool kShaped>
 __device__ __forceinline__ Schedule make_schedule(const PrefillParams& p) {
   Schedule s;
   s.pairs = (p.N + kRowsPerItem - 1) / kRowsPerItem;
+  if constexpr (kShaped) s.pairs *= p.splits;   // (pair, split): pair * splits + split
   s.heads = p.B * p.Hq;
   const int G = p.Hq / p.Hkv;
   const int rounds = s.pairs >= 32 ? 4 : 2;                 // grid rounds per group
@@ -232,7 +235,12 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
   const int gh = min(s.group, s.heads - g * s.group);       // heads in this (maybe last) group
   const int rank = rem / gh;
   const int bh = g * s.group + (rem - rank * gh);
-  const int pair = s.pairs - 1 - rank;
+  int pair = s.pairs - 1 - rank;
+  x.split = 0;
+  if constexpr (kShaped) {
+    x.split = pair % p.splits;
+    pair /= p.splits;
+  }
   x.b = bh / p.Hq;
   x.h = bh - x.b * p.Hq;
   x.base = pair * kRowsPerItem;
@@ -261,7 +269,7 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
   const bool has_b = x.base + BM < x.L;
   if constexpr (kShaped) {
     // the bounds are monotone: a tile's first row has its lowest key, its last row its highest
-    x.n[0] = x.n[1] = 0;
+    x.n[0] = x.n[1] = x.all_lo[0] = x.all_lo[1] = x.all_top[0] = x.all_top[1] = 0;
     x.jbot = 1 << 30;
     if (x.valid) {
 #pragma unroll
@@ -271,10 +279,16 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
         const int lo = shape_lo(p.shape, (long long)x.row0 + first, first + x.off);
         const int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
         if (lo < hi) {
-          x.top[t] = (hi + BN - 1) / BN;
-          x.n[t] = x.top[t] - lo / BN;
-          x.jtop = max(x.jtop, x.top[t]);
-          x.jbot = min(x.jbot, lo / BN);
+          const int t0 = lo / BN, n = (hi + BN - 1) / BN - t0;
+          x.all_lo[t] = t0;
+          x.all_top[t] = t0 + n;
+          const int from = t0 + (int)((long long)n * x.split / p.splits);
+          x.top[t] = t0 + (int)((long long)n * (x.split + 1) / p.splits);
+          x.n[t] = x.top[t] - from;
+          if (x.n[t] > 0) {
+            x.jtop = max(x.jtop, x.top[t]);
+            x.jbot = min(x.jbot, from);
+          }
         }
       }
     }
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kOffHolder);
 
-  const Schedule sch = make_schedule(p);
+  const Schedule sch = make_schedule<kShaped>(p);
   const int G = p.Hq / p.Hkv;
 
   if (warp < 4) {
@@ -861,7 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nt == 0) {
         release_mask();
         if constexpr (kShaped) {  // no row of the tile sees a key: O = 0, lse = -inf
-          if (row < x.L) {
+          if (row < x.L && p.splits > 1) {  // an empty partial
+            p.lse_part[((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split] = -CUDART_INF_F;
+          } else if (row < x.L) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
                                                   ((size_t)(x.row0 + row) * p.Hq + x.h) * D);
 #pragma unroll
@@ -884,7 +900,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         lo = shape_lo(p.shape, (long long)x.row0 + rc, rc + x.off);
         lim = shape_hi(p.shape, (long long)x.row0 + rc, rc + x.off, x.Lk, p.causal);
         // ranges that are not monotone: the row's keys are not all among its tile's
-        if (lo < lim && (lo < (kv_hi - nt) * BN || lim > kv_hi * BN)) record_status(p.status, kStatusDeviceCheck);
+        if (lo < lim && (lo < (t ? x.all_lo[1] : x.all_lo[0]) * BN || lim > (t ? x.all_top[1] : x.all_top[0]) * BN))
+          record_status(p.status, kStatusDeviceCheck);
         if (kBias && p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
       } else {
         lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;
@@ -1384,6 +1401,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a row the mask left with no key: O = 0, lse = -inf
       const float inv = ((kMasked || kShaped) && l == 0.f) ? 0.f : (kFp8 ? p.v_descale : 1.f) / l;
       const int wrow0 = x.base + t * BM + q4 * 32;  // this warp's first row
+      if (kShaped && kPaged && p.splits > 1) {
+        // a partial: O / l in fp32, and the logsumexp of the run's keys
+        float* orow = p.o_part + (((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(o_col + 32 * c, u);
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(orow + 32 * c)[e] =
+                  make_float4(__uint_as_float(u[4 * e]) * inv, __uint_as_float(u[4 * e + 1]) * inv,
+                              __uint_as_float(u[4 * e + 2]) * inv, __uint_as_float(u[4 * e + 3]) * inv);
+          }
+        }
+        if (live)
+          p.lse_part[((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split] =
+              l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+        continue;
+      }
       if (wrow0 + 32 <= x.L) {
         // all 32 rows of the warp lie in the sequence: stage each 64-column half in the
         // warp's slot (row `lane` at 128 lane, 16-byte chunk c at c ^ (lane mod 8): the
@@ -1460,7 +1497,7 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtens
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
   if (e != cudaSuccess) return e;
   const long long pairs = (p.N + kRowsPerItem - 1) / kRowsPerItem;
-  const long long items = (long long)p.B * p.Hq * pairs;
+  const long long items = (long long)p.B * p.Hq * pairs * (mode_shaped(kMode) ? p.splits : 1);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int grid = (int)(items < num_sms ? items : num_sms);
   kern<<<grid, kThreads, Lay::kBytes, stream>>>(tq, tk, tv, to, p);
@@ -1485,7 +1522,57 @@ cudaError_t launch_shaped(const PrefillParams& p, const CUtensorMap& tq, const C
   return launch_shaped_t<D, 0>(p, tq, tk, tv, to, num_sms, stream);
 }
 
+// Partials joined with the rescaling rule: lse = ln sum_s e^{lse_s}, O = sum_s e^{lse_s - lse} O_s. A thread
+// takes 4 columns of a (query, head) row; grid (rows of the longest chunk, sequences). Bound by the partials'
+// bytes; chunks that the attention kernel skipped (inconsistent lengths) are skipped here too.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const PrefillParams p) {
+  const int b = blockIdx.y, lanes = p.d / 4;
+  const int start = __ldg(p.cu_seqlens + b), end = __ldg(p.cu_seqlens + b + 1), lk = __ldg(p.seqlens_k + b);
+  if (start < 0 || end < start || end > p.total_rows || end - start > p.N || lk < end - start ||
+      lk > p.max_pages * p.page_size)
+    return;
+  const long long at = (long long)blockIdx.x * (kMergeThreads / lanes) + threadIdx.x / lanes;  // query * Hq + head
+  if (at >= (long long)(end - start) * p.Hq) return;
+  const size_t row = (size_t)start * p.Hq + at;
+  const int c = (threadIdx.x % lanes) * 4;
+  const float* lp = p.lse_part + row * p.splits;
+  const float4* op = reinterpret_cast<const float4*>(p.o_part + row * p.splits * p.d + c);
+  float m = -CUDART_INF_F;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldg(lp + s));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float ls = __ldg(lp + s);
+    if (ls == -CUDART_INF_F) continue;   // an empty run: its row was never written
+    const float w = ex2((ls - m) * kLog2e);
+    const float4 v = __ldg(op + (size_t)s * lanes);
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+    sum += w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a NaN sum stays one
+  uint2 o;
+  o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * p.d + c) = o;
+  if (p.lse && c == 0) {
+    const long long i = at / p.Hq;
+    p.lse[(size_t)(at - i * p.Hq) * p.total_rows + start + i] = sum == 0.f ? -CUDART_INF_F : m + logf(sum);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream) {
+  const int rows = kMergeThreads / (p.d / 4);
+  const dim3 grid((unsigned)(((long long)p.N * p.Hq + rows - 1) / rows), p.B);
+  prefill_merge_kernel<<<grid, kMergeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& to, int num_sms, cudaStream_t stream) {

@@ -58,8 +58,9 @@ SIGNATURES_OPS = {
     "fattn_rope_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                      _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _i, _f, _vp]),
     "fattn_fwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _vp, _vp, _vp]),
+    "fattn_fwd_paged_shaped_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fattn_fwd_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
-                                    _f, _vp, _i, _vp, _vp, _vp]),
+                                    _f, _vp, _i, _vp, _vp, _i, _vp, _sz, _vp]),
     "fattn_bwd_shaped_workspace_size": (_sz, [_i, _i, _i]),
     "fattn_bwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i,
                               _vp, _vp, _vp, _sz, _vp]),
@@ -716,6 +717,16 @@ def rope_append_paged(q, k, v, kcache, vcache, block_table, seqlens_k, cu_seqlen
     return out
 
 
+_sms: dict = {}
+
+
+def _num_sms(device: int) -> int:
+    """SM count of a device (a property of the machine, looked up once)."""
+    if device not in _sms:
+        _sms[device] = torch.cuda.get_device_properties(device).multi_processor_count
+    return _sms[device]
+
+
 # ------------------------------------------------------------------ shaped scores
 def document_ranges(doc_ids, prefix_len=None):
     """Key ranges (key_begin, key_end), int32 [B, N], of packed documents: ``doc_ids`` [B, N] names
@@ -778,11 +789,42 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
     return out, lse
 
 
+def fwd_paged_shaped_workspace_size(total_q: int, Hq: int, d: int, num_splits: int) -> int:
+    return int(load_library().fattn_fwd_paged_shaped_workspace_size(total_q, Hq, d, num_splits))
+
+
+def choose_chunk_splits(batch: int, Hq: int, d: int, max_seqlen_q: int, max_context: int,
+                        num_sms: int | None = None) -> int:
+    """Split count of ``fwd_paged_shaped``, 16 at most: the S whose estimate is lowest, in units of a step of one SM
+    over 128 keys (about 1.7 us): rounds of items over the SMs, each of its run's steps and 2 more, and for S > 1 the
+    joining launch (4) with the fp32 partials' way through memory (1 per million elements).
+
+    Measured, S = 1 against the choice: 16 queries over 32768 keys, 8 heads 465 -> 55 us (S 16); 256 over 32768, 32 heads
+    657 -> 186 (4); 2 x 512 over 4096, 16 heads 94 -> 69 (2); 3 x 517 over 9000, 16 heads stay at 1 (136; 2: 150)."""
+    items = batch * Hq * -(-max_seqlen_q // 256)
+    if items <= 0:
+        return 1
+    if num_sms is None:
+        num_sms = _num_sms(torch.cuda.current_device())
+    if items >= 4 * num_sms:
+        return 1
+    steps, join = max_context / 128, batch * max_seqlen_q * Hq * d * 1e-6
+    best, best_cost = 1, -(-items // num_sms) * (steps + 2)
+    for S in range(2, min(16, -(-max_context // 128)) + 1):
+        cost = -(-items * S // num_sms) * (steps / S + 2) + 4 + S * join
+        if cost < best_cost:
+            best, best_cost = S, cost
+    return best
+
+
 def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int, causal: bool = True,
                      scale: float | None = None, softcap: float = 0.0, slopes=None, window: int = 0, key_begin=None,
-                     key_end=None, out=None, lse=None, want_lse: bool = True, stream=None):
+                     key_end=None, out=None, lse=None, want_lse: bool = True, num_splits: int | None = None,
+                     workspace=None, stream=None):
     """``fwd_paged`` with the shaped scores of ``fwd_shaped``; a chunk's queries sit at the last positions
-    of their sequence's context. key_begin / key_end int32 [Tq], keys of the row's sequence.
+    of their sequence's context. key_begin / key_end int32 [Tq], keys of the row's sequence. ``num_splits`` cuts
+    every query tile's keys into runs that are joined at the end (None: ``choose_chunk_splits``); their partials
+    take a ``workspace`` of fwd_paged_shaped_workspace_size bytes (allocated when None).
     Returns (O [Tq,Hq,d], lse [Hq,Tq])."""
     lib = load_library()
     _need_cuda(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, out, lse)
@@ -807,11 +849,22 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    if num_splits is None:
+        context = block_table.shape[1] * page_size
+        if window > 0:
+            context = min(context, int(window) + int(max_seqlen_q))
+        num_splits = choose_chunk_splits(B, Hq, d, int(max_seqlen_q), context)
+    _need_cuda(workspace)
+    if workspace is None and num_splits > 1:
+        workspace = torch.empty(max(fwd_paged_shaped_workspace_size(Tq, Hq, d, num_splits), 1), dtype=torch.uint8,
+                                device=q.device)
     st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
                                     _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                     block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
                                     float(scale), float(softcap), _ptr(slopes), int(window), _ptr(key_begin),
-                                    _ptr(key_end), _stream_handle(stream))
+                                    _ptr(key_end), int(num_splits), _ptr(workspace),
+                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                    _stream_handle(stream))
     _check("fattn_fwd_paged_shaped", st)
     return out, lse
 

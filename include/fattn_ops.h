@@ -126,17 +126,29 @@ fattn_status fattn_fwd_shaped(const void* q, const void* k, const void* v, void*
                               const int32_t* key_begin, const int32_t* key_end, cudaStream_t stream);
 
 /*
+ * fattn_fwd_paged_shaped_workspace_size — bytes of scratch that num_splits > 1 needs:
+ * the partials lse [total_q, Hq, S] and O [total_q, Hq, S, d], fp32, each region 256-byte
+ * aligned. Returns 0 for num_splits <= 1 or non-positive arguments.
+ */
+size_t fattn_fwd_paged_shaped_workspace_size(int total_q, int Hq, int d, int num_splits);
+
+/*
  * fattn_fwd_paged_shaped — query chunks over the paged cache: fattn_fwd_paged with
  * shaped scores; the position of a chunk's query i is i + seqlens_k[b] - Lq_b.
  * Pages before token 128 floor(t / 128), t the first token that any row of the
  * chunk sees, are not read, nor are their table entries.
+ * num_splits = S >= 1: with few query tiles and long contexts the work is split along
+ *   the keys: every 128-row query tile's K/V tiles are cut into S runs, worked on
+ *   independently and joined with the online-softmax rule by a second launch. workspace: DEVICE
+ *   scratch of fattn_fwd_paged_shaped_workspace_size bytes, 256-byte aligned, contents ignored
+ *   (S = 1: none, NULL). INVALID_ARG for S < 1, WORKSPACE for a missing, small or misaligned one.
  */
 fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
                                     const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B,
                                     int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
                                     int total_q, int max_seqlen_q, int causal, float scale, float softcap,
                                     const float* slopes, int window, const int32_t* key_begin, const int32_t* key_end,
-                                    cudaStream_t stream);
+                                    int num_splits, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * fattn_bwd_shaped_workspace_size — bytes of scratch fattn_bwd_shaped needs: fattn_bwd's

@@ -104,7 +104,7 @@ def _calls(lib, kw):
     yield lib.fattn_fwd_shaped(g("q", A), A, A, A, None, g("B", 2), g("Hq", 4), 2, g("N", 300), g("d", 128), 1, sc, cap,
                                sl, win, kb, ke, None)
     yield lib.fattn_fwd_paged_shaped(g("q", A), A, A, A, A, A, A, None, g("B", 2), g("Hq", 4), 2, g("d", 128), 16, 8, 64,
-                                     100, g("N", 300), 1, sc, cap, sl, win, kb, ke, None)
+                                     100, g("N", 300), 1, sc, cap, sl, win, kb, ke, g("S", 1), g("ws", None), g("wsb", 0), None)
     yield lib.fattn_bwd_shaped(g("q", A), A, A, A, A, A, A, A, A, g("B", 2), g("Hq", 4), 2, g("N", 300), g("d", 128), 1,
                                sc, cap, sl, win, kb, ke, A, 1 << 20, None)
     if "kb" not in kw and "ke" not in kw and "N" not in kw and "B" not in kw:
@@ -128,6 +128,20 @@ def test_shaped_calls_limits_and_empty(lib):
                                     size, None) == F.FATTN_ERR_WORKSPACE
     assert lib.fattn_fwd_shaped(A, A, A, A, None, 1 << 15, 1 << 10, 1, 1 << 15, 64, 1, 0.1, 0.0, None, 0, None, None,
                                 None) == F.FATTN_ERR_UNSUPPORTED
+
+
+def test_chunk_splits(lib):
+    paged = lambda **kw: list(_calls(lib, kw))[1]
+    need = lib.fattn_fwd_paged_shaped_workspace_size(100, 4, 128, 3)
+    assert need == -(-100 * 4 * 3 * 4 // 256) * 256 + 100 * 4 * 3 * 128 * 4
+    assert lib.fattn_fwd_paged_shaped_workspace_size(100, 4, 128, 1) == 0
+    assert paged(S=0) == F.FATTN_ERR_INVALID_ARG and paged(S=-1) == F.FATTN_ERR_INVALID_ARG
+    for ws, size in ((None, need), (A, need - 1), (A + 16, need)):
+        assert paged(S=3, ws=ws, wsb=size) == F.FATTN_ERR_WORKSPACE
+    for case, S in (((4, 32, 128, 4096, 100000), 1), ((3, 16, 64, 517, 9000), 1), ((1, 8, 128, 16, 32768), 16),
+                    ((2, 16, 128, 512, 4096), 2), ((1, 8, 128, 2048, 16384), 2), ((1, 8, 128, 16, 100), 1),
+                    ((0, 8, 128, 16, 900), 1), ((1, 1, 64, 1, 1), 1)):
+        assert F.choose_chunk_splits(*case, 152) == S, case
 
 
 def test_document_ranges():

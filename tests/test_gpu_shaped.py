@@ -209,15 +209,52 @@ def test_paged_chunks(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window, ranged):
         # pages before the first visible tile of 128 are not read: their entries may be anything
         table[b, :(max(int(lo.min()), 0) // 128) * 128 // P] = -5
     dev = lambda t: None if t is None else t.cuda()
-    o = torch.full((T + pad, Hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
-    lse = torch.full((Hq, T + pad), 3.0, device="cuda")
-    fa.fwd_paged_shaped(dev(q), dev(kc), dev(vc), dev(table), torch.tensor(lk, dtype=torch.int32).cuda(),
-                        torch.from_numpy(cu).int().cuda(), max(lq), causal=causal, scale=0.15, softcap=cap, slopes=dev(slopes),
-                        window=window, key_begin=dev(begin), key_end=dev(end), out=o, lse=lse)
+    # S runs of every tile's keys: their join adds a few fp32 roundings (2^-24 each), inside the scores' allowance;
+    # S = 16 leaves most runs of the short contexts empty
+    for S in (1, None, 3, 16):
+        o = torch.full((T + pad, Hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((Hq, T + pad), 3.0, device="cuda")
+        fa.fwd_paged_shaped(dev(q), dev(kc), dev(vc), dev(table), torch.tensor(lk, dtype=torch.int32).cuda(),
+                            torch.from_numpy(cu).int().cuda(), max(lq), causal=causal, scale=0.15, softcap=cap,
+                            slopes=dev(slopes), window=window, key_begin=dev(begin), key_end=dev(end), out=o, lse=lse,
+                            num_splits=S)
+        assert fa.debug_read_status() == 0
+        for b in range(B):
+            check_fwd(o[cu[b]:cu[b + 1]], lse[:, cu[b]:cu[b + 1]], want[b], f"chunk {b}, {S} runs")
+        assert bool((o[T:] == 3).all()) and bool((lse[:, T:] == 3).all())  # rows behind the last chunk
+
+
+def test_split_chunk_keeps_nan_rows_and_repeats():
+    """A NaN query row stays NaN through the join, the others are untouched by it, and a second run (and a replay
+    of a captured one, over the previous run's partials) gives the same bits."""
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(4)
+    kc, vc = (torch.randn(40, 64, 2, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(300, 4, 128, generator=g).to(torch.bfloat16).cuda()
+    table = torch.randperm(40, generator=g).int().reshape(1, 40).cuda()
+    ws = torch.full((fa.fwd_paged_shaped_workspace_size(300, 4, 128, 5),), 255, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(4, 300, device="cuda")
+    args = (q, kc, vc, table, torch.tensor([2500], dtype=torch.int32).cuda(), torch.tensor([0, 300], dtype=torch.int32).cuda(), 300)
+    run = lambda: fa.fwd_paged_shaped(*args, window=900, softcap=20.0, num_splits=5, workspace=ws, out=o, lse=lse)
+    run()
+    clean = o.clone(), lse.clone()
+    q[17, 1] = float("nan")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    graph.replay()
+    assert bool(o[17, 1].isnan().all()) and bool(lse[1, 17].isnan())
+    keep = torch.ones(300, 4, dtype=torch.bool, device="cuda")
+    keep[17, 1] = False
+    # (a warp rescales its rows together, so others may round elsewhere: P and O by 2^-8 each, in both results)
+    assert float((o.float() - clean[0].float())[keep].abs().max()) <= 4 * H * float(vc.float().abs().max())
+    assert float((lse - clean[1]).T[keep].abs().max()) <= 4 * H
+    q[17, 1] = 0.5
+    graph.replay()
+    again = o.clone(), lse.clone()
+    graph.replay()
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1]) and bool(torch.isfinite(o).all())
     assert fa.debug_read_status() == 0
-    for b in range(B):
-        check_fwd(o[cu[b]:cu[b + 1]], lse[:, cu[b]:cu[b + 1]], want[b], f"chunk {b}")
-    assert bool((o[T:] == 3).all()) and bool((lse[:, T:] == 3).all())  # rows behind the last chunk
 
 
 @pytest.mark.parametrize("P,Hq,Hkv,d,lens,S,cap,sl,window", [
