@@ -8,7 +8,7 @@
 // heads of that KV head's GQA group (up to 16), so each K/V byte is read once,
 // and an empty split costs one atomic instead of a thread block. Each of the
 // 4 warps streams its own 16-token chunks through a 2-stage cp.async pipeline
-// (16-byte copies, L1 bypassed; three CTAs per SM at d = 128), finds each token's page
+// (16-byte copies, L1 bypassed; two CTAs per SM at d = 128, set by registers), finds each token's page
 // through the block table, and runs the two small products on the tensor
 // cores with mma.sync (S = Q K^T with the group's heads as the 16 rows,
 // O += P V with P kept in registers). Each warp keeps its own running (m, l, O)
@@ -350,11 +350,13 @@ __device__ __forceinline__ void merge_group(const DecodeParams& p, int b, int h0
   }
 }
 
-// (Held to the registers of three CTAs per SM, which is what shared memory admits at d = 128: left alone the
-// compiler takes up to 246, two CTAs, and 199k context tokens of 8 KV heads take 184 us in 8 splits instead of
-// 152, with a cap 195 instead of 150.)
+// CTAs per SM: the plain kernel takes the registers it wants (up to 246, two CTAs at d = 128): a CTA streams 25 %
+// faster, which wins while there are about as many items as CTAs (149k context tokens in 16 splits 102 us, with
+// three CTAs 118). The shaped one, whose chunks take longer, is held to the registers of three, what shared memory
+// admits at d = 128: capped, 199k context tokens of 8 KV heads take 150 us in 8 splits and 155 in 16 (two CTAs 195
+// and 162), one of 131k tokens 110 in 38 splits (109).
 template <int D, bool kPage16, bool kShaped>
-__global__ void __launch_bounds__(kWarps * 32, 3) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_item, s_last;
   const int G = p.Hq / p.Hkv;
