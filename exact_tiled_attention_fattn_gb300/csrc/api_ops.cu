@@ -86,13 +86,15 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
   return launch_rope(p, true, interleaved != 0, true, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-// A score shape's own checks; fills *out. `scale` is the call's.
+// A score shape's own checks; fills *out. `scale` is the call's, `keys` the most that a sequence has: a window of that
+// many hides nothing, and the kernels' sums of positions and windows stay small without it.
 static fattn_status check_shape(float scale, float softcap, const float* slopes, int window, const int32_t* key_begin,
-                                const int32_t* key_end, ScoreShape* out) {
+                                const int32_t* key_end, long long keys, ScoreShape* out) {
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return FATTN_ERR_INVALID_ARG;
   // the cap's argument 2 log2(e) scale / softcap must be a number
   if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
   if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
+  if (window >= keys) window = 0;
   *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, -1.f};
   out->sl2 = scale * 1.4426950408889634f;
   out->cap2 = softcap * 1.4426950408889634f;
@@ -125,7 +127,7 @@ extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const voi
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(lse, 4))
     return FATTN_ERR_INVALID_ARG;
   PrefillParams p{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &p.shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, N, &p.shape);
   if (st != FATTN_OK) return st;
   if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
   const long long rows = (long long)B * N;
@@ -165,7 +167,8 @@ extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache
                                                const int32_t* key_end, int num_splits, void* workspace,
                                                size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end,
+                                      (long long)max_pages_per_seq * page_size, &shape);
   if (st != FATTN_OK) return st;
   if (num_splits < 1) return FATTN_ERR_INVALID_ARG;
   return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
@@ -186,7 +189,7 @@ extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const voi
                                          const int32_t* key_begin, const int32_t* key_end, void* workspace,
                                          size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, &shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, N, &shape);
   if (st != FATTN_OK) return st;
   return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, &shape, workspace,
                   workspace_bytes, stream);
@@ -199,12 +202,12 @@ extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kca
                                                   const float* slopes, int window, void* workspace,
                                                   size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, nullptr, nullptr, &shape);
+  const fattn_status st =
+      check_shape(scale, softcap, slopes, window, nullptr, nullptr, (long long)max_pages_per_seq * page_size, &shape);
   if (st != FATTN_OK) return st;
   return decode_paged_impl(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
                            max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
 }
-
 
 extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const int32_t* block_table,
                                                 const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const float* lse,
@@ -217,7 +220,8 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
       max_pages_per_seq <= 0 || num_pages <= 0 || lse_head < 0 || lse_row < 0)
     return FATTN_ERR_INVALID_ARG;
   KeyWeightsParams p{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, nullptr, nullptr, &p.shape);
+  const fattn_status st =
+      check_shape(scale, softcap, slopes, window, nullptr, nullptr, (long long)max_pages_per_seq * page_size, &p.shape);
   if (st != FATTN_OK) return st;
   if (Hq % Hkv != 0 || !std::isfinite(decay)) return FATTN_ERR_INVALID_ARG;
   if (B == 0) return FATTN_OK;
@@ -234,7 +238,7 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
   p.q = q; p.kcache = kcache; p.block_table = block_table; p.seqlens_k = seqlens_k; p.cu_seqlens = cu_seqlens_q;
   p.lse = lse; p.lse_head = lse_head; p.lse_row = lse_row; p.w_in = weights_in; p.w_out = weights_out;
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages = max_pages_per_seq;
-  p.num_pages = num_pages; p.total_q = total_q;
+  p.num_pages = num_pages; p.total_q = total_q; p.max_q = max_seqlen_q;
   p.causal = causal ? 1 : 0; p.scale = scale; p.decay = decay;
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;

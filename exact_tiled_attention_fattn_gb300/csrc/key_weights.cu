@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
   const int key0 = blockIdx.x / p.Hkv * kKeys;
   const int cap = p.max_pages * p.page_size;
   const int q0 = __ldg(p.cu_seqlens + b), q1 = __ldg(p.cu_seqlens + b + 1), m = q1 - q0;
-  if (n < 0 || n > cap || q0 < 0 || m < 0 || q1 > p.total_q || m > n) {
+  if (n < 0 || n > cap || q0 < 0 || m < 0 || q1 > p.total_q || m > n || m > p.max_q) {
     if (key0 == 0 && hkv == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
     return;  // the sequence is skipped
   }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
   if (p.causal) i0 = max(0, key0 - off);
   if (p.shape.window > 0) {
     i1 = (int)min((long long)m, (long long)key0 + nkeys - 1 + p.shape.window - off);
-    if (!p.causal) i0 = max(0, key0 - off - p.shape.window + 1);
+    if (!p.causal) i0 = (int)max(0ll, (long long)key0 - off - p.shape.window + 1);
   }
   const long long u0 = (long long)i0 * G, u1 = (long long)max(i0, i1) * G;
   const int steps = (int)((u1 - u0 + kQRows - 1) / kQRows);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
   const int cap = p.max_pages * p.page_size, G = p.Hq / p.Hkv;
   const int n = __ldg(p.seqlens_k + b);
   const int q0 = __ldg(p.cu_seqlens + b), q1 = __ldg(p.cu_seqlens + b + 1), m = q1 - q0;
-  if (n < 0 || n > cap || q0 < 0 || m < 0 || q1 > p.total_q || m > n || (long long)m * G > 8 * NT) {
+  if (n < 0 || n > cap || q0 < 0 || m < 0 || q1 > p.total_q || m > n || m > p.max_q) {
     if (key0 == 0 && hkv == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
     return;  // the sequence is skipped
   }

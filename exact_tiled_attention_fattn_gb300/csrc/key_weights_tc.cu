@@ -112,7 +112,7 @@ __device__ __forceinline__ KwItem kw_item(const KeyWeightsParams& p, int it, int
   x.q0 = __ldg(p.cu_seqlens + x.b);
   const int q1 = __ldg(p.cu_seqlens + x.b + 1);
   x.m = q1 - x.q0;
-  x.valid = x.n >= 0 && x.n <= p.max_pages * p.page_size && x.q0 >= 0 && x.m >= 0 && q1 <= p.total_q && x.m <= x.n;
+  x.valid = x.n >= 0 && x.n <= p.max_pages * p.page_size && x.q0 >= 0 && x.m >= 0 && q1 <= p.total_q && x.m <= x.n && x.m <= p.max_q;
   x.off = x.n - x.m;
   x.i0 = x.steps = x.f0 = x.e0 = x.f1 = x.e1 = 0;
   if (!x.valid || x.key0 >= x.n) return x;
@@ -125,7 +125,7 @@ __device__ __forceinline__ KwItem kw_item(const KeyWeightsParams& p, int it, int
     if (p.causal) lo = max(0, a - x.off);
     if (p.shape.window > 0) {
       e = min(e, (long long)last + p.shape.window - x.off);
-      if (!p.causal) lo = max(0, a - x.off - p.shape.window + 1);
+      if (!p.causal) lo = (int)max(0ll, (long long)a - x.off - p.shape.window + 1);
     }
     hi = (int)max(e, (long long)lo);
   };
@@ -450,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = x.key0 + t * BT + r;
         const int first = x.i0 + s * per + x.off;              // position of column 0
         int va = 0, vb = min(per, x.m - x.i0 - s * per) * G;
-        if (p.causal) va = max(va, min(key - first, per) * G);
+        if (p.causal) va = min(max(key - first, 0), per) * G;
         if (p.shape.window > 0) {
           const long long hi = (long long)key + p.shape.window - first;
           if (hi < per) vb = min(vb, (int)max(hi, 0ll) * G);
-          if (!p.causal) va = max(va, (int)min((long long)key - p.shape.window + 1 - first, (long long)per) * G);
+          if (!p.causal) va = (int)min(max((long long)key - p.shape.window + 1 - first, 0ll), (long long)per) * G;
         }
         const uint32_t vec = sb + Lay::kOffVec + buf * 2 * BT * 4;
         const float w = sum_columns<kShape>(p, s_base + buf * BT, vec, vec + BT * 4, sb + Lay::kOffCol, (float)(first - key),

@@ -45,6 +45,7 @@ struct KeyWeightsParams {
   const float* w_in;          // [B, Hkv, max_pages * page_size] or nullptr
   float* w_out;               // likewise; may be w_in
   int B, Hq, Hkv, d, page_size, max_pages, num_pages, total_q;
+  int max_q;                  // queries of a sequence at most
   int causal;
   float scale, decay;
   ScoreShape shape;           // no key ranges

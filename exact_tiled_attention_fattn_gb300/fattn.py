@@ -51,7 +51,7 @@ SIGNATURES = {
 }
 
 # Every entry point declared in include/fattn_ops.h
-_ll, _d = ctypes.c_longlong, ctypes.c_double
+_ll = ctypes.c_longlong
 SIGNATURES_OPS = {
     "fattn_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _ll, _ll,
                         _i, _i, _f, _i, _vp]),
@@ -530,6 +530,9 @@ def debug_set_wait_limit(limit_ns: int = 0, stall: bool = False) -> None:
 
 
 # ------------------------------------------------------------------ rotary positions
+_INT_MAX = 2 ** 31 - 1
+
+
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
                      original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
     """(inv_freq float64 [rotary_dim / 2], amplitude) for ``rope``: angle per position of
@@ -631,6 +634,8 @@ def rope(q, k=None, inv_freq=None, positions=None, interleaved: bool = False, am
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
     rows = math.prod(lead)
+    if rows > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 rows")
     Hq, Hk = q.shape[-2], 0 if k is None else k.shape[-2]
     strides = [*_row_strides(q, "q")]
     if out_q is None:
@@ -783,7 +788,7 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
     if lse is None and want_lse:
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     st = lib.fattn_fwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
-                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
+                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX),
                               _ptr(key_begin), _ptr(key_end), _stream_handle(stream))
     _check("fattn_fwd_shaped", st)
     return out, lse
@@ -861,7 +866,7 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
     st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
                                     _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                     block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
-                                    float(scale), float(softcap), _ptr(slopes), int(window), _ptr(key_begin),
+                                    float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX), _ptr(key_begin),
                                     _ptr(key_end), int(num_splits), _ptr(workspace),
                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
                                     _stream_handle(stream))
@@ -904,7 +909,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
         workspace = torch.empty(max(bwd_shaped_workspace_size(B, Hq, N), 1), dtype=torch.uint8, device=q.device)
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
-                              int(window), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
+                              min(int(window), _INT_MAX), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check("fattn_bwd_shaped", st)
     return dq, dk, dv
@@ -944,7 +949,7 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
     st = lib.fattn_decode_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
                                        num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                        block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
-                                       int(window), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       min(int(window), _INT_MAX), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream_handle(stream))
     _check("fattn_decode_paged_shaped", st)
     return out, lse
@@ -986,7 +991,7 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
     st = lib.fattn_key_weights_paged(_ptr(q), _ptr(kcache), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q),
                                      _ptr(lse), lse.stride(0), lse.stride(1), _ptr(weights), _ptr(out), B, Hq, Hkv, d,
                                      page_size, block_table.shape[1], num_pages, Tq, int(max_seqlen_q),
-                                     1 if causal else 0, float(scale), float(softcap), _ptr(slopes), int(window),
+                                     1 if causal else 0, float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX),
                                      float(decay), _stream_handle(stream))
     _check("fattn_key_weights_paged", st)
     return out

@@ -330,3 +330,27 @@ def test_key_weights_refusals():
                 dict(lse=lse.cpu())):
         with pytest.raises((ValueError, TypeError, fa.FattnError)):
             call(**bad)
+
+
+@pytest.mark.parametrize("P,Hq,lq", [(16, 4, 3), (16, 8, 40), (16, 128, 1), (3, 4, 40)])   # streaming, tensor cores, one query a step, mma
+def test_key_weights_windows_of_any_size(P, Hq, lq):
+    """A window that holds every key is no window, whatever its size, to the bit; and one query too many for
+    max_seqlen_q leaves its sequence's weights alone."""
+    fa = need_gpu()
+    kc, _, table, _, g = pool(5, [300, 90], P, 1, 64, fill=0)
+    q = torch.randn(2 * lq, Hq, 64, generator=g).to(torch.bfloat16).cuda()
+    lse = torch.full((Hq, 2 * lq), 3.0, device="cuda")
+    args = (q, kc.cuda(), table.cuda(), i32([300, 90]), i32([0, lq, 2 * lq]))
+    for causal in (True, False):
+        plain = fa.key_weights_paged(*args, lq, lse, causal=causal)
+        for window in (table.shape[1] * P, 10 ** 9, 2 ** 31 - 1, 2 ** 40):
+            assert torch.equal(fa.key_weights_paged(*args, lq, lse, causal=causal, window=window), plain), window
+        near = fa.key_weights_paged(*args, lq, lse, causal=causal, window=299)
+        # the first sequence's last query alone no longer sees key 0
+        assert torch.equal(near[:, :, 1:], plain[:, :, 1:]) and bool((near[0, :, 0] < plain[0, :, 0]).all())
+        assert torch.equal(near[1], plain[1])
+    assert fa.debug_read_status() == 0
+    out = torch.full((2, 1, table.shape[1] * P), -2.0, device="cuda")
+    fa.key_weights_paged(q, kc.cuda(), table.cuda(), i32([300, 90]), i32([0, lq + 1, 2 * lq]), lq, lse, out=out)
+    assert fa.debug_read_status() == fa.FATTN_ERR_DEVICE_CHECK
+    assert bool((out[0] == -2).all()) and (bool((out[1, :, :90] > 0).all()) if lq > 1 else bool((out[1] == 0).all()))

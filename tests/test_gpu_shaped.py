@@ -353,3 +353,25 @@ def test_refusals():
             fa.bwd_shaped(q, k, v, q, torch.zeros(1, 4, 40, device="cuda"), do, **bad)
     with pytest.raises(fa.FattnError):
         fa.fwd_shaped(torch.zeros(1, 4, 2, 96, device="cuda", dtype=torch.bfloat16), *(torch.zeros(1, 4, 2, 96, device="cuda", dtype=torch.bfloat16),) * 2)
+
+
+def test_windows_of_any_size():
+    """A window that holds every key is no window, whatever its size, to the bit."""
+    fa = need_gpu()
+    q, k, v, do = (x.cuda() for x in make(11, 2, 300, 4, 2, 64))
+    g = torch.Generator().manual_seed(2)
+    kc, vc = (torch.randn(40, 16, 2, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    table = torch.randperm(40, generator=g).int().reshape(2, 20).cuda()
+    lens, cu = torch.tensor([300, 77], dtype=torch.int32).cuda(), torch.tensor([0, 60, 137], dtype=torch.int32).cuda()
+    qc, qd = q[0, :137].contiguous(), q[0, :2].contiguous()
+    for causal in (True, False):
+        kw = dict(causal=causal, softcap=9.0)
+        o, lse = fa.fwd_shaped(q, k, v, **kw)
+        calls = [lambda w: fa.fwd_shaped(q, k, v, window=w, **kw), lambda w: fa.bwd_shaped(q, k, v, o, lse, do, window=w, **kw),
+                 lambda w: fa.fwd_paged_shaped(qc, kc, vc, table, lens, cu, 77, window=w, num_splits=2, **kw),
+                 lambda w: fa.decode_paged_shaped(qd, kc, vc, table, lens, 2, softcap=9.0, window=w)]
+        for call in calls:
+            plain = call(0)
+            for w in (320, 10 ** 9, 2 ** 31 - 1, 2 ** 40):
+                assert all(torch.equal(x, y) for x, y in zip(call(w), plain)), w
+    assert fa.debug_read_status() == 0
