@@ -354,3 +354,40 @@ def test_key_weights_windows_of_any_size(P, Hq, lq):
     fa.key_weights_paged(q, kc.cuda(), table.cuda(), i32([300, 90]), i32([0, lq + 1, 2 * lq]), lq, lse, out=out)
     assert fa.debug_read_status() == fa.FATTN_ERR_DEVICE_CHECK
     assert bool((out[0] == -2).all()) and (bool((out[1, :, :90] > 0).all()) if lq > 1 else bool((out[1] == 0).all()))
+
+
+@pytest.mark.parametrize("P,lq", [(16, 1), (16, 40), (8, 40)])
+def test_pages_past_32_bits(P, lq):
+    """A cache of more than 2^31 elements: the serving step, weights and eviction on its last pages give what they
+    give on the first ones."""
+    fa = need_gpu()
+    Hq, Hkv, d, n = 8, 8, 128, 150
+    pages = 2 ** 31 // (P * Hkv * d) + 2 * (-(-n // P)) + 2
+    per = -(-n // P)
+    kc, vc = (torch.empty(pages, P, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(6)
+    old = [torch.randn(per, P, Hkv, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    q, k, v = (torch.randn(lq, h, d, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+    f = fa.rope_frequencies(d)[0].cuda()
+    lens, cu, got = i32([n]), i32([0, lq]), []
+    assert (pages - per) * P * Hkv * d > 2 ** 31
+    for base in (0, pages - per):
+        table, dst = (i32([list(range(x, x + per))]) for x in (base, base - per if base else per))
+        kc[base:base + per], vc[base:base + per] = old
+        qr = fa.rope_append_paged(q, k, v, kc, vc, table, lens, cu, f)
+        if lq == 1:
+            o, lse = fa.decode_paged_shaped(qr, kc, vc, table, lens, 2, softcap=20.0, window=100)
+            lse = lse.t()
+        elif P >= 16:
+            o, lse = fa.fwd_paged_shaped(qr, kc, vc, table, lens, cu, lq, softcap=20.0, window=100)
+        else:
+            o, lse = qr, torch.full((Hq, lq), 5.0, device="cuda")
+        w = fa.key_weights_paged(qr, kc, table, lens, cu, lq, lse, softcap=20.0, window=100)
+        m, w2, kept = fa.evict_paged(kc, vc, table, lens, w, 70, recent=20, first=3, dst_table=dst)
+        x = dst[0].long()
+        moved = [c[x].reshape(-1, Hkv, d)[:70].clone() for c in (kc, vc)]
+        fa.evict_paged(kc, vc, table, lens, w, 70, recent=20, first=3)
+        got.append((o, lse.contiguous(), w, m, w2, kept, *moved, *(c[base:base + per].clone() for c in (kc, vc))))
+        assert fa.debug_read_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(got[0][8].reshape(-1, Hkv, d)[:70], got[0][6])     # in place as into other pages
