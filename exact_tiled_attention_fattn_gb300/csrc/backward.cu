@@ -1104,8 +1104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ per-row vectors
     // For this CTA's items in order, D and -lse log2(e) of the tile's 128 rows into the
-    // workspace (warp 2 rows 0-63, warp 3 rows 64-127), at most two items ahead of the
-    // element-wise warps; they read the vectors back once the block count shows them
+    // workspace (warp 2 rows 0-63, warp 3 rows 64-127), at most three items ahead of the
+    // element-wise warps; they read the vectors back once the warp's count shows them
     // written, and the dK/dV pass (launched after this one) reads them all.
     if constexpr (kShaped) {
       if (warp == 3) write_key_ranges(p, blockIdx.x, gridDim.x, lane);

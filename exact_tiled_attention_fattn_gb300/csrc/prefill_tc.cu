@@ -45,6 +45,11 @@
 // both requested before the wait for the scores. FP8 variant (FlashAttention-3
 // row of "The FlashAttention family"): E4M3 Q, K and V (kind::f8f6f4 products,
 // V read in place as an MN-major operand), P rounded to E4M3 in shared memory.
+// Shaped variants (a tanh cap, a distance bias, windows and per-row key ranges; dense
+// or paged): a row's range is [lo, hi), both bounds monotone over the rows, so a Q
+// tile visits the key tiles between its first row's lo and its last row's hi, and masks only
+// at their edges. Paged, a tile's key tiles may be cut into runs, items of their own whose fp32 partials
+// prefill_merge_kernel joins: few query tiles over long contexts leave most SMs idle otherwise.
 //
 // P_X aliases S_X: S_X(j) is issued right after O_X += P_X(j-1) V by the same
 // thread, and tcgen05.mma operations issued by one thread execute in order, so
@@ -122,11 +127,12 @@ enum : int {
 };
 
 enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4 };
-// Shaped variants: kModeShaped plus what the scores get (key ranges and the window always) and
-// whether K/V come through a block table. One kernel for each, as the softmax loop of the one
+// Shaped variants: kModeShaped plus what the scores get (key ranges and the window always),
+// whether K/V come through a block table, and then whether key tiles are cut into runs (the
+// epilogue's second form costs the others up to 25 %, in registers). One kernel for each, as the softmax loop of the one
 // with everything under run-time switches is 6 % slower without a cap or bias: its unrolled
 // forms no longer stay in the instruction cache.
-enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4 };
+enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4, kShapeSplit = 16 };
 __host__ __device__ constexpr bool mode_shaped(int m) { return m >= kModeShaped; }
 
 template <int D, int kMode>
@@ -181,7 +187,7 @@ struct Item {
   // shaped variant: tile t visits K/V tiles [top[t] - n[t], top[t]); the item's steps run from
   // tile jtop - 1 down to jbot, over both tiles' ranges (n = 0 as well where no row sees a key)
   int top[2], jtop, jbot;
-  int split, all_lo[2], all_top[2];  // the run of key tiles that the item takes, and tile t's whole range
+  int split;  // the run of key tiles that the item takes
   bool valid;
 };
 
@@ -202,11 +208,11 @@ struct Schedule {
   int pairs, heads, group, total;
 };
 
-template <bool kShaped>
+template <bool kSplits>
 __device__ __forceinline__ Schedule make_schedule(const PrefillParams& p) {
   Schedule s;
   s.pairs = (p.N + kRowsPerItem - 1) / kRowsPerItem;
-  if constexpr (kShaped) s.pairs *= p.splits;   // (pair, split): pair * splits + split
+  if constexpr (kSplits) s.pairs *= p.splits;   // (pair, split): pair * splits + split
   s.heads = p.B * p.Hq;
   const int G = p.Hq / p.Hkv;
   const int rounds = s.pairs >= 32 ? 4 : 2;                 // grid rounds per group
@@ -225,7 +231,7 @@ __device__ __forceinline__ int item_index(const Schedule& s, int k) {
   return idx < s.total ? idx : -1;
 }
 
-template <bool kShaped>
+template <bool kShaped, bool kSplits>
 __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedule& s, int it) {
   Item x;
   x.top[0] = x.top[1] = x.jtop = x.jbot = 0;
@@ -237,7 +243,7 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
   const int bh = g * s.group + (rem - rank * gh);
   int pair = s.pairs - 1 - rank;
   x.split = 0;
-  if constexpr (kShaped) {
+  if constexpr (kSplits) {
     x.split = pair % p.splits;
     pair /= p.splits;
   }
@@ -269,7 +275,7 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
   const bool has_b = x.base + BM < x.L;
   if constexpr (kShaped) {
     // the bounds are monotone: a tile's first row has its lowest key, its last row its highest
-    x.n[0] = x.n[1] = x.all_lo[0] = x.all_lo[1] = x.all_top[0] = x.all_top[1] = 0;
+    x.n[0] = x.n[1] = 0;
     x.jbot = 1 << 30;
     if (x.valid) {
 #pragma unroll
@@ -280,10 +286,12 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
         const int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
         if (lo < hi) {
           const int t0 = lo / BN, n = (hi + BN - 1) / BN - t0;
-          x.all_lo[t] = t0;
-          x.all_top[t] = t0 + n;
-          const int from = t0 + (int)((long long)n * x.split / p.splits);
-          x.top[t] = t0 + (int)((long long)n * (x.split + 1) / p.splits);
+          int from = t0;
+          x.top[t] = t0 + n;
+          if constexpr (kSplits) {
+            from = t0 + (int)((long long)n * x.split / p.splits);
+            x.top[t] = t0 + (int)((long long)n * (x.split + 1) / p.splits);
+          }
           x.n[t] = x.top[t] - from;
           if (x.n[t] > 0) {
             x.jtop = max(x.jtop, x.top[t]);
@@ -357,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kSparse = kMode == kModeSparse;  // fixed block mask, zero blocks skipped
   constexpr bool kPaged = kMode == kModePaged || (mode_shaped(kMode) && (kMode & kShapePaged));  // K/V through a block table
   constexpr bool kShaped = mode_shaped(kMode);    // window and key ranges
+  constexpr bool kSplits = kShaped && (kMode & kShapeSplit);  // a query tile's key tiles are cut into runs
   constexpr bool kCap = kShaped && (kMode & kShapeCap);    // and the scores' tanh cap
   constexpr bool kBias = kShaped && (kMode & kShapeBias);  // and distance bias
   constexpr bool kMasked = kMode == kModeMasked;  // additive bf16 mask M on the scores
@@ -403,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kOffHolder);
 
-  const Schedule sch = make_schedule<kShaped>(p);
+  const Schedule sch = make_schedule<kSplits>(p);
   const int G = p.Hq / p.Hkv;
 
   if (warp < 4) {
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0;; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item<kShaped>(p, sch, it);
+        const Item x = decode_item<kShaped, kSplits>(p, sch, it);
         if (!x.valid) continue;
         const int hkv = x.h / G;
         const int n = kShaped ? x.jtop - x.jbot : max(x.n[0], x.n[1]);
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item<kShaped>(p, sch, it);
+        const Item x = decode_item<kShaped, kSplits>(p, sch, it);
         if (!x.valid) continue;
         if constexpr (kSparse) {
           // walk the blocks either tile keeps: per block j, O_t += P_t(prev) V_prev for each tile
@@ -780,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0;; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item<kShaped>(p, sch, it);
+      const Item x = decode_item<kShaped, kSplits>(p, sch, it);
       if (!x.valid) continue;
       if (!warp_wait(bar(kBarMaskEmpty + nm % kMaskSlots), ((nm / kMaskSlots) & 1) ^ 1, abort, p.status, p.wait_ns)) break;
       uint32_t* w = reinterpret_cast<uint32_t*>(smem + Lay::kOffMask + (nm % kMaskSlots) * kMaskSlotBytes);
@@ -849,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item<kShaped>(p, sch, it);
+      const Item x = decode_item<kShaped, kSplits>(p, sch, it);
       if (!x.valid) continue;
       const uint32_t* mw = nullptr;
       // this tile's K/V tile count, selected rather than indexed (a run-time index into the
@@ -875,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nt == 0) {
         release_mask();
         if constexpr (kShaped) {  // no row of the tile sees a key: O = 0, lse = -inf
-          if (row < x.L && p.splits > 1) {  // an empty partial
+          if (kSplits && row < x.L) {  // an empty partial
             p.lse_part[((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split] = -CUDART_INF_F;
           } else if (row < x.L) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
@@ -900,8 +909,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         lo = shape_lo(p.shape, (long long)x.row0 + rc, rc + x.off);
         lim = shape_hi(p.shape, (long long)x.row0 + rc, rc + x.off, x.Lk, p.causal);
         // ranges that are not monotone: the row's keys are not all among its tile's
-        if (lo < lim && (lo < (t ? x.all_lo[1] : x.all_lo[0]) * BN || lim > (t ? x.all_top[1] : x.all_top[0]) * BN))
+        if constexpr (kSplits) {
+          const int r0 = x.base + t * BM, r1 = min(r0 + BM, x.L) - 1;
+          if (lo < lim && (lo < shape_lo(p.shape, (long long)x.row0 + r0, r0 + x.off) / BN * BN ||
+                           lim > (shape_hi(p.shape, (long long)x.row0 + r1, r1 + x.off, x.Lk, p.causal) + BN - 1) / BN * BN))
+            record_status(p.status, kStatusDeviceCheck);
+        } else if (lo < lim && (lo < (kv_hi - nt) * BN || lim > kv_hi * BN)) {
           record_status(p.status, kStatusDeviceCheck);
+        }
         if (kBias && p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
       } else {
         lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;
@@ -1401,7 +1416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a row the mask left with no key: O = 0, lse = -inf
       const float inv = ((kMasked || kShaped) && l == 0.f) ? 0.f : (kFp8 ? p.v_descale : 1.f) / l;
       const int wrow0 = x.base + t * BM + q4 * 32;  // this warp's first row
-      if (kShaped && kPaged && p.splits > 1) {
+      if constexpr (kSplits) {
         // a partial: O / l in fp32, and the logsumexp of the run's keys
         float* orow = p.o_part + (((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split) * D;
 #pragma unroll
@@ -1507,8 +1522,9 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtens
 template <int D, int kShape>
 cudaError_t launch_shaped_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& to, int num_sms, cudaStream_t stream) {
-  return p.block_table ? launch_t<D, kModeShaped + kShape + kShapePaged>(p, tq, tk, tv, to, num_sms, stream)
-                       : launch_t<D, kModeShaped + kShape>(p, tq, tk, tv, to, num_sms, stream);
+  if (!p.block_table) return launch_t<D, kModeShaped + kShape>(p, tq, tk, tv, to, num_sms, stream);
+  return p.splits > 1 ? launch_t<D, kModeShaped + kShape + kShapePaged + kShapeSplit>(p, tq, tk, tv, to, num_sms, stream)
+                      : launch_t<D, kModeShaped + kShape + kShapePaged>(p, tq, tk, tv, to, num_sms, stream);
 }
 
 template <int D>

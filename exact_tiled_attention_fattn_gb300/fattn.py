@@ -804,8 +804,8 @@ def choose_chunk_splits(batch: int, Hq: int, d: int, max_seqlen_q: int, max_cont
     over 128 keys (about 1.7 us): rounds of items over the SMs, each of its run's steps and 2 more, and for S > 1 the
     joining launch (4) with the fp32 partials' way through memory (1 per million elements).
 
-    Measured, S = 1 against the choice: 16 queries over 32768 keys, 8 heads 465 -> 55 us (S 16); 256 over 32768, 32 heads
-    657 -> 186 (4); 2 x 512 over 4096, 16 heads 94 -> 69 (2); 3 x 517 over 9000, 16 heads stay at 1 (136; 2: 150)."""
+    Measured, S = 1 against the choice: 16 queries over 32768 keys, 8 heads 476 -> 51 us (S 16); 256 over 32768, 32 heads
+    673 -> 186 (4); 2 x 512 over 4096, 16 heads 74 -> 57 (2); 3 x 517 over 9000, 16 heads stay at 1 (135; 2: 147)."""
     items = batch * Hq * -(-max_seqlen_q // 256)
     if items <= 0:
         return 1
