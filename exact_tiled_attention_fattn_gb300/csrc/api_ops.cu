@@ -86,6 +86,17 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
   return launch_rope(p, true, interleaved != 0, true, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
+// The cap as a polynomial: tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) on |z| <= z_max, folded into powers of
+// u = z softcap / scale. Outside the range of scale / softcap where every folded coefficient is an ordinary
+// float the kernels do without.
+static void fold_cap(float scale, float softcap, const double (&c)[5], double z_max, ScoreShape* out) {
+  const double k = (double)scale / (softcap > 0.f ? softcap : 1.0);
+  if (!(softcap > 0.f && std::fabs(k) >= 5e-4 && std::fabs(k) <= 1e2 && softcap < 1e6f)) return;
+  double pw = k * softcap * 1.4426950408889634;
+  for (int i = 0; i < 5; ++i, pw *= k * k) out->poly[i] = make_float2((float)(c[i] * pw), (float)(c[i] * pw));
+  out->poly_limit = (float)(z_max / std::fabs(k));
+}
+
 // A score shape's own checks; fills *out. `scale` is the call's, `keys` the most that a sequence has: a window of that
 // many hides nothing, and the kernels' sums of positions and windows stay small without it.
 static fattn_status check_shape(float scale, float softcap, const float* slopes, int window, const int32_t* key_begin,
@@ -100,16 +111,10 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
   out->cap2 = softcap * 1.4426950408889634f;
   out->capk = softcap > 0.f ? 2.f * out->sl2 / softcap : 0.f;
   out->nicap2 = softcap > 0.f ? -1.f / (out->cap2 * out->cap2) : 0.f;
-  // tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) with an absolute error below 2.5e-7 on |z| <= 0.75 (minimax,
-  // by linear programming), folded into powers of u = z softcap / scale. Outside the range of
-  // scale / softcap where every folded coefficient is an ordinary float the kernels do without.
+  // the cap on |z| <= 0.75, with an absolute error below 2.5e-7 (minimax, by linear programming)
+  const double c[5] = {0.9999966, -0.33322031, 0.13220438, -0.04915907, 0.012229};
+  fold_cap(scale, softcap, c, 0.75, out);
   const double k = (double)scale / (softcap > 0.f ? softcap : 1.0);
-  if (softcap > 0.f && std::fabs(k) >= 5e-4 && std::fabs(k) <= 1e2 && softcap < 1e6f) {
-    const double c[5] = {0.9999966, -0.33322031, 0.13220438, -0.04915907, 0.012229};
-    double pw = k * softcap * 1.4426950408889634;
-    for (int i = 0; i < 5; ++i, pw *= k * k) out->poly[i] = make_float2((float)(c[i] * pw), (float)(c[i] * pw));
-    out->poly_limit = (float)(0.75 / std::fabs(k));
-  }
   // 2 log2(e) softcap tanh(k u) <= 96
   const double ratio = 48.0 / (1.4426950408889634 * softcap);
   if (softcap > 0.f && std::fabs(k) > 0.0)
@@ -223,6 +228,10 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
   const fattn_status st =
       check_shape(scale, softcap, slopes, window, nullptr, nullptr, (long long)max_pages_per_seq * page_size, &p.shape);
   if (st != FATTN_OK) return st;
+  // the weights stay in fp32: the cap within 1e-8 of tanh, on a shorter range (interpolation in Chebyshev nodes; the
+  // attention's P and dS are rounded to bf16)
+  const double c[5] = {0.9999999868, -0.3333306794, 0.133247505, -0.05298423883, 0.01713134443};
+  fold_cap(scale, softcap, c, 0.5, &p.shape);
   if (Hq % Hkv != 0 || !std::isfinite(decay)) return FATTN_ERR_INVALID_ARG;
   if (B == 0) return FATTN_OK;
   if (!kcache || !block_table || !seqlens_k || !cu_seqlens_q || !weights_out) return FATTN_ERR_INVALID_ARG;
