@@ -376,7 +376,7 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   const long long npad = ((long long)N + 127) / 128 * 128;
   if (rows > 0x7fffffffLL || (long long)B * Hq * npad > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
   const size_t vectors = fattn_bwd_workspace_size(B, Hq, N);
-  const size_t need = shape ? fattn_bwd_shaped_workspace_size(B, Hq, N) : vectors;
+  const size_t need = shape ? fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d) : vectors;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FATTN_ERR_WORKSPACE;
 
@@ -392,6 +392,8 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
     p.shaped = 1;
     p.shape = *shape;
     p.ws_keys = reinterpret_cast<int2*>(static_cast<char*>(workspace) + vectors);
+    if (bwd_per_head(p))
+      p.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + vectors + align256((size_t)B * npad * sizeof(int2)));
   }
   p.status = status_ptr(&err);
   if (err) return FATTN_ERR_CUDA;

@@ -181,11 +181,12 @@ extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache
                         workspace_bytes, stream);
 }
 
-extern "C" size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int N) {
+extern "C" size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int Hkv, int N, int d) {
   const size_t vectors = fattn_bwd_workspace_size(B, Hq, N);
-  if (vectors == 0) return 0;
+  if (vectors == 0 || Hkv <= 0 || d <= 0) return 0;
   const size_t npad = ((size_t)N + 127) / 128 * 128;
-  return vectors + ((size_t)B * npad * 8 + 255) / 256 * 256;
+  const size_t shares = bwd_shares(B, Hq, Hkv, N) ? 2 * (size_t)B * N * Hq * d * sizeof(float) : 0;
+  return vectors + ((size_t)B * npad * 8 + 255) / 256 * 256 + (shares + 255) / 256 * 256;
 }
 
 extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const void* v, const void* o, const float* lse,

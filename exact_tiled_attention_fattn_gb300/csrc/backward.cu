@@ -309,6 +309,23 @@ __device__ __forceinline__ void store_row(uint32_t t_col, float mul, __nv_bfloat
   }
 }
 
+// The same in fp32.
+template <int D>
+__device__ __forceinline__ void store_row_f32(uint32_t t_col, float mul, float* dst, bool live) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t u[32];
+    tmem_ld32(t_col + 32 * c, u);
+    if (live) {
+      float4* q = reinterpret_cast<float4*>(dst + 32 * c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        q[e] = make_float4(__uint_as_float(u[4 * e]) * mul, __uint_as_float(u[4 * e + 1]) * mul,
+                           __uint_as_float(u[4 * e + 2]) * mul, __uint_as_float(u[4 * e + 3]) * mul);
+    }
+  }
+}
+
 // dS = P o (dP - Dvec) over this warpgroup's 64 columns (pv[c] is column
 // 64 g + c), written as bf16 over the first 32 of them, 32 columns at a time:
 // pass q reads dP columns [32q, 32q + 32) and then writes packed columns
@@ -530,7 +547,9 @@ enum : int {
   kAccFull = 10, kAccEmpty = 11, kMmaDone = 12, kDvFull = 13
 };
 
-template <int D, int kShape>
+// kPerHead (shaped only): an item is a query head's share of dK and dV, written in fp32 to p.ws_part for
+// sum_heads_kernel to add over the group; else the group's heads follow one another in an item.
+template <int D, int kShape, bool kPerHead>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -574,14 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(small + Lay::kOffHolder);
 
   const int nt = (p.N + BT - 1) / BT;
-  const int G = p.Hq / p.Hkv;
-  const BwdSchedule sch = make_bwd_schedule(p.B * p.Hkv, nt, 1);
-  // item: (sequence, KV head, key tile j); rank 0 = j 0, the most query tiles under the causal rule
+  const int G = kPerHead ? 1 : p.Hq / p.Hkv, heads = kPerHead ? p.Hq : p.Hkv;
+  const BwdSchedule sch = make_bwd_schedule(p.B * heads, nt, 1);
+  // item: (sequence, KV head, or query head with kPerHead, key tile j); rank 0 = j 0, the most query tiles under the causal rule
   auto item = [&](int it, int& b, int& hkv, int& j) {
     int head;
     bwd_decode(sch, it, head, j);
-    b = head / p.Hkv;
-    hkv = head - b * p.Hkv;
+    b = head / heads;
+    hkv = head - b * heads;
   };
   // query tiles [i0, i0 + ni) of an item
   auto tiles = [&](int b, int j, int& i0, int& ni) {
@@ -604,8 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         item(it, b, hkv, j);
         if (!mbar_wait(bar(kKvEmpty), (nkv & 1) ^ 1, abort, p.status, p.wait_ns)) break;
         mbar_arrive_expect_tx(bar(kKvFull), 2 * Lay::kTile);
-        load_tile<D>(sb + Lay::kOffK, &tk, bar(kKvFull), hkv, b * p.N + j * BT, pol_kv);
-        load_tile<D>(sb + Lay::kOffV, &tv, bar(kKvFull), hkv, b * p.N + j * BT, pol_kv);
+        const int kv_head = kPerHead ? hkv / (p.Hq / p.Hkv) : hkv;
+        load_tile<D>(sb + Lay::kOffK, &tk, bar(kKvFull), kv_head, b * p.N + j * BT, pol_kv);
+        load_tile<D>(sb + Lay::kOffV, &tv, bar(kKvFull), kv_head, b * p.N + j * BT, pol_kv);
         ++nkv;
         int i0, ni;
         tiles(b, j, i0, ni);
@@ -849,17 +869,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int key = j * BT + r;
       const bool live = key < p.N;
-      const size_t off = (((size_t)b * p.N + (live ? key : 0)) * p.Hkv + hkv) * D + wg * (D / 2);
+      const size_t off = (((size_t)b * p.N + (live ? key : 0)) * heads + hkv) * D + wg * (D / 2);
       const int wkey0 = j * BT + q4 * 32;  // the warp's first key row
       const bool staged = Lay::kStoreTma && wkey0 + 32 <= p.N;
-      if (staged)
+      if constexpr (kPerHead)
+        store_row_f32<D / 2>(acc_col + wg * (D / 2), 1.f, p.ws_part + off, live);
+      else if (staged)
         stage_out(acc_col + wg * (D / 2), 1.f, &tdv, wg * (D / 2), hkv, b * p.N + wkey0);
       else
         store_row<D / 2>(acc_col + wg * (D / 2), 1.f, static_cast<__nv_bfloat16*>(p.dv) + off, live);
       if (!warp_wait(bar(kAccFull), nacc & 1, abort, p.status, p.wait_ns)) break;
       ++nacc;
       tc_fence_after();
-      if (staged)
+      if constexpr (kPerHead)
+        store_row_f32<D / 2>(acc_col + D + wg * (D / 2), p.scale, p.ws_part + (size_t)p.B * p.N * p.Hq * D + off, live);
+      else if (staged)
         stage_out(acc_col + D + wg * (D / 2), p.scale, &tdk, wg * (D / 2), hkv, b * p.N + wkey0);
       else
         store_row<D / 2>(acc_col + D + wg * (D / 2), p.scale, static_cast<__nv_bfloat16*>(p.dk) + off, live);
@@ -1261,6 +1285,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// dV (blockIdx.y 0) and dK (1) of the KV heads: the sums, in order, of their query heads' fp32 shares. A thread takes 4
+// columns of a (row, KV head); bound by the shares' bytes.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) sum_heads_kernel(const BwdParams p) {
+  const int lanes = p.d / 4, G = p.Hq / p.Hkv;
+  const long long at = (long long)blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;  // row * Hkv + KV head
+  if (at >= (long long)p.B * p.N * p.Hkv) return;
+  const int c = (threadIdx.x % lanes) * 4;
+  const float4* src = reinterpret_cast<const float4*>(p.ws_part + (blockIdx.y ? (size_t)p.B * p.N * p.Hq * p.d : 0) +
+                                                      (size_t)at * G * p.d + c);
+  float4 sum = __ldg(src);
+#pragma unroll 4
+  for (int g = 1; g < G; ++g) {
+    const float4 v = __ldg(src + (size_t)g * lanes);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  uint2 o;
+  o.x = pack_bf16x2(sum.x, sum.y);
+  o.y = pack_bf16x2(sum.z, sum.w);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(blockIdx.y ? p.dk : p.dv) + (size_t)at * p.d + c) = o;
+}
+
+template <int D, int kShape, bool kPerHead>
+cudaError_t launch_dkdv(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
+                        cudaStream_t stream) {
+  const int nt = (p.N + BT - 1) / BT;
+  auto kern = bwd_dkdv_kernel<D, kShape, kPerHead>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)p.B * (kPerHead ? p.Hq : p.Hkv) * nt;
+  const int grid = (int)std::min<long long>(items, num_sms);
+  kern<<<grid, kThreads, DkdvLayout<D>::kBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
+  e = cudaGetLastError();
+  if (!kPerHead || e != cudaSuccess) return e;
+  const int rows = kSumThreads / (D / 4);
+  sum_heads_kernel<<<dim3((unsigned)(((long long)p.B * p.N * p.Hkv + rows - 1) / rows), 2), kSumThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, int kShape>
 cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
@@ -1277,16 +1344,10 @@ cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtens
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  {
-    auto kern = bwd_dkdv_kernel<D, kShape>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    const long long items = (long long)p.B * p.Hkv * nt;
-    const int grid = (int)std::min<long long>(items, num_sms);
-    kern<<<grid, kThreads, DkdvLayout<D>::kBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
-    e = cudaGetLastError();
+  if constexpr (kShape != kPlain) {
+    if (p.ws_part) return launch_dkdv<D, kShape, true>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   }
-  return e;
+  return launch_dkdv<D, kShape, false>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
 }
 
 template <int D>

@@ -145,6 +145,7 @@ struct BwdParams {
   float* ws_nl2;              // [B * Hq, Npad]: -lse * log2(e), -inf past N
   float* ws_d;                // [B * Hq, Npad]: rowsum(dO o O), 0 past N
   int2* ws_keys;              // shaped: [B, Npad], the query rows [x, y) that see each key
+  float* ws_part;             // shaped, per query head: dV, then dK, [B * N, Hq, d] fp32; else nullptr
   int B, Hq, Hkv, N, d, Npad; // Npad = N rounded up to 128
   int causal;
   float scale;
@@ -157,6 +158,34 @@ struct BwdParams {
   unsigned long long wait_ns;
   int debug_stall;
 };
+
+// The shaped backward's dK/dV pass per query head, its fp32 shares added up afterwards, or per KV head, the group's heads
+// one after the other in an item. Room for the shares is asked for (bwd_shares) where there are no more (key tile, KV
+// head) items than SMs and they could leave SMs idle; bwd_per_head then weighs, in steps of 128 queries (about 1.2 us),
+// the longest item or the SMs' mean against the same with single heads, the shares' way through memory and the
+// launch that adds them. A key tile is seen from all query tiles, at a mean half of them with causal, from a window's, and
+// with key ranges, which the host does not know, from a quarter.
+// Whole calls, causal, per KV head and per query head, d = 128 unless said: 997 rows, 8 heads over 2, d = 64 87 and 51 us; 2048
+// rows, 32 over 8 188 and 159 us (a window of 512: 97 and 119 us); 8192 rows, 32 over 1, d = 64 4059 and 1533 us; 4096
+// rows, 32 over 8 (256 items) 437 and 484 us.
+constexpr long long kPerHeadItems = 152;
+inline bool bwd_shares(int B, int Hq, int Hkv, int N) {
+  return Hq > Hkv && (long long)B * Hkv * (((long long)N + 127) / 128) <= kPerHeadItems;
+}
+inline bool bwd_per_head(const BwdParams& p) {
+  if (!bwd_shares(p.B, p.Hq, p.Hkv, p.N)) return false;
+  const double nt = (p.N + 127) / 128, items = p.B * p.Hkv * nt, G = p.Hq / p.Hkv;
+  double most = nt, mean = p.causal ? (nt + 1) / 2 : nt;
+  if (p.shape.window > 0) {
+    const double seen = (p.causal ? 1.0 : 2.0) * p.shape.window / 128 + 1;
+    if (seen < most) most = seen;
+  }
+  if ((p.shape.key_begin || p.shape.key_end) && most > nt / 4) most = nt / 4 > 1 ? nt / 4 : 1;
+  if (mean > most) mean = most;
+  const double all = items * G * mean / kPerHeadItems;
+  const double join = 2 + 2.0 * p.B * p.N * p.Hq * p.d * 1.3e-6;   // 8 bytes an element, 5 TB/s
+  return (most > all ? most : all) + join < (G * most > all ? G * most : all);
+}
 
 // dQ pass (which also writes the workspace's two vectors) and dK/dV pass, in that
 // order on `stream`. Tensor maps are over the packed [B * N, H, d] views of q, k, v

@@ -61,7 +61,7 @@ SIGNATURES_OPS = {
     "fattn_fwd_paged_shaped_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fattn_fwd_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                     _f, _vp, _i, _vp, _vp, _i, _vp, _sz, _vp]),
-    "fattn_bwd_shaped_workspace_size": (_sz, [_i, _i, _i]),
+    "fattn_bwd_shaped_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fattn_bwd_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i,
                               _vp, _vp, _vp, _sz, _vp]),
     "fattn_decode_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
@@ -874,8 +874,8 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
     return out, lse
 
 
-def bwd_shaped_workspace_size(B: int, Hq: int, N: int) -> int:
-    return int(load_library().fattn_bwd_shaped_workspace_size(B, Hq, N))
+def bwd_shaped_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
+    return int(load_library().fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d))
 
 
 def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
@@ -906,7 +906,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(max(bwd_shaped_workspace_size(B, Hq, N), 1), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), 1), dtype=torch.uint8, device=q.device)
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
                               min(int(window), _INT_MAX), _ptr(key_begin), _ptr(key_end), _ptr(workspace),

@@ -153,16 +153,17 @@ fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache, const voi
 /*
  * fattn_bwd_shaped_workspace_size — bytes of scratch fattn_bwd_shaped needs: fattn_bwd's
  * two fp32 arrays, then the queries that see each key, int32 pairs [B, Npad], 256-byte
- * aligned. Returns 0 for non-positive arguments.
+ * aligned, and, with Hq > Hkv and few key tiles, room for the query heads' shares of dV
+ * and dK, fp32 [2, B, N, Hq, d]. Returns 0 for non-positive arguments.
  */
-size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int N);
+size_t fattn_bwd_shaped_workspace_size(int B, int Hq, int Hkv, int N, int d);
 
 /*
  * fattn_bwd_shaped — gradients of fattn_fwd_shaped with respect to q, k and v:
  * fattn_bwd with P rebuilt from the shaped scores and dS multiplied by the cap's
  * derivative 1 - tanh^2. o and lse are fattn_fwd_shaped's for the same arguments;
  * the slopes are constants (no gradient). Rows that see no key and keys that no row
- * sees get gradient 0. workspace: DEVICE, >= fattn_bwd_shaped_workspace_size(B, Hq, N)
+ * sees get gradient 0. workspace: DEVICE, >= fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d)
  * bytes, 256-byte aligned, contents ignored.
  */
 fattn_status fattn_bwd_shaped(const void* q, const void* k, const void* v, const void* o, const float* lse,

@@ -121,11 +121,14 @@ def test_shaped_calls_limits_and_empty(lib):
     assert set(_calls(lib, dict(d=96))) == {F.FATTN_ERR_UNSUPPORTED}
     assert set(_calls(lib, dict(B=0, q=None))) == {F.FATTN_OK}
     assert set(_calls(lib, dict(N=0, q=None))) == {F.FATTN_OK}
-    need = lib.fattn_bwd_shaped_workspace_size(2, 4, 300)
-    assert need == lib.fattn_bwd_workspace_size(2, 4, 300) + 2 * 384 * 8 and lib.fattn_bwd_shaped_workspace_size(2, 0, 3) == 0
-    for ws, size in ((A, need - 1), (None, need), (A + 16, need)):
+    size = lib.fattn_bwd_shaped_workspace_size
+    need, vectors = size(2, 4, 2, 300, 128), lib.fattn_bwd_workspace_size(2, 4, 300)
+    assert need == vectors + 2 * 384 * 8 + 2 * 2 * 300 * 4 * 128 * 4            # few key tiles: shares per query head
+    assert size(2, 4, 4, 300, 128) == vectors + 2 * 384 * 8 and size(2, 0, 1, 3, 64) == size(2, 4, 0, 3, 64) == 0
+    assert size(64, 4, 2, 300, 128) == lib.fattn_bwd_workspace_size(64, 4, 300) + 64 * 384 * 8
+    for ws, n in ((A, need - 1), (None, need), (A + 16, need)):
         assert lib.fattn_bwd_shaped(A, A, A, A, A, A, A, A, A, 2, 4, 2, 300, 128, 1, 0.1, 0.0, None, 0, None, None, ws,
-                                    size, None) == F.FATTN_ERR_WORKSPACE
+                                    n, None) == F.FATTN_ERR_WORKSPACE
     assert lib.fattn_fwd_shaped(A, A, A, A, None, 1 << 15, 1 << 10, 1, 1 << 15, 64, 1, 0.1, 0.0, None, 0, None, None,
                                 None) == F.FATTN_ERR_UNSUPPORTED
 

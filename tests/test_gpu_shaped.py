@@ -77,6 +77,9 @@ CASES = {
     "prefix128": (1, 400, 2, 2, 128, False, 0.0, False, 0, [400], 150),
     "all": (2, 650, 4, 2, 128, True, 30.0, True, 90, [123, 27, 400], None),
     "all64": (1, 650, 8, 1, 64, False, 15.0, True, 200, [300, 250], 40),
+    # so many key tiles that a group's heads share an item of the dK/dV pass (the cases above take theirs apart)
+    "many": (52, 140, 4, 2, 64, True, 20.0, True, 50, [60, 70], None),
+    "many128": (40, 130, 6, 2, 128, True, 0.0, False, 0, None, None),
 }
 
 
@@ -314,7 +317,7 @@ def test_streams_graphs_and_timeouts():
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     bufs = [torch.zeros_like(t) for t in (o, lse, *ref)]
-    ws = torch.empty(fa.bwd_shaped_workspace_size(1, 2, 600), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.bwd_shaped_workspace_size(1, 2, 1, 600, 128), dtype=torch.uint8, device="cuda")
     g = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(g, stream=s):
