@@ -44,6 +44,12 @@
 // warpgroup packs its bf16 P^T or dS^T into the first 32 columns of its own 64,
 // so the two never touch each other's columns and the MMA reads its TMEM
 // operand from the two halves; the dQ pass writes dS to columns 384-511.
+// Shaped variants (fattn_ops.h): P is rebuilt from the shaped score and dS gets the
+// cap's derivative; the dQ pass walks the key tiles of its rows' ranges, the dK/dV pass the
+// query tiles that see its keys (ranges turned over by the dQ pass's warp 3), per KV head or
+// per query head (bwd_per_head). Bound by the element-wise warps: the cap's polynomial and
+// derivative are ten packed operations a pair of scores. Packed documents of 540 to 1260 rows,
+// B=4 H=32 N=4096 d=128: 762 us, capped 1115 (the whole triangle 1605 and 2327; plain 1600).
 // Every pipeline wait is bounded as in the forward kernel: a wait past its
 // limit records FATTN_ERR_TIMEOUT, every role stops, copies and MMAs are
 // drained and TMEM is freed.

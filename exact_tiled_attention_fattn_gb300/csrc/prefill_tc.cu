@@ -48,7 +48,9 @@
 // Shaped variants (a tanh cap, a distance bias, windows and per-row key ranges; dense
 // or paged): a row's range is [lo, hi), both bounds monotone over the rows, so a Q
 // tile visits the key tiles between its first row's lo and its last row's hi, and masks only
-// at their edges. Paged, a tile's key tiles may be cut into runs, items of their own whose fp32 partials
+// at their edges. Bound by the softmax warps: a bias costs two more packed operations a pair of
+// scores, a cap six (B=2 N=8192, 32 heads over 8, d=128, causal: 947 us, bias 1054, cap 1338, cap and
+// a window of 4096 1020; the plain variant 912). Paged, a tile's key tiles may be cut into runs, items of their own whose fp32 partials
 // prefill_merge_kernel joins: few query tiles over long contexts leave most SMs idle otherwise.
 //
 // P_X aliases S_X: S_X(j) is issued right after O_X += P_X(j-1) V by the same
