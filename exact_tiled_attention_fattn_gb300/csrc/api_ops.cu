@@ -299,7 +299,7 @@ extern "C" fattn_status fattn_evict_paged(void* kcache, void* vcache, const int3
   if (seqlens_out == seqlens || (weights_out == weights_in && dst_max_pages != max_pages_per_seq))
     return FATTN_ERR_INVALID_ARG;
   if (d % 8 != 0 || d > 1024) return FATTN_ERR_UNSUPPORTED;
-  if (cap > 0x7fffffffLL - 4096 || dst_cap > 0x7fffffffLL - 4096 || keep > 0x7fffffff - 4096 ||
+  if (cap > 0x7fffffffLL - 32768 || dst_cap > 0x7fffffffLL - 4096 || keep > 0x7fffffff - 4096 ||
       (long long)B * Hkv > 65535)
     return FATTN_ERR_UNSUPPORTED;
   int err = 0;

@@ -1,7 +1,7 @@
 // Eviction: every KV head of every sequence cut down to `keep` tokens — the first `first`, the
 // last `recent` and the heaviest of the others — compacted in order.
 //
-// select_kernel, one block per (sequence, KV head): the weights of the middle tokens as
+// select_kernel, one block (or a cluster) per (sequence, KV head): the weights of the middle tokens as
 // order-preserving 32-bit integers, the threshold by three passes of an 11-bit histogram from the top
 // digit down (its first digit tells quarter octaves apart: few lanes of a warp meet in a bin, where the
 // 8-bit digit of an exponent brought most of them together), then a scan in index order that counts what is kept and the ties already taken
@@ -30,40 +30,61 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kPer = 16;                        // weights per thread and tile
-constexpr int kTile = kSelThreads * kPer;       // 16384 tokens
+constexpr int kTile = 16 * kSelThreads;         // 16384 tokens
 constexpr int kBins = 2048;
 static_assert(kBins == 2 * kSelThreads, "two bins per thread");
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
-  __shared__ int s_hist[kBins];
+// The blocks of a cluster: all of them at the barrier, and a pair of words in another one's shared memory.
+template <int C>
+__device__ __forceinline__ void cluster_sync() {
+  if constexpr (C == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ int2 read_block(const int* local, int rank) {
+  int2 v;
+  asm volatile(
+      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %2, %3;\nld.shared::cluster.v2.s32 {%0, %1}, [a];\n}"
+      : "=r"(v.x), "=r"(v.y)
+      : "r"(smem_u32(local)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// C blocks, a cluster, per (sequence, KV head): each takes 1 / C of every tile.
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
+  constexpr int kPer = kTile / kSelThreads / C;   // weights per thread and tile
+  __shared__ __align__(8) int s_hists[2][kBins];  // in turn: a block may still read the last pass's of another
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   __shared__ int s_warp[32];
   __shared__ int s_cnt[kPer * 32];   // per 32 consecutive tokens of a tile: kept above the threshold | ties << 16
-  __shared__ int s_tile[2];          // of the tile
-  const int b = blockIdx.y, h = blockIdx.x;
+  __shared__ __align__(8) int s_tile[2];   // of the block's part of the tile
+  const int b = blockIdx.y, h = blockIdx.x / C, rank = blockIdx.x % C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages * p.page_size;
   const int out_cap = p.dst_max_pages * p.page_size;
   int n = __ldg(p.seqlens + b);
   if (n < 0 || n > cap) {
-    if (h == 0 && tid == 0) record_status(p.status, kStatusDeviceCheck);
+    if (h == 0 && rank == 0 && tid == 0) record_status(p.status, kStatusDeviceCheck);
     n = 0;
   }
   const int m = min(n, p.keep);
-  if (h == 0 && tid == 0) p.seqlens_out[b] = m;
+  if (h == 0 && rank == 0 && tid == 0) p.seqlens_out[b] = m;
   const float* w = p.w_in + ((size_t)b * p.Hkv + h) * cap;
   float* wo = p.w_out + ((size_t)b * p.Hkv + h) * out_cap;
   int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.keep;
 
-  // A tile's weights in registers (token tile + 1024 i + tid in x[i]): the loads are on their way together,
-  // and with a single tile (16384 tokens) they are read once for all the passes.
+  // A tile's weights in registers (token mine + tile + 1024 i + tid in x[i]): the loads are on their way
+  // together, and with a single tile (16384 tokens) they are read once for all the passes.
+  const int mine = rank * kPer * kSelThreads + tid;
   float x[kPer];
   auto load = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + i * kSelThreads + tid;
+      const int t = t0 + i * kSelThreads + mine;
       x[i] = t < n ? w[t] : 0.f;
     }
   };
@@ -80,6 +101,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     for (int pass = 0; pass < 3; ++pass) {   // digits of 11, 11 and 10 bits
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      int* s_hist = s_hists[pass & 1];
       s_hist[tid] = s_hist[tid + kSelThreads] = 0;
       __syncthreads();
       const uint32_t prefix = s_prefix;
@@ -88,17 +110,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         if (n > kTile) load(t0);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int t = t0 + i * kSelThreads + tid;
-          if (t0 + i * kSelThreads >= n) break;
+          const int t = t0 + i * kSelThreads + mine;
+          if (t - tid >= n) break;
           if (t >= lo && t < hi) {
             const uint32_t k = order_key(x[i]);
             if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&s_hist[(k >> shift) & digits], 1);
           }
         }
       }
-      __syncthreads();
-      // the threshold's digit: thread i counts bins 2047 - 2 i and 2046 - 2 i, after all that are higher
-      const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
+      cluster_sync<C>();
+      // the threshold's digit, found by every block: thread i counts bins 2047 - 2 i and 2046 - 2 i, after all that
+      // are higher
+      int c0 = 0, c1 = 0;
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        const int* pair = s_hist + kBins - 2 - 2 * tid;
+        const int2 v = C == 1 ? *reinterpret_cast<const int2*>(pair) : read_block(pair, r);
+        c1 += v.x;
+        c0 += v.y;
+      }
       int v = c0 + c1;
       for (int o = 1; o < 32; o <<= 1) {
         const int a = __shfl_up_sync(0xffffffffu, v, o);
@@ -128,7 +158,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   int done = 0, tied = 0;
   for (int t0 = 0; t0 < n; t0 += kTile) {
     if (n > kTile) load(t0);
-    const int batches = min(kPer, (n - t0 + kSelThreads - 1) / kSelThreads);
+    const int batches = min(kPer, max(0, n - t0 - (mine - tid) + kSelThreads - 1) / kSelThreads);
     uint32_t gts = 0, eqs = 0;   // bit i: this thread's token of batch i
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -136,7 +166,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         if (lane == 0) s_cnt[i * 32 + warp] = 0;
         continue;
       }
-      const int t = t0 + i * kSelThreads + tid;
+      const int t = t0 + i * kSelThreads + mine;
       const bool in = t < n, mid = in && t >= lo && t < hi;
       const uint32_t k = order_key(x[i]);
       const bool gt = in && (!mid || (need > 0 && k > thr)), eq = mid && need > 0 && k == thr;
@@ -146,7 +176,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       if (lane == 0) s_cnt[i * 32 + warp] = __popc(bg) | (__popc(be) << 16);
     }
     __syncthreads();
-    if (warp == 0) {   // exclusive scan of the 512 counts (the sums stay below 2^15 and 2^16: 16384 tokens)
+    if (warp == 0) {   // exclusive scan of the 32 kPer counts (the sums stay below 2^15 and 2^16: 16384 tokens)
       int c[kPer], sum = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -169,7 +199,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         v += c[i];
       }
     }
-    __syncthreads();
+    cluster_sync<C>();   // (in place: every block's weights of the tile are in registers)
+    int done_next = done, tied_next = tied;
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+      const int2 v = C == 1 ? *reinterpret_cast<const int2*>(s_tile) : read_block(s_tile, r);
+      done += r < rank ? v.x : 0;
+      tied += r < rank ? v.y : 0;
+      done_next += v.x;
+      tied_next += v.y;
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (i >= batches) break;
@@ -181,16 +220,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       const int e_before = tied + (before >> 16) + __popc(be & below);
       if (gt || (eq && e_before < ties)) {
         const int at = g_before + min(e_before, ties);
-        kept[at] = t0 + i * kSelThreads + tid;
+        kept[at] = t0 + i * kSelThreads + mine;
         wo[at] = x[i];
       }
     }
-    done += s_tile[0];
-    tied += s_tile[1];
-    __syncthreads();   // (the counts are read; in place, a tile is written before the next is loaded below it)
+    done = done_next;
+    tied = tied_next;
+    cluster_sync<C>();   // (the counts are read, here and by the other blocks)
   }
-  for (int t = m + tid; t < p.keep; t += kSelThreads) kept[t] = -1;
-  for (int t = m + tid; t < out_cap; t += kSelThreads) wo[t] = 0.f;
+  for (int t = m + rank * kSelThreads + tid; t < p.keep; t += C * kSelThreads) kept[t] = -1;
+  for (int t = m + rank * kSelThreads + tid; t < out_cap; t += C * kSelThreads) wo[t] = 0.f;
 }
 
 // Slot of token t of sequence b, in 16-byte units of head h's row; -1 if its page is not in the pool.
@@ -264,7 +303,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_in_place_kernel(const Evict
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream) {
-  select_kernel<<<dim3(p.Hkv, p.B), kSelThreads, 0, stream>>>(p);
+  // a cluster of four blocks for tables of more than one tile and few heads: the passes' re-reads go four times as fast
+  // (8 heads of 131072 tokens, the whole call: 189 us with one block a head, 128 with four); up to a tile the
+  // cluster's barriers cost what they bring (64 heads of 16384: 58 and 57 us), and with many heads more (512 heads of
+  // 16384: 135 and 173 us)
+  if ((long long)p.max_pages * p.page_size > kTile && (long long)p.B * p.Hkv * 4 <= num_sms)
+    select_kernel<4><<<dim3(p.Hkv * 4, p.B), kSelThreads, 0, stream>>>(p);
+  else
+    select_kernel<1><<<dim3(p.Hkv, p.B), kSelThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int heads = p.B * p.Hkv;

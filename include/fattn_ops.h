@@ -17,7 +17,9 @@
  * The conventions of fattn.h hold: DEVICE pointers owned by the caller, host
  * checks before anything is launched, work enqueued on `stream`, no
  * allocation, no synchronisation, problems found on the device recorded in the
- * status word (fattn_debug_read_status). Strides count elements.
+ * status word (fattn_debug_read_status). Strides count elements. Calls that join
+ * partials (num_splits > 1, shares per query head) leave outputs of no meaning after a
+ * wait that ran out (FATTN_ERR_TIMEOUT), the others do not write them.
  */
 #ifndef FATTN_OPS_H
 #define FATTN_OPS_H
@@ -235,7 +237,7 @@ fattn_status fattn_key_weights_paged(const void* q, const void* kcache, const in
  *   is not moved; both record FATTN_ERR_DEVICE_CHECK. bf16 caches, any page_size >= 1.
  * Errors: INVALID_ARG (NULL or misaligned pointers, non-positive sizes, first + recent > keep, kept tokens
  *   that do not fit dst_max_pages, seqlens_out == seqlens); UNSUPPORTED (d not a multiple of 8 up to
- *   1024, B * Hkv > 65535).
+ *   1024, B * Hkv > 65535, tables of 2^31 - 32768 tokens or more).
  */
 fattn_status fattn_evict_paged(void* kcache, void* vcache, const int32_t* block_table, const int32_t* seqlens,
                                const float* weights_in, const int32_t* dst_table, int32_t* seqlens_out,

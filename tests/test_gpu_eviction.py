@@ -146,7 +146,11 @@ def same(a, b):
     (16, 1, 64, [2500], 1, 0, 0, "ties"),
     (16, 2, 64, [500, 400], 123, 5, 2, "special"),
     (16, 1, 64, [50, 20], 64, 0, 0, "random"),
-    (128, 1, 1024, [300], 150, 0, 0, "random")])
+    (128, 1, 1024, [300], 150, 0, 0, "random"),
+    (16, 2, 8, [40001, 17000, 3], 5000, 100, 4, "random"),     # more than 16384 tokens: four blocks a head
+    (32, 1, 8, [33000, 16385, 0], 20000, 0, 0, "ties"),
+    (64, 1, 8, [20000], 19999, 300, 0, "special"),
+    (16, 2, 8, [17000] + [40] * 19, 1000, 9, 9, "ties")])       # and with more heads one block
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict(P, Hkv, d, lens, keep, recent, first, kind, in_place):
     fa = need_gpu()
