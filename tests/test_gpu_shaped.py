@@ -378,3 +378,50 @@ def test_windows_of_any_size():
             for w in (320, 10 ** 9, 2 ** 31 - 1, 2 ** 40):
                 assert all(torch.equal(x, y) for x, y in zip(call(w), plain)), w
     assert fa.debug_read_status() == 0
+
+
+def test_two_streams_at_once():
+    """Split chunks and per-head gradients of two streams that run at the same time: each as alone, to the bit."""
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(8)
+    calls = []
+    for i in range(2):
+        q, k, v, do = (x.cuda() for x in make(40 + i, 1, 700 + 200 * i, 8, 2, 64 + 64 * i))
+        kw = dict(causal=True, softcap=15.0 + i)
+        o, lse = fa.fwd_shaped(q, k, v, **kw)
+        kc, vc = (torch.randn(90, 32, 2, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+        qc, table = torch.randn(70, 4, 128, generator=g).to(torch.bfloat16).cuda(), torch.randperm(90, generator=g).int().reshape(1, 90).cuda()
+        lens, cu = torch.tensor([2800], dtype=torch.int32).cuda(), torch.tensor([0, 70], dtype=torch.int32).cuda()
+        calls.append(lambda s, a=(q, k, v, o, lse, do), kw=kw, c=(qc, kc, vc, table, lens, cu, 70): (
+            *fa.bwd_shaped(*a, stream=s, **kw), *fa.fwd_paged_shaped(*c, softcap=9.0, num_splits=6, stream=s)))
+    alone = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(c(None))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, b in zip(alone, got) for x, y in zip(a, b))
+    assert fa.debug_read_status() == 0
+
+
+def test_per_head_gradients_against_one_head_at_a_time():
+    """The shares of a group's query heads: dk and dv are the sum of the single heads' (fp32 in between, one rounding)."""
+    fa = need_gpu()
+    q, k, v, do = (x.cuda() for x in make(44, 1, 500, 6, 2, 128))
+    kw = dict(causal=True, window=300, softcap=12.0)
+    o, lse = fa.fwd_shaped(q, k, v, **kw)
+    dq, dk, dv = fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+    sk, sv, mk, mv = (torch.zeros(1, 500, 2, 128, device="cuda") for _ in range(4))
+    for h in range(6):
+        one = lambda t, j: t[:, :, j:j + 1].contiguous()
+        a = fa.bwd_shaped(one(q, h), one(k, h // 3), one(v, h // 3), one(o, h), lse[:, h:h + 1].contiguous(), one(do, h), **kw)
+        assert torch.equal(a[0], one(dq, h))
+        for t, m, x in ((sk, mk, a[1]), (sv, mv, a[2])):
+            t[:, :, h // 3:h // 3 + 1] += x.float()
+            m[:, :, h // 3:h // 3 + 1] += x.float().abs()
+    # each single head's result and the sum are rounded to bf16: half a step of each
+    assert ((dk.float() - sk).abs() <= 1.01 * H * (mk + sk.abs()) + 1e-30).all()
+    assert ((dv.float() - sv).abs() <= 1.01 * H * (mv + sv.abs()) + 1e-30).all()
