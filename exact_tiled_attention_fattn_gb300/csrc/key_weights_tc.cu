@@ -4,7 +4,7 @@
 // queries first, in alternating direction round by round. The K tiles stay in shared memory while the
 // group's query rows stream by, R of them a step (R = G floor(128 / G), row u the query u / G of the
 // step and head u mod G, which is how one TMA box of G heads x R / G queries lands). Two tiles share a
-// step's rows: with one, the rows (32 KB of L2 for every 2^21 multiply-adds) bound the kernel.
+// step's rows: with one, the rows (32 KB of L2 for every 2^21 multiply-adds) take 6.4 TB/s.
 //   warp 0      TMA producer: K tiles (page by page, eight lanes) into a ring of three, Q tiles
 //               into another
 //   warp 1      MMA issuer (one thread): S^T = K Q^T of each unit (step, tile) into one of four
@@ -14,8 +14,10 @@
 //               other unit; at the end of the item the second warpgroup hands its sums to the
 //               first, which writes w_out. Fixed order, no atomics.
 // One product per pair of tiles and no P V leaves an exponential per 2 d flops. Two prompts of 2048 and 1536 queries
-// over 8.6k tokens, 32 heads over 8: 128 us, 800 TFLOP/s, bound by the rows' 6.4 TB/s from L2 with one tile per
-// item; four of 4096 over 8192 each, two tiles: 981 us, 1120 TFLOP/s.
+// over 8.6k tokens, 32 heads over 8: 128 us, 800 TFLOP/s; four of 4096 over 8192 each: 981 us, 1120 TFLOP/s.
+// Bound by the chain of a unit (product, TMEM load, exponentials, release): tensor pipe and special function unit are
+// both busy 38 % (50 % in the second); wider loads, a third summing warpgroup or pairs of CTAs that share the
+// rows by multicast (137 us) do not shorten it.
 // Every wait is bounded, as in the other tensor-core kernels.
 #include "device_common.cuh"
 #include "ops_internal.h"
