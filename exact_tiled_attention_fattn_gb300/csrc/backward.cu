@@ -599,14 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(small + Lay::kOffHolder);
 
   const int nt = (p.N + BT - 1) / BT;
-  const int G = kPerHead ? 1 : p.Hq / p.Hkv, heads = kPerHead ? p.Hq : p.Hkv;
-  const BwdSchedule sch = make_bwd_schedule(p.B * heads, nt, 1);
+  const int G = kPerHead ? 1 : p.Hq / p.Hkv;
+  const BwdSchedule sch = make_bwd_schedule(p.B * (kPerHead ? p.Hq : p.Hkv), nt, 1);
   // item: (sequence, KV head, or query head with kPerHead, key tile j); rank 0 = j 0, the most query tiles under the causal rule
   auto item = [&](int it, int& b, int& hkv, int& j) {
     int head;
     bwd_decode(sch, it, head, j);
-    b = head / heads;
-    hkv = head - b * heads;
+    b = head / (kPerHead ? p.Hq : p.Hkv);
+    hkv = head - b * (kPerHead ? p.Hq : p.Hkv);
   };
   // query tiles [i0, i0 + ni) of an item
   auto tiles = [&](int b, int j, int& i0, int& ni) {
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int key = j * BT + r;
       const bool live = key < p.N;
-      const size_t off = (((size_t)b * p.N + (live ? key : 0)) * heads + hkv) * D + wg * (D / 2);
+      const size_t off = (((size_t)b * p.N + (live ? key : 0)) * (kPerHead ? p.Hq : p.Hkv) + hkv) * D + wg * (D / 2);
       const int wkey0 = j * BT + q4 * 32;  // the warp's first key row
       const bool staged = Lay::kStoreTma && wkey0 + 32 <= p.N;
       if constexpr (kPerHead)
