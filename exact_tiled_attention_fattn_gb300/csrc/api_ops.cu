@@ -86,15 +86,25 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
   return launch_rope(p, true, interleaved != 0, true, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-// The cap as a polynomial: tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) on |z| <= z_max, folded into powers of
-// u = z softcap / scale. Outside the range of scale / softcap where every folded coefficient is an ordinary
-// float the kernels do without.
+// The cap as a polynomial: tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) on |z| <= z_max, folded into powers of u =
+// z softcap / scale. Fewer terms on a shorter range where the last coefficient would not be an ordinary float (at d = 128
+// and its usual scale with caps above 3000): the Taylor terms 1, -1/3, 2/15 on |z| <= 0.08 (off by 17/315 z^6, 1.4e-8;
+// caps up to 1e8), or the first alone on |z| <= 1e-4 (z^2 / 3, 3e-9): with such caps that holds every score of use. (With a
+// scale / softcap above 10^4 and a cap above 1, scores past the short range are off by 2^-22 of the cap.) Caps below 1e-15
+// go without: 1 / cap^2 has to be a float, and 2^-22 of such a cap is nothing.
 static void fold_cap(float scale, float softcap, const double (&c)[5], double z_max, ScoreShape* out) {
-  const double k = (double)scale / (softcap > 0.f ? softcap : 1.0);
-  if (!(softcap > 0.f && std::fabs(k) >= 5e-4 && std::fabs(k) <= 1e2 && softcap < 1e6f)) return;
-  double pw = k * softcap * 1.4426950408889634;
-  for (int i = 0; i < 5; ++i, pw *= k * k) out->poly[i] = make_float2((float)(c[i] * pw), (float)(c[i] * pw));
-  out->poly_limit = (float)(z_max / std::fabs(k));
+  out->poly_limit = -1.f;
+  if (!(softcap >= 1e-15f)) return;
+  const double k = (double)scale / softcap, k2 = k * k, s = (double)scale * 1.4426950408889634;
+  const double taylor[3] = {1.0, -1.0 / 3.0, 2.0 / 15.0}, third = std::fabs(s) * k2 * k2, fifth = third * k2 * k2;
+  const int terms = fifth > 1e-36 && fifth < 1e38 ? 5 : third > 1e-36 && third < 1e38 ? 3 : 1;
+  double pw = s;
+  for (int i = 0; i < 5; ++i, pw *= k2) {
+    const float a = i >= terms ? 0.f : (float)((terms == 5 ? c[i] : taylor[i]) * pw);
+    out->poly[i] = make_float2(a, a);
+  }
+  const double limit = (terms == 5 ? z_max : terms == 3 ? 0.08 : 1e-4) / std::fabs(k);   // (scale 0: infinite)
+  out->poly_limit = (float)(limit < 1e18 ? limit : 1e18);   // (its square is a float)
 }
 
 // A score shape's own checks; fills *out. `scale` is the call's, `keys` the most that a sequence has: a window of that
@@ -106,6 +116,9 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
   if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
   if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
   if (window >= keys) window = 0;
+  // a cap of 2^100 moves no score up to 2^88 in 32 bits (tanh z is z within z^3 / 3), and above that, as without it, the
+  // largest score takes all the weight
+  if (softcap >= 0x1p100f) softcap = 0.f;
   *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, -1.f};
   out->sl2 = scale * 1.4426950408889634f;
   out->cap2 = softcap * 1.4426950408889634f;

@@ -369,7 +369,9 @@ __device__ __forceinline__ void write_ds(uint32_t dp_col, const float (&pv)[64],
 
 // ------------------------------------------------------------------ shaped scores
 // Variants of both kernels: kPlain, or what the shaped scores get (key ranges and the window always).
-enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2 };
+// kShapeFar: a cap above 128, under which cap (1 - 2 r), off by 2^-22 of the cap, is not as good as the fp32 sum of
+// a small product next to a large one. (A kernel of its own: under a run-time switch the others lose 2 to 3 %.)
+enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2, kShapeFar = 4 };
 // Key tiles [top - n, top) that the rows of query tile i see, n >= 1: a tile whose rows see no
 // key visits one tile with everything masked (its dQ is the zero that this gives).
 __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n) {
@@ -470,6 +472,15 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
         const float r = tanh_r(__uint_as_float(u[c]) * sh.capk);
         y[c] = fmaf(-2.f * sh.cap2, r, sh.cap2);
         f[c] = 4.f * r * (1.f - r);
+      }
+      if constexpr (kShape & kShapeFar) {  // products in the polynomial's range keep it
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float y0, y1;
+          f2_unpack(capped_pair(sh, __uint_as_float(u[c]), __uint_as_float(u[c + 1])), y0, y1);
+          if (fabsf(__uint_as_float(u[c])) <= sh.poly_limit) y[c] = y0;
+          if (fabsf(__uint_as_float(u[c + 1])) <= sh.poly_limit) y[c + 1] = y1;
+        }
       }
     }
   } else {
@@ -1362,6 +1373,9 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
                          cudaStream_t stream) {
   if (!p.shaped) return launch_bwd_t<D, kPlain>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   const bool cap = p.shape.cap > 0.f, bias = p.shape.slopes != nullptr;
+  if (p.shape.cap > 128.f)
+    return bias ? launch_bwd_t<D, kShapeCap + kShapeBias + kShapeFar>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream)
+                : launch_bwd_t<D, kShapeCap + kShapeFar>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   if (cap && bias) return launch_bwd_t<D, kShapeCap + kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   if (cap) return launch_bwd_t<D, kShapeCap>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   if (bias) return launch_bwd_t<D, kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);

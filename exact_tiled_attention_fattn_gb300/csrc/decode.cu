@@ -198,6 +198,17 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
       mma_bf16(s[0], qa[kk], b0, b1);
       mma_bf16(s[1], qa[kk], b2, b3);
     }
+    if constexpr (kShaped) {
+      if (p.shape.cap > 0.f) {
+        float u[2][4];   // rows g (both token tiles), rows g + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[0][i] = s[i >> 1][i & 1], u[1][i] = s[i >> 1][2 + (i & 1)];
+        cap_in_place(p.shape, u[0]);
+        if (high_rows) cap_in_place(p.shape, u[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] = u[0][i], s[i >> 1][2 + (i & 1)] = u[1][i];
+      }
+    }
     // scale into the log2 domain, mask missing tokens, running max per row
     float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
     // shaped: distance of this thread's first token
@@ -214,7 +225,7 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
             s[nt][j] = -CUDART_INF_F;
             continue;
           }
-          y = p.shape.cap > 0.f ? fmaf(-2.f * p.shape.cap2, tanh_r(s[nt][j] * p.shape.capk), p.shape.cap2) : s[nt][j] * sl2;
+          y = p.shape.cap > 0.f ? s[nt][j] : s[nt][j] * sl2;
           if (p.shape.slopes) y = fmaf(j < 2 ? slope0 : slope1, dist - (float)(nt * 8 + (j & 1)), y);
         } else {
           y = s[nt][j] * sl2;

@@ -157,8 +157,6 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
       ldsm4(sb + unit_at<D>(warp * 32 + mt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, kk * 2 + (lane >> 4)), ka[mt][kk]);
 
   const float sl2 = p.scale * kLog2e;
-  const float cap2 = p.shape.cap * kLog2e;
-  const float capk = p.shape.cap > 0.f ? 2.f * sl2 / p.shape.cap : 0.f;
   const int g = lane >> 2;
   const int kg = key0 + warp * 32 + g;        // this thread's keys: kg, + 8, + 16, + 24
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -180,6 +178,12 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
           mma(c[mt][1], ka[mt][kk], bq[2], bq[3]);
         }
       }
+      if (p.shape.cap > 0.f) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int n8 = 0; n8 < 2; ++n8) cap_in_place(p.shape, c[mt][n8]);
+      }
 #pragma unroll
       for (int n8 = 0; n8 < 2; ++n8)
 #pragma unroll
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
             for (int hf = 0; hf < 2; ++hf) {
               const int dist = pos - (kg + mt * 16 + hf * 8);
               const float x = c[mt][n8][hf * 2 + e];
-              float y = p.shape.cap > 0.f ? fmaf(-2.f * cap2, tanh_r(x * capk), cap2) : x * sl2;
+              float y = p.shape.cap > 0.f ? x : x * sl2;
               y = fmaf(v.y, fabsf((float)dist), y);
               bool see = !p.causal || dist >= 0;
               if (p.shape.window > 0) see = see && abs(dist) < p.shape.window;
@@ -360,6 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
     __syncwarp();   // the stage is read: it may take the chunk kStages on
     if (c + kStages < mine) issue(c + kStages, next);
     next = find(c + kStages + 1);
+    if (sh.cap > 0.f) cap_in_place(sh, *reinterpret_cast<float(*)[NT * 4]>(&s[0][0]));
     float acc[2] = {0.f, 0.f};   // keys kt + g and kt + g + 8
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
           const float x = s[nt][hf * 2 + e];
           float y;
           if (sh.cap > 0.f)
-            y = fmaf(-2.f * sh.cap2, tanh_r(x * sh.capk), sh.cap2) + nl[nt][e];
+            y = x + nl[nt][e];
           else
             y = fmaf(x, sh.sl2, nl[nt][e]);
           if (sh.slopes) y = fmaf(slope[nt][e], fabsf((float)dist), y);

@@ -217,19 +217,7 @@ __device__ __forceinline__ float sum_columns(const KeyWeightsParams& p, uint32_t
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             m[i] = fmax3(m[i], fabsf(__uint_as_float(u[e + i])), fabsf(__uint_as_float(u[e + 4 + i])));
-        if (fmax3(fmaxf(m[0], m[1]), m[2], m[3]) <= sh.poly_limit) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x = f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), w = f2_mul(x, x);
-            uint64_t t = f2_bits(sh.poly[4]);
-#pragma unroll
-            for (int i = 3; i >= 0; --i) t = f2_fma(t, w, f2_bits(sh.poly[i]));
-            f2_unpack(f2_mul(x, t), y[e], y[e + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), sh.cap2);
-        }
+        capped_scores(sh, u, fmax3(fmaxf(m[0], m[1]), m[2], m[3]), y);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(u[e]);

@@ -1029,7 +1029,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], fabsf(__uint_as_float(u[28 + i])));
             return fmax3(fmaxf(a[0], a[1]), a[2], a[3]);
           };
-          auto bound = [&](float amax) -> float { return fmaf(-2.f * sh.cap2, tanh_r(amax * fabsf(sh.capk)), sh.cap2); };
+          auto bound = [&](float amax) -> float {
+            float y, same;
+            f2_unpack(capped_pair(sh, amax, amax), y, same);
+            return fabsf(amax <= sh.poly_limit ? y : capped_far(sh, amax));
+          };
           // 2^(u P(u^2) - base) arguments of a pair
           auto poly_arg = [&](uint32_t x0, uint32_t x1, uint64_t add) -> uint64_t {
             const uint64_t u2 = f2_pack(__uint_as_float(x0), __uint_as_float(x1)), w2 = f2_mul(u2, u2);
@@ -1115,19 +1119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!form && vis) mx = fmaxf(mx, bound(amax));
               if (kBias || __any_sync(0xffffffffu, form)) {
                 if (form) {
-                  if ((small >> c) & 1u) {
+                  float y[32];
+                  capped_scores(sh, u, amax, y);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                      float y0, y1;
-                      f2_unpack(poly_arg(u[e], u[e + 1], 0ull), y0, y1);
-                      u[e] = __float_as_uint(y0);
-                      u[e + 1] = __float_as_uint(y1);
-                    }
-                  } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                      u[e] = __float_as_uint(fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), sh.cap2));
-                  }
+                  for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(y[e]);
                   if constexpr (kBias) {
                     const float dist = (float)(pos - j * BN - 32 * c);
 #pragma unroll
@@ -1168,9 +1163,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) f2_unpack(poly_arg(u[e], u[e + 1], nbase2), e2[e], e2[e + 1]);
               } else {
-                const float top = sh.cap2 - base;
+                capped_scores(sh, u, INFINITY, e2);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) e2[e] = fmaf(-2.f * sh.cap2, tanh_r(__uint_as_float(u[e]) * sh.capk), top);
+                for (int e = 0; e < 32; ++e) e2[e] -= base;
               }
               if (edge) {
                 const uint32_t vis = visible(c);

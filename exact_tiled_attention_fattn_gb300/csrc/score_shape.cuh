@@ -15,12 +15,54 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(z) = 1 - 2 r with r = 1 / (1 + e^{2z}): one exponential and one reciprocal. The absolute
-// error is a few 2^-24 (what counts: the capped score is cap tanh(z), an exponent), where the
-// hardware tanh's 2^-11 would move a score under a cap of 50 by 0.02. Its derivative is
+// tanh(z) = 1 - 2 r with r = 1 / (1 + e^{2z}): one exponential and one reciprocal. Its derivative is
 // 1 - tanh^2 = 4 r (1 - r), which keeps its relative precision where tanh saturates.
 // k2z = 2 z log2(e).
 __device__ __forceinline__ float tanh_r(float k2z) { return rcp_approx(1.f + ex2(k2z)); }
+
+// The capped score of the raw product u as cap (1 - 2 r), log2 units. It is off by 2^-22 of the cap: as good as the score
+// itself where |z| is above 0.5 or so, and of no use where the cap is much larger than the score (a cap of 10^6 would
+// move it by 0.1). There it is the polynomial, relative 1e-7 whatever the cap is.
+__device__ __forceinline__ float capped_far(const ScoreShape& s, float u) {
+  return fmaf(-2.f * s.cap2, tanh_r(u * s.capk), s.cap2);
+}
+// A pair of capped scores, both |u| <= poly_limit: three packed FMAs and products a score, no special function.
+__device__ __forceinline__ uint64_t capped_pair(const ScoreShape& s, float u0, float u1) {
+  const uint64_t u2 = f2_pack(u0, u1), w2 = f2_mul(u2, u2);
+  uint64_t q = f2_bits(s.poly[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) q = f2_fma(q, w2, f2_bits(s.poly[i]));
+  return f2_mul(u2, q);
+}
+// The scores of 32 raw products of a thread, m the largest of their magnitudes.
+__device__ __forceinline__ void capped_scores(const ScoreShape& s, const uint32_t (&u)[32], float m, float (&y)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) f2_unpack(capped_pair(s, __uint_as_float(u[i]), __uint_as_float(u[i + 1])), y[i], y[i + 1]);
+  if (!(m <= s.poly_limit)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (fabsf(__uint_as_float(u[i])) > s.poly_limit) y[i] = capped_far(s, __uint_as_float(u[i]));
+  }
+}
+// n (even) raw products of a thread replaced by their capped scores.
+template <int n>
+__device__ __forceinline__ void cap_in_place(const ScoreShape& s, float (&x)[n]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < n; i += 2) m = fmax3(m, fabsf(x[i]), fabsf(x[i + 1]));
+  if (m <= s.poly_limit) {
+#pragma unroll
+    for (int i = 0; i < n; i += 2) f2_unpack(capped_pair(s, x[i], x[i + 1]), x[i], x[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+      float y0, y1;
+      f2_unpack(capped_pair(s, x[i], x[i + 1]), y0, y1);
+      x[i] = fabsf(x[i]) <= s.poly_limit ? y0 : capped_far(s, x[i]);
+      x[i + 1] = fabsf(x[i + 1]) <= s.poly_limit ? y1 : capped_far(s, x[i + 1]);
+    }
+  }
+}
 
 // Keys that the query at position pos (key coordinates; row = its index in the packed rows) sees.
 // Both bounds are non-decreasing over the rows of a sequence (the ranges are required to be).

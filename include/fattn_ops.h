@@ -102,7 +102,8 @@ fattn_status fattn_rope_append_paged(const void* q, void* q_out, const void* k, 
  *   |i - j| < window                         if window > 0,
  *   key_begin[row] <= j < key_end[row]       where given (either may be NULL).
  * O = softmax(s) V over the visible keys, lse the logsumexp; a row that sees no
- * key gets O = 0, lse = -inf.
+ * key gets O = 0, lse = -inf. A capped score keeps the relative precision of a 32-bit
+ * score whatever the cap is; from 2^100 on a cap is none.
  *
  * slopes: DEVICE fp32 [Hq], any sign. key_begin, key_end: DEVICE int32, one per
  * query row ([B, N]; [total_q] for chunks), keys of the row's own sequence; they
