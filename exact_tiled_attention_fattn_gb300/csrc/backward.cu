@@ -403,6 +403,8 @@ __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker,
       a1 = end(i);
       b0 = begin(i - 1);
       b1 = begin(i);
+      // ranges that decrease cannot be turned over: the gradients of the keys concerned would be wrong
+      if (a0 > a1 || b0 > b1) record_status(p.status, kStatusDeviceCheck);
     }
     int2* out = p.ws_keys + (size_t)b * p.Npad;
     for (int l = 0; l < 32; ++l) {
@@ -1212,8 +1214,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (qrow < p.N) {
           klo = shape_lo(p.shape, (long long)b * p.N + qrow, qrow);
           khi = shape_hi(p.shape, (long long)b * p.N + qrow, qrow, p.N, p.causal);
-          // ranges that are not monotone: the row's keys are not all among its tile's
-          if (klo < khi && (klo < (top - jn) * BT || khi > top * BT)) record_status(p.status, kStatusDeviceCheck);
         }
       }
       const size_t vrow = (size_t)(b * p.Hq + h) * p.Npad + qrow;

@@ -882,10 +882,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nm;
         }
       };
-      const int row = x.base + t * BM + r;
+      const int row = x.base + t * BM + r, pos = row + x.off;
+      const int kv_hi = kShaped ? (t ? x.top[1] : x.top[0]) : nt;
+      // ranges that are not monotone: a row's keys [lo, hi) are not all among its tile's (of all the runs)
+      auto check_range = [&](int lo, int hi) {
+        bool out = nt == 0 || lo < (kv_hi - nt) * BN || hi > kv_hi * BN;
+        if constexpr (kSplits) {
+          const int r0 = x.base + t * BM, r1 = min(r0 + BM, x.L) - 1;
+          const int a = shape_lo(p.shape, (long long)x.row0 + r0, r0 + x.off);
+          const int e = shape_hi(p.shape, (long long)x.row0 + r1, r1 + x.off, x.Lk, p.causal);
+          out = a >= e || lo < a / BN * BN || hi > (e + BN - 1) / BN * BN;
+        }
+        if (lo < hi && out) record_status(p.status, kStatusDeviceCheck);
+      };
       if (nt == 0) {
         release_mask();
         if constexpr (kShaped) {  // no row of the tile sees a key: O = 0, lse = -inf
+          if (row < x.L)
+            check_range(shape_lo(p.shape, (long long)x.row0 + row, pos),
+                        shape_hi(p.shape, (long long)x.row0 + row, pos, x.Lk, p.causal));
           if (kSplits && row < x.L) {  // an empty partial
             p.lse_part[((size_t)(x.row0 + row) * p.Hq + x.h) * p.splits + x.split] = -CUDART_INF_F;
           } else if (row < x.L) {
@@ -902,23 +917,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int lo = 0;  // keys lo <= j < lim are visible (lo > 0: shaped variant only)
       int lim;
-      const int kv_hi = kShaped ? (t ? x.top[1] : x.top[0]) : nt;
-      const int pos = row + x.off;
       float slope2 = 0.f;  // distance bias: -slope_h log2(e) per key of distance
       if constexpr (kShaped) {
         // (rows past the sequence take its last row's range: they are not written)
         const int rc = min(row, x.L - 1);
         lo = shape_lo(p.shape, (long long)x.row0 + rc, rc + x.off);
         lim = shape_hi(p.shape, (long long)x.row0 + rc, rc + x.off, x.Lk, p.causal);
-        // ranges that are not monotone: the row's keys are not all among its tile's
-        if constexpr (kSplits) {
-          const int r0 = x.base + t * BM, r1 = min(r0 + BM, x.L) - 1;
-          if (lo < lim && (lo < shape_lo(p.shape, (long long)x.row0 + r0, r0 + x.off) / BN * BN ||
-                           lim > (shape_hi(p.shape, (long long)x.row0 + r1, r1 + x.off, x.Lk, p.causal) + BN - 1) / BN * BN))
-            record_status(p.status, kStatusDeviceCheck);
-        } else if (lo < lim && (lo < (kv_hi - nt) * BN || lim > kv_hi * BN)) {
-          record_status(p.status, kStatusDeviceCheck);
-        }
+        check_range(lo, lim);
         if (kBias && p.shape.slopes) slope2 = -__ldg(p.shape.slopes + x.h) * kLog2e;
       } else {
         lim = p.causal ? min(row + x.off + 1, x.Lk) : x.Lk;

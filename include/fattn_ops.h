@@ -107,12 +107,14 @@ fattn_status fattn_rope_append_paged(const void* q, void* q_out, const void* k, 
  *
  * slopes: DEVICE fp32 [Hq], any sign. key_begin, key_end: DEVICE int32, one per
  * query row ([B, N]; [total_q] for chunks), keys of the row's own sequence; they
- * must not decrease from a row to the next of its sequence (rows that see
- * nothing repeat their neighbour's begin as end). Packed documents (begin = the
- * document's first row, end = one past its last), prefixes (end = max(i + 1,
+ * must not decrease from a row to the next of its sequence (a row that sees nothing
+ * has begin = end, at least the previous row's end and at most the next row's begin:
+ * padding behind a document begins and ends where the document ends). Packed documents
+ * (begin = the document's first row, end = one past its last), prefixes (end = max(i + 1,
  * prefix end)) and padding are such ranges; so are their unions with causal and
- * window. Ranges that decrease make the rows concerned wrong and are recorded as
- * FATTN_ERR_DEVICE_CHECK where a row's keys are outside its tile's.
+ * window. Ranges that decrease are recorded as FATTN_ERR_DEVICE_CHECK: by the
+ * attention calls where a row's keys are outside its tile's (its output is wrong then, and
+ * right otherwise), by the gradient always (the keys' gradients would be wrong).
  * Work goes by 128 x 128 tiles: a tile in which no row sees a key is not computed,
  * and keys before the lowest one that 256 consecutive rows see, rounded down to a
  * multiple of 128, are not read for them. Within the computed tiles hidden keys

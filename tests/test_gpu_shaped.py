@@ -425,3 +425,63 @@ def test_per_head_gradients_against_one_head_at_a_time():
     # each single head's result and the sum are rounded to bf16: half a step of each
     assert ((dk.float() - sk).abs() <= 1.01 * H * (mk + sk.abs()) + 1e-30).all()
     assert ((dv.float() - sv).abs() <= 1.01 * H * (mv + sv.abs()) + 1e-30).all()
+
+
+def _decreasing(kind):
+    """(begin, end) of 300 rows whose ranges decrease, the rows that lose their keys by it, and whether the forward is concerned."""
+    b, e = torch.zeros(300, dtype=torch.int32), torch.full((300,), 300, dtype=torch.int32)
+    if kind == "last row":                 # a tile's last row sees nothing: its end is below the others'
+        e[127] = 0
+    elif kind == "padding":                # padding behind a document with an end of 0
+        e[:100], e[100:] = 100, 0
+    elif kind == "begin":                  # a tile whose first row begins behind its last row's end
+        b[0], e[:128] = 290, 128
+    elif kind == "inside":                 # inside the tile's range: the forward is right, the gradient of the keys would not be
+        e[100] = 60
+    elif kind == "begin inside":
+        b[40] = 90
+    return b, e, kind not in ("inside", "begin inside")
+
+
+@pytest.mark.parametrize("kind", ["last row", "padding", "begin", "inside", "begin inside"])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_every_decrease_is_recorded(kind, cap):
+    """Rows that would lose keys leave DEVICE_CHECK in the status word: in the forward where their keys are outside
+    their tile's, in the gradient always."""
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(6, 1, 300, 2, 1, 64))
+    b, e, forward = _decreasing(kind)
+    kw = dict(key_begin=b[None].cuda(), key_end=e[None].cuda(), softcap=cap)
+    o, lse = fa.fwd_shaped(q, k, v, **kw)
+    assert fa.debug_read_status() == (fa.FATTN_ERR_DEVICE_CHECK if forward else 0)
+    fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+    assert fa.debug_read_status() == fa.FATTN_ERR_DEVICE_CHECK
+    table = torch.arange(19, dtype=torch.int32).view(1, 19).cuda()
+    kc, vc = (torch.zeros(19, 16, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n, cu = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([300], [0, 300]))
+    for S in (1, 3, 16):
+        fa.fwd_paged_shaped(q[0], kc, vc, table, n, cu, 300, causal=False, key_begin=b.cuda(), key_end=e.cuda(), softcap=cap, num_splits=S)
+        assert fa.debug_read_status() == (fa.FATTN_ERR_DEVICE_CHECK if forward else 0), S
+
+
+def test_rows_that_see_nothing_record_nothing():
+    """Leading, middle and trailing rows without keys whose ranges do not decrease: whole tiles of them, and empty runs."""
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(7, 1, 700, 2, 1, 64))
+    b, e = torch.zeros(700, dtype=torch.int32), torch.zeros(700, dtype=torch.int32)
+    b[150:400], e[150:400] = 20, 130                   # rows 0 .. 149 see nothing (begin = end = 0)
+    b[400:550], e[400:550] = 130, 130                  # nothing again, at the end of the rows before
+    b[550:560], e[550:560] = 140, 300
+    b[560:], e[560:] = 300, 300
+    kw = dict(key_begin=b[None].cuda(), key_end=e[None].cuda())
+    o, lse = fa.fwd_shaped(q, k, v, **kw)
+    fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+    assert fa.debug_read_status() == 0
+    live = (b < e).cuda()
+    assert torch.equal(torch.isneginf(lse[0, 0]), ~live) and bool((o[0, ~live] == 0).all())
+    table = torch.arange(44, dtype=torch.int32).view(1, 44).cuda()
+    kc, vc = (torch.zeros(44, 16, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n, cu = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([700], [0, 700]))
+    for S in (1, 5):
+        fa.fwd_paged_shaped(q[0], kc, vc, table, n, cu, 700, causal=False, key_begin=b.cuda(), key_end=e.cuda(), num_splits=S)
+        assert fa.debug_read_status() == 0
