@@ -44,13 +44,14 @@ __device__ __forceinline__ void capped_scores(const ScoreShape& s, const uint32_
       if (fabsf(__uint_as_float(u[i])) > s.poly_limit) y[i] = capped_far(s, __uint_as_float(u[i]));
   }
 }
-// n (even) raw products of a thread replaced by their capped scores.
+// n (even) raw products of each thread of a warp replaced by their capped scores (in place: with 16 of them, in the key
+// weights of 32 rows, copies spill, 68 and 74 us).
 template <int n>
 __device__ __forceinline__ void cap_in_place(const ScoreShape& s, float (&x)[n]) {
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < n; i += 2) m = fmax3(m, fabsf(x[i]), fabsf(x[i + 1]));
-  if (m <= s.poly_limit) {
+  if (__all_sync(0xffffffffu, m <= s.poly_limit)) {
 #pragma unroll
     for (int i = 0; i < n; i += 2) f2_unpack(capped_pair(s, x[i], x[i + 1]), x[i], x[i + 1]);
   } else {
