@@ -395,7 +395,7 @@ __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker,
     const long long row0 = (long long)b * p.N;
     auto begin = [&](int r) { return r < 0 ? 0 : r >= p.N ? p.Npad : min(shape_lo(p.shape, row0 + r, r), p.N); };
     auto end = [&](int r) {
-      return r < 0 ? 0 : r >= p.N ? p.Npad : max(shape_hi(p.shape, row0 + r, r, p.N, p.causal), 0);
+      return r < 0 ? 0 : r >= p.N ? p.Npad : shape_hi(p.shape, row0 + r, r, p.N, p.causal);
     };
     int a0 = 0, a1 = 0, b0 = 0, b1 = 0;      // this lane's keys: qa = i for [a0, a1), qb = i for [b0, b1)
     if (i <= p.N) {

@@ -79,7 +79,7 @@ __device__ __forceinline__ int shape_hi(const ScoreShape& s, long long row, int 
     hi = min(hi, pos + 1);
   else if (s.window > 0 && s.window < Lk - pos)
     hi = pos + s.window;
-  if (s.key_end) hi = min(hi, __ldg(s.key_end + row));
+  if (s.key_end) hi = min(hi, max(__ldg(s.key_end + row), 0));  // (any int32: differences of bounds stay in 32 bits)
   return hi;
 }
 

@@ -485,3 +485,21 @@ def test_rows_that_see_nothing_record_nothing():
     for S in (1, 5):
         fa.fwd_paged_shaped(q[0], kc, vc, table, n, cu, 700, causal=False, key_begin=b.cuda(), key_end=e.cuda(), num_splits=S)
         assert fa.debug_read_status() == 0
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("causal", [False, True])
+def test_ends_far_below_zero_and_begins_far_past_the_keys(cap, causal):
+    """Any int32 is a bound: leading rows with the lowest end and trailing ones with the highest begin see nothing."""
+    fa = need_gpu()
+    q, k, v, do = (t.cuda() for t in make(8, 1, 300, 2, 1, 128))
+    b, e = torch.full((300,), 3, dtype=torch.int32), torch.full((300,), 2 ** 31 - 1, dtype=torch.int32)
+    e[:40], b[280:] = -2 ** 31, 2 ** 31 - 1
+    kw = dict(key_begin=b[None].cuda(), key_end=e[None].cuda(), causal=causal, softcap=cap)
+    o, lse = fa.fwd_shaped(q, k, v, **kw)
+    grads = fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+    near = dict(kw, key_begin=b.clamp(0, 300)[None].cuda(), key_end=e.clamp(0, 300)[None].cuda())
+    o2, lse2 = fa.fwd_shaped(q, k, v, **near)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(x, y) for x, y in zip(grads, fa.bwd_shaped(q, k, v, o2, lse2, do, **near)))
+    assert bool((o[0, :40] == 0).all()) and bool((o[0, 280:] == 0).all()) and fa.debug_read_status() == 0
