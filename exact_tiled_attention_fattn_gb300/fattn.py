@@ -5,6 +5,10 @@ checks tensor shapes/dtypes, allocates outputs with PyTorch when the caller
 does not pass them, and forwards raw device pointers and the current CUDA
 stream. There is no fallback: if ``libfattn.so`` is missing or fails to load,
 every call raises.
+
+``stream=s`` runs a call on another stream than the current one. Workspaces that are not passed then come
+from the memory of ``s``; outputs that are not passed come from the current stream's, as the caller's own tensors
+do, so ``s`` has to be ordered behind the current stream (``s.wait_stream``) as for the inputs.
 """
 from __future__ import annotations
 
@@ -113,6 +117,16 @@ def _stream_handle(stream) -> int:
     if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {stream.device} but the current CUDA device is cuda:{torch.cuda.current_device()}")
     return int(stream.cuda_stream)
+
+
+def _scratch(need: int, device, stream):
+    """A workspace that the caller never sees, from the memory of the stream that the call runs on: dropped at return, it
+    goes to what that stream does next. (From the current stream's memory the next tensor there could have it
+    while ``stream`` still writes to it.)"""
+    if stream is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
 
 
 def _ptr(t):
@@ -382,7 +396,7 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     dv = torch.empty_like(v) if dv is None else dv
     need = bwd_workspace_size(B, Hq, N)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     st = lib.fattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                        B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), _ptr(workspace),
                        workspace.numel() * workspace.element_size(), _stream_handle(stream))
@@ -437,7 +451,7 @@ def decode_paged(q, kcache, vcache, block_table, seqlens, num_splits: int, scale
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     need = decode_workspace_size(B, Hq, d, num_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     st = lib.fattn_decode_paged(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), num_splits,
                                 _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size, maxp, num_pages, float(scale),
@@ -861,8 +875,7 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
         num_splits = choose_chunk_splits(B, Hq, d, int(max_seqlen_q), context)
     _need_cuda(workspace)
     if workspace is None and num_splits > 1:
-        workspace = torch.empty(max(fwd_paged_shaped_workspace_size(Tq, Hq, d, num_splits), 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(fwd_paged_shaped_workspace_size(Tq, Hq, d, num_splits), q.device, stream)
     st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
                                     _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                     block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
@@ -906,7 +919,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(max(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), q.device, stream)
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
                               min(int(window), _INT_MAX), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
@@ -945,7 +958,7 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(max(decode_workspace_size(B, Hq, d, num_splits), 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(decode_workspace_size(B, Hq, d, num_splits), q.device, stream)
     st = lib.fattn_decode_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
                                        num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                        block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),

@@ -503,3 +503,30 @@ def test_ends_far_below_zero_and_begins_far_past_the_keys(cap, causal):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert all(torch.equal(x, y) for x, y in zip(grads, fa.bwd_shaped(q, k, v, o2, lse2, do, **near)))
     assert bool((o[0, :40] == 0).all()) and bool((o[0, 280:] == 0).all()) and fa.debug_read_status() == 0
+
+
+def test_hidden_workspaces_on_another_stream():
+    """Calls on a busy stream of their own, with tensors taken and filled on the current one meanwhile: as without them."""
+    fa = need_gpu()
+    q, k, v, do = (x.cuda() for x in make(50, 1, 900, 8, 2, 128))
+    o, lse = fa.fwd_shaped(q, k, v, causal=True)
+    g = torch.Generator().manual_seed(3)
+    kc, vc = (torch.randn(90, 32, 2, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    table, lens, cu = torch.randperm(90, generator=g).int().reshape(1, 90).cuda(), *(
+        torch.tensor(x, dtype=torch.int32).cuda() for x in ([2800], [0, 70]))
+    calls = {fa.bwd_shaped_workspace_size(1, 8, 2, 900, 128): lambda s: fa.bwd_shaped(q, k, v, o, lse, do, causal=True, stream=s),
+             fa.bwd_workspace_size(1, 8, 900): lambda s: fa.bwd(q, k, v, o, lse, do, causal=True, stream=s),
+             fa.fwd_paged_shaped_workspace_size(70, 8, 128, 6): lambda s: fa.fwd_paged_shaped(q[0, :70], kc, vc, table, lens, cu, 70, num_splits=6, stream=s),
+             fa.decode_workspace_size(1, 8, 128, 9): lambda s: fa.decode_paged_shaped(q[0, :1], kc, vc, table, lens, 9, stream=s)}
+    s = torch.cuda.Stream()
+    for need, call in calls.items():
+        alone = call(None)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)          # about 10 ms: the call below starts behind it
+        got = call(s)
+        for _ in range(4):
+            torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(alone, got))
+    assert fa.debug_read_status() == 0
