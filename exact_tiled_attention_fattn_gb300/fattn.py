@@ -574,7 +574,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None
     elif scaling == "bands":
         def pair(turns):  # index (real) of the pair that turns `turns` times over the original length
             return half * math.log(original_length / (2.0 * math.pi * turns)) / math.log(base)
-        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), half - 1)
+        lo, hi = math.floor(pair(beta_fast)), math.ceil(pair(beta_slow))  # (outside the head too: the ramp keeps its slope)
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         f = f * (1.0 - ramp) + f / factor * ramp
         amplitude = 0.1 * math.log(factor) + 1.0

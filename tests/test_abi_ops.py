@@ -1,5 +1,6 @@
 """include/fattn_ops.h without a GPU: every declared entry point is exported and bound, and bad
 arguments are refused on the host before CUDA is touched."""
+import math
 import os
 import re
 
@@ -87,6 +88,25 @@ def test_rope_frequencies():
                 dict(rotary_dim=8, factor=0.5), dict(rotary_dim=8, base=0.0)):
         with pytest.raises(ValueError):
             F.rope_frequencies(**bad)
+
+
+@pytest.mark.parametrize("base,dim,length,factor", [(10000.0, 128, 4096, 8.0), (10000.0, 128, 131072, 4.0),
+                                                    (10000.0, 64, 128, 2.0), (500000.0, 128, 8192, 16.0), (10000.0, 2, 4096, 4.0)])
+def test_rope_bands_follow_the_turns(base, dim, length, factor):
+    """Pairs that turn more than beta_fast times over the original length keep their frequency, less than beta_slow have it
+    divided, and the ramp between is linear in the pair index with both of its ends where the turns put them, outside the
+    head as well."""
+    f, _ = F.rope_frequencies(dim, base)
+    g, _ = F.rope_frequencies(dim, base, scaling="bands", factor=factor, original_length=length)
+    turns = f * length / (2 * math.pi)
+    assert torch.equal(g[turns > 32], f[turns > 32])
+    assert torch.allclose(g[turns < 1], f[turns < 1] / factor, rtol=1e-14)
+    share = (1 - g / f) / (1 - 1 / factor)
+    lo, hi = (dim / 2 * math.log(length / (2 * math.pi * t)) / math.log(base) for t in (32, 1))
+    want = ((torch.arange(dim // 2) - math.floor(lo)) / (math.ceil(hi) - math.floor(lo))).clamp(0, 1)
+    assert torch.allclose(share, want.double(), atol=1e-6)
+    if (base, dim, length) == (10000.0, 128, 131072):
+        assert abs((g / f)[63].item() - 0.46) < 1e-12 and abs((g / f)[60].item() - 0.55) < 1e-12
 
 
 SHAPE_BAD = [dict(cap=-1.0), dict(cap=float("nan")), dict(cap=1e-44), dict(win=-1), dict(sl=A + 2), dict(kb=A + 1),
