@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
         const long long i = w / G;
         const int h = hkv * G + (int)(w - i * G);
         const float lse = __ldg(p.lse + h * p.lse_head + (q0 + i) * p.lse_row);
-        // a row that saw no key (lse = -inf) gives no weight
-        if (lse > -CUDART_INF_F) v.x = -lse * kLog2e;
+        // a row that saw no key (lse = -inf) gives no weight; a NaN stays one
+        if (lse != -CUDART_INF_F) v.x = -lse * kLog2e;
         if (p.shape.slopes) v.y = -__ldg(p.shape.slopes + h) * kLog2e;
         v.z = __int_as_float((int)i + off);
       }
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
       pos[nt][e] = iu + off;
       if (u < rows) {
         const float lse = __ldg(p.lse + h * p.lse_head + (long long)(q0 + iu) * p.lse_row);
-        if (lse > -CUDART_INF_F) nl[nt][e] = -lse * kLog2e;   // a row that saw no key gives no weight
+        if (lse != -CUDART_INF_F) nl[nt][e] = -lse * kLog2e;   // a row that saw no key gives no weight; a NaN stays one
         if (p.shape.slopes) slope[nt][e] = -__ldg(p.shape.slopes + h) * kLog2e;
       }
     }

@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (loaded != s) load(s);
         float w[BT / 32];
 #pragma unroll
-        for (int e = 0; e < BT / 32; ++e)  // rows past R or the chunk, and rows that saw no key, give nothing
-          w[e] = v[e] > -CUDART_INF_F ? -v[e] * kLog2e : -CUDART_INF_F;
+        for (int e = 0; e < BT / 32; ++e)  // rows past R or the chunk, and rows that saw no key, give nothing; a NaN stays one
+          w[e] = v[e] != -CUDART_INF_F ? -v[e] * kLog2e : -CUDART_INF_F;
         x.unit(j + 2, s2, t2);
         load(s2);
         if (!warp_wait(bar(kSFree + buf), phase, abort, p.status, p.wait_ns)) {

@@ -203,7 +203,8 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
  * q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: as fattn_fwd_paged (for single
  *   tokens q is [B, Hq, d] and cu_seqlens_q = 0, 1, ..., B); any page_size >= 1.
  * lse: DEVICE fp32, head h and row r at lse[h * lse_head + r * lse_row]: fattn_fwd_paged's [Hq,
- *   total_q] (total_q, 1) and fattn_decode_paged's [B, Hq] (1, Hq) both serve. A row of -inf gives nothing.
+ *   total_q] (total_q, 1) and fattn_decode_paged's [B, Hq] (1, Hq) both serve. A row of -inf gives nothing,
+ *   one of NaN makes the weights of the keys that it sees NaN.
  * weights_in (NULL: zeros; then decay is not used), weights_out: DEVICE fp32
  *   [B, Hkv, max_pages_per_seq * page_size]; they may be the same array.
  * max_seqlen_q: host upper bound on the chunks' queries; it chooses between the streaming kernel (few

@@ -395,3 +395,22 @@ def test_pages_past_32_bits(P, lq):
         assert fa.debug_read_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert torch.equal(got[0][8].reshape(-1, Hkv, d)[:70], got[0][6])     # in place as into other pages
+
+
+@pytest.mark.parametrize("P,Hq,lq", [(16, 4, 2), (16, 16, 2), (16, 8, 40), (3, 4, 40)])   # streaming (8, 32 rows), tensor cores, mma.sync
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_key_weights_of_a_nan_lse_are_nan(P, Hq, lq, cap):
+    """A NaN lse reaches every key that its query sees, and no other: -inf alone says that a row saw nothing."""
+    fa = need_gpu()
+    n = 300
+    kc, _, table, _, g = pool(5, [n], P, 1, 64, fill=0)
+    q = torch.randn(lq, Hq, 64, generator=g).to(torch.bfloat16).cuda()
+    lse = torch.full((Hq, lq), 3.0, device="cuda")
+    run = lambda: fa.key_weights_paged(q, kc.cuda(), table.cuda(), i32([n]), i32([0, lq]), lq, lse, softcap=cap)
+    clean = run()
+    lse[1, 0] = float("nan")                         # query 0 of the chunk, position n - lq
+    out = run()
+    seen = n - lq + 1
+    assert bool(out[0, 0, :seen].isnan().all()) and torch.equal(out[0, 0, seen:], clean[0, 0, seen:])
+    lse[1, 0] = -float("inf")
+    assert bool(torch.isfinite(run()).all()) and fa.debug_read_status() == 0
