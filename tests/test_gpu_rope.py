@@ -166,3 +166,42 @@ def test_append_skips_bad_tables():
                          i32([0, 1, 2, 3, 4]), f)
     assert fa.debug_read_status() == fa.FATTN_ERR_DEVICE_CHECK
     assert bool((vc[2, 3] == 1).all()) and vc.sum() == 64
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_fp32_precision(inter):
+    """Relative error of fp32 rotation, in the mean square. Rounding to p bits leaves an error of step / sqrt(12): an angle
+    within a quarter of half a turn, 24 bits, pi 2^-26 0.76 / 3.46 = 1.0e-8 (0.76: the mean square of the steps over the
+    binades below the quarter); sine and cosine 1.6e-8 each, 2.3e-8; the two products and their sum 3.4e-8 together:
+    4.2e-8 in all. An angle held in 24 bits of the whole half turn alone adds four times the first, 4.1e-8."""
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(1)
+    T, d = 2000, 128
+    x = torch.randn(T, 8, d, generator=g)
+    pos = torch.randint(0, 2 ** 20, (T,), generator=g, dtype=torch.int32)
+    f = fa.rope_frequencies(d)[0]
+    for inverse in (False, True):
+        y = fa.rope(x.cuda(), None, f.cuda(), pos.cuda(), interleaved=inter, inverse=inverse)
+        want, _ = rotate64(x.double().numpy(), pos.numpy(), f.numpy(), inter, 1.0, inverse)
+        err = np.sqrt(((y.double().cpu().numpy() - want) ** 2).sum() / (want ** 2).sum())
+        assert err < 5.0e-8, err
+
+
+def test_rope_quarter_turns():
+    """Angles at and next to the quarter turns, of either sign, where sine and cosine swap: 2^k turns of a position."""
+    fa = need_gpu()
+    turns = torch.tensor([0.25, 0.5, 0.75, 1.0, 0.125, 0.375, 0.625, 0.875, 0.25 - 1e-9, 0.25 + 1e-9, 0.125 - 1e-9, 0.125 + 1e-9,
+                          1e-9, 1 - 1e-9, 0.5 - 1e-9, 0.5 + 1e-9], dtype=torch.float64)
+    f = turns * 2 * np.pi
+    pos = torch.tensor([0, 1, -1, 2, 3, -3, 5, -7, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    x = torch.randn(len(pos), 2, 32)
+    for dtype in (torch.float32, torch.bfloat16):
+        for inverse in (False, True):
+            for inter in (False, True):
+                xd = x.to(dtype)
+                y = fa.rope(xd.cuda(), None, f.cuda(), pos.cuda(), interleaved=inter, inverse=inverse)
+                near = pos.abs().long() < 100          # (far out the reference's product with 2 pi is off by more)
+                near[-2:] = False
+                want, mag = rotate64(xd.double().numpy(), pos.numpy(), f.numpy(), inter, 1.0, inverse)
+                close(y[near.cuda()], want[near.numpy()], mag[near.numpy()], dtype)
+                assert bool(torch.isfinite(y).all())
