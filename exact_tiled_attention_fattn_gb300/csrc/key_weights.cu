@@ -238,7 +238,7 @@ template <int D>
 struct StreamLayout {
   static constexpr int kStage = kChunk * D * 2;    // 64-column halves of 16 rows x 128 bytes, 128-byte swizzle
   static constexpr int kOffBar = kWarps * kStages * kStage;
-  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
+  static constexpr int kOffAbort = kOffBar + kWarps * (kStages + 1) * 8;   // (and a barrier that nothing arrives on: test hook)
   static constexpr int kBytes = kOffAbort + kWarps * 8 + 1024;  // + slack to align the base to 1024 B
 };
 
@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = sb + warp * kStages * Lay::kStage, bars = sb + Lay::kOffBar + warp * kStages * 8;
+  const uint32_t ring = sb + warp * kStages * Lay::kStage, bars = sb + Lay::kOffBar + warp * (kStages + 1) * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + Lay::kOffAbort + warp * 8);
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) sm100::mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i <= kStages; ++i) sm100::mbar_init(bars + 8 * i, 1);
     *abort = 0;
     sm100::fence_mbar_init();
   }
@@ -343,7 +343,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) stream_kernel(const
   // whether a key of the sequence can be hidden from a query (one query sees all that come before it)
   const bool partial = (p.causal && m > 1) || sh.window > 0;
   int c = 0;
-  for (; c < mine; ++c) {
+  // test hook: a wait that runs out, with the first copies on their way
+  bool stalled = false;
+  if (p.debug_stall) {
+    if (lane == 0) stalled = !sm100::mbar_wait(bars + 8 * kStages, 0, abort, p.status, p.wait_ns);
+    stalled = __any_sync(0xffffffffu, stalled);
+  }
+  for (; c < mine && !stalled; ++c) {
     const int kt = first_key(c), key = kt + g + 8 * (lane & 1);   // (what lanes 0 and 1 of a quad write)
     float w_in = 0.f;
     if (p.w_in && (lane & 3) < 2 && key < end) w_in = __ldg(p.w_in + w_row + key);

@@ -414,3 +414,24 @@ def test_key_weights_of_a_nan_lse_are_nan(P, Hq, lq, cap):
     assert bool(out[0, 0, :seen].isnan().all()) and torch.equal(out[0, 0, seen:], clean[0, 0, seen:])
     lse[1, 0] = -float("inf")
     assert bool(torch.isfinite(run()).all()) and fa.debug_read_status() == 0
+
+
+def test_key_weights_stream_wait_runs_out():
+    """The streaming kernel's bounded waits: its copies in flight are waited for, no weight of a token is written, and
+    the next call is right."""
+    fa = need_gpu()
+    for n, d, Hq in ((500, 64, 2), (5, 128, 16)):
+        kc, _, table, _, g = pool(6, [n], 16, 1, d)
+        q, lse = torch.randn(1, Hq, d, generator=g).to(torch.bfloat16).cuda(), torch.zeros(Hq, 1, device="cuda")
+        args = (q, kc.cuda(), table.cuda(), i32([n]), i32([0, 1]), 1, lse)
+        want = fa.key_weights_paged(*args)
+        assert fa.debug_read_status() == 0
+        out = torch.full_like(want, -1.0)
+        fa.debug_set_wait_limit(1_000_000, True)
+        try:
+            fa.key_weights_paged(*args, out=out)
+            st = fa.debug_read_status()
+        finally:
+            fa.debug_set_wait_limit(0, False)
+        assert st == fa.FATTN_ERR_TIMEOUT and bool((out[..., :n] == -1).all())
+        assert torch.equal(fa.key_weights_paged(*args), want) and fa.debug_read_status() == 0
