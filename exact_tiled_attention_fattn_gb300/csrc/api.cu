@@ -380,6 +380,8 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FATTN_ERR_WORKSPACE;
 
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
   int err = 0;
   BwdParams p{};
   p.q = q; p.k = k; p.v = v; p.o = o; p.dout = dout; p.lse = lse;
@@ -392,7 +394,7 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
     p.shaped = 1;
     p.shape = *shape;
     p.ws_keys = reinterpret_cast<int2*>(static_cast<char*>(workspace) + vectors);
-    if (bwd_per_head(p))
+    if (bwd_per_head(p, sms))
       p.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + vectors + align256((size_t)B * npad * sizeof(int2)));
   }
   p.status = status_ptr(&err);
@@ -403,8 +405,6 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
       !encode_rows_map(&tv, v, (int)rows, Hkv, d, 128) || !encode_rows_map(&tdo, dout, (int)rows, Hq, d, 128) ||
       !encode_rows_map(&tdk, dk, (int)rows, Hkv, d, 32) || !encode_rows_map(&tdv, dv, (int)rows, Hkv, d, 32))
     return FATTN_ERR_CUDA;
-  const int sms = num_sms_current();
-  if (sms <= 0) return FATTN_ERR_CUDA;
   return launch_backward(p, tq, tk, tv, tdo, tdk, tdv, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 

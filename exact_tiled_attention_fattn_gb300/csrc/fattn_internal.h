@@ -161,8 +161,8 @@ struct BwdParams {
 
 // The shaped backward's dK/dV pass per query head, its fp32 shares added up afterwards, or per KV head, the group's heads
 // one after the other in an item. Room for the shares is asked for (bwd_shares) where there are no more (key tile, KV
-// head) items than SMs and they could leave SMs idle; bwd_per_head then weighs, in steps of 128 queries (about 1.2 us),
-// the longest item or the SMs' mean against the same with single heads, the shares' way through memory and the
+// head) items than the whole chip has SMs, a constant, as the workspace's size knows no device; bwd_per_head then weighs,
+// for the SMs that there are and in steps of 128 queries (about 1.2 us), the longest item or the SMs' mean against the same with single heads, the shares' way through memory and the
 // launch that adds them. A key tile is seen from all query tiles, at a mean half of them with causal, from a window's, and
 // with key ranges, which the host does not know, from a quarter.
 // Whole calls, causal, per KV head and per query head, d = 128 unless said: 997 rows, 8 heads over 2, d = 64 87 and 51 us; 2048
@@ -172,7 +172,7 @@ constexpr long long kPerHeadItems = 152;
 inline bool bwd_shares(int B, int Hq, int Hkv, int N) {
   return Hq > Hkv && (long long)B * Hkv * (((long long)N + 127) / 128) <= kPerHeadItems;
 }
-inline bool bwd_per_head(const BwdParams& p) {
+inline bool bwd_per_head(const BwdParams& p, int num_sms) {
   if (!bwd_shares(p.B, p.Hq, p.Hkv, p.N)) return false;
   const double nt = (p.N + 127) / 128, items = p.B * p.Hkv * nt, G = p.Hq / p.Hkv;
   double most = nt, mean = p.causal ? (nt + 1) / 2 : nt;
@@ -182,7 +182,7 @@ inline bool bwd_per_head(const BwdParams& p) {
   }
   if ((p.shape.key_begin || p.shape.key_end) && most > nt / 4) most = nt / 4 > 1 ? nt / 4 : 1;
   if (mean > most) mean = most;
-  const double all = items * G * mean / kPerHeadItems;
+  const double all = items * G * mean / num_sms;
   const double join = 2 + 2.0 * p.B * p.N * p.Hq * p.d * 1.3e-6;   // 8 bytes an element, 5 TB/s
   return (most > all ? most : all) + join < (G * most > all ? G * most : all);
 }
