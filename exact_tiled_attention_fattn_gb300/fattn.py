@@ -975,8 +975,9 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
     """Attention weight that cached tokens received: out[b, hkv, t] = decay * weights[b, hkv, t] + the sum over
     the heads of the group and the queries of chunk b of exp(s - lse), fp32 [B, Hkv, max_pages * page_size].
     q [Tq,Hq,d] and the chunk arguments as in ``fwd_paged``; ``lse`` [Hq,Tq] from the attention call, any strides
-    (``lse.t()`` of ``decode_paged``). ``weights`` None starts from zero; ``out`` may be ``weights``. Slots past a
-    sequence's length are 0, or, with ``out`` the same tensor as ``weights``, left as they are."""
+    (``lse.t()`` of ``decode_paged``). ``weights`` None starts from zero; ``out`` may be ``weights`` (which a call
+    whose bounded waits ran out leaves partly updated). Slots past a sequence's length are 0, or, with ``out`` the
+    same tensor as ``weights``, left as they are."""
     lib = load_library()
     _need_cuda(q, kcache, block_table, seqlens_k, cu_seqlens_q, weights, out)
     _need_cuda(lse, contiguous=False)

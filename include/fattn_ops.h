@@ -17,9 +17,11 @@
  * The conventions of fattn.h hold: DEVICE pointers owned by the caller, host
  * checks before anything is launched, work enqueued on `stream`, no
  * allocation, no synchronisation, problems found on the device recorded in the
- * status word (fattn_debug_read_status). Strides count elements. Calls that join
- * partials (num_splits > 1, shares per query head) leave outputs of no meaning after a
- * wait that ran out (FATTN_ERR_TIMEOUT), the others do not write them.
+ * status word (fattn_debug_read_status). Strides count elements. After a wait that ran
+ * out (FATTN_ERR_TIMEOUT) the outputs of the call have no meaning: what was finished before
+ * is written, the rest is not. fattn_key_weights_paged with weights_out == weights_in has
+ * then changed a part of its input: to repeat it, restore the weights first, or give it
+ * another weights_out from the start.
  */
 #ifndef FATTN_OPS_H
 #define FATTN_OPS_H
