@@ -249,9 +249,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   if (r >= rows) return;
   uint4* kc = static_cast<uint4*>(p.kcache);
   uint4* vc = static_cast<uint4*>(p.vcache);
-  for (int s = blockIdx.x * rows + r; s < m; s += gridDim.x * rows) {
+  // (unsigned: with tables of nearly 2^31 tokens the step past the last row leaves the int range)
+  for (unsigned s = blockIdx.x * rows + r; s < (unsigned)m; s += gridDim.x * rows) {
     const long long a = slot_unit(p, p.block_table, p.max_pages, b, h, __ldg(kept + s));
-    const long long d = slot_unit(p, p.dst_table, p.dst_max_pages, b, h, s);
+    const long long d = slot_unit(p, p.dst_table, p.dst_max_pages, b, h, (int)s);
     if (a < 0 || d < 0) {
       record_status(p.status, kStatusDeviceCheck);
       continue;

@@ -435,3 +435,18 @@ def test_key_weights_stream_wait_runs_out():
             fa.debug_set_wait_limit(0, False)
         assert st == fa.FATTN_ERR_TIMEOUT and bool((out[..., :n] == -1).all())
         assert torch.equal(fa.key_weights_paged(*args), want) and fa.debug_read_status() == 0
+
+
+def test_evict_of_nearly_2_31_tokens():
+    """The longest table: the walk of the moving blocks passes its last row without leaving 32 bits. Every token lies in
+    the pool's first page and goes to its second."""
+    fa = need_gpu()
+    P, pages = 65536, 32767
+    n = P * pages                                       # 2^31 - 65536
+    kc, vc = (torch.zeros(2, P, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc[0], vc[0] = 1.0, 2.0
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    w = torch.ones(1, 1, n, device="cuda")
+    m, _, kept = fa.evict_paged(kc, vc, table, i32([n]), w, n, dst_table=table + 1)
+    assert fa.debug_read_status() == 0 and m.item() == n and kept[0, 0, -1].item() == n - 1
+    assert bool((kc[1] == 1).all()) and bool((vc[1] == 2).all())
