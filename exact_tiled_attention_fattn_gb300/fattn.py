@@ -547,6 +547,14 @@ def debug_set_wait_limit(limit_ns: int = 0, stall: bool = False) -> None:
 _INT_MAX = 2 ** 31 - 1
 
 
+def _int(x, name: str) -> int:
+    """A C int argument (ctypes would take the lowest 32 bits of a larger one)."""
+    x = int(x)
+    if not -_INT_MAX - 1 <= x <= _INT_MAX:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
                      original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
     """(inv_freq float64 [rotary_dim / 2], amplitude) for ``rope``: angle per position of
@@ -802,7 +810,7 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
     if lse is None and want_lse:
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     st = lib.fattn_fwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
-                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX),
+                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"),
                               _ptr(key_begin), _ptr(key_end), _stream_handle(stream))
     _check("fattn_fwd_shaped", st)
     return out, lse
@@ -873,14 +881,15 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
         if window > 0:
             context = min(context, int(window) + int(max_seqlen_q))
         num_splits = choose_chunk_splits(B, Hq, d, int(max_seqlen_q), context)
+    num_splits = _int(num_splits, "num_splits")
     _need_cuda(workspace)
     if workspace is None and num_splits > 1:
         workspace = _scratch(fwd_paged_shaped_workspace_size(Tq, Hq, d, num_splits), q.device, stream)
     st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
                                     _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
-                                    block_table.shape[1], num_pages, Tq, int(max_seqlen_q), 1 if causal else 0,
-                                    float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX), _ptr(key_begin),
-                                    _ptr(key_end), int(num_splits), _ptr(workspace),
+                                    block_table.shape[1], num_pages, Tq, _int(max_seqlen_q, "max_seqlen_q"), 1 if causal else 0,
+                                    float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"), _ptr(key_begin),
+                                    _ptr(key_end), num_splits, _ptr(workspace),
                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
                                     _stream_handle(stream))
     _check("fattn_fwd_paged_shaped", st)
@@ -922,7 +931,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
         workspace = _scratch(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), q.device, stream)
     st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                               B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
-                              min(int(window), _INT_MAX), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
+                              _int(min(window, _INT_MAX), "window"), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check("fattn_bwd_shaped", st)
     return dq, dk, dv
@@ -951,6 +960,7 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
     _expect(out, q.shape, "out", q.dtype)
     _expect(lse, (B, Hq), "lse", torch.float32)
     _check_shape(slopes, Hq, None, None, None)
+    num_splits = _int(num_splits, "num_splits")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -962,7 +972,7 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
     st = lib.fattn_decode_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
                                        num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
                                        block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
-                                       min(int(window), _INT_MAX), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _int(min(window, _INT_MAX), "window"), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream_handle(stream))
     _check("fattn_decode_paged_shaped", st)
     return out, lse
@@ -1004,8 +1014,8 @@ def key_weights_paged(q, kcache, block_table, seqlens_k, cu_seqlens_q, max_seqle
         out = torch.empty(shape, dtype=torch.float32, device=q.device)
     st = lib.fattn_key_weights_paged(_ptr(q), _ptr(kcache), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q),
                                      _ptr(lse), lse.stride(0), lse.stride(1), _ptr(weights), _ptr(out), B, Hq, Hkv, d,
-                                     page_size, block_table.shape[1], num_pages, Tq, int(max_seqlen_q),
-                                     1 if causal else 0, float(scale), float(softcap), _ptr(slopes), min(int(window), _INT_MAX),
+                                     page_size, block_table.shape[1], num_pages, Tq, _int(max_seqlen_q, "max_seqlen_q"),
+                                     1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"),
                                      float(decay), _stream_handle(stream))
     _check("fattn_key_weights_paged", st)
     return out
@@ -1024,6 +1034,7 @@ def evict_paged(kcache, vcache, block_table, seqlens, weights, keep: int, recent
         raise TypeError("evict_paged takes bf16 caches")
     if seqlens.dtype != torch.int32:
         raise TypeError("seqlens must be int32")
+    keep, recent, first = _int(keep, "keep"), _int(recent, "recent"), _int(first, "first")
     B = seqlens.numel()
     _expect(seqlens, (B,), "seqlens")
     _check_paged_cache(kcache, vcache, block_table, B)
@@ -1038,16 +1049,16 @@ def evict_paged(kcache, vcache, block_table, seqlens, weights, keep: int, recent
     _expect(weights, (B, Hkv, maxp * page_size), "weights", torch.float32)
     _expect(out_weights, (B, Hkv, dst_pages * page_size), "out_weights", torch.float32)
     _expect(out_seqlens, (B,), "out_seqlens", torch.int32)
-    _expect(kept, (B, Hkv, int(keep)), "kept", torch.int32)
+    _expect(kept, (B, Hkv, keep), "kept", torch.int32)
     if out_weights is None:
         out_weights = torch.empty((B, Hkv, dst_pages * page_size), dtype=torch.float32, device=kcache.device)
     if out_seqlens is None:
         out_seqlens = torch.empty_like(seqlens)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(int(keep), 0)), dtype=torch.int32, device=kcache.device)
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=kcache.device)
     st = lib.fattn_evict_paged(_ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), _ptr(weights),
                                _ptr(dst_table), _ptr(out_seqlens), _ptr(out_weights), _ptr(kept), B, Hkv, d, page_size,
-                               maxp, num_pages, dst_pages, int(keep), int(recent), int(first),
+                               maxp, num_pages, dst_pages, keep, recent, first,
                                _stream_handle(stream))
     _check("fattn_evict_paged", st)
     return out_seqlens, out_weights, kept
