@@ -471,8 +471,8 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
     } else {
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        const float r = tanh_r(__uint_as_float(u[c]) * sh.capk);
-        y[c] = fmaf(-2.f * sh.cap2, r, sh.cap2);
+        const float z = __uint_as_float(u[c]) * sh.capk, r = tanh_r(fabsf(z));  // r <= 1/2: 4 r (1 - r) keeps its digits
+        y[c] = copysignf(fmaf(-2.f * sh.cap2, r, sh.cap2), z);
         f[c] = 4.f * r * (1.f - r);
       }
       if constexpr (kShape & kShapeFar) {  // products in the polynomial's range keep it

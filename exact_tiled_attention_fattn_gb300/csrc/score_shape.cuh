@@ -16,7 +16,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // tanh(z) = 1 - 2 r with r = 1 / (1 + e^{2z}): one exponential and one reciprocal. Its derivative is
-// 1 - tanh^2 = 4 r (1 - r), which keeps its relative precision where tanh saturates.
+// 1 - tanh^2 = 4 r (1 - r), which for z >= 0 keeps its relative precision where tanh saturates.
 // k2z = 2 z log2(e).
 __device__ __forceinline__ float tanh_r(float k2z) { return rcp_approx(1.f + ex2(k2z)); }
 

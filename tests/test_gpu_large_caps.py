@@ -100,3 +100,26 @@ def test_key_weights(cap, far, P, lq):
     tol = (1.1e-4 + 2e-6 * mag + lq * Hq * 2.0 ** -24) * want + 1e-30
     got = f64(out[0, :, :n])
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,d,causal,scale", [(16, 7, 1, 128, True, 0.3), (47, 9, 3, 64, False, 0.3), (300, 2, 1, 128, True, -0.3)])
+def test_gradient_of_saturated_scores(N, Hq, Hkv, d, causal, scale):
+    """Scores six to nine times the cap, positive ones in every other row, negative ones in the rest: the cap's derivative,
+    here 1e-5 to 1e-7, keeps its relative precision (a score's error of 1e-6 of itself moves it by 2 / cap times that,
+    2e-5: inside the gradients' bound)."""
+    fa = need_gpu()
+    cap = 5.0
+    q, k, v, do = (x * s for x, s in zip(make(N, 1, N, Hq, Hkv, d), (0.25, 0.25, 1, 1)))
+    q[..., 0] = 8.0 * (1 - 2 * (torch.arange(N) % 2))[:, None]
+    k[..., 0] = (torch.linspace(6, 9, N) * cap / (8.0 * scale))[torch.randperm(N, generator=torch.Generator().manual_seed(N))][:, None]
+    kw = dict(causal=causal, softcap=cap, scale=scale)
+    o, lse = fa.fwd_shaped(dev(q), dev(k), dev(v), **kw)
+    got = dict(zip(("dq", "dk", "dv"), fa.bwd_shaped(dev(q), dev(k), dev(v), o, lse, dev(do), **kw)))
+    assert fa.debug_read_status() == 0
+    lo, hi = R.ranges(N, N, 0, causal, 0)
+    ref = R.forward(f64(q[0]), f64(k[0]), f64(v[0]), scale, cap, None, lo, hi)
+    check_fwd(o[0], lse[0], ref)
+    g, a, e = R.backward(f64(q[0]), f64(k[0]), f64(v[0]), f64(o[0]), f64(lse[0]), f64(do[0]), scale, cap, None, lo, hi)
+    for n in got:
+        tol = H * 1.02 * (a[n] + np.abs(g[n])) + 2 * score_err(ref[3].max()) * e[n] + 1e-30
+        assert (np.abs(f64(got[n][0]) - g[n]) <= tol).all(), (n, (np.abs(f64(got[n][0]) - g[n]) / tol).max())
