@@ -89,7 +89,7 @@ extern "C" fattn_status fattn_rope_append_paged(const void* q, void* q_out, cons
 // The cap as a polynomial: tanh(z) = z (c0 + c1 z^2 + ... + c4 z^8) on |z| <= z_max, folded into powers of u =
 // z softcap / scale. Fewer terms on a shorter range where the last coefficient would not be an ordinary float (at d = 128
 // and its usual scale with caps above 3000): the Taylor terms 1, -1/3, 2/15 on |z| <= 0.08 (off by 17/315 z^6, 1.4e-8;
-// caps up to 1e8), or the first alone on |z| <= 1e-4 (z^2 / 3, 3e-9): with such caps that holds every score of use. (With a
+// caps to some 10^7), or the first alone on |z| <= 1e-4 (z^2 / 3, 3e-9): with such caps that holds every score of use. (With a
 // scale / softcap above 10^4 and a cap above 1, scores past the short range are off by 2^-22 of the cap.) Caps below 1e-15
 // go without: 1 / cap^2 has to be a float, and 2^-22 of such a cap is nothing.
 static void fold_cap(float scale, float softcap, const double (&c)[5], double z_max, ScoreShape* out) {

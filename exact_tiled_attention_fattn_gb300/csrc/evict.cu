@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_in_place_kernel(const Evict
 
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream) {
   // a cluster of four blocks for tables of more than one tile and few heads: the passes' re-reads go four times as fast
-  // (8 heads of 131072 tokens, the whole call: 189 us with one block a head, 128 with four); up to a tile the
+  // (8 heads of 131072 tokens, the whole call: 189 us with one block a head, 126 with four); up to a tile the
   // cluster's barriers cost what they bring (64 heads of 16384: 58 and 57 us), and with many heads more (512 heads of
   // 16384: 135 and 173 us)
   if ((long long)p.max_pages * p.page_size > kTile && (long long)p.B * p.Hkv * 4 <= num_sms)

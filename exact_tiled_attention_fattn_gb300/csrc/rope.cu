@@ -5,7 +5,7 @@
 // head, so the block forms the rows x rot / 2 (cos, sin) pairs once in shared
 // memory and then walks the tokens' heads in units of two 16-byte accesses, the first
 // ones loaded before the angles. About four units per thread (16384 tokens of 32 + 8 heads
-// of 128, bf16, 336 MB: 58 us, with one unit 66, with two loaded ahead 66, with four 94:
+// of 128, bf16, 336 MB: 58 us back to back, with one unit 66, with two loaded ahead 66, with four 94:
 // the registers cost more blocks than the loads bring).
 //
 // An angle is position * frequency modulo one turn. In fp32 the product loses a
