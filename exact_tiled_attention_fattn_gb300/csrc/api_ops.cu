@@ -108,18 +108,22 @@ static void fold_cap(float scale, float softcap, const double (&c)[5], double z_
 }
 
 // A score shape's own checks; fills *out. `scale` is the call's, `keys` the most that a sequence has: a window of that
-// many hides nothing, and the kernels' sums of positions and windows stay small without it.
-static fattn_status check_shape(float scale, float softcap, const float* slopes, int window, const int32_t* key_begin,
-                                const int32_t* key_end, long long keys, ScoreShape* out) {
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return FATTN_ERR_INVALID_ARG;
+// many hides nothing, nor does one whose sinks reach it, and the kernels' sums of positions, windows and sinks stay small
+// without them.
+static fattn_status check_shape(float scale, float softcap, const float* slopes, int window, int sinks, bool causal,
+                                const int32_t* key_begin, const int32_t* key_end, long long keys, ScoreShape* out) {
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0 || sinks < 0)
+    return FATTN_ERR_INVALID_ARG;
   // the cap's argument 2 log2(e) scale / softcap must be a number
   if (softcap > 0.f && !std::isfinite(2.f * 1.4426951f * scale / softcap)) return FATTN_ERR_INVALID_ARG;
   if (misaligned(slopes, 4) || misaligned(key_begin, 4) || misaligned(key_end, 4)) return FATTN_ERR_INVALID_ARG;
-  if (window >= keys) window = 0;
+  if (sinks > 0 && (key_begin || key_end)) return FATTN_ERR_UNSUPPORTED;
+  if (window >= keys || (sinks > 0 && sinks >= (causal ? keys - window : keys))) window = 0;
+  if (window == 0) sinks = 0;
   // a cap of 2^100 moves no score up to 2^88 in 32 bits (tanh z is z within z^3 / 3), and above that, as without it, the
   // largest score takes all the weight
   if (softcap >= 0x1p100f) softcap = 0.f;
-  *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, -1.f};
+  *out = {softcap, slopes, window, key_begin, key_end, 0.f, 0.f, 0.f, 0.f, {}, -1.f, -1.f, sinks};
   out->sl2 = scale * 1.4426950408889634f;
   out->cap2 = softcap * 1.4426950408889634f;
   out->capk = softcap > 0.f ? 2.f * out->sl2 / softcap : 0.f;
@@ -136,17 +140,18 @@ static fattn_status check_shape(float scale, float softcap, const float* slopes,
   return FATTN_OK;
 }
 
-extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
-                                         int Hkv, int N, int d, int causal, float scale, float softcap,
-                                         const float* slopes, int window, const int32_t* key_begin,
-                                         const int32_t* key_end, cudaStream_t stream) {
+// fattn_fwd_shaped and fattn_fwd_sinks.
+static fattn_status fwd_shaped_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                                    int Hkv, int N, int d, int causal, float scale, float softcap, const float* slopes,
+                                    int window, int sinks, const int32_t* key_begin, const int32_t* key_end,
+                                    cudaStream_t stream) {
   if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FATTN_ERR_INVALID_ARG;
   if (B == 0 || N == 0) return FATTN_OK;
   if (!q || !k || !v || !o || Hq % Hkv != 0) return FATTN_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(lse, 4))
     return FATTN_ERR_INVALID_ARG;
   PrefillParams p{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, N, &p.shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, sinks, causal != 0, key_begin, key_end, N, &p.shape);
   if (st != FATTN_OK) return st;
   if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
   const long long rows = (long long)B * N;
@@ -171,6 +176,21 @@ extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const voi
   return launch_prefill_tc(p, tq, tk, tv, to, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
+extern "C" fattn_status fattn_fwd_shaped(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                                         int Hkv, int N, int d, int causal, float scale, float softcap,
+                                         const float* slopes, int window, const int32_t* key_begin,
+                                         const int32_t* key_end, cudaStream_t stream) {
+  return fwd_shaped_impl(q, k, v, o, lse, B, Hq, Hkv, N, d, causal, scale, softcap, slopes, window, 0, key_begin, key_end,
+                         stream);
+}
+
+extern "C" fattn_status fattn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                                        int Hkv, int N, int d, int causal, float scale, float softcap,
+                                        const float* slopes, int window, int sinks, cudaStream_t stream) {
+  return fwd_shaped_impl(q, k, v, o, lse, B, Hq, Hkv, N, d, causal, scale, softcap, slopes, window, sinks, nullptr,
+                         nullptr, stream);
+}
+
 extern "C" size_t fattn_fwd_paged_shaped_workspace_size(int total_q, int Hq, int d, int num_splits) {
   if (total_q <= 0 || Hq <= 0 || d <= 0 || num_splits <= 1) return 0;
   const size_t rows = (size_t)total_q * Hq * num_splits;
@@ -186,7 +206,24 @@ extern "C" fattn_status fattn_fwd_paged_shaped(const void* q, const void* kcache
                                                const int32_t* key_end, int num_splits, void* workspace,
                                                size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end,
+  const fattn_status st = check_shape(scale, softcap, slopes, window, 0, causal != 0, key_begin, key_end,
+                                      (long long)max_pages_per_seq * page_size, &shape);
+  if (st != FATTN_OK) return st;
+  if (num_splits < 1) return FATTN_ERR_INVALID_ARG;
+  return fwd_paged_impl(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
+                        max_pages_per_seq, num_pages, total_q, max_seqlen_q, causal, scale, &shape, num_splits, workspace,
+                        workspace_bytes, stream);
+}
+
+extern "C" fattn_status fattn_fwd_paged_sinks(const void* q, const void* kcache, const void* vcache,
+                                              const int32_t* block_table, const int32_t* seqlens_k,
+                                              const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
+                                              int d, int page_size, int max_pages_per_seq, int num_pages, int total_q,
+                                              int max_seqlen_q, int causal, float scale, float softcap,
+                                              const float* slopes, int window, int sinks, int num_splits, void* workspace,
+                                              size_t workspace_bytes, cudaStream_t stream) {
+  ScoreShape shape{};
+  const fattn_status st = check_shape(scale, softcap, slopes, window, sinks, causal != 0, nullptr, nullptr,
                                       (long long)max_pages_per_seq * page_size, &shape);
   if (st != FATTN_OK) return st;
   if (num_splits < 1) return FATTN_ERR_INVALID_ARG;
@@ -209,7 +246,19 @@ extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const voi
                                          const int32_t* key_begin, const int32_t* key_end, void* workspace,
                                          size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st = check_shape(scale, softcap, slopes, window, key_begin, key_end, N, &shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, 0, causal != 0, key_begin, key_end, N, &shape);
+  if (st != FATTN_OK) return st;
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, &shape, workspace,
+                  workspace_bytes, stream);
+}
+
+extern "C" fattn_status fattn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                        const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
+                                        int d, int causal, float scale, float softcap, const float* slopes, int window,
+                                        int sinks, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  ScoreShape shape{};
+  const fattn_status st =
+      check_shape(scale, softcap, slopes, window, sinks, causal != 0, nullptr, nullptr, N, &shape);
   if (st != FATTN_OK) return st;
   return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, &shape, workspace,
                   workspace_bytes, stream);
@@ -221,9 +270,20 @@ extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kca
                                                   int max_pages_per_seq, int num_pages, float scale, float softcap,
                                                   const float* slopes, int window, void* workspace,
                                                   size_t workspace_bytes, cudaStream_t stream) {
+  return fattn_decode_paged_sinks(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
+                                  max_pages_per_seq, num_pages, scale, softcap, slopes, window, 0, workspace,
+                                  workspace_bytes, stream);
+}
+
+extern "C" fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const void* vcache,
+                                                 const int32_t* block_table, const int32_t* seqlens, int num_splits,
+                                                 void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                                 int max_pages_per_seq, int num_pages, float scale, float softcap,
+                                                 const float* slopes, int window, int sinks, void* workspace,
+                                                 size_t workspace_bytes, cudaStream_t stream) {
   ScoreShape shape{};
-  const fattn_status st =
-      check_shape(scale, softcap, slopes, window, nullptr, nullptr, (long long)max_pages_per_seq * page_size, &shape);
+  const fattn_status st = check_shape(scale, softcap, slopes, window, sinks, true, nullptr, nullptr,
+                                      (long long)max_pages_per_seq * page_size, &shape);
   if (st != FATTN_OK) return st;
   return decode_paged_impl(q, kcache, vcache, block_table, seqlens, num_splits, o, lse, B, Hq, Hkv, d, page_size,
                            max_pages_per_seq, num_pages, scale, &shape, workspace, workspace_bytes, stream);
@@ -241,7 +301,8 @@ extern "C" fattn_status fattn_key_weights_paged(const void* q, const void* kcach
     return FATTN_ERR_INVALID_ARG;
   KeyWeightsParams p{};
   const fattn_status st =
-      check_shape(scale, softcap, slopes, window, nullptr, nullptr, (long long)max_pages_per_seq * page_size, &p.shape);
+      check_shape(scale, softcap, slopes, window, 0, causal != 0, nullptr, nullptr, (long long)max_pages_per_seq * page_size,
+                  &p.shape);
   if (st != FATTN_OK) return st;
   // every weight is an fp32 output: within 1.3e-8, on a shorter range
   const double c[5] = {0.9999999868, -0.3333306794, 0.133247505, -0.05298423883, 0.01713134443};

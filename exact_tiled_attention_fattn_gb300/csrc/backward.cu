@@ -376,17 +376,25 @@ __device__ __forceinline__ void write_ds(uint32_t dp_col, const float (&pv)[64],
 enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2, kShapeFar = 4 };
 // Key tiles [top - n, top) that the rows of query tile i see, n >= 1: a tile whose rows see no
 // key visits one tile with everything masked (its dQ is the zero that this gives).
-__device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n) {
+// With sinks the walk down goes on below the window: step tile t < cut is key tile t - gap.
+__device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n, int& cut,
+                                                 int& gap) {
   const int first = i * BT, last = min(first + BT, p.N) - 1;
   const int lo = shape_lo(p.shape, (long long)b * p.N + first, first);
   const int hi = shape_hi(p.shape, (long long)b * p.N + last, last, p.N, p.causal);
   const int t0 = min(lo / BT, nt - 1);
   top = lo < hi ? (hi + BT - 1) / BT : t0 + 1;
-  n = max(top - t0, 1);
+  cut = gap = 0;
+  if (p.shape.sinks > 0) {
+    top = max(top, (shape_sinks(p.shape, last, p.N, p.causal) + BT - 1) / BT);
+    cut = t0;
+    gap = max(t0 - sink_blocks(p.shape.sinks, BT), 0);
+  }
+  n = max(top - (p.shape.sinks > 0 ? gap : t0), 1);
 }
 // The ranges seen from the keys: the queries that see key j are [qa_j, qb_j), as the bounds are
 // monotone: qa_j the first row whose end is above j, qb_j the first whose begin is. The dQ pass's
-// warps 2-3 write them for the dK/dV pass, 32 rows a warp at a time: row i is qa of the keys
+// warps 2-3 write them (a sink is seen to the last row, from its own on or, without causal, from the first) for the dK/dV pass, 32 rows a warp at a time: row i is qa of the keys
 // [end_{i-1}, end_i) and qb of the keys [begin_{i-1}, begin_i), row N that of the rest, and the
 // whole warp writes each row's keys. (Searching them per key and item in the dK/dV pass took 2 to 3 us
 // at the start of every item: packed documents, B=4 H=32 N=4096, 966 us for the whole call.)
@@ -413,8 +421,8 @@ __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker,
       const int r = (w - b * blocks) * 32 + l;
       const int x0 = __shfl_sync(0xffffffffu, a0, l), x1 = __shfl_sync(0xffffffffu, a1, l);
       const int y0 = __shfl_sync(0xffffffffu, b0, l), y1 = __shfl_sync(0xffffffffu, b1, l);
-      for (int k = x0 + lane; k < x1; k += 32) out[k].x = r;
-      for (int k = y0 + lane; k < y1; k += 32) out[k].y = r;
+      for (int k = x0 + lane; k < x1; k += 32) out[k].x = k < p.shape.sinks && !p.causal ? 0 : r;
+      for (int k = y0 + lane; k < y1; k += 32) out[k].y = k < p.shape.sinks ? p.N : r;
     }
   }
 }
@@ -422,7 +430,8 @@ __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker,
 // visits one with everything masked: its dK and dV are the zeros that this gives).
 __device__ __forceinline__ void shaped_query_tiles(const BwdParams& p, int b, int j, int nt, int& i0, int& n) {
   const int2* keys = p.ws_keys + (size_t)b * p.Npad;
-  const int first = __ldg(&keys[j * BT].x), last = __ldg(&keys[min((j + 1) * BT, p.N) - 1].y);
+  const int first = __ldg(&keys[j * BT].x);
+  const int last = max(__ldg(&keys[j * BT].y), __ldg(&keys[min((j + 1) * BT, p.N) - 1].y));  // (the first key: a sink's end)
   // (clamped, so that even a workspace the dQ pass did not finish keeps the tiles inside the sequence)
   i0 = max(min(first / BT, nt - 1), 0);
   n = max(min(last / BT + (last % BT != 0), nt) - i0, 1);
@@ -430,16 +439,16 @@ __device__ __forceinline__ void shaped_query_tiles(const BwdParams& p, int b, in
 
 // One thread's 32 columns of raw products u: pv = P o f with P = 2^(score + nl) and f the factor that
 // the cap puts on dS (1 - tanh^2), and P itself as bf16 pairs into pk (kPack). Column c lies at
-// distance |dist + step c| and is visible iff va <= c < vb; nl is its row's -lse log2(e), per column
+// distance |dist + step c| and is visible iff va <= c < vb or c < vs; nl is its row's -lse log2(e), per column
 // (kCols, nlv) or one for all.
 template <int kShape, bool kCols, bool kPack>
 __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uint32_t (&u)[32], float dist, float step,
-                                           int va, int vb, const float* nlv, float nl, float* pv, uint32_t* pk) {
+                                           int va, int vb, int vs, const float* nlv, float nl, float* pv, uint32_t* pk) {
   const ScoreShape& sh = p.shape;
-  const bool edge = !__all_sync(0xffffffffu, va <= 0 && vb >= 32);
-  const uint32_t vis = vb <= 0 || va >= 32 || va >= vb
-                           ? 0u
-                           : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)));
+  const bool edge = !__all_sync(0xffffffffu, (va <= 0 && vb >= 32) || vs >= 32);
+  const uint32_t vis = (vb <= 0 || va >= 32 || va >= vb
+                            ? 0u
+                            : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)))) | low_bits(vs);
   constexpr bool cap = kShape & kShapeCap, bias = kShape & kShapeBias;
   float y[32], f[32];
   if constexpr (cap) {
@@ -834,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t u[32];
             tmem_ld32(s_col + 32 * q, u);
             const int i32 = i * BT + cb + 32 * q;  // query of the first column
-            shaped_p32<kShape, true, true>(p, slope2, u, (float)(i32 - (j * BT + r)), 1.f, qa - i32, qb - i32,
+            shaped_p32<kShape, true, true>(p, slope2, u, (float)(i32 - (j * BT + r)), 1.f, qa - i32, qb - i32, 0,
                                    vec + cb + 32 * q, 0.f, pv + 32 * q, pk);
             tmem_st16(s_col + 16 * q, pk);
           }
@@ -1011,12 +1020,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = head / p.Hq;
     h = head - b * p.Hq;
   };
-  // key tiles [top - jn, top) of an item, from the highest down
-  auto tiles = [&](int b, int i, int& top, int& jn) {
-    if constexpr (kShaped)
-      shaped_key_tiles(p, b, i, nt, top, jn);
-    else
+  // key tiles [top - jn, top) of an item, from the highest down; with sinks tile t < cut stands for t - gap
+  auto tiles = [&](int b, int i, int& top, int& jn, int& cut, int& gap) {
+    if constexpr (kShaped) {
+      shaped_key_tiles(p, b, i, nt, top, jn, cut, gap);
+    } else {
       top = jn = p.causal ? i + 1 : nt;
+      cut = gap = 0;
+    }
   };
 
   if (warp == 0) {
@@ -1028,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
         int b, h, i;
         item(it, b, h, i);
-        int top, jn;
-        tiles(b, i, top, jn);
+        int top, jn, cut, gap;
+        tiles(b, i, top, jn, cut, gap);
         const int hkv = h / G;
         for (int j = 0; j < jn; ++j) {
           // K_j (stage j mod 3) and V_j (stage j mod 2) land on one barrier, QKvFull j mod 2:
@@ -1043,7 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(bar(kQKvFull + vs), 2 * Lay::kTile);
-          const int kt = top - 1 - j;  // key tiles from the diagonal down
+          int kt = top - 1 - j;  // key tiles from the diagonal down
+          if (kShaped && kt < cut) kt -= gap;
           load_tile<D>(sb + Lay::kOffK + ks * Lay::kTile, &tk, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           load_tile<D>(sb + Lay::kOffV + vs * Lay::kTile, &tv, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           ++nk;
@@ -1102,8 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
         int b, h, i;
         item(it, b, h, i);
-        int top, jn;
-        tiles(b, i, top, jn);
+        int top, jn, cut, gap;
+        tiles(b, i, top, jn, cut, gap);
         if (!mbar_wait(bar(kQFull), nq & 1, abort, p.status, p.wait_ns)) break;
         ++nq;
         if (!issue_s(n) || !issue_dp(n)) break;
@@ -1207,13 +1219,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
       int b, h, i;
       item(it, b, h, i);
-      int top, jn;
-      tiles(b, i, top, jn);
+      int top, jn, cut, gap;
+      tiles(b, i, top, jn, cut, gap);
       const int qrow = i * BT + r;
-      // shaped: the keys [klo, khi) that this thread's query sees
-      int klo = 0, khi = 0;
+      // shaped: the keys [klo, khi) and [0, ksink) that this thread's query sees
+      int klo = 0, khi = 0, ksink = 0;
       if constexpr (kShaped) {
         if (qrow < p.N) {
+          ksink = shape_sinks(p.shape, qrow, p.N, p.causal);
           klo = shape_lo(p.shape, (long long)b * p.N + qrow, qrow);
           khi = shape_hi(p.shape, (long long)b * p.N + qrow, qrow, p.N, p.causal);
         }
@@ -1239,9 +1252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 2; ++q) {
             uint32_t u[32];
             tmem_ld32(s_col + 32 * q, u);
-            const int kb = (top - 1 - j) * BT + cb + 32 * q;  // key of the first column
-            shaped_p32<kShape, false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, nullptr, nl2, pv + 32 * q,
-                                     nullptr);
+            const int vt = top - 1 - j;
+            const int kb = (vt - (vt < cut ? gap : 0)) * BT + cb + 32 * q;  // key of the first column
+            shaped_p32<kShape, false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, ksink - kb, nullptr, nl2,
+                                             pv + 32 * q, nullptr);
           }
         } else {
           uint32_t u[64];

@@ -81,10 +81,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // Partial (lse_s, O_s / l_s) of one non-empty split [t0, t1) of sequence b
 // for the query heads h0 .. h0 + rows_valid - 1 of KV head hkv.
-// Shaped: the scores get p.shape's cap and distance bias; the query sits at position `qpos`.
+// Shaped: the scores get p.shape's cap and distance bias; the query sits at position `qpos`. With sinks [t0, t1) counts
+// tokens without the ones between sinks and window: from `cut` on token t is t + gap, and tokens below `lo` that are no
+// sinks are hidden.
 template <int D, bool kPage16, bool kShaped>
 __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* smem, int split, int b, int hkv, int h0,
-                                             int rows_valid, int t0, int t1, int qpos) {
+                                             int rows_valid, int t0, int t1, int qpos, int cut, int gap, int lo) {
   using Lay = DecodeLayout<D>;
   constexpr int U = D / 8;
   const uint32_t sbase = smem_u32(smem);
@@ -122,14 +124,16 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
   auto load_chunk = [&](int c, int st) -> uint32_t {
     const int tb = t0 + c * kChunk;
     const int r = lane & 15;
-    const int t = tb + r;
+    int t = tb + r;
     int page = 0;
     bool ok = false;
     if (lane < 16 && t < t1) {
+      if (kShaped && t >= cut) t += gap;
       const int pi = kPage16 ? (t >> 4) : t / p.page_size;
       page = table[pi];
       ok = (unsigned)page < (unsigned)p.num_pages;
       if (!ok) record_status(p.status, kStatusDeviceCheck);
+      if (kShaped && t < lo && t >= p.shape.sinks) ok = false;
     }
     const uint32_t vmask = __ballot_sync(0xffffffffu, ok);
     const uint32_t kdst = wbase + st * Lay::kStageUnits * 16;
@@ -140,7 +144,8 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
       const int rr = idx / U, u = idx % U;
       const int pg = __shfl_sync(0xffffffffu, page, rr);
       const bool okr = (vmask >> rr) & 1u;
-      const int tt = tb + rr;
+      int tt = tb + rr;
+      if (kShaped && tt >= cut) tt += gap;
       const int slot = kPage16 ? (tt & 15) : (tt % p.page_size);
       const size_t off = okr ? ((((size_t)pg * p.page_size + slot) * p.Hkv + hkv) * D + u * 8) : 0;
       const int nbytes = okr ? 16 : 0;
@@ -211,8 +216,9 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
     }
     // scale into the log2 domain, mask missing tokens, running max per row
     float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-    // shaped: distance of this thread's first token
-    const float dist = kShaped ? (float)(qpos - (t0 + (warp + i * kWarps) * kChunk + 2 * (lane & 3))) : 0.f;
+    // shaped: distance of this thread's first token (the gap is whole pages: it may end inside a chunk of small ones)
+    const int tok0 = t0 + (warp + i * kWarps) * kChunk + 2 * (lane & 3);
+    const float dist = kShaped ? (float)(qpos - tok0) : 0.f;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
@@ -226,7 +232,11 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
             continue;
           }
           y = p.shape.cap > 0.f ? s[nt][j] : s[nt][j] * sl2;
-          if (p.shape.slopes) y = fmaf(j < 2 ? slope0 : slope1, dist - (float)(nt * 8 + (j & 1)), y);
+          if (p.shape.slopes) {
+            float away = dist - (float)(nt * 8 + (j & 1));
+            if (tok0 + nt * 8 + (j & 1) >= cut) away -= (float)gap;
+            y = fmaf(j < 2 ? slope0 : slope1, away, y);
+          }
         } else {
           y = s[nt][j] * sl2;
         }
@@ -380,7 +390,8 @@ __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(co
   // most that W consecutive tokens touch, counted from the page of the first visible token
   int seen_pages = p.max_pages_per_seq;
   if (kShaped && p.shape.window > 0 && p.shape.window <= cap - p.page_size)
-    seen_pages = min(seen_pages, (p.shape.window + p.page_size - 2) / p.page_size + 1);
+    seen_pages = min(seen_pages, (p.shape.window + p.page_size - 2) / p.page_size + 1 +
+                                     sink_blocks(p.shape.sinks, p.page_size));
   const int chunk_pages = (seen_pages + p.num_splits - 1) / p.num_splits;
   const long long span = (long long)chunk_pages * p.page_size;
   for (;;) {
@@ -407,6 +418,14 @@ __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(co
       lo = L - p.shape.window;
       first = lo / p.page_size * p.page_size;
     }
+    // with sinks the tokens between them and the window's first page are left out of the count
+    int cut = 0x7fffffff, gap = 0;
+    if (kShaped && p.shape.sinks > 0 && first > 0) {
+      cut = min(sink_blocks(p.shape.sinks, p.page_size), first / p.page_size) * p.page_size;
+      gap = first - cut;
+      L -= gap;
+      first = 0;
+    }
     const int nvalid = (int)((L - first + span - 1) / span);   // non-empty splits of this sequence
     const long long t0 = first + (long long)split * span;
     if (t0 >= L) {  // empty split: mark it, and a sequence with no key at all gets O = 0, lse = -inf
@@ -415,8 +434,9 @@ __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(co
       if (split == 0) merge_group<D>(p, b, h0, rows_valid, 0);
       continue;
     }
-    decode_split<D, kPage16, kShaped>(p, smem, split, b, hkv, h0, rows_valid, max((int)t0, lo),
-                                      (int)min((long long)L, t0 + span), L - 1);
+    const int from = kShaped && p.shape.sinks > 0 ? (int)t0 : max((int)t0, lo);
+    decode_split<D, kPage16, kShaped>(p, smem, split, b, hkv, h0, rows_valid, from, (int)min((long long)L, t0 + span),
+                                      L + gap - 1, cut, gap, lo);
     // publish the partial, count it, and let the last split of the group merge
     __threadfence();
     __syncthreads();

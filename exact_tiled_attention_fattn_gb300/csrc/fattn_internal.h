@@ -32,7 +32,11 @@ struct ScoreShape {
   // largest |u| whose cap, taken as a bound of capped scores of either sign, is at most 96 (log2
   // units) above them: exponents against it are those of normal floats
   float bound_limit;
+  int sinks;                // with a window: keys below this stay visible (j <= pos still holds if causal); no key ranges then
 };
+
+// Blocks (pages, tiles) that the first `sinks` keys touch.
+__host__ __device__ inline int sink_blocks(int sinks, int block) { return sinks > 0 ? (sinks - 1) / block + 1 : 0; }
 
 // Problem description shared by both prefill kernels.
 struct PrefillParams {
@@ -178,7 +182,8 @@ inline bool bwd_per_head(const BwdParams& p, int num_sms) {
   double most = nt, mean = p.causal ? (nt + 1) / 2 : nt;
   if (p.shape.window > 0) {
     const double seen = (p.causal ? 1.0 : 2.0) * p.shape.window / 128 + 1;
-    if (seen < most) most = seen;
+    if (seen < mean) mean = seen;
+    if (seen < most && !p.shape.sinks) most = seen;   // (the sinks' tile is seen from all query tiles)
   }
   if ((p.shape.key_begin || p.shape.key_end) && most > nt / 4) most = nt / 4 > 1 ? nt / 4 : 1;
   if (mean > most) mean = most;

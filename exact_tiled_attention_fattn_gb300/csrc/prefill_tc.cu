@@ -190,6 +190,9 @@ struct Item {
   // shaped variant: tile t visits K/V tiles [top[t] - n[t], top[t]); the item's steps run from
   // tile jtop - 1 down to jbot, over both tiles' ranges (n = 0 as well where no row sees a key)
   int top[2], jtop, jbot;
+  // shaped, with sinks: steps count tiles without the ones that no row sees between the sinks and the window, so tile
+  // j < cut is K/V tile j - gap (both tiles of the item go by the first one's window)
+  int cut, gap;
   int split;  // the run of key tiles that the item takes
   bool valid;
 };
@@ -237,7 +240,7 @@ __device__ __forceinline__ int item_index(const Schedule& s, int k) {
 template <bool kShaped, bool kSplits>
 __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedule& s, int it) {
   Item x;
-  x.top[0] = x.top[1] = x.jtop = x.jbot = 0;
+  x.top[0] = x.top[1] = x.jtop = x.jbot = x.cut = x.gap = 0;
   const int per_group = s.group * s.pairs;
   const int g = it / per_group;
   const int rem = it - g * per_group;
@@ -281,14 +284,20 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
     x.n[0] = x.n[1] = 0;
     x.jbot = 1 << 30;
     if (x.valid) {
+      const bool sinks = p.shape.sinks > 0;
+      if (sinks) {
+        x.cut = shape_lo(p.shape, (long long)x.row0 + x.base, x.base + x.off) / BN;
+        x.gap = max(x.cut - sink_blocks(p.shape.sinks, BN), 0);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t && !has_b) continue;
         const int first = x.base + t * BM, last = min(first + BM, x.L) - 1;
         const int lo = shape_lo(p.shape, (long long)x.row0 + first, first + x.off);
-        const int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
+        int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
+        if (sinks) hi = max(hi, shape_sinks(p.shape, last + x.off, x.Lk, p.causal));
         if (lo < hi) {
-          const int t0 = lo / BN, n = (hi + BN - 1) / BN - t0;
+          const int t0 = sinks ? x.gap : lo / BN, n = (hi + BN - 1) / BN - t0;
           int from = t0;
           x.top[t] = t0 + n;
           if constexpr (kSplits) {
@@ -468,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // same swizzled layout as one 128-row box (page_size is a multiple of 8 rows).
         auto issue_kv = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, int j, bool is_v) {
           (void)is_v;
+          if constexpr (kShaped) j -= j < x.cut ? x.gap : 0;
           if constexpr (kPaged) {
             const int P = p.page_size, per = BN / P;  // per <= 8 (page_size >= 16)
             const int i = lane;                       // this lane's page of the tile
@@ -894,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int e = shape_hi(p.shape, (long long)x.row0 + r1, r1 + x.off, x.Lk, p.causal);
           out = a >= e || lo < a / BN * BN || hi > (e + BN - 1) / BN * BN;
         }
-        if (lo < hi && out) record_status(p.status, kStatusDeviceCheck);
+        if (lo < hi && out && p.shape.sinks == 0) record_status(p.status, kStatusDeviceCheck);
       };
       if (nt == 0) {
         release_mask();
@@ -1003,19 +1013,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++ns;
         tc_fence_after();
+        // first key of the tile; shaped: the row's sinks are keys [0, sink_lim)
+        const int kbase = (kShaped ? (j < x.cut ? j - x.gap : j) : j) * BN;
+        const int sink_lim = kShaped ? shape_sinks(p.shape, pos, x.Lk, p.causal) : 0;
+        // columns [32 c, 32 c + 32) that are visible, as bits: keys [lo, lim) and the sinks
+        auto visible = [&](int c) -> uint32_t {
+          const int first = kbase + 32 * c, a = max(lo - first, 0), e = min(lim - first, 32);
+          return (a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u) | low_bits(sink_lim - first);
+        };
         if constexpr (kCap) {
           // ---- capped scores: two rolled walks over the tile's 128 columns, 32 at a time from TMEM. The
           // cap triples the instructions of a column; unrolled over 128 of them (12 KB and more, two
           // forms) the eight warps starved for instructions (1.2 of 5 cycles an issue), rolled they stay
           // in the instruction cache.
           const ScoreShape& sh = p.shape;
-          const int v0 = lo - j * BN, v1 = lim - j * BN;  // visible columns [v0, v1)
-          const bool edge = __any_sync(0xffffffffu, v0 > 0 || v1 < BN);
-          // columns [32 c, 32 c + 32) that are visible, as bits
-          auto visible = [&](int c) -> uint32_t {
-            const int a = max(v0 - 32 * c, 0), e = min(v1 - 32 * c, 32);
-            return a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u;
-          };
+          const bool edge = __any_sync(0xffffffffu, (kbase < lo || kbase + BN > lim) && kbase + BN > sink_lim);
           // Against what a row's exponentials are taken, by row, so that a row does not depend on its
           // neighbours: while no |u| of 32 columns exceeds bound_limit, the cap of the largest |u| bounds
           // their capped scores and lies so close to the largest of them that the exponentials against
@@ -1130,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(y[e]);
                   if constexpr (kBias) {
-                    const float dist = (float)(pos - j * BN - 32 * c);
+                    const float dist = (float)(pos - kbase - 32 * c);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                       u[e] = __float_as_uint(fmaf(slope2, fabsf(dist - (float)e), __uint_as_float(u[e])));
@@ -1200,7 +1212,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
         float s[BN];
-        const int kbase = j * BN;
         bool masked = kbase + BN > lim;  // causal diagonal tile or sequence end
         if constexpr (kMasked) {
           // masked scores s scale + M (natural-log units; log2(e) is applied with the
@@ -1256,8 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarSFree + t));
           }
         }
-        const bool edge = kShaped && (masked || kbase < lo);
-        const uint32_t span = kShaped ? (uint32_t)max(lim - lo, 0) : 0u, first_key = (uint32_t)(lo - kbase);
+        const bool edge = kShaped && (masked || kbase < lo) && kbase + BN > sink_lim;
         if constexpr (kBias) {
           const float dist = (float)(pos - kbase);
           const float mul = p.shape.sl2;
@@ -1279,8 +1289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kShaped) {
           if (edge) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if ((uint32_t)c - first_key >= span) s[c] = !kBias && neg ? CUDART_INF_F : -CUDART_INF_F;
+            for (int w = 0; w < BN / 32; ++w) {
+              const uint32_t vis = visible(w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((vis >> c) & 1u)) s[32 * w + c] = !kBias && neg ? CUDART_INF_F : -CUDART_INF_F;
+            }
           }
           masked = false;
         }

@@ -83,4 +83,11 @@ __device__ __forceinline__ int shape_hi(const ScoreShape& s, long long row, int 
   return hi;
 }
 
+// Keys [0, this) of the query at pos are visible beside [lo, hi): the sinks.
+__device__ __forceinline__ int shape_sinks(const ScoreShape& s, int pos, int Lk, bool causal) {
+  return min(s.sinks, causal ? min(pos + 1, Lk) : Lk);
+}
+// The lowest n of 32 bits, any n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 }  // namespace fattn

@@ -70,6 +70,13 @@ SIGNATURES_OPS = {
                               _vp, _vp, _vp, _sz, _vp]),
     "fattn_decode_paged_shaped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
                                        _i, _vp, _sz, _vp]),
+    "fattn_fwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i, _vp]),
+    "fattn_bwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i,
+                             _vp, _sz, _vp]),
+    "fattn_fwd_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                   _f, _vp, _i, _i, _i, _vp, _sz, _vp]),
+    "fattn_decode_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
+                                      _i, _i, _vp, _sz, _vp]),
     "fattn_key_weights_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                                      _i, _i, _f, _f, _vp, _i, _f, _vp]),
     "fattn_evict_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
@@ -784,13 +791,23 @@ def _check_shape(slopes, Hq, key_begin, key_end, range_shape):
     _expect(key_end, range_shape, "key_end", torch.int32)
 
 
+def _sinks(sinks, key_begin=None, key_end=None) -> int:
+    """The sinks argument; 0 takes the call without them."""
+    sinks = _int(min(sinks, _INT_MAX), "sinks")
+    if sinks and (key_begin is not None or key_end is not None):
+        raise ValueError("sinks and key ranges exclude each other")
+    return sinks
+
+
 def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softcap: float = 0.0, slopes=None,
-               window: int = 0, key_begin=None, key_end=None, out=None, lse=None, want_lse: bool = True, stream=None):
+               window: int = 0, key_begin=None, key_end=None, out=None, lse=None, want_lse: bool = True, stream=None,
+               sinks: int = 0):
     """Prefill with shaped scores: s = scale q.k, then s = softcap tanh(s / softcap) (softcap > 0), then
     s -= slopes[h] |i - j| (slopes fp32 [Hq]); key j is visible iff j <= i (causal), |i - j| < window
     (window > 0) and key_begin[b, i] <= j < key_end[b, i] (int32 [B, N], non-decreasing along N:
-    ``document_ranges``). q [B,N,Hq,d], k, v [B,N,Hkv,d] bf16, d 64 or 128. Returns (O, lse [B,Hq,N]); a row that
-    sees no key gets O = 0, lse = -inf."""
+    ``document_ranges``). ``sinks``: with a window, the first keys of the sequence that stay visible to every row
+    (j <= i if causal; not with key ranges). q [B,N,Hq,d], k, v [B,N,Hkv,d] bf16, d 64 or 128. Returns (O, lse [B,Hq,N]);
+    a row that sees no key gets O = 0, lse = -inf."""
     lib = load_library()
     _need_cuda(q, k, v, out, lse)
     if not (q.dtype == k.dtype == v.dtype == torch.bfloat16):
@@ -809,10 +826,13 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
-    st = lib.fattn_fwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d,
-                              1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"),
-                              _ptr(key_begin), _ptr(key_end), _stream_handle(stream))
-    _check("fattn_fwd_shaped", st)
+    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d, 1 if causal else 0, float(scale),
+            float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
+    sinks = _sinks(sinks, key_begin, key_end)
+    if sinks:
+        _check("fattn_fwd_sinks", lib.fattn_fwd_sinks(*head, sinks, _stream_handle(stream)))
+    else:
+        _check("fattn_fwd_shaped", lib.fattn_fwd_shaped(*head, _ptr(key_begin), _ptr(key_end), _stream_handle(stream)))
     return out, lse
 
 
@@ -847,8 +867,8 @@ def choose_chunk_splits(batch: int, Hq: int, d: int, max_seqlen_q: int, max_cont
 def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int, causal: bool = True,
                      scale: float | None = None, softcap: float = 0.0, slopes=None, window: int = 0, key_begin=None,
                      key_end=None, out=None, lse=None, want_lse: bool = True, num_splits: int | None = None,
-                     workspace=None, stream=None):
-    """``fwd_paged`` with the shaped scores of ``fwd_shaped``; a chunk's queries sit at the last positions
+                     workspace=None, stream=None, sinks: int = 0):
+    """``fwd_paged`` with the shaped scores (and sinks) of ``fwd_shaped``; a chunk's queries sit at the last positions
     of their sequence's context. key_begin / key_end int32 [Tq], keys of the row's sequence. ``num_splits`` cuts
     every query tile's keys into runs that are joined at the end (None: ``choose_chunk_splits``); their partials
     take a ``workspace`` of fwd_paged_shaped_workspace_size bytes (allocated when None).
@@ -879,20 +899,22 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
     if num_splits is None:
         context = block_table.shape[1] * page_size
         if window > 0:
-            context = min(context, int(window) + int(max_seqlen_q))
+            context = min(context, int(window) + int(max_seqlen_q) + int(sinks))
         num_splits = choose_chunk_splits(B, Hq, d, int(max_seqlen_q), context)
     num_splits = _int(num_splits, "num_splits")
     _need_cuda(workspace)
     if workspace is None and num_splits > 1:
         workspace = _scratch(fwd_paged_shaped_workspace_size(Tq, Hq, d, num_splits), q.device, stream)
-    st = lib.fattn_fwd_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k),
-                                    _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
-                                    block_table.shape[1], num_pages, Tq, _int(max_seqlen_q, "max_seqlen_q"), 1 if causal else 0,
-                                    float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"), _ptr(key_begin),
-                                    _ptr(key_end), num_splits, _ptr(workspace),
-                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                    _stream_handle(stream))
-    _check("fattn_fwd_paged_shaped", st)
+    head = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q), _ptr(out),
+            _ptr(lse), B, Hq, Hkv, d, page_size, block_table.shape[1], num_pages, Tq, _int(max_seqlen_q, "max_seqlen_q"),
+            1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
+    tail = (num_splits, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream_handle(stream))
+    sinks = _sinks(sinks, key_begin, key_end)
+    if sinks:
+        _check("fattn_fwd_paged_sinks", lib.fattn_fwd_paged_sinks(*head, sinks, *tail))
+    else:
+        _check("fattn_fwd_paged_shaped", lib.fattn_fwd_paged_shaped(*head, _ptr(key_begin), _ptr(key_end), *tail))
     return out, lse
 
 
@@ -902,7 +924,7 @@ def bwd_shaped_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
 
 def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
                slopes=None, window: int = 0, key_begin=None, key_end=None, dq=None, dk=None, dv=None, workspace=None,
-               stream=None):
+               stream=None, sinks: int = 0):
     """Gradients of ``fwd_shaped`` (same arguments; o and lse are its outputs) with respect to q, k and v;
     the slopes are constants. Returns (dq, dk, dv), bf16 in the input layouts."""
     lib = load_library()
@@ -929,20 +951,24 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
         workspace = _scratch(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), q.device, stream)
-    st = lib.fattn_bwd_shaped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
-                              B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
-                              _int(min(window, _INT_MAX), "window"), _ptr(key_begin), _ptr(key_end), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check("fattn_bwd_shaped", st)
+    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
+            1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
+    tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    sinks = _sinks(sinks, key_begin, key_end)
+    if sinks:
+        _check("fattn_bwd_sinks", lib.fattn_bwd_sinks(*head, sinks, *tail))
+    else:
+        _check("fattn_bwd_shaped", lib.fattn_bwd_shaped(*head, _ptr(key_begin), _ptr(key_end), *tail))
     return dq, dk, dv
 
 
 def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int, scale: float | None = None,
                         softcap: float = 0.0, slopes=None, window: int = 0, out=None, lse=None, workspace=None,
-                        want_lse: bool = True, stream=None):
-    """``decode_paged`` with the cap, distance bias and window of ``fwd_shaped`` (the query is the
+                        want_lse: bool = True, stream=None, sinks: int = 0):
+    """``decode_paged`` with the cap, distance bias, window and sinks of ``fwd_shaped`` (the query is the
     sequence's last token). With a window, num_splits cuts the pages that it touches: pass
-    choose_num_splits their count, min(max_pages, (window + page_size - 2) // page_size + 1).
+    choose_num_splits their count, min(max_pages, (window + page_size - 2) // page_size + 1), with
+    sinks ceil(sinks / page_size) more.
     Returns (O [B,Hq,d], lse [B,Hq])."""
     lib = load_library()
     _need_cuda(q, kcache, vcache, block_table, seqlens, out, lse, workspace)
@@ -969,12 +995,15 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = _scratch(decode_workspace_size(B, Hq, d, num_splits), q.device, stream)
-    st = lib.fattn_decode_paged_shaped(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens),
-                                       num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
-                                       block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
-                                       _int(min(window, _INT_MAX), "window"), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _stream_handle(stream))
-    _check("fattn_decode_paged_shaped", st)
+    head = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seqlens), num_splits, _ptr(out), _ptr(lse), B, Hq,
+            Hkv, d, page_size, block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
+            _int(min(window, _INT_MAX), "window"))
+    tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    sinks = _sinks(sinks)
+    if sinks:
+        _check("fattn_decode_paged_sinks", lib.fattn_decode_paged_sinks(*head, sinks, *tail))
+    else:
+        _check("fattn_decode_paged_shaped", lib.fattn_decode_paged_shaped(*head, *tail))
     return out, lse
 
 

@@ -194,6 +194,41 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
                                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Windows with sinks. The shaped scores with one more rule: beside its window a query always sees the first
+ * `sinks` keys of its sequence. Key j is visible iff
+ *   (|i - j| < window  or  j < sinks)  and  j <= i if causal != 0;
+ * window = 0 hides nothing (sinks then mean nothing). Key ranges are not taken. Tiles and pages between the
+ * sinks and the window are neither read nor computed, so memory may have been reclaimed there: their table
+ * entries are not read either (chunks: from the first 128-key tile past the sinks to the window of the first
+ * of 256 consecutive rows, rounded down to a multiple of 128).
+ * Arguments, layouts, workspaces and errors are those of the shaped calls, with INVALID_ARG for sinks < 0.
+ *
+ * fattn_fwd_sinks         — dense prefill (fattn_fwd_shaped).
+ * fattn_bwd_sinks         — its gradient (fattn_bwd_shaped, and its workspace). A sink's dK and dV sum over every later row.
+ * fattn_fwd_paged_sinks   — query chunks over the paged cache (fattn_fwd_paged_shaped, and its workspace).
+ * fattn_decode_paged_sinks — single tokens (fattn_decode_paged_shaped). The splits share the pages of the sinks and of
+ *   the window: n = min(max_pages_per_seq, (window + page_size - 2) / page_size + 1 + ceil(sinks / page_size)).
+ */
+fattn_status fattn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                             int N, int d, int causal, float scale, float softcap, const float* slopes, int window,
+                             int sinks, cudaStream_t stream);
+fattn_status fattn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
+                             int causal, float scale, float softcap, const float* slopes, int window, int sinks,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+fattn_status fattn_fwd_paged_sinks(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
+                                   const int32_t* seqlens_k, const int32_t* cu_seqlens_q, void* o, float* lse, int B,
+                                   int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int num_pages,
+                                   int total_q, int max_seqlen_q, int causal, float scale, float softcap,
+                                   const float* slopes, int window, int sinks, int num_splits, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
+                                      const int32_t* seqlens, int num_splits, void* o, float* lse, int B, int Hq, int Hkv,
+                                      int d, int page_size, int max_pages_per_seq, int num_pages, float scale,
+                                      float softcap, const float* slopes, int window, int sinks, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * fattn_key_weights_paged — the attention weight that the tokens of a paged cache
  * receive from query chunks:
  *   weights_out[b, hkv, t] = decay weights_in[b, hkv, t]
