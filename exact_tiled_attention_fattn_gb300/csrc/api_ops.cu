@@ -388,3 +388,189 @@ extern "C" fattn_status fattn_evict_paged(void* kcache, void* vcache, const int3
   if (sms <= 0) return FATTN_ERR_CUDA;
   return launch_evict(p, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
+
+static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// An 8-bit cache's own arguments.
+static fattn_status check_cache_fp8(const void* kcache, const void* vcache, const float* kscale, const float* vscale,
+                                    const int32_t* block_table, const int32_t* seqlens, int d, int page_size,
+                                    int max_pages_per_seq, int num_pages) {
+  if (!kcache || !vcache || !kscale || !vscale || !block_table || !seqlens) return FATTN_ERR_INVALID_ARG;
+  if (misaligned(kcache, 16) || misaligned(vcache, 16) || misaligned(kscale, 4) || misaligned(vscale, 4) ||
+      misaligned(block_table, 4) || misaligned(seqlens, 4))
+    return FATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FATTN_ERR_UNSUPPORTED;
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL - 1024 || (long long)num_pages * page_size > 0x7fffffffLL)
+    return FATTN_ERR_UNSUPPORTED;
+  return FATTN_OK;
+}
+
+extern "C" fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, const void* k, const void* v, void* kcache,
+                                                    void* vcache, float* kscale, float* vscale, const int32_t* block_table,
+                                                    const int32_t* seqlens_k, const int32_t* cu_seqlens_q,
+                                                    const int32_t* positions, const double* inv_freq, int B, int total_q,
+                                                    int Hq, int Hkv, int d, int rotary_dim, int page_size,
+                                                    int max_pages_per_seq, int num_pages, long long q_row, long long q_head,
+                                                    long long k_row, long long k_head, long long v_row, long long v_head,
+                                                    int interleaved, float amplitude, cudaStream_t stream) {
+  fattn_status st = check_rotary(inv_freq, total_q, q ? Hq : 0, Hkv, d, rotary_dim, amplitude);
+  if (st != FATTN_OK) return st;
+  if (B < 0 || Hkv <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0) return FATTN_ERR_INVALID_ARG;
+  if (q_row < 0 || q_head < 0 || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return FATTN_ERR_INVALID_ARG;
+  if (B == 0 || total_q == 0) return FATTN_OK;
+  if ((q != nullptr) != (q_out != nullptr) || (q && Hq <= 0) || !k || !v || !cu_seqlens_q) return FATTN_ERR_INVALID_ARG;
+  if (misaligned(q, 2) || misaligned(q_out, 2) || misaligned(k, 2) || misaligned(v, 2) || misaligned(cu_seqlens_q, 4) ||
+      misaligned(positions, 4))
+    return FATTN_ERR_INVALID_ARG;
+  st = check_cache_fp8(kcache, vcache, kscale, vscale, block_table, seqlens_k, d, page_size, max_pages_per_seq, num_pages);
+  if (st != FATTN_OK) return st;
+  if (total_q / page_size + 2ll * B > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+  int err = 0;
+  AppendFp8Params p{};
+  p.q = {q, q_out, q ? Hq : 0, q_row, q_head, (long long)Hq * d, d};
+  p.k = {k, kcache, Hkv, k_row, k_head, 0, 0};
+  p.v = {v, vcache, Hkv, v_row, v_head, 0, 0};
+  p.kscale = kscale; p.vscale = vscale; p.positions = positions; p.inv_freq = inv_freq;
+  p.cu_seqlens = cu_seqlens_q; p.seqlens_k = seqlens_k; p.block_table = block_table;
+  p.rows = total_q; p.B = B; p.d = d; p.rot = rotary_dim; p.interleaved = interleaved != 0;
+  p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages; p.amplitude = amplitude;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return FATTN_ERR_CUDA;
+  return launch_append_fp8(p, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+// Workspace of the streaming kernel: partial logsumexps and outputs of `rows` query rows, then its counters.
+struct StreamWorkspace {
+  size_t o, counters, bytes;
+};
+static StreamWorkspace stream_workspace(long long rows, int Hq, int d, int num_splits, long long groups) {
+  const size_t n = (size_t)rows * Hq * num_splits;
+  StreamWorkspace w;
+  w.o = round256(n * 4);
+  w.counters = w.o + round256(n * d * 4);
+  w.bytes = w.counters + round256((size_t)(1 + groups) * 4);
+  return w;
+}
+
+extern "C" fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
+                                               const float* vscale, const int32_t* block_table, const int32_t* seqlens,
+                                               int num_splits, void* o, float* lse, int B, int Hq, int Hkv, int d,
+                                               int page_size, int max_pages_per_seq, int num_pages, float scale,
+                                               float softcap, const float* slopes, int window, int sinks, void* workspace,
+                                               size_t workspace_bytes, cudaStream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 ||
+      num_splits <= 0)
+    return FATTN_ERR_INVALID_ARG;
+  StreamFp8Params p{};
+  fattn_status st = check_shape(scale, softcap, slopes, window, sinks, true, nullptr, nullptr,
+                                (long long)max_pages_per_seq * page_size, &p.shape);
+  if (st != FATTN_OK) return st;
+  if (B == 0) return FATTN_OK;
+  if (!q || !o || Hq % Hkv != 0 || misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4)) return FATTN_ERR_INVALID_ARG;
+  st = check_cache_fp8(kcache, vcache, kscale, vscale, block_table, seqlens, d, page_size, max_pages_per_seq, num_pages);
+  if (st != FATTN_OK) return st;
+  if ((long long)B * Hq * num_splits > 0x7fffffffLL / 512) return FATTN_ERR_UNSUPPORTED;
+  const StreamWorkspace w = stream_workspace(B, Hq, d, num_splits, (long long)B * Hq);
+  if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;
+  int err = 0;
+  p.q = q; p.kcache = kcache; p.vcache = vcache; p.kscale = kscale; p.vscale = vscale; p.block_table = block_table;
+  p.seqlens_k = seqlens; p.o = o; p.lse = lse; p.lse_head = 1; p.lse_row = Hq;
+  p.lse_part = static_cast<float*>(workspace);
+  p.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
+  p.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.counters);
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages = max_pages_per_seq;
+  p.num_pages = num_pages; p.num_splits = num_splits; p.rows = B; p.max_q = 1; p.causal = 1; p.scale = scale;
+  p.status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  return launch_stream_fp8(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+// Workspace of the chunks' call: the streaming kernel's, or the pages' copies in bf16, their table and the prefill's splits.
+struct ChunkWorkspace {
+  bool stream;
+  StreamWorkspace s;
+  size_t v, table, splits, bytes;
+};
+static ChunkWorkspace chunk_workspace(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int total_q, int max_q,
+                                      int num_splits) {
+  ChunkWorkspace w{};
+  const long long rows = (long long)max_q * (Hq / Hkv);
+  w.stream = rows <= kStreamFp8Rows;
+  if (w.stream) {
+    w.s = stream_workspace(total_q, Hq, d, num_splits, stream_fp8_groups(B, Hkv, rows));
+    w.bytes = w.s.bytes;
+    return w;
+  }
+  const size_t copy = round256((size_t)B * max_pages * page_size * Hkv * d * 2);
+  w.v = copy;
+  w.table = 2 * copy;
+  w.splits = w.table + round256((size_t)B * max_pages * 4);
+  w.bytes = w.splits + fattn_fwd_paged_shaped_workspace_size(total_q, Hq, d, num_splits);
+  return w;
+}
+
+extern "C" size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
+                                                     int total_q, int max_seqlen_q, int num_splits) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || d <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || total_q <= 0 ||
+      max_seqlen_q <= 0 || num_splits <= 0)
+    return 0;
+  return chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits).bytes;
+}
+
+extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
+                                            const float* vscale, const int32_t* block_table, const int32_t* seqlens_k,
+                                            const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv, int d,
+                                            int page_size, int max_pages_per_seq, int num_pages, int total_q,
+                                            int max_seqlen_q, int causal, float scale, float softcap, const float* slopes,
+                                            int window, int sinks, int num_splits, void* workspace, size_t workspace_bytes,
+                                            cudaStream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 || total_q < 0 ||
+      max_seqlen_q < 0 || num_splits <= 0)
+    return FATTN_ERR_INVALID_ARG;
+  StreamFp8Params p{};
+  fattn_status st = check_shape(scale, softcap, slopes, window, sinks, causal != 0, nullptr, nullptr,
+                                (long long)max_pages_per_seq * page_size, &p.shape);
+  if (st != FATTN_OK) return st;
+  if (B == 0 || total_q == 0 || max_seqlen_q == 0) return FATTN_OK;
+  if (!q || !o || !cu_seqlens_q || Hq % Hkv != 0 || misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) ||
+      misaligned(cu_seqlens_q, 4))
+    return FATTN_ERR_INVALID_ARG;
+  st = check_cache_fp8(kcache, vcache, kscale, vscale, block_table, seqlens_k, d, page_size, max_pages_per_seq, num_pages);
+  if (st != FATTN_OK) return st;
+  const long long rows = (long long)max_seqlen_q * (Hq / Hkv);
+  if (rows > 0x7fffffffLL || (long long)total_q * Hq > 0x7fffffffLL / num_splits ||
+      ((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || B > 65535 ||
+      stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits)
+    return FATTN_ERR_UNSUPPORTED;
+  const ChunkWorkspace w =
+      chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits);
+  if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  int err = 0;
+  int* status = status_ptr(&err);
+  if (err) return FATTN_ERR_CUDA;
+  if (w.stream) {
+    p.q = q; p.kcache = kcache; p.vcache = vcache; p.kscale = kscale; p.vscale = vscale; p.block_table = block_table;
+    p.seqlens_k = seqlens_k; p.cu_seqlens = cu_seqlens_q; p.o = o; p.lse = lse; p.lse_head = total_q; p.lse_row = 1;
+    p.lse_part = static_cast<float*>(workspace);
+    p.o_part = reinterpret_cast<float*>(ws + w.s.o);
+    p.counters = reinterpret_cast<int*>(ws + w.s.counters);
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.page_size = page_size; p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages; p.num_splits = num_splits; p.rows = total_q; p.max_q = max_seqlen_q;
+    p.causal = causal ? 1 : 0; p.scale = scale; p.status = status;
+    return launch_stream_fp8(p, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+  }
+  ExpandFp8Params e{};
+  e.kcache = kcache; e.vcache = vcache; e.kscale = kscale; e.vscale = vscale; e.block_table = block_table;
+  e.seqlens_k = seqlens_k; e.cu_seqlens = cu_seqlens_q;
+  e.kout = ws; e.vout = ws + w.v; e.table = reinterpret_cast<int32_t*>(ws + w.table);
+  e.B = B; e.Hkv = Hkv; e.d = d; e.page_size = page_size; e.max_pages = max_pages_per_seq; e.num_pages = num_pages;
+  e.total_q = total_q; e.window = p.shape.window; e.sinks = p.shape.sinks; e.status = status;
+  if (launch_expand_fp8(e, stream) != cudaSuccess) return FATTN_ERR_CUDA;
+  return fwd_paged_impl(q, e.kout, e.vout, e.table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
+                        max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale, &p.shape, num_splits,
+                        num_splits > 1 ? ws + w.splits : nullptr, num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
+}

@@ -445,10 +445,11 @@ template <int kShape, bool kCols, bool kPack>
 __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uint32_t (&u)[32], float dist, float step,
                                            int va, int vb, int vs, const float* nlv, float nl, float* pv, uint32_t* pk) {
   const ScoreShape& sh = p.shape;
-  const bool edge = !__all_sync(0xffffffffu, (va <= 0 && vb >= 32) || vs >= 32);
-  const uint32_t vis = (vb <= 0 || va >= 32 || va >= vb
-                            ? 0u
-                            : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)))) | low_bits(vs);
+  const bool edge = !__all_sync(0xffffffffu, va <= 0 && vb >= 32);
+  uint32_t vis = 0xffffffffu;
+  if (edge)
+    vis = (vb <= 0 || va >= 32 || va >= vb ? 0u : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)))) |
+          low_bits(vs);
   constexpr bool cap = kShape & kShapeCap, bias = kShape & kShapeBias;
   float y[32], f[32];
   if constexpr (cap) {

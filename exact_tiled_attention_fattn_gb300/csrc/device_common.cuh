@@ -66,6 +66,19 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
   return d;
 }
 
+// Amplitude times (cos, sin) of an angle in turns * 2^64, wrapped. The nearest quarter turn comes off in integers: the rest,
+// at most an eighth of a turn, has its 24 bits to itself.
+__device__ __forceinline__ float2 turn_of(long long ang, float amplitude) {
+  const unsigned hi = (unsigned)(ang >> 32);             // 2^-32 turns
+  const int quarter = (int)((hi + (1u << 29)) >> 30);    // 0 .. 3
+  float s0, c0;
+  sincospif((float)(int)(hi - ((unsigned)quarter << 30)) * (1.f / 2147483648.f), &s0, &c0);
+  float cs = quarter & 1 ? s0 : c0, sn = quarter & 1 ? c0 : s0;
+  if ((quarter + 1) & 2) cs = -cs;
+  if (quarter & 2) sn = -sn;
+  return make_float2(cs * amplitude, sn * amplitude);
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -2,7 +2,7 @@
 // checks happen in api_ops.cu before these are called.
 #pragma once
 
-#include "fattn.h"
+#include "fattn_ops.h"
 #include "fattn_internal.h"
 
 namespace fattn {
@@ -82,6 +82,76 @@ struct EvictParams {
 };
 
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
+
+// 8-bit paged cache: E4M3 codes [num_pages, page_size, Hkv, d], scales [num_pages, Hkv].
+constexpr int kAppendMaxHeads = 64;   // KV heads that a block of the append has room for
+
+struct AppendFp8Params {
+  RopeTensor q, k, v;         // bf16; out of k and v = the code caches
+  float* kscale;
+  float* vscale;
+  const int32_t* positions;   // nullptr: the token's index in its sequence
+  const double* inv_freq;
+  const int32_t* cu_seqlens;
+  const int32_t* seqlens_k;
+  const int32_t* block_table;
+  int rows, B, d, rot, interleaved, page_size, max_pages, num_pages;
+  float amplitude;
+  int* status;
+};
+
+cudaError_t launch_append_fp8(const AppendFp8Params& p, int num_sms, cudaStream_t stream);
+
+struct ExpandFp8Params {
+  const void* kcache;
+  const void* vcache;
+  const float* kscale;
+  const float* vscale;
+  const int32_t* block_table;
+  const int32_t* seqlens_k;
+  const int32_t* cu_seqlens;
+  void* kout;                 // bf16 [B * max_pages, page_size, Hkv, d]
+  void* vout;
+  int32_t* table;             // [B, max_pages], the copy's own
+  int B, Hkv, d, page_size, max_pages, num_pages, total_q;
+  int window, sinks;
+  int* status;
+};
+
+// Visible pages of the 8-bit cache as bf16 pages of their own.
+cudaError_t launch_expand_fp8(const ExpandFp8Params& p, cudaStream_t stream);
+
+struct StreamFp8Params {
+  const void* q;              // [rows, Hq, d] bf16
+  const void* kcache;
+  const void* vcache;
+  const float* kscale;
+  const float* vscale;
+  const int32_t* block_table;
+  const int32_t* seqlens_k;
+  const int32_t* cu_seqlens;  // nullptr: one query per sequence
+  void* o;
+  float* lse;                 // of head h, row r at lse[h * lse_head + r * lse_row]; or nullptr
+  long long lse_head, lse_row;
+  float* lse_part;            // [rows, Hq, S]
+  float* o_part;              // [rows, Hq, S, d]
+  int* counters;              // work counter, then one arrival counter per group of rows
+  int B, Hq, Hkv, d, page_size, max_pages, num_pages, num_splits;
+  int rows, max_q, causal;
+  float scale;
+  ScoreShape shape;           // no key ranges
+  int* status;
+};
+
+// Rows (queries x heads of a group) that a group of the streaming kernel takes, and its groups per (sequence, KV head).
+inline int stream_fp8_rows(int max_rows) { return max_rows <= 8 ? 8 : 16; }
+inline long long stream_fp8_groups(int B, int Hkv, long long max_rows) {
+  const int r = stream_fp8_rows((int)(max_rows < 16 ? max_rows : 16));
+  return (long long)B * Hkv * ((max_rows + r - 1) / r);
+}
+// Query rows of a KV head up to which a chunk goes to the streaming kernel.
+constexpr int kStreamFp8Rows = FATTN_FP8_STREAM_ROWS;
+cudaError_t launch_stream_fp8(const StreamFp8Params& p, cudaStream_t stream);
 
 // From api.cu: the device status word of the current device (nullptr and *err != 0 on
 // failure), the pipeline waits' limit and stall flag, a bf16 [rows, H, d] tensor map, and the

@@ -1013,13 +1013,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++ns;
         tc_fence_after();
-        // first key of the tile; shaped: the row's sinks are keys [0, sink_lim)
-        const int kbase = (kShaped ? (j < x.cut ? j - x.gap : j) : j) * BN;
-        const int sink_lim = kShaped ? shape_sinks(p.shape, pos, x.Lk, p.causal) : 0;
+        const int kbase = (kShaped ? (j < x.cut ? j - x.gap : j) : j) * BN;  // first key of the tile
         // columns [32 c, 32 c + 32) that are visible, as bits: keys [lo, lim) and the sinks
         auto visible = [&](int c) -> uint32_t {
           const int first = kbase + 32 * c, a = max(lo - first, 0), e = min(lim - first, 32);
-          return (a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u) | low_bits(sink_lim - first);
+          return (a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u) |
+                 low_bits(shape_sinks(p.shape, pos, x.Lk, p.causal) - first);
         };
         if constexpr (kCap) {
           // ---- capped scores: two rolled walks over the tile's 128 columns, 32 at a time from TMEM. The
@@ -1027,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // forms) the eight warps starved for instructions (1.2 of 5 cycles an issue), rolled they stay
           // in the instruction cache.
           const ScoreShape& sh = p.shape;
-          const bool edge = __any_sync(0xffffffffu, (kbase < lo || kbase + BN > lim) && kbase + BN > sink_lim);
+          const bool edge = __any_sync(0xffffffffu, kbase < lo || kbase + BN > lim);
           // Against what a row's exponentials are taken, by row, so that a row does not depend on its
           // neighbours: while no |u| of 32 columns exceeds bound_limit, the cap of the largest |u| bounds
           // their capped scores and lies so close to the largest of them that the exponentials against
@@ -1267,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarSFree + t));
           }
         }
-        const bool edge = kShaped && (masked || kbase < lo) && kbase + BN > sink_lim;
+        const bool edge = kShaped && (masked || kbase < lo);
         if constexpr (kBias) {
           const float dist = (float)(pos - kbase);
           const float mul = p.shape.sl2;

@@ -209,16 +209,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 8 : 0) rope_ker
       } else {
         pos = (row0 + r) % p.period;
       }
-      const long long ang = (long long)(f * (unsigned long long)pos);   // turns * 2^64, wrapped
-      // the nearest quarter turn comes off in integers: the rest, at most an eighth of a turn, has its 24 bits to itself
-      const unsigned hi = (unsigned)(ang >> 32);             // 2^-32 turns
-      const int quarter = (int)((hi + (1u << 29)) >> 30);    // 0 .. 3
-      float s0, c0;
-      sincospif((float)(int)(hi - ((unsigned)quarter << 30)) * (1.f / 2147483648.f), &s0, &c0);
-      float cs = quarter & 1 ? s0 : c0, sn = quarter & 1 ? c0 : s0;
-      if ((quarter + 1) & 2) cs = -cs;
-      if (quarter & 2) sn = -sn;
-      s_cs[r * half + at] = make_float2(cs * p.amplitude, (p.inverse ? -sn : sn) * p.amplitude);
+      const float2 w = turn_of((long long)(f * (unsigned long long)pos), p.amplitude);
+      s_cs[r * half + at] = make_float2(w.x, p.inverse ? -w.y : w.y);
     }
   }
   __syncthreads();

@@ -77,6 +77,13 @@ SIGNATURES_OPS = {
                                    _f, _vp, _i, _i, _i, _vp, _sz, _vp]),
     "fattn_decode_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
                                       _i, _i, _vp, _sz, _vp]),
+    "fattn_rope_append_paged_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                                         _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _ll, _i, _f, _vp]),
+    "fattn_decode_paged_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f,
+                                    _vp, _i, _i, _vp, _sz, _vp]),
+    "fattn_fwd_paged_fp8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "fattn_fwd_paged_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                 _f, _f, _vp, _i, _i, _i, _vp, _sz, _vp]),
     "fattn_key_weights_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                                      _i, _i, _f, _f, _vp, _i, _f, _vp]),
     "fattn_evict_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
@@ -828,7 +835,7 @@ def fwd_shaped(q, k, v, causal: bool = False, scale: float | None = None, softca
         lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     head = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, k.shape[2], N, d, 1 if causal else 0, float(scale),
             float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
-    sinks = _sinks(sinks, key_begin, key_end)
+    sinks = sinks and _sinks(sinks, key_begin, key_end)
     if sinks:
         _check("fattn_fwd_sinks", lib.fattn_fwd_sinks(*head, sinks, _stream_handle(stream)))
     else:
@@ -910,7 +917,7 @@ def fwd_paged_shaped(q, kcache, vcache, block_table, seqlens_k, cu_seqlens_q, ma
             1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
     tail = (num_splits, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
             _stream_handle(stream))
-    sinks = _sinks(sinks, key_begin, key_end)
+    sinks = sinks and _sinks(sinks, key_begin, key_end)
     if sinks:
         _check("fattn_fwd_paged_sinks", lib.fattn_fwd_paged_sinks(*head, sinks, *tail))
     else:
@@ -954,7 +961,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
             1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    sinks = _sinks(sinks, key_begin, key_end)
+    sinks = sinks and _sinks(sinks, key_begin, key_end)
     if sinks:
         _check("fattn_bwd_sinks", lib.fattn_bwd_sinks(*head, sinks, *tail))
     else:
@@ -999,11 +1006,179 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
             Hkv, d, page_size, block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
             _int(min(window, _INT_MAX), "window"))
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    sinks = _sinks(sinks)
+    sinks = sinks and _sinks(sinks)
     if sinks:
         _check("fattn_decode_paged_sinks", lib.fattn_decode_paged_sinks(*head, sinks, *tail))
     else:
         _check("fattn_decode_paged_shaped", lib.fattn_decode_paged_shaped(*head, *tail))
+    return out, lse
+
+
+# ------------------------------------------------------------------ a cache in 8 bits
+FP8_STREAM_ROWS = 256  # FATTN_FP8_STREAM_ROWS: query rows of a KV head up to which chunks stream the codes
+
+
+def _check_fp8_cache(kcache, vcache, kscale, vscale, block_table, B):
+    if kcache.dtype not in (torch.float8_e4m3fn, torch.uint8) or vcache.dtype != kcache.dtype:
+        raise TypeError("8-bit caches are E4M3 tensors (float8_e4m3fn or uint8 codes)")
+    _check_paged_cache(kcache, vcache, block_table, B)
+    shape = (kcache.shape[0], kcache.shape[2])
+    _expect(kscale, shape, "kscale", torch.float32)
+    _expect(vscale, shape, "vscale", torch.float32)
+
+
+def rope_append_paged_fp8(q, k, v, kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_seqlens_q, inv_freq,
+                          positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """``rope_append_paged`` into a cache in 8 bits: kcache, vcache [pages, page_size, Hkv, d] E4M3 codes (float8_e4m3fn or
+    uint8), kscale, vscale fp32 [pages, Hkv], value = scale * code. A page's scale is the least power of two that holds its
+    largest magnitude; a page that new tokens outgrow has its old codes re-scaled. Pages are not shared while they are
+    appended to. q, k and v bf16, any row and head strides; d 64 or 128, page_size 16, 32, 64 or 128. Returns the rotated
+    q [Tq,Hq,d], packed (None without q)."""
+    lib = load_library()
+    _need_cuda(q, k, v, inv_freq, contiguous=False)
+    _need_cuda(kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_seqlens_q, positions, out)
+    if not (k.dtype == v.dtype == torch.bfloat16) or (q is not None and q.dtype != torch.bfloat16):
+        raise TypeError("rope_append_paged_fp8 takes bf16 q, k and v")
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [Tq, Hkv, d]")
+    Tq, Hkv, d = k.shape
+    rot = _check_freq(inv_freq, d)
+    if seqlens_k.dtype != torch.int32 or cu_seqlens_q.dtype != torch.int32:
+        raise TypeError("seqlens_k and cu_seqlens_q must be int32")
+    B = cu_seqlens_q.numel() - 1
+    _expect(seqlens_k, (B,), "seqlens_k")
+    _check_fp8_cache(kcache, vcache, kscale, vscale, block_table, B)
+    _expect(kcache, (*kcache.shape[:2], Hkv, d), "kcache")
+    if positions is not None:
+        _expect(positions, (Tq,), "positions", torch.int32)
+    Hq, qs = 0, (0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != Tq or q.shape[2] != d:
+            raise ValueError(f"q must be [{Tq}, Hq, {d}]")
+        Hq = q.shape[1]
+        qs = _row_strides(q, "q")
+        _expect(out, q.shape, "out", q.dtype)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out is not None:
+        raise ValueError("out without q")
+    st = lib.fattn_rope_append_paged_fp8(_ptr(q), _ptr(out), _ptr(k), _ptr(v), _ptr(kcache), _ptr(vcache), _ptr(kscale),
+                                         _ptr(vscale), _ptr(block_table), _ptr(seqlens_k), _ptr(cu_seqlens_q),
+                                         _ptr(positions), _ptr(inv_freq), B, Tq, Hq, Hkv, d, rot, kcache.shape[1],
+                                         block_table.shape[1], kcache.shape[0], *qs, *_row_strides(k, "k"),
+                                         *_row_strides(v, "v"), 1 if interleaved else 0, float(amplitude),
+                                         _stream_handle(stream))
+    _check("fattn_rope_append_paged_fp8", st)
+    return out
+
+
+def decode_paged_fp8(q, kcache, vcache, kscale, vscale, block_table, seqlens, num_splits: int, scale: float | None = None,
+                     softcap: float = 0.0, slopes=None, window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None,
+                     want_lse: bool = True, stream=None):
+    """``decode_paged_shaped`` (cap, distance bias, window, sinks) over a cache in 8 bits: kcache, vcache
+    [pages, page_size, Hkv, d] E4M3 codes, kscale, vscale fp32 [pages, Hkv] (``rope_append_paged_fp8``). q [B,Hq,d] bf16.
+    ``num_splits`` and the ``workspace`` (decode_workspace_size bytes) as there. Returns (O [B,Hq,d], lse [B,Hq])."""
+    lib = load_library()
+    _need_cuda(q, kcache, vcache, kscale, vscale, block_table, seqlens, slopes, out, lse, workspace)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if seqlens.dtype != torch.int32:
+        raise TypeError("block_table and seqlens must be int32")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _check_fp8_cache(kcache, vcache, kscale, vscale, block_table, B)
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _expect(kcache, (num_pages, page_size, Hkv, d), "kcache")
+    _expect(seqlens, (B,), "seqlens")
+    _expect(slopes, (Hq,), "slopes", torch.float32)
+    _expect(out, q.shape, "out", q.dtype)
+    _expect(lse, (B, Hq), "lse", torch.float32)
+    num_splits = _int(num_splits, "num_splits")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _scratch(decode_workspace_size(B, Hq, d, num_splits), q.device, stream)
+    st = lib.fattn_decode_paged_fp8(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(kscale), _ptr(vscale), _ptr(block_table),
+                                    _ptr(seqlens), num_splits, _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size,
+                                    block_table.shape[1], num_pages, float(scale), float(softcap), _ptr(slopes),
+                                    _int(min(window, _INT_MAX), "window"), _sinks(sinks), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check("fattn_decode_paged_fp8", st)
+    return out, lse
+
+
+def fwd_paged_fp8_workspace_size(B: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages_per_seq: int, total_q: int,
+                                 max_seqlen_q: int, num_splits: int) -> int:
+    return int(load_library().fattn_fwd_paged_fp8_workspace_size(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q,
+                                                                 max_seqlen_q, num_splits))
+
+
+def choose_fp8_splits(batch: int, Hq: int, Hkv: int, d: int, page_size: int, max_seqlen_q: int, max_context: int,
+                      num_sms: int | None = None) -> int:
+    """Split count of ``fwd_paged_fp8`` for contexts of ``max_context`` visible tokens: ``choose_num_splits`` over the groups
+    of 16 query rows where the codes are streamed, else ``choose_chunk_splits``."""
+    if num_sms is None:
+        num_sms = _num_sms(torch.cuda.current_device())
+    rows = max_seqlen_q * (Hq // max(Hkv, 1))
+    if rows > FP8_STREAM_ROWS:
+        return choose_chunk_splits(batch, Hq, d, max_seqlen_q, max_context, num_sms)
+    return choose_num_splits(batch * -(-rows // 16), Hkv, -(-max_context // page_size), num_sms)
+
+
+def fwd_paged_fp8(q, kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int,
+                  causal: bool = True, scale: float | None = None, softcap: float = 0.0, slopes=None, window: int = 0,
+                  sinks: int = 0, out=None, lse=None, want_lse: bool = True, num_splits: int | None = None, workspace=None,
+                  stream=None):
+    """``fwd_paged_shaped`` (cap, distance bias, window, sinks) over a cache in 8 bits: query chunks q [Tq,Hq,d] bf16
+    packed by ``cu_seqlens_q`` against kcache, vcache [pages, page_size, Hkv, d] E4M3 codes with kscale, vscale fp32
+    [pages, Hkv]. Up to FP8_STREAM_ROWS query rows per KV head stream the codes; more read a bf16 copy of the pages in the
+    ``workspace`` (fwd_paged_fp8_workspace_size bytes, allocated when None). ``num_splits`` None: ``choose_fp8_splits``.
+    Returns (O [Tq,Hq,d], lse [Hq,Tq])."""
+    lib = load_library()
+    _need_cuda(q, kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_seqlens_q, slopes, out, lse, workspace)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if seqlens_k.dtype != torch.int32 or cu_seqlens_q.dtype != torch.int32:
+        raise TypeError("seqlens_k and cu_seqlens_q must be int32")
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, d]")
+    Tq, Hq, d = q.shape
+    B = cu_seqlens_q.numel() - 1
+    _check_fp8_cache(kcache, vcache, kscale, vscale, block_table, B)
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _expect(kcache, (num_pages, page_size, Hkv, d), "kcache")
+    _expect(seqlens_k, (B,), "seqlens_k")
+    _expect(slopes, (Hq,), "slopes", torch.float32)
+    _expect(out, q.shape, "out", q.dtype)
+    _expect(lse, (Hq, Tq), "lse", torch.float32)
+    max_seqlen_q = _int(max_seqlen_q, "max_seqlen_q")
+    maxp = block_table.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    if num_splits is None:
+        context = maxp * page_size
+        if window > 0:
+            context = min(context, int(window) + max_seqlen_q + int(sinks))
+        num_splits = choose_fp8_splits(B, Hq, Hkv, d, page_size, max_seqlen_q, context)
+    num_splits = _int(num_splits, "num_splits")
+    if workspace is None:
+        workspace = _scratch(fwd_paged_fp8_workspace_size(B, Hq, Hkv, d, page_size, maxp, Tq, max_seqlen_q, num_splits),
+                             q.device, stream)
+    st = lib.fattn_fwd_paged_fp8(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(kscale), _ptr(vscale), _ptr(block_table),
+                                 _ptr(seqlens_k), _ptr(cu_seqlens_q), _ptr(out), _ptr(lse), B, Hq, Hkv, d, page_size, maxp,
+                                 num_pages, Tq, max_seqlen_q, 1 if causal else 0, float(scale), float(softcap), _ptr(slopes),
+                                 _int(min(window, _INT_MAX), "window"), _sinks(sinks), num_splits, _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check("fattn_fwd_paged_fp8", st)
     return out, lse
 
 

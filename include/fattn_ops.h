@@ -10,6 +10,9 @@
  *     (fattn_fwd_shaped, its gradient fattn_bwd_shaped, query chunks and single
  *     tokens over the paged cache: fattn_fwd_paged_shaped,
  *     fattn_decode_paged_shaped);
+ *   - a cache in 8 bits: new tokens rotated, quantized and put into their pages
+ *     (fattn_rope_append_paged_fp8), and attention over it (fattn_decode_paged_fp8,
+ *     fattn_fwd_paged_fp8);
  *   - a budget for the cache: the attention weight that its tokens receive
  *     (fattn_key_weights_paged), and the eviction of all but the heaviest
  *     (fattn_evict_paged).
@@ -227,6 +230,71 @@ fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const v
                                       int d, int page_size, int max_pages_per_seq, int num_pages, float scale,
                                       float softcap, const float* slopes, int window, int sinks, void* workspace,
                                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The 8-bit cache: kcache, vcache [num_pages, page_size, Hkv, d] E4M3 codes ('fn' variant: no
+ * infinities), kscale, vscale fp32 [num_pages, Hkv]; token t of a sequence is slot t % page_size of page
+ * block_table[b * max_pages_per_seq + t / page_size], its k in head h is kscale[page, h] * code, its v
+ * likewise. Scales of pages in use are positive and finite; the append writes powers of two. d in {64, 128},
+ * page_size in {16, 32, 64, 128}.
+ *
+ * fattn_rope_append_paged_fp8 — fattn_rope_append_paged into the 8-bit cache: q and k of new tokens
+ * rotated, q written to q_out (bf16), k and v as codes, in one launch. Per page, head and cache, with a the
+ * largest finite magnitude of the page's new values (k rotated, in fp32):
+ *   need = the least power of two with a <= 448 need, at least 2^-100;
+ *   a page whose slots before the new tokens hold context has scale max(old, need), and if that is above the
+ *   old one its codes become RN(code * old / new); any other page has scale need (its old one is not read);
+ *   new codes = RN(value / scale); infinities and NaN become NaN codes.
+ * Which slots hold context follows from seqlens_k alone. A page that is appended to must not be shared with another sequence, and
+ * no two tokens of a call share a slot. Everything else (chunks, positions, padding rows, strides, skipped rows) is as in
+ * fattn_rope_append_paged. Errors: as there; UNSUPPORTED also for other d or page sizes, or
+ * num_pages * page_size >= 2^31; codes must be 16-byte aligned.
+ */
+fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, const void* k, const void* v, void* kcache,
+                                         void* vcache, float* kscale, float* vscale, const int32_t* block_table,
+                                         const int32_t* seqlens_k, const int32_t* cu_seqlens_q, const int32_t* positions,
+                                         const double* inv_freq, int B, int total_q, int Hq, int Hkv, int d,
+                                         int rotary_dim, int page_size, int max_pages_per_seq, int num_pages,
+                                         long long q_row, long long q_head, long long k_row, long long k_head,
+                                         long long v_row, long long v_head, int interleaved, float amplitude,
+                                         cudaStream_t stream);
+
+/*
+ * fattn_decode_paged_fp8 — one query token per sequence over the 8-bit cache: fattn_decode_paged_sinks with its
+ * arguments, splits, outputs and workspace (fattn_decode_workspace_size). q bf16. Products of q with codes are exact in
+ * fp32 sums, weights are rounded to fp16 (11 bits) for the product with V. B == 0 is an empty problem. A table entry outside the
+ * pool hides its tokens and records FATTN_ERR_DEVICE_CHECK, as do lengths outside the table.
+ */
+fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
+                                    const float* vscale, const int32_t* block_table, const int32_t* seqlens,
+                                    int num_splits, void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                    int max_pages_per_seq, int num_pages, float scale, float softcap, const float* slopes,
+                                    int window, int sinks, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fattn_fwd_paged_fp8_workspace_size — bytes of scratch fattn_fwd_paged_fp8 needs. Few query rows
+ * (max_seqlen_q * Hq / Hkv <= FATTN_FP8_STREAM_ROWS): the splits' partials, as for single tokens. More: a bf16 copy of the
+ * sequences' pages, 4 Hkv d page_size bytes for each of B * max_pages_per_seq, their table, and the partials of
+ * fattn_fwd_paged_shaped_workspace_size. Returns 0 for non-positive arguments.
+ */
+#define FATTN_FP8_STREAM_ROWS 256
+size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int total_q,
+                                          int max_seqlen_q, int num_splits);
+
+/*
+ * fattn_fwd_paged_fp8 — query chunks over the 8-bit cache: fattn_fwd_paged_sinks with its arguments and outputs.
+ * Few query rows stream the codes as single tokens do; with more, the pages that any of them sees are expanded to
+ * bf16 (exact for scales that are powers of two, else one rounding) in the workspace and read by the tensor-core prefill.
+ * num_splits >= 1 cuts the keys in both. workspace: 256-byte aligned, contents ignored, always needed.
+ * Errors: those of fattn_fwd_paged_sinks and of the cache; UNSUPPORTED also for (B * max_pages_per_seq + 1) * page_size
+ *   >= 2^31.
+ */
+fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
+                                 const float* vscale, const int32_t* block_table, const int32_t* seqlens_k,
+                                 const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv, int d,
+                                 int page_size, int max_pages_per_seq, int num_pages, int total_q, int max_seqlen_q,
+                                 int causal, float scale, float softcap, const float* slopes, int window, int sinks,
+                                 int num_splits, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * fattn_key_weights_paged — the attention weight that the tokens of a paged cache
