@@ -442,6 +442,12 @@ extern "C" fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, 
   return launch_append_fp8(p, sms, stream) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
+// The streaming kernel counts the steps (16 tokens of a group of rows) of all sequences in an int.
+static bool countable_steps(int B, int Hkv, long long rows, int max_pages, int page_size) {
+  const long long steps = (long long)max_pages * page_size / 16 + 1;
+  return stream_fp8_groups(B, Hkv, rows) <= 0x7fffffffLL / steps;
+}
+
 // Workspace of the streaming kernel: partial logsumexps and outputs of `rows` query rows, then its counters.
 struct StreamWorkspace {
   size_t o, counters, bytes;
@@ -472,7 +478,9 @@ extern "C" fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache
   if (!q || !o || Hq % Hkv != 0 || misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4)) return FATTN_ERR_INVALID_ARG;
   st = check_cache_fp8(kcache, vcache, kscale, vscale, block_table, seqlens, d, page_size, max_pages_per_seq, num_pages);
   if (st != FATTN_OK) return st;
-  if ((long long)B * Hq * num_splits > 0x7fffffffLL / 512) return FATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hq * num_splits > 0x7fffffffLL / 512 ||
+      !countable_steps(B, Hkv, Hq / Hkv, max_pages_per_seq, page_size))
+    return FATTN_ERR_UNSUPPORTED;
   const StreamWorkspace w = stream_workspace(B, Hq, d, num_splits, (long long)B * Hq);
   if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;
   int err = 0;
@@ -545,6 +553,7 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
       ((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || B > 65535 ||
       stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits)
     return FATTN_ERR_UNSUPPORTED;
+  if (rows <= kStreamFp8Rows && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size)) return FATTN_ERR_UNSUPPORTED;
   const ChunkWorkspace w =
       chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits);
   if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;

@@ -232,11 +232,12 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const AppendFp8Par
     uint8_t* base = static_cast<uint8_t*>(u < nkv ? p.k.out : p.v.out);
     return reinterpret_cast<uint32_t*>(base + (((size_t)page * P + s) * p.k.heads + h) * D + e);
   };
-  // tokens that were there, in pages that outgrew their scale: RN(code * old / new)
+  // the other slots of pages that outgrew their scale: RN(code * old / new)
   for (int u = 0; u < 2 * nkv && slot0 > 0; ++u) {
     const float ratio = s_ratio[u];
     if (ratio == 1.f) continue;
-    for (int s = warp * kPer + sub; s < slot0; s += kWarps * kPer) {
+    for (int s = warp * kPer + sub; s < P; s += kWarps * kPer) {
+      if (s >= slot0 && s < slot0 + n) continue;
       uint32_t* c = slot(u, s);
       const uint32_t w = *c;
       const float2 a = values2(w), z = values2(w >> 16);

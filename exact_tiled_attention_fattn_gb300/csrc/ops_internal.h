@@ -141,6 +141,9 @@ struct StreamFp8Params {
   float scale;
   ScoreShape shape;           // no key ranges
   int* status;
+  // set by the launch: heads of a KV head, groups of rows of a sequence, their reciprocals, log2 of the page size
+  int group, subs, page_shift;
+  unsigned long long by_group, by_subs;
 };
 
 // Rows (queries x heads of a group) that a group of the streaming kernel takes, and its groups per (sequence, KV head).

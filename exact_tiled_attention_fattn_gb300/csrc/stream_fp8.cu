@@ -28,8 +28,14 @@
 namespace fattn {
 namespace {
 
-constexpr int kWarps = 4;
+// Warps of a CTA, two CTAs an SM: what the registers of one or two tiles of 8 query rows leave.
+template <int NT>
+constexpr int kWarps = 6;
+// Chunks of 16 tokens that a warp works on together.
+template <int NT>
+constexpr int kTogether = NT == 1 ? 2 : 1;
 constexpr int kChunk = 16;       // tokens of a step
+constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
 constexpr float kLazy = 8.f;     // log2 units that scores may exceed the running maximum by
 
 __device__ __forceinline__ uint4 ldg16(const void* p) {
@@ -66,14 +72,56 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The rows of a group: row r is query i = r / G of the sequence, head r % G of the KV head's group.
+// u / d by a multiplication with m = ceil(2^42 / d), for u d < 2^42 (a division by a run-time number takes some 40 cycles
+// a piece's first and last steps wait for).
+__device__ __forceinline__ int quotient(int u, unsigned long long m) { return (int)(((unsigned long long)(unsigned)u * m) >> 42); }
+
+// The rows of a group: row r is query i = r / G of the sequence, head r % G of the KV head's group. The tokens that they
+// can see are counted without those between the sinks and the window's first page: from cut on token v is v + gap.
 struct Group {
-  int b, hkv;
-  int r0, rows;       // first row, rows of this group
+  int b, r0, rows;    // sequence; first row, rows of this group
   int q0;             // packed row of the sequence's query 0
   int off, L;         // position of query 0, context tokens
   int lo, hi;         // keys that some row sees beside its sinks
+  int cut, gap;
+  int chunks;         // steps of 16 tokens; at least 1 where there are rows (they are written, whatever they see)
 };
+
+// The v-th group of rows: sequence v / nsub, rows from (v % nsub) R on; inconsistent lengths: no rows.
+template <int R>
+__device__ __forceinline__ Group describe(const StreamFp8Params& p, int v, bool tell) {
+  const int cap = p.max_pages << p.page_shift;
+  Group x;
+  x.b = p.subs == 1 ? v : quotient(v, p.by_subs);
+  x.r0 = (v - x.b * p.subs) * R;
+  x.L = __ldg(p.seqlens_k + x.b);
+  x.q0 = x.b;
+  int lq = 1;
+  bool bad;
+  if (p.cu_seqlens) {
+    x.q0 = __ldg(p.cu_seqlens + x.b);
+    lq = __ldg(p.cu_seqlens + x.b + 1) - x.q0;
+    bad = x.q0 < 0 || lq < 0 || lq > p.rows - x.q0 || lq > p.max_q || x.L < lq || x.L > cap;
+    if (bad) lq = 0;
+  } else {
+    bad = x.L < 0 || x.L > cap;
+    x.L = min(max(x.L, 0), cap);
+  }
+  if (bad && tell && x.r0 == 0) record_status(p.status, kStatusDeviceCheck);
+  x.rows = min(R, lq * p.group - x.r0);
+  x.chunks = 0;
+  if (x.rows <= 0) return x;
+  x.off = x.L - lq;
+  const int W = p.shape.window, at0 = x.off + quotient(x.r0, p.by_group), at1 = x.off + quotient(x.r0 + x.rows - 1, p.by_group);
+  x.lo = W > 0 ? max(at0 - W + 1, 0) : 0;
+  x.hi = p.causal ? at1 + 1 : W > 0 && W < x.L - at1 ? at1 + W : x.L;
+  const int first = x.lo >> p.page_shift;
+  x.cut = min(p.shape.sinks > 0 ? ((p.shape.sinks - 1) >> p.page_shift) + 1 : 0, first) << p.page_shift;
+  x.gap = (first << p.page_shift) - x.cut;
+  const int n = max(x.hi, shape_sinks(p.shape, at1, x.L, p.causal)) - x.gap;
+  x.chunks = max((n + kChunk - 1) / kChunk, 1);
+  return x;
+}
 
 __device__ __forceinline__ void store_row(const StreamFp8Params& p, int row, int head, int d, int col, const float4& v, float lse) {
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)row * p.Hq + head) * d + col) =
@@ -81,93 +129,140 @@ __device__ __forceinline__ void store_row(const StreamFp8Params& p, int row, int
   if (p.lse && col == 0) p.lse[head * p.lse_head + row * p.lse_row] = lse;
 }
 
+// What a row sees: keys [lo, hi) and [0, sk); pos its position.
+struct Sight {
+  int lo, hi, sk, pos;
+  __device__ __forceinline__ bool sees(int t) const { return (t >= lo && t < hi) || t < sk; }
+};
+// A piece's rows, kept out of registers: they are looked at where a chunk holds tokens that not every row sees.
+template <int D, int R>
+struct Shared {
+  uint2 q[R / 8][D / 16][32];   // Q^T's fragments
+  Sight rows[R], all, any;      // of each row, what all of them see, and what at least one does
+  float slope[R], fac[R];
+};
+
 // Raw codes of 16 tokens: K of tokens g, g + 8 and V of tokens 2c, 2c + 1, 2c + 8, 2c + 9.
 template <int D>
-struct Codes {
-  uint32_t k[2][D / 16], v[4][D / 32];
+struct KCodes {
+  uint32_t w[2][D / 16];
 };
-// What a warp knows of 32 chunks ahead, one per lane: the chunk's first row in the pool (-1: none) and its page's scales.
+template <int D>
+struct VCodes {
+  uint32_t w[4][D / 32];
+};
+// What a warp knows of 32 chunks ahead, one per lane: the chunk's page (-1: none) and first row in the pool, and its
+// page's scales.
 struct Meta {
-  int row;
-  float ks, vs;
+  int page, row;
+  float ks, lv, ivs;   // K's scale; log2 and the reciprocal of V's
 };
 
 template <int D, int NT, bool kScores>
-__device__ __forceinline__ void stream_split(const StreamFp8Params& p, float* scratch, const Group& x, int split, int v0,
-                                             int v1, int cut, int gap, bool alone) {
+__device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* scratch, Shared<D, 8 * NT>& sh, const Group& x,
+                                             int hkv, int chunk0, int nchunks, int piece, bool alone) {
+  constexpr int W = kWarps<NT>, Y = kTogether<NT>, kBatch = 32 / Y;   // steps that a warp looks ahead for at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int G = p.Hq / p.Hkv;
-  const int nchunks = (v1 - v0 + kChunk - 1) / kChunk;
-  const int n_mine = warp < nchunks ? (nchunks - warp + kWarps - 1) / kWarps : 0;
+  const int G = p.group;
+  // (the last step's second chunk may not exist)
+  const int nsteps = (nchunks + Y - 1) / Y, n_mine = warp < nsteps ? (nsteps - warp + W - 1) / W : 0;
   const int32_t* table = p.block_table + (size_t)x.b * p.max_pages;
   const size_t token_bytes = (size_t)p.Hkv * D;
-  const uint8_t* kc = static_cast<const uint8_t*>(p.kcache) + (size_t)x.hkv * D;
-  const uint8_t* vc = static_cast<const uint8_t*>(p.vcache) + (size_t)x.hkv * D;
-  const int P = p.page_size;
-  // chunk i of this warp: tokens from this one on (v0 is a multiple of 16, pages are as well)
-  auto token = [&](int i) -> int {
-    const int v = v0 + (warp + i * kWarps) * kChunk;
-    return v >= cut ? v + gap : v;
+  const uint8_t* kc = static_cast<const uint8_t*>(p.kcache) + (size_t)hkv * D + 16 * c + g * token_bytes;
+  const uint8_t* vc = static_cast<const uint8_t*>(p.vcache) + (size_t)hkv * D + (D / 8) * g + 2 * c * token_bytes;
+  // chunk y of this warp's step i: its number in the piece, and its tokens from this one on
+  auto number = [&](int i, int y) -> int { return Y * (warp + i * W) + y; };
+  auto token = [&](int i, int y) -> int {
+    const int v = (chunk0 + number(i, y)) * kChunk;
+    return v >= x.cut ? v + x.gap : v;
   };
   auto look = [&](int i0) -> Meta {
-    Meta m{-1, 1.f, 1.f};
-    if (i0 + lane < n_mine) {
-      const int t = token(i0 + lane), pi = t / P;
-      const int page = __ldg(table + pi);
-      if (page >= 0 && page < p.num_pages) {
-        m.row = page * P + (t - pi * P);
-        m.ks = __ldg(p.kscale + (size_t)page * p.Hkv + x.hkv);
-        m.vs = __ldg(p.vscale + (size_t)page * p.Hkv + x.hkv);
+    Meta m{-1, 0, 1.f, 0.f, 1.f};
+    const int i = i0 + lane / Y, y = lane % Y;
+    if (i < n_mine && number(i, y) < nchunks) {
+      const int t = token(i, y);
+      if (t >= x.L) return m;                          // (a group that sees nothing: one chunk, all hidden)
+      m.page = __ldg(table + (t >> p.page_shift));
+      if (m.page >= 0 && m.page < p.num_pages) {
+        m.row = (m.page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
       } else {
         record_status(p.status, kStatusDeviceCheck);
+        m.page = -1;
       }
     }
     return m;
   };
-  auto load_k = [&](Codes<D>& w, int row) {
-    const uint8_t* src = kc + (size_t)max(row, 0) * token_bytes + 16 * c;
+  auto scales = [&](Meta& m) {
+    if (m.page < 0) return;
+    const size_t at = (size_t)m.page * p.Hkv + hkv;
+    m.ks = __ldg(p.kscale + at);
+    const float vs = __ldg(p.vscale + at);
+    const uint32_t b = __float_as_uint(vs);            // a power of two has both exactly
+    m.lv = (b & 0x7fffffu) == 0 ? (float)((int)(b >> 23) - 127) : log2f(vs);
+    m.ivs = (b & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - b) : 1.f / vs;
+  };
+  auto load_k = [&](KCodes<D>& k, int row) {
+    const uint8_t* src = kc + (size_t)row * token_bytes;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int u = 0; u < D / 64; ++u) {
-        const uint4 a = ldg16(src + (size_t)(g + 8 * t) * token_bytes + 64 * u);
-        w.k[t][4 * u] = a.x, w.k[t][4 * u + 1] = a.y, w.k[t][4 * u + 2] = a.z, w.k[t][4 * u + 3] = a.w;
+        const uint4 a = ldg16(src + 8 * t * token_bytes + 64 * u);
+        k.w[t][4 * u] = a.x, k.w[t][4 * u + 1] = a.y, k.w[t][4 * u + 2] = a.z, k.w[t][4 * u + 3] = a.w;
       }
   };
-  auto load_v = [&](Codes<D>& w, int row) {
-    const uint8_t* src = vc + (size_t)max(row, 0) * token_bytes + (D / 8) * g;
+  auto load_v = [&](VCodes<D>& v, int row) {
+    const uint8_t* src = vc + (size_t)row * token_bytes;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const uint8_t* at = src + (size_t)(2 * c + (t & 1) + 8 * (t >> 1)) * token_bytes;
+      const uint8_t* at = src + ((t & 1) + 8 * (t >> 1)) * token_bytes;
       if constexpr (D == 128) {
         const uint4 a = ldg16(at);
-        w.v[t][0] = a.x, w.v[t][1] = a.y, w.v[t][2] = a.z, w.v[t][3] = a.w;
+        v.w[t][0] = a.x, v.w[t][1] = a.y, v.w[t][2] = a.z, v.w[t][3] = a.w;
       } else {
         const uint2 a = ldg8(at);
-        w.v[t][0] = a.x, w.v[t][1] = a.y;
+        v.w[t][0] = a.x, v.w[t][1] = a.y;
       }
     }
   };
-
-  // the first chunks' codes are on their way while Q is brought to fp16
-  Meta meta = look(0), ahead = look(32);
-  Codes<D> w[2];
-  const int row_0 = __shfl_sync(0xffffffffu, meta.row, 0), row_1 = __shfl_sync(0xffffffffu, meta.row, 1);
-  if (n_mine > 0) load_k(w[0], row_0), load_v(w[0], row_0);
-  if (n_mine > 1) load_k(w[1], row_1), load_v(w[1], row_1);
-
-  // Q^T: columns are rows g of each tile of 8; and the factors of the lane's two score columns 2c, 2c + 1
-  uint32_t q[NT][D / 16][2];
-  float fac[NT][2], slope[NT][2];
-  int lo[NT][2], hi[NT][2], sk[NT][2], pos[NT][2];
+  // the first step's codes are on their way while Q is brought to fp16 (a chunk without a page reads the pool's first)
+  Meta meta = look(0), ahead = meta;
+  KCodes<D> kw[Y];
+  VCodes<D> vw[Y];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = x.r0 + 8 * n + g;
+  for (int y = 0; y < Y; ++y) {
+    const int row = __shfl_sync(0xffffffffu, meta.row, y);
+    load_k(kw[y], row);
+    load_v(vw[y], row);
+  }
+  scales(meta);
+  if (n_mine > kBatch) {
+    ahead = look(kBatch);
+    scales(ahead);
+  }
+
+  if (threadIdx.x < 8 * NT) {
+    const int r = x.r0 + min((int)threadIdx.x, x.rows - 1), query = quotient(r, p.by_group);
+    const int W0 = p.shape.window;
+    auto sight = [&](int at) -> Sight {
+      return {W0 > 0 ? max(at - W0 + 1, 0) : 0, p.causal ? at + 1 : W0 > 0 && W0 < x.L - at ? at + W0 : x.L,
+              shape_sinks(p.shape, at, x.L, p.causal), at};
+    };
+    sh.rows[threadIdx.x] = sight(x.off + query);
+    sh.slope[threadIdx.x] = kScores && p.shape.slopes ? -__ldg(p.shape.slopes + hkv * G + r - query * G) * kLog2e : 0.f;
+    if (threadIdx.x == 0) {
+      const Sight a = sight(x.off + quotient(x.r0, p.by_group)), e = sight(x.off + quotient(x.r0 + x.rows - 1, p.by_group));
+      sh.all = {e.lo, a.hi, a.sk, 0};
+      sh.any = {a.lo, e.hi, e.sk, 0};
+    }
+  }
+  // Q^T, a tile of 8 rows a warp: columns are rows g; and the factors of its rows' scores
+  if (warp >= W - NT) {
+    const int n = W - 1 - warp, r = x.r0 + min(8 * n + g, x.rows - 1), query = quotient(r, p.by_group);
     const bool live = 8 * n + g < x.rows;
-    float f[D / 4];
-    float m = 0.f;
+    float f[D / 4], m = 0.f;
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                               ((size_t)(x.q0 + (live ? r / G : 0)) * p.Hq + x.hkv * G + (live ? r % G : 0)) * D;
+                               ((size_t)(x.q0 + query) * p.Hq + hkv * G + r - query * G) * D;
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
@@ -188,151 +283,157 @@ __device__ __forceinline__ void stream_split(const StreamFp8Params& p, float* sc
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[n][4 * u + j][0] = pack_f16x2(f[16 * u + 4 * j] * mul, f[16 * u + 4 * j + 1] * mul);
-        q[n][4 * u + j][1] = pack_f16x2(f[16 * u + 4 * j + 2] * mul, f[16 * u + 4 * j + 3] * mul);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = 2 * c + i;
-      fac[n][i] = __shfl_sync(0xffffffffu, back, col * 4) * (kScores && p.shape.cap > 0.f ? 1.f : p.scale * kLog2e);
-      const int rr = x.r0 + min(8 * n + col, x.rows - 1);
-      const int at = x.off + rr / G;
-      pos[n][i] = at;
-      lo[n][i] = p.shape.window > 0 ? max(at - p.shape.window + 1, 0) : 0;
-      hi[n][i] = p.causal ? at + 1 : p.shape.window > 0 && p.shape.window < x.L - at ? at + p.shape.window : x.L;
-      sk[n][i] = shape_sinks(p.shape, at, x.L, p.causal);
-      slope[n][i] = kScores && p.shape.slopes ? -__ldg(p.shape.slopes + x.hkv * G + rr % G) * kLog2e : 0.f;
-    }
+      for (int j = 0; j < 4; ++j)
+        sh.q[n][4 * u + j][lane] = make_uint2(pack_f16x2(f[16 * u + 4 * j] * mul, f[16 * u + 4 * j + 1] * mul),
+                                              pack_f16x2(f[16 * u + 4 * j + 2] * mul, f[16 * u + 4 * j + 3] * mul));
+    if (c == 0) sh.fac[8 * n + g] = back * (kScores && p.shape.cap > 0.f ? 1.f : p.scale * kLog2e);
   }
-  // tokens that every row of the group sees: [all_lo, all_hi) and [0, all_sk)
-  const int at0 = x.off + x.r0 / G, at1 = x.off + (x.r0 + x.rows - 1) / G;
-  const int all_lo = p.shape.window > 0 ? max(at1 - p.shape.window + 1, 0) : 0;
-  const int all_hi = p.causal ? at0 + 1 : p.shape.window > 0 && p.shape.window < x.L - at0 ? at0 + p.shape.window : x.L;
-  const int all_sk = shape_sinks(p.shape, at0, x.L, p.causal);
-  const int any_sk = shape_sinks(p.shape, at1, x.L, p.causal);
-
-  float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  __syncthreads();
+  float fac[NT][2], o[NT][D / 16][4];
+  float m[NT][2], limit[NT][2], l[NT][2];   // limit: m + kLazy once there is a maximum
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-    m[n][0] = m[n][1] = -CUDART_INF_F;
-    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      fac[n][z] = sh.fac[8 * n + 2 * c + z];
+      m[n][z] = limit[n][z] = kNone;
+      l[n][z] = 0.f;
+    }
   }
 
-  auto step = [&](int i, Codes<D>& cur) {
-    const int row = __shfl_sync(0xffffffffu, meta.row, i & 31);
-    const float ks = __shfl_sync(0xffffffffu, meta.ks, i & 31), vs = __shfl_sync(0xffffffffu, meta.vs, i & 31);
-    const int t0 = token(i);
-    float s[NT][4];
+  for (int i = 0; i < n_mine; ++i) {
+    if (i % kBatch == 0 && i > 0) {
+      meta = ahead;
+      if (i + kBatch < n_mine) {
+        ahead = look(i + kBatch);
+        scales(ahead);
+      }
+    }
+    float s[Y][NT][4], ivs[Y];
+    const bool last = i + 1 == n_mine, wrap = i % kBatch == kBatch - 1;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[y][n][0] = s[y][n][1] = s[y][n][2] = s[y][n][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-      uint32_t a0, a1, a2, a3;
-      cvt4(cur.k[0][j], a0, a2);
-      cvt4(cur.k[1][j], a1, a3);
+      uint2 b[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f16(s[n], a0, a1, a2, a3, q[n][j][0], q[n][j][1]);
-    }
-    // chunk i + 2 takes the registers
-    const bool more_chunks = i + 2 < n_mine;
-    const int next_row = __shfl_sync(0xffffffffu, ((i + 2) & 31) < 2 ? ahead.row : meta.row, (i + 2) & 31);
-    if (more_chunks) load_k(cur, next_row);
-    // the page's scales; log2 of a power of two is exact
-    const uint32_t vb = __float_as_uint(vs);
-    const float lv = (vb & 0x7fffffu) == 0 ? (float)((int)(vb >> 23) - 127) : log2f(vs);
-    const float ivs = (vb & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - vb) : 1.f / vs;
+      for (int n = 0; n < NT; ++n) b[n] = sh.q[n][j][lane];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float f0 = fac[n][0] * ks, f1 = fac[n][1] * ks;
-      s[n][0] *= f0, s[n][1] *= f1, s[n][2] *= f0, s[n][3] *= f1;
-      if constexpr (kScores) {
-        if (p.shape.cap > 0.f) cap_in_place(p.shape, s[n]);
-        if (p.shape.slopes) {
-          const int t = t0 + g;
-          s[n][0] = fmaf(slope[n][0], fabsf((float)(pos[n][0] - t)), s[n][0]);
-          s[n][1] = fmaf(slope[n][1], fabsf((float)(pos[n][1] - t)), s[n][1]);
-          s[n][2] = fmaf(slope[n][0], fabsf((float)(pos[n][0] - t - 8)), s[n][2]);
-          s[n][3] = fmaf(slope[n][1], fabsf((float)(pos[n][1] - t - 8)), s[n][3]);
-        }
+      for (int y = 0; y < Y; ++y) {
+        uint32_t a0, a1, a2, a3;
+        cvt4(kw[y].w[0][j], a0, a2);
+        cvt4(kw[y].w[1][j], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(s[y][n], a0, a1, a2, a3, b[n].x, b[n].y);
       }
     }
-    // hidden tokens: -inf, and V codes that mean nothing must not meet a weight of 0
-    if (row < 0 || !((t0 >= all_lo && t0 + kChunk <= all_hi) || t0 + kChunk <= all_sk)) {
+    int next[Y];   // the next step's rows: its keys take the registers
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int y = 0; y < Y; ++y) {
+      next[y] = __shfl_sync(0xffffffffu, wrap ? ahead.row : meta.row, ((i + 1) % kBatch) * Y + y);
+      if (!last) load_k(kw[y], next[y]);
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = t0 + g + 8 * (k >> 1), y = k & 1;
-          if (row < 0 || !((t >= lo[n][y] && t < hi[n][y]) || t < sk[n][y])) s[n][k] = -CUDART_INF_F;
-        }
+    for (int y = 0; y < Y; ++y) {
+      const int from = (i % kBatch) * Y + y;
+      const bool none = __shfl_sync(0xffffffffu, meta.page, from) < 0;
+      const float ks = __shfl_sync(0xffffffffu, meta.ks, from), lv = __shfl_sync(0xffffffffu, meta.lv, from);
+      ivs[y] = __shfl_sync(0xffffffffu, meta.ivs, from);
+      const int t0 = token(i, y);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = t0 + 2 * c + (k & 1) + 8 * (k >> 1);
-        if (row < 0 || !((t >= x.lo && t < x.hi) || t < any_sk)) {
+      for (int n = 0; n < NT; ++n) {
+        float (&u)[4] = s[y][n];
+        const float f0 = fac[n][0] * ks, f1 = fac[n][1] * ks;
+        if constexpr (kScores) {
+          u[0] *= f0, u[1] *= f1, u[2] *= f0, u[3] *= f1;
+          if (p.shape.cap > 0.f) cap_in_place(p.shape, u);
+          if (p.shape.slopes) {
+            const int t = t0 + g, r = 8 * n + 2 * c;
+            const float away0 = (float)(sh.rows[r].pos - t), away1 = (float)(sh.rows[r + 1].pos - t);
+            const float slope0 = sh.slope[r], slope1 = sh.slope[r + 1];
+            u[0] = fmaf(slope0, fabsf(away0), u[0]);
+            u[1] = fmaf(slope1, fabsf(away1), u[1]);
+            u[2] = fmaf(slope0, fabsf(away0 - 8.f), u[2]);
+            u[3] = fmaf(slope1, fabsf(away1 - 8.f), u[3]);
+          }
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) cur.v[k][e] = 0;
+          for (int k = 0; k < 4; ++k) u[k] += lv;
+        } else {
+          u[0] = fmaf(u[0], f0, lv), u[1] = fmaf(u[1], f1, lv);
+          u[2] = fmaf(u[2], f0, lv), u[3] = fmaf(u[3], f1, lv);
         }
       }
+      // hidden tokens: -inf, and V codes that mean nothing must not meet a weight of 0
+      if (none || !((t0 >= sh.all.lo && t0 + kChunk <= sh.all.hi) || t0 + kChunk <= sh.all.sk)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (none || !sh.rows[8 * n + 2 * c + (k & 1)].sees(t0 + g + 8 * (k >> 1))) s[y][n][k] = -CUDART_INF_F;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (none || !sh.any.sees(t0 + 2 * c + (k & 1) + 8 * (k >> 1))) {
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) vw[y].w[k][e] = 0;
+          }
+      }
     }
+    auto top_of = [&](int n, int z) -> float {
+      return Y == 2 ? fmaxf(fmax3(s[0][n][z], s[0][n][2 + z], s[Y - 1][n][z]), s[Y - 1][n][2 + z]) : fmaxf(s[0][n][z], s[0][n][2 + z]);
+    };
     bool more = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][k] += lv;
-      more |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kLazy || fmaxf(s[n][1], s[n][3]) > m[n][1] + kLazy;
-    }
+    for (int n = 0; n < NT; ++n) more |= top_of(n, 0) > limit[n][0] || top_of(n, 1) > limit[n][1];
     if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float mx = fmaxf(s[n][y], s[n][2 + y]);
+        for (int z = 0; z < 2; ++z) {
+          float mx = top_of(n, z);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float next = fmaxf(m[n][y], mx);
-          const float a = next == -CUDART_INF_F ? 1.f : ex2(m[n][y] - next);
-          m[n][y] = next;
-          l[n][y] *= a;
+          const float top = fmaxf(m[n][z], mx), a = ex2(m[n][z] - top);
+          m[n][z] = top;
+          limit[n][z] = top + kLazy;
+          l[n][z] *= a;
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) o[n][e][y] *= a, o[n][e][2 + y] *= a;
+          for (int e = 0; e < D / 16; ++e) o[n][e][z] *= a, o[n][e][2 + z] *= a;
         }
     }
-    uint32_t pt[NT][2];
+    uint32_t pt[Y][NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float b0 = m[n][0] == -CUDART_INF_F ? 0.f : m[n][0], b1 = m[n][1] == -CUDART_INF_F ? 0.f : m[n][1];
-      const float p0 = ex2(s[n][0] - b0), p1 = ex2(s[n][1] - b1), p2 = ex2(s[n][2] - b0), p3 = ex2(s[n][3] - b1);
-      l[n][0] = fmaf(p0 + p2, ivs, l[n][0]);
-      l[n][1] = fmaf(p1 + p3, ivs, l[n][1]);
-      pt[n][0] = transpose8x8(pack_f16x2(p0, p1));
-      pt[n][1] = transpose8x8(pack_f16x2(p2, p3));
-    }
+    for (int y = 0; y < Y; ++y)
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const uint32_t sel = y ? 0x7362 : 0x5140;    // codes 2y, 2y + 1 of two tokens, token by token
-        uint32_t a0, a1, a2, a3;
-        cvt4(__byte_perm(cur.v[0][e], cur.v[1][e], sel), a0, a1);
-        cvt4(__byte_perm(cur.v[2][e], cur.v[3][e], sel), a2, a3);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * e + y], a0, a1, a2, a3, pt[n][0], pt[n][1]);
+      for (int n = 0; n < NT; ++n) {
+        const float (&u)[4] = s[y][n];
+        const float p0 = ex2(u[0] - m[n][0]), p1 = ex2(u[1] - m[n][1]), p2 = ex2(u[2] - m[n][0]), p3 = ex2(u[3] - m[n][1]);
+        l[n][0] = fmaf(p0 + p2, ivs[y], l[n][0]);
+        l[n][1] = fmaf(p1 + p3, ivs[y], l[n][1]);
+        pt[y][n][0] = transpose8x8(pack_f16x2(p0, p1));
+        pt[y][n][1] = transpose8x8(pack_f16x2(p2, p3));
       }
+#pragma unroll
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t sel = z ? 0x7362 : 0x5140;    // codes 2z, 2z + 1 of two tokens, token by token
+          uint32_t a0, a1, a2, a3;
+          cvt4(__byte_perm(vw[y].w[0][e], vw[y].w[1][e], sel), a0, a1);
+          cvt4(__byte_perm(vw[y].w[2][e], vw[y].w[3][e], sel), a2, a3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * e + z], a0, a1, a2, a3, pt[y][n][0], pt[y][n][1]);
+        }
+    if (!last) {
+#pragma unroll
+      for (int y = 0; y < Y; ++y) load_v(vw[y], next[y]);
     }
-    if (more_chunks) load_v(cur, next_row);
-  };
-  for (int i = 0; i < n_mine; i += 2) {
-    if ((i & 31) == 0 && i > 0) {
-      meta = ahead;
-      ahead = look(i + 32);
-    }
-    step(i, w[0]);
-    if (i + 1 < n_mine) step(i + 1, w[1]);
   }
 
   // ---- the warps' states joined: scratch[w] = { m[R], l[R], O[R][D] }
@@ -356,168 +457,225 @@ __device__ __forceinline__ void stream_split(const StreamFp8Params& p, float* sc
   }
   __syncthreads();
   constexpr int C4 = D / 4;
-  for (int idx = threadIdx.x; idx < x.rows * C4; idx += kWarps * 32) {
+  for (int idx = threadIdx.x; idx < x.rows * C4; idx += W * 32) {
     const int r = idx / C4, col = (idx - r * C4) * 4;
-    float top = -CUDART_INF_F;
+    float top = kNone;
 #pragma unroll
-    for (int u = 0; u < kWarps; ++u) top = fmaxf(top, scratch[u * kWs + r]);
+    for (int u = 0; u < W; ++u) top = fmaxf(top, scratch[u * kWs + r]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    if (top != -CUDART_INF_F) {
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u) {
-        const float f = ex2(scratch[u * kWs + r] - top);
-        const float4 a = *reinterpret_cast<const float4*>(scratch + u * kWs + 2 * R + r * D + col);
-        acc.x = fmaf(f, a.x, acc.x), acc.y = fmaf(f, a.y, acc.y);
-        acc.z = fmaf(f, a.z, acc.z), acc.w = fmaf(f, a.w, acc.w);
-        sum = fmaf(f, scratch[u * kWs + R + r], sum);
-      }
+    for (int u = 0; u < W; ++u) {
+      const float f = ex2(scratch[u * kWs + r] - top);
+      const float4 a = *reinterpret_cast<const float4*>(scratch + u * kWs + 2 * R + r * D + col);
+      acc.x = fmaf(f, a.x, acc.x), acc.y = fmaf(f, a.y, acc.y);
+      acc.z = fmaf(f, a.z, acc.z), acc.w = fmaf(f, a.w, acc.w);
+      sum = fmaf(f, scratch[u * kWs + R + r], sum);
     }
     // (a NaN sum stays one; no key seen: 0 and -inf)
     const float inv = sum == 0.f ? 0.f : 1.f / sum, lse = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
     acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-    const int rr = x.r0 + r;
-    const size_t out = (size_t)(x.q0 + rr / G) * p.Hq + x.hkv * G + rr % G;
+    const int query = quotient(x.r0 + r, p.by_group), head = hkv * G + x.r0 + r - query * G;
+    const size_t out = (size_t)(x.q0 + query) * p.Hq + head;
     if (alone) {
-      store_row(p, x.q0 + rr / G, x.hkv * G + rr % G, D, col, acc, lse);
+      store_row(p, x.q0 + query, head, D, col, acc, lse);
     } else {
-      *reinterpret_cast<float4*>(p.o_part + (out * p.num_splits + split) * D + col) = acc;
-      if (col == 0) p.lse_part[out * p.num_splits + split] = lse;
+      *reinterpret_cast<float4*>(p.o_part + (out * p.num_splits + piece) * D + col) = acc;
+      if (col == 0) p.lse_part[out * p.num_splits + piece] = lse;
     }
   }
 }
 
-// The group's rows from their non-empty splits: lse = ln sum_s e^{lse_s}, O = sum_s e^{lse_s - lse} O_s.
-template <int D>
-__device__ __forceinline__ void merge_group(const StreamFp8Params& p, const Group& x, int nvalid) {
-  constexpr int C4 = D / 4;
-  const int G = p.Hq / p.Hkv;
-  for (int idx = threadIdx.x; idx < x.rows * C4; idx += kWarps * 32) {
-    const int r = x.r0 + idx / C4, col = (idx % C4) * 4;
-    const size_t prow = ((size_t)(x.q0 + r / G) * p.Hq + x.hkv * G + r % G) * p.num_splits;
-    float top = -CUDART_INF_F;
-    for (int s = 0; s < nvalid; ++s) top = fmaxf(top, __ldcg(p.lse_part + prow + s));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < nvalid; ++s) {
-      const float ls = __ldcg(p.lse_part + prow + s);
-      const float f = ls == -CUDART_INF_F ? 0.f : ex2((ls - top) * kLog2e);
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(p.o_part + (prow + s) * D + col));
-      acc.x = fmaf(f, a.x, acc.x), acc.y = fmaf(f, a.y, acc.y), acc.z = fmaf(f, a.z, acc.z), acc.w = fmaf(f, a.w, acc.w);
-      sum += f;
+// The group's rows from their pieces: lse = ln sum_s e^{lse_s}, O = sum_s e^{lse_s - lse} O_s. kRound pieces of all of a
+// thread's rows are loaded together (they cost a trip to the L2 cache each otherwise).
+template <int D, int NT>
+__device__ __forceinline__ void join_pieces(const StreamFp8Params& p, const Group& x, int hkv, int pieces) {
+  constexpr int C4 = D / 4, kPer = kWarps<NT> * 32 / C4, kRows = (8 * NT + kPer - 1) / kPer, kRound = 12 / kRows;
+  const int col = threadIdx.x % C4 * 4;
+  size_t prow[kRows];
+  int query[kRows], head[kRows];
+  float4 acc[kRows];
+  float sum[kRows], top[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = x.r0 + min((int)threadIdx.x / C4 + k * kPer, x.rows - 1);
+    query[k] = quotient(r, p.by_group);
+    head[k] = hkv * p.group + r - query[k] * p.group;
+    prow[k] = ((size_t)(x.q0 + query[k]) * p.Hq + head[k]) * p.num_splits;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum[k] = 0.f;
+    top[k] = kNone;
+  }
+  for (int s0 = 0; s0 < pieces; s0 += kRound) {
+    float ls[kRows][kRound];
+    float4 a[kRows][kRound];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int s = 0; s < kRound; ++s) {
+        const size_t at = prow[k] + min(s0 + s, pieces - 1);
+        ls[k][s] = __ldcg(p.lse_part + at);
+        a[k][s] = __ldcg(reinterpret_cast<const float4*>(p.o_part + at * D + col));
+      }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      float mx = top[k];
+#pragma unroll
+      for (int s = 0; s < kRound; ++s) {
+        ls[k][s] = s0 + s < pieces ? ls[k][s] * kLog2e : -CUDART_INF_F;
+        mx = fmaxf(mx, ls[k][s]);
+      }
+      const float keep = ex2(top[k] - mx);
+      top[k] = mx;
+      acc[k].x *= keep, acc[k].y *= keep, acc[k].z *= keep, acc[k].w *= keep, sum[k] *= keep;
+#pragma unroll
+      for (int s = 0; s < kRound; ++s) {
+        const float f = ex2(ls[k][s] - mx);
+        acc[k].x = fmaf(f, a[k][s].x, acc[k].x), acc[k].y = fmaf(f, a[k][s].y, acc[k].y);
+        acc[k].z = fmaf(f, a[k][s].z, acc[k].z), acc[k].w = fmaf(f, a[k][s].w, acc[k].w);
+        sum[k] += f;
+      }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-    store_row(p, x.q0 + r / G, x.hkv * G + r % G, D, col, acc, sum == 0.f ? -CUDART_INF_F : top + logf(sum));
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if ((int)threadIdx.x / C4 + k * kPer >= x.rows) continue;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+    acc[k].x *= inv, acc[k].y *= inv, acc[k].z *= inv, acc[k].w *= inv;
+    store_row(p, x.q0 + query[k], head[k], D, col, acc[k], sum[k] == 0.f ? -CUDART_INF_F : (top[k] + log2f(sum[k])) * kLn2);
   }
 }
 
-// Persistent grid over items (group of rows, split) from a counter, highest split first, as in decode.cu; the groups of one
-// KV head follow each other, so that their reads of it meet in the L2 cache. The CTA that finishes the last non-empty split
-// of a group joins them.
+// All groups' steps in one line, (group of rows, KV head) after (group of rows, KV head), cut into equal shares, one a CTA:
+// every SM streams the same number of bytes whatever the sequences' lengths are. A share is long enough that no group is
+// cut into more than num_splits pieces. A group that lies in one share is written at once; else its pieces' partials
+// are joined by the CTA that finishes the last of them.
 template <int D, int NT, bool kScores>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) stream_fp8_kernel(const StreamFp8Params p) {
-  __shared__ __align__(16) float scratch[kWarps * 8 * NT * (D + 2)];
-  __shared__ int s_item, s_last;
-  const int G = p.Hq / p.Hkv, P = p.page_size;
-  const int R = 8 * NT;
-  const int nsub = (int)(((long long)p.max_q * G + R - 1) / R);
-  const int groups = p.B * p.Hkv * nsub, total = p.num_splits * groups;
-  const int cap = p.max_pages * P;
-  // pages that a group's rows can see, which the splits share
-  const long long width = (p.causal ? 1ll : 2ll) * p.shape.window + (R - 1) / G + 1;
-  int seen = p.max_pages;
-  if (p.shape.window > 0)
-    seen = (int)min((long long)seen, (width + P - 2) / P + 1 + sink_blocks(p.shape.sinks, P));
-  const long long span = (long long)((seen + p.num_splits - 1) / p.num_splits) * P;
-  for (;;) {
-    if (threadIdx.x == 0) s_item = atomicAdd(p.counters, 1);
-    __syncthreads();
-    const int item = s_item;
-    __syncthreads();
-    if (item < 0 || item >= total) break;
-    const int split = p.num_splits - 1 - item / groups;
-    const int gi = item % groups;
-    Group x;
-    const int sub = gi % nsub;
-    x.hkv = gi / nsub % p.Hkv;
-    x.b = gi / nsub / p.Hkv;
-    x.L = __ldg(p.seqlens_k + x.b);
-    int lq = 1;
-    if (p.cu_seqlens) {
-      x.q0 = __ldg(p.cu_seqlens + x.b);
-      lq = __ldg(p.cu_seqlens + x.b + 1) - x.q0;
-      if (x.q0 < 0 || lq < 0 || lq > p.rows - x.q0 || lq > p.max_q || x.L < lq || x.L > cap) {
-        if (threadIdx.x == 0 && split == 0) record_status(p.status, kStatusDeviceCheck);
-        continue;
+__global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const StreamFp8Params p) {
+  constexpr int R = 8 * NT, W = kWarps<NT>, Y = kTogether<NT>, T = W * 32;
+  __shared__ __align__(16) float scratch[W * R * (D + 2)];
+  __shared__ Shared<D, R> sh;
+  __shared__ Group s_x;
+  __shared__ int s_sum[W], s_most[W], s_off, s_v, s_last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int V = p.B * p.subs;                          // groups of rows, each with Hkv groups
+  // a thread's groups of rows, and the steps before them (the host has made sure that all of them are an int)
+  const int per = (V + T - 1) / T;
+  const int mine0 = min((int)threadIdx.x * per, V), mine1 = min(mine0 + per, V);
+  int sum = 0, most = 0;
+  Group x;
+  for (int v = mine0; v < mine1; ++v) {
+    x = describe<R>(p, v, blockIdx.x == 0);
+    sum += x.chunks * p.Hkv;
+    most = max(most, x.chunks);
+  }
+  int before = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, m);
+    if (lane >= m) before += y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) s_sum[warp] = before, s_most[warp] = most;
+  before -= sum;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+    most = max(most, s_most[w]);
+  }
+  // equal shares in whole rounds of the warps; one piece a group: the groups that begin in the share, whole
+  const bool whole = p.num_splits == 1;
+  unsigned share = ((unsigned)total + gridDim.x - 1) / gridDim.x;
+  if (!whole) share = max(share, ((unsigned)most + p.num_splits - 2) / (p.num_splits - 1));
+  share = (max(share, 1u) + Y * W - 1) / (Y * W) * (Y * W);
+  if ((unsigned long long)share * blockIdx.x >= total) return;
+  int at = (int)(share * blockIdx.x);                  // in steps
+  const int stop = (int)min((unsigned long long)share * (blockIdx.x + 1ull), (unsigned long long)total);
+  const int end = whole ? total : stop;
+  if (at >= before && at < before + sum) {
+    int y = before;
+    for (int v = mine0; v < mine1; ++v) {
+      if (per > 1) x = describe<R>(p, v, false);
+      const int n = x.chunks * p.Hkv;
+      if (at < y + n) {
+        s_v = v;
+        s_off = at - y;
+        s_x = x;
+        break;
       }
-    } else {
-      x.q0 = x.b;
-      if (x.L < 0 || x.L > cap) {
-        if (threadIdx.x == 0 && split == 0) record_status(p.status, kStatusDeviceCheck);
-        x.L = x.L < 0 ? 0 : cap;
-      }
+      y += n;
     }
-    x.r0 = sub * R;
-    x.rows = min(R, lq * G - x.r0);
-    if (x.rows <= 0) continue;
-    x.off = x.L - lq;
-    const int at0 = x.off + x.r0 / G, at1 = x.off + (x.r0 + x.rows - 1) / G;
-    x.lo = p.shape.window > 0 ? max(at0 - p.shape.window + 1, 0) : 0;
-    x.hi = p.causal ? at1 + 1 : p.shape.window > 0 && p.shape.window < x.L - at1 ? at1 + p.shape.window : x.L;
-    // the tokens of the group, counted without those between the sinks and the window's first page: from cut on token v is
-    // v + gap
-    const int first = x.lo / P * P, sinks = shape_sinks(p.shape, at1, x.L, p.causal);
-    const int cut = min(sink_blocks(p.shape.sinks, P), first / P) * P, gap = first - cut;
-    const int n = max(x.hi, sinks) - gap;
-    const int nvalid = (int)((n + span - 1) / span);
-    const long long v0 = (long long)split * span;
-    if (v0 >= n) {   // nothing here; rows that see no token at all are written by split 0
-      if (split == 0) merge_group<D>(p, x, 0);
-      continue;
+  }
+  __syncthreads();
+  int v = s_v;
+  x = s_x;
+  int hkv = (unsigned)s_off / (unsigned)x.chunks, first = s_off - hkv * x.chunks;
+  if (whole && first > 0) {                            // (its first step lies in a share before)
+    at += x.chunks - first;
+    first = 0;
+    ++hkv;
+  }
+  while (at < stop) {
+    if (hkv == p.Hkv) {
+      hkv = 0;
+      do x = describe<R>(p, ++v, false);
+      while (x.chunks == 0);
     }
-    stream_split<D, NT, kScores>(p, scratch, x, split, (int)v0, (int)min((long long)n, v0 + span), cut, gap, nvalid == 1);
-    if (nvalid > 1) {
+    const int n = min(x.chunks - first, end - at);
+    const int begin = at - first;                      // the group's first step
+    const int c0 = (unsigned)begin / share, c1 = (unsigned)(begin + x.chunks - 1) / share;
+    const int pieces = whole ? 1 : c1 - c0 + 1;
+    stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, first, n, (int)blockIdx.x - c0, pieces == 1);
+    if (pieces > 1) {
       __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(p.counters + 1 + gi, 1) == nvalid - 1;
+      if (threadIdx.x == 0) s_last = atomicAdd(p.counters + v * p.Hkv + hkv, 1) == pieces - 1;
       __syncthreads();
       if (s_last) {
         __threadfence();
-        merge_group<D>(p, x, nvalid);
+        join_pieces<D, NT>(p, x, hkv, pieces);
       }
     }
-    __syncthreads();   // the scratch is read
+    __syncthreads();                                   // the scratch is read
+    at += n;
+    first = 0;
+    ++hkv;
   }
 }
 
 template <int D, int NT, bool kScores>
 cudaError_t launch_t(const StreamFp8Params& p, cudaStream_t stream) {
-  auto kern = stream_fp8_kernel<D, NT, kScores>;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWarps * 32, 0);
-  if (e != cudaSuccess) return e;
   const int sms = num_sms_current();
-  if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidValue;
-  const int G = p.Hq / p.Hkv;
-  const long long groups = stream_fp8_groups(p.B, p.Hkv, (long long)p.max_q * G), items = groups * p.num_splits;
-  e = cudaMemsetAsync(p.counters, 0, (size_t)(1 + groups) * sizeof(int), stream);
-  if (e != cudaSuccess) return e;
-  kern<<<(int)std::min<long long>(items, (long long)sms * per_sm), kWarps * 32, 0, stream>>>(p);
+  if (sms <= 0) return cudaErrorInvalidValue;
+  const long long groups = (long long)p.B * p.subs * p.Hkv;
+  if (p.num_splits > 1) {
+    const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
+    if (e != cudaSuccess) return e;
+  }
+  const long long pieces = groups * p.num_splits;
+  stream_fp8_kernel<D, NT, kScores><<<(int)std::min<long long>(pieces, 2ll * sms), kWarps<NT> * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const StreamFp8Params& p, cudaStream_t stream) {
   const bool scores = p.shape.cap > 0.f || p.shape.slopes;
-  if ((long long)p.max_q * (p.Hq / p.Hkv) <= 8) return scores ? launch_t<D, 1, true>(p, stream) : launch_t<D, 1, false>(p, stream);
+  if ((long long)p.max_q * p.group <= 8) return scores ? launch_t<D, 1, true>(p, stream) : launch_t<D, 1, false>(p, stream);
   return scores ? launch_t<D, 2, true>(p, stream) : launch_t<D, 2, false>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_stream_fp8(const StreamFp8Params& p, cudaStream_t stream) {
+cudaError_t launch_stream_fp8(const StreamFp8Params& p0, cudaStream_t stream) {
+  StreamFp8Params p = p0;
+  p.group = p.Hq / p.Hkv;
+  p.subs = (int)(stream_fp8_groups(p.B, p.Hkv, (long long)p.max_q * p.group) / ((long long)p.B * p.Hkv));
+  p.by_group = ((1ull << 42) + p.group - 1) / p.group;
+  p.by_subs = ((1ull << 42) + p.subs - 1) / p.subs;
+  p.page_shift = p.page_size == 16 ? 4 : p.page_size == 32 ? 5 : p.page_size == 64 ? 6 : 7;
   return p.d == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
 }
 

@@ -243,7 +243,8 @@ fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const v
  * largest finite magnitude of the page's new values (k rotated, in fp32):
  *   need = the least power of two with a <= 448 need, at least 2^-100;
  *   a page whose slots before the new tokens hold context has scale max(old, need), and if that is above the
- *   old one its codes become RN(code * old / new); any other page has scale need (its old one is not read);
+ *   old one the codes of its other slots become RN(code * old / new); any other page has scale need (its old one is not
+ *   read) and its other slots mean nothing;
  *   new codes = RN(value / scale); infinities and NaN become NaN codes.
  * Which slots hold context follows from seqlens_k alone. A page that is appended to must not be shared with another sequence, and
  * no two tokens of a call share a slot. Everything else (chunks, positions, padding rows, strides, skipped rows) is as in

@@ -128,7 +128,7 @@ def test_append(P, Hq, Hkv, d, rot, inter, lk, lq, odd, pos, amp):
                 if kept:
                     ratio = (np.float32(1) * f64(old_scale)[pg] / s).astype(np.float32).astype(np.float64)
                     grown = np.where(s > f64(old_scale)[pg], ratio, 1.0)
-                    expect[pg, :kept] = round_e4m3(expect[pg, :kept] * grown[:, None])
+                    expect[pg] = round_e4m3(expect[pg] * grown[:, None])              # (and the slots past the new tokens)
                 y = rows / s[:, None]
                 have = got[pg, kept:kept + e - a]
                 if turned:
