@@ -444,7 +444,7 @@ extern "C" fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, 
 
 // The streaming kernel counts the steps (16 tokens of a group of rows) of all sequences in an int.
 static bool countable_steps(int B, int Hkv, long long rows, int max_pages, int page_size) {
-  const long long steps = (long long)max_pages * page_size / 16 + 1;
+  const long long steps = (long long)max_pages * page_size / 16 + 64;   // (and the turns between them)
   return stream_fp8_groups(B, Hkv, rows) <= 0x7fffffffLL / steps;
 }
 

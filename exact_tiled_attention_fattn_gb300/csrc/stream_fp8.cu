@@ -34,6 +34,8 @@ constexpr int kWarps = 6;
 // Chunks of 16 tokens that a warp works on together.
 template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
+// What going from one group to the next costs a CTA, in chunks: it counts in the shares.
+constexpr int kTurn = 16;
 constexpr int kChunk = 16;       // tokens of a step
 constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
 constexpr float kLazy = 8.f;     // log2 units that scores may exceed the running maximum by
@@ -151,11 +153,11 @@ template <int D>
 struct VCodes {
   uint32_t w[4][D / 32];
 };
-// What a warp knows of 32 chunks ahead, one per lane: the chunk's page (-1: none) and first row in the pool, and its
-// page's scales.
+// What a warp knows of 32 chunks, one per lane: the chunk's page (-1: none) and first row in the pool, and its page's
+// scales. It is asked for in two trips, each many steps before it is used: the table's entry, then the scales.
 struct Meta {
   int page, row;
-  float ks, lv, ivs;   // K's scale; log2 and the reciprocal of V's
+  float ks, vs;
 };
 
 template <int D, int NT, bool kScores>
@@ -176,30 +178,21 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     const int v = (chunk0 + number(i, y)) * kChunk;
     return v >= x.cut ? v + x.gap : v;
   };
-  auto look = [&](int i0) -> Meta {
-    Meta m{-1, 0, 1.f, 0.f, 1.f};
-    const int i = i0 + lane / Y, y = lane % Y;
-    if (i < n_mine && number(i, y) < nchunks) {
-      const int t = token(i, y);
-      if (t >= x.L) return m;                          // (a group that sees nothing: one chunk, all hidden)
-      m.page = __ldg(table + (t >> p.page_shift));
-      if (m.page >= 0 && m.page < p.num_pages) {
-        m.row = (m.page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-      } else {
-        record_status(p.status, kStatusDeviceCheck);
-        m.page = -1;
-      }
-    }
-    return m;
+  auto look = [&](Meta& m, int i0) {
+    const int i = i0 + lane / Y, y = lane % Y, t = token(i, y);
+    // (a group that sees nothing: one chunk, all hidden, past the sequence's end)
+    m.page = i < n_mine && number(i, y) < nchunks && t < x.L ? __ldg(table + (t >> p.page_shift)) : -1;
   };
-  auto scales = [&](Meta& m) {
-    if (m.page < 0) return;
-    const size_t at = (size_t)m.page * p.Hkv + hkv;
+  auto scales = [&](Meta& m, int i0) {
+    const int i = i0 + lane / Y, y = lane % Y, t = token(i, y);
+    if (m.page < 0 || m.page >= p.num_pages) {
+      if (i < n_mine && number(i, y) < nchunks && t < x.L) record_status(p.status, kStatusDeviceCheck);
+      m.page = -1;
+    }
+    const size_t at = (size_t)max(m.page, 0) * p.Hkv + hkv;
+    m.row = m.page < 0 ? 0 : (m.page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
     m.ks = __ldg(p.kscale + at);
-    const float vs = __ldg(p.vscale + at);
-    const uint32_t b = __float_as_uint(vs);            // a power of two has both exactly
-    m.lv = (b & 0x7fffffu) == 0 ? (float)((int)(b >> 23) - 127) : log2f(vs);
-    m.ivs = (b & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - b) : 1.f / vs;
+    m.vs = __ldg(p.vscale + at);
   };
   auto load_k = [&](KCodes<D>& k, int row) {
     const uint8_t* src = kc + (size_t)row * token_bytes;
@@ -226,7 +219,10 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     }
   };
   // the first step's codes are on their way while Q is brought to fp16 (a chunk without a page reads the pool's first)
-  Meta meta = look(0), ahead = meta;
+  Meta meta, ahead{-1, 0, 1.f, 1.f};
+  look(meta, 0);
+  look(ahead, kBatch);
+  scales(meta, 0);
   KCodes<D> kw[Y];
   VCodes<D> vw[Y];
 #pragma unroll
@@ -234,11 +230,6 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     const int row = __shfl_sync(0xffffffffu, meta.row, y);
     load_k(kw[y], row);
     load_v(vw[y], row);
-  }
-  scales(meta);
-  if (n_mine > kBatch) {
-    ahead = look(kBatch);
-    scales(ahead);
   }
 
   if (threadIdx.x < 8 * NT) {
@@ -303,13 +294,20 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     }
   }
 
+  float lv_of = 0.f, iv_of = 1.f;
   for (int i = 0; i < n_mine; ++i) {
-    if (i % kBatch == 0 && i > 0) {
-      meta = ahead;
-      if (i + kBatch < n_mine) {
-        ahead = look(i + kBatch);
-        scales(ahead);
+    if (i % kBatch == 0) {
+      if (i > 0) {
+        meta = ahead;
+        look(ahead, i + kBatch);
       }
+      // log2 and the reciprocal of V's scale; a power of two has both exactly
+      const uint32_t b = __float_as_uint(meta.vs);
+      if (meta.page < 0) meta.ks = 1.f;
+      lv_of = meta.page < 0 ? 0.f : (b & 0x7fffffu) == 0 ? (float)((int)(b >> 23) - 127) : log2f(meta.vs);
+      iv_of = meta.page < 0 ? 1.f : (b & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - b) : 1.f / meta.vs;
+    } else if (i % kBatch == kBatch / 2) {
+      scales(ahead, i + kBatch / 2);
     }
     float s[Y][NT][4], ivs[Y];
     const bool last = i + 1 == n_mine, wrap = i % kBatch == kBatch - 1;
@@ -341,8 +339,8 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     for (int y = 0; y < Y; ++y) {
       const int from = (i % kBatch) * Y + y;
       const bool none = __shfl_sync(0xffffffffu, meta.page, from) < 0;
-      const float ks = __shfl_sync(0xffffffffu, meta.ks, from), lv = __shfl_sync(0xffffffffu, meta.lv, from);
-      ivs[y] = __shfl_sync(0xffffffffu, meta.ivs, from);
+      const float ks = __shfl_sync(0xffffffffu, meta.ks, from), lv = __shfl_sync(0xffffffffu, lv_of, from);
+      ivs[y] = __shfl_sync(0xffffffffu, iv_of, from);
       const int t0 = token(i, y);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -546,19 +544,20 @@ __device__ __forceinline__ void join_pieces(const StreamFp8Params& p, const Grou
   }
 }
 
-// All groups' steps in one line, (group of rows, KV head) after (group of rows, KV head), cut into equal shares, one a CTA:
-// every SM streams the same number of bytes whatever the sequences' lengths are. A share is long enough that no group is
-// cut into more than num_splits pieces. A group that lies in one share is written at once; else its pieces' partials
-// are joined by the CTA that finishes the last of them.
+// The groups' steps in one line, group of rows after group of rows, cut into equal shares, one for Hkv CTAs, which take a KV
+// head each: every SM streams the same number of bytes whatever the sequences' lengths are, and the heads of a page, side
+// by side in memory, are read at about the same time (reading the pages of 8 heads of 128 alone: 58.5 us for 393 MB so,
+// 64 to 66 with head after head). A share is long enough that no group is cut into more than num_splits pieces. A group that lies
+// in one share is written at once; else its pieces' partials are joined by the CTA that finishes the last of them.
 template <int D, int NT, bool kScores>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const StreamFp8Params p) {
   constexpr int R = 8 * NT, W = kWarps<NT>, Y = kTogether<NT>, T = W * 32;
   __shared__ __align__(16) float scratch[W * R * (D + 2)];
   __shared__ Shared<D, R> sh;
   __shared__ Group s_x;
-  __shared__ int s_sum[W], s_most[W], s_off, s_v, s_last;
+  __shared__ int s_sum[W], s_most[W], s_begin, s_v, s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int V = p.B * p.subs;                          // groups of rows, each with Hkv groups
+  const int V = p.B * p.subs;                          // groups of rows
   // a thread's groups of rows, and the steps before them (the host has made sure that all of them are an int)
   const int per = (V + T - 1) / T;
   const int mine0 = min((int)threadIdx.x * per, V), mine1 = min(mine0 + per, V);
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   Group x;
   for (int v = mine0; v < mine1; ++v) {
     x = describe<R>(p, v, blockIdx.x == 0);
-    sum += x.chunks * p.Hkv;
+    sum += x.chunks > 0 ? kTurn + x.chunks : 0;
     most = max(most, x.chunks);
   }
   int before = sum;
@@ -588,21 +587,23 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   }
   // equal shares in whole rounds of the warps; one piece a group: the groups that begin in the share, whole
   const bool whole = p.num_splits == 1;
-  unsigned share = ((unsigned)total + gridDim.x - 1) / gridDim.x;
+  const unsigned block = blockIdx.x / p.Hkv, blocks = gridDim.x / p.Hkv;
+  const int hkv = blockIdx.x - block * p.Hkv;
+  unsigned share = ((unsigned)total + blocks - 1) / blocks;
   if (!whole) share = max(share, ((unsigned)most + p.num_splits - 2) / (p.num_splits - 1));
-  share = (max(share, 1u) + Y * W - 1) / (Y * W) * (Y * W);
-  if ((unsigned long long)share * blockIdx.x >= total) return;
-  int at = (int)(share * blockIdx.x);                  // in steps
-  const int stop = (int)min((unsigned long long)share * (blockIdx.x + 1ull), (unsigned long long)total);
+  share = max(share, (unsigned)(Y * W));               // (a step for every warp)
+  if ((unsigned long long)share * block >= total) return;
+  int at = (int)(share * block);                       // in steps
+  const int stop = (int)min((unsigned long long)share * (block + 1ull), (unsigned long long)total);
   const int end = whole ? total : stop;
   if (at >= before && at < before + sum) {
     int y = before;
     for (int v = mine0; v < mine1; ++v) {
       if (per > 1) x = describe<R>(p, v, false);
-      const int n = x.chunks * p.Hkv;
+      const int n = x.chunks > 0 ? kTurn + x.chunks : 0;
       if (at < y + n) {
         s_v = v;
-        s_off = at - y;
+        s_begin = y;
         s_x = x;
         break;
       }
@@ -610,39 +611,31 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
     }
   }
   __syncthreads();
-  int v = s_v;
+  int v = s_v, begin = s_begin;                        // the group, and where it begins in the line
   x = s_x;
-  int hkv = (unsigned)s_off / (unsigned)x.chunks, first = s_off - hkv * x.chunks;
-  if (whole && first > 0) {                            // (its first step lies in a share before)
-    at += x.chunks - first;
-    first = 0;
-    ++hkv;
-  }
-  while (at < stop) {
-    if (hkv == p.Hkv) {
-      hkv = 0;
-      do x = describe<R>(p, ++v, false);
-      while (x.chunks == 0);
-    }
-    const int n = min(x.chunks - first, end - at);
-    const int begin = at - first;                      // the group's first step
-    const int c0 = (unsigned)begin / share, c1 = (unsigned)(begin + x.chunks - 1) / share;
-    const int pieces = whole ? 1 : c1 - c0 + 1;
-    stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, first, n, (int)blockIdx.x - c0, pieces == 1);
-    if (pieces > 1) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(p.counters + v * p.Hkv + hkv, 1) == pieces - 1;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        join_pieces<D, NT>(p, x, hkv, pieces);
+  for (;;) {
+    const int zero = begin + kTurn;                    // of its first chunk
+    const int from = whole ? (at <= begin ? zero : zero + x.chunks) : max(at, zero), to = min(end, zero + x.chunks);
+    if (from < to) {
+      const int c0 = (unsigned)zero / share, c1 = (unsigned)(zero + x.chunks - 1) / share;
+      const int pieces = whole ? 1 : c1 - c0 + 1;
+      stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from - zero, to - from, (int)block - c0, pieces == 1);
+      if (pieces > 1) {
+        __syncthreads();                               // the partial is written
+        if (threadIdx.x == 0) {
+          __threadfence();
+          s_last = atomicAdd(p.counters + v * p.Hkv + hkv, 1) == pieces - 1;
+          __threadfence();
+        }
+        __syncthreads();
+        if (s_last) join_pieces<D, NT>(p, x, hkv, pieces);
       }
+      __syncthreads();                                 // the scratch is read
     }
-    __syncthreads();                                   // the scratch is read
-    at += n;
-    first = 0;
-    ++hkv;
+    begin = zero + x.chunks;
+    if (begin >= stop) break;
+    do x = describe<R>(p, ++v, false);
+    while (x.chunks == 0);
   }
 }
 
@@ -655,8 +648,8 @@ cudaError_t launch_t(const StreamFp8Params& p, cudaStream_t stream) {
     const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
     if (e != cudaSuccess) return e;
   }
-  const long long pieces = groups * p.num_splits;
-  stream_fp8_kernel<D, NT, kScores><<<(int)std::min<long long>(pieces, 2ll * sms), kWarps<NT> * 32, 0, stream>>>(p);
+  const long long blocks = std::min<long long>((long long)p.B * p.subs * p.num_splits, std::max(2 * sms / p.Hkv, 1));
+  stream_fp8_kernel<D, NT, kScores><<<(int)(blocks * p.Hkv), kWarps<NT> * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
