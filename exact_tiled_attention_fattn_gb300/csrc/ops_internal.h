@@ -146,10 +146,14 @@ struct StreamFp8Params {
   unsigned long long by_group, by_subs;
 };
 
-// Rows (queries x heads of a group) that a group of the streaming kernel takes, and its groups per (sequence, KV head).
-inline int stream_fp8_rows(int max_rows) { return max_rows <= 8 ? 8 : 16; }
+// Rows (queries x heads of a KV head) that a group of the streaming kernel takes, 8 to 32 in steps of 8, equal groups
+// of them, and the groups of all sequences and KV heads.
+inline int stream_fp8_rows(long long max_rows) {
+  const long long groups = (max_rows + 31) / 32;
+  return groups <= 1 ? (int)((max_rows + 7) / 8 * 8) : (int)((max_rows + 8 * groups - 1) / (8 * groups) * 8);
+}
 inline long long stream_fp8_groups(int B, int Hkv, long long max_rows) {
-  const int r = stream_fp8_rows((int)(max_rows < 16 ? max_rows : 16));
+  const int r = stream_fp8_rows(max_rows);
   return (long long)B * Hkv * ((max_rows + r - 1) / r);
 }
 // Query rows of a KV head up to which a chunk goes to the streaming kernel.

@@ -28,9 +28,9 @@
 namespace fattn {
 namespace {
 
-// Warps of a CTA, two CTAs an SM: what the registers of one or two tiles of 8 query rows leave.
+// Warps of a CTA, two CTAs an SM: what the registers of one to four tiles of 8 query rows leave.
 template <int NT>
-constexpr int kWarps = 6;
+constexpr int kWarps = NT <= 2 ? 6 : 4;
 // Chunks of 16 tokens that a warp works on together.
 template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
@@ -552,7 +552,7 @@ __device__ __forceinline__ void join_pieces(const StreamFp8Params& p, const Grou
 template <int D, int NT, bool kScores>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const StreamFp8Params p) {
   constexpr int R = 8 * NT, W = kWarps<NT>, Y = kTogether<NT>, T = W * 32;
-  __shared__ __align__(16) float scratch[W * R * (D + 2)];
+  extern __shared__ __align__(16) float scratch[];     // kScratch<D, NT> bytes
   __shared__ Shared<D, R> sh;
   __shared__ Group s_x;
   __shared__ int s_sum[W], s_most[W], s_begin, s_v, s_last;
@@ -639,6 +639,9 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   }
 }
 
+template <int D, int NT>
+constexpr int kScratch = kWarps<NT> * 8 * NT * (D + 2) * 4;
+
 template <int D, int NT, bool kScores>
 cudaError_t launch_t(const StreamFp8Params& p, cudaStream_t stream) {
   const int sms = num_sms_current();
@@ -649,15 +652,28 @@ cudaError_t launch_t(const StreamFp8Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const long long blocks = std::min<long long>((long long)p.B * p.subs * p.num_splits, std::max(2 * sms / p.Hkv, 1));
-  stream_fp8_kernel<D, NT, kScores><<<(int)(blocks * p.Hkv), kWarps<NT> * 32, 0, stream>>>(p);
+  auto kern = stream_fp8_kernel<D, NT, kScores>;
+  if (kScratch<D, NT> > 40 * 1024) {   // (without asking, 48 KB with the static part)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScratch<D, NT>);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(int)(blocks * p.Hkv), kWarps<NT> * 32, kScratch<D, NT>, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_n(const StreamFp8Params& p, cudaStream_t stream) {
+  return p.shape.cap > 0.f || p.shape.slopes ? launch_t<D, NT, true>(p, stream) : launch_t<D, NT, false>(p, stream);
 }
 
 template <int D>
 cudaError_t launch_d(const StreamFp8Params& p, cudaStream_t stream) {
-  const bool scores = p.shape.cap > 0.f || p.shape.slopes;
-  if ((long long)p.max_q * p.group <= 8) return scores ? launch_t<D, 1, true>(p, stream) : launch_t<D, 1, false>(p, stream);
-  return scores ? launch_t<D, 2, true>(p, stream) : launch_t<D, 2, false>(p, stream);
+  switch (stream_fp8_rows((long long)p.max_q * p.group)) {
+    case 8: return launch_n<D, 1>(p, stream);
+    case 16: return launch_n<D, 2>(p, stream);
+    case 24: return launch_n<D, 3>(p, stream);
+    default: return launch_n<D, 4>(p, stream);
+  }
 }
 
 }  // namespace

@@ -1121,14 +1121,14 @@ def fwd_paged_fp8_workspace_size(B: int, Hq: int, Hkv: int, d: int, page_size: i
 def choose_fp8_splits(batch: int, Hq: int, Hkv: int, d: int, page_size: int, max_seqlen_q: int, max_context: int,
                       num_sms: int | None = None) -> int:
     """Split count of ``fwd_paged_fp8`` for contexts of ``max_context`` visible tokens. Where the codes are streamed the
-    splits only bound the pieces that a group of 16 query rows may be cut into, so that every CTA (two an SM) takes an equal
+    splits only bound the pieces that a group of up to 32 query rows may be cut into, so that every CTA (two an SM) takes an equal
     share of the steps: enough for sequences twice as long as the mean. Else ``choose_chunk_splits``."""
     if num_sms is None:
         num_sms = _num_sms(torch.cuda.current_device())
     rows = max_seqlen_q * (Hq // max(Hkv, 1))
     if rows > FP8_STREAM_ROWS:
         return choose_chunk_splits(batch, Hq, d, max_seqlen_q, max_context, num_sms)
-    groups = max(1, batch * Hkv * -(-rows // 16))
+    groups = max(1, batch * Hkv * -(-rows // 32))
     return max(1, min(-(-max_context // 64), 2 * -(-2 * num_sms // groups) + 1))
 
 
