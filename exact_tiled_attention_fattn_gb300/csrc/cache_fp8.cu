@@ -37,227 +37,347 @@ __device__ __forceinline__ float2 values2(uint32_t codes) {   // of the low two 
 }
 
 // ------------------------------------------------------------------ append
-// A block takes one page of one sequence, as far as the call's new tokens reach into it, and a share of the heads: KV head h
-// of a page is worked on by this block alone, so its scale and the old codes change without atomics on global memory. The
-// rows' angles are formed once in shared memory (as in rope.cu, 64-bit fixed point); a warp then takes a row of one head at
-// a time, four elements a lane, the other halves of its pairs from the lane that has them. Per page: the magnitudes of K
-// and V (shared-memory maxima), q rotated meanwhile, the scales, old codes of pages that outgrew theirs, and K and V
-// again (from the L1 cache) into codes. Bound by the bytes of q, k and v for prompts, by the chain of loads for single tokens.
+// Two kinds of blocks in one launch. A block of K and V takes one page of one sequence, as far as the call's new tokens
+// reach into it, and a share of the KV heads: a head of a page is worked on by this block alone, so its scale and the old
+// codes change without atomics on global memory. It forms the magnitudes (shared-memory maxima), the scales, re-scales old
+// codes of pages that outgrew theirs, and reads K and V again (from the caches) to make them codes. A block of q takes a
+// few rows with all their heads. The rows' angles are formed once in a block's shared memory (as in rope.cu, 64-bit fixed
+// point): with q's heads shared out over the pages' blocks, angles were half of the work. A lane has eight elements of a
+// row, both halves of its four pairs among them, so that D / 8 lanes take a row and a warp two or four rows at a time.
+// Bound by the bytes of q, k and v for prompts, by the chain of loads for single tokens.
 //
-// kFast: 8-byte aligned rows and heads, and pairs that never split a lane's four elements; else element by element.
-struct Row4 {
-  float x[4];
+// kFast: 8-byte aligned rows and heads, and pairs that never split a lane's elements; else element by element.
+struct Eight {
+  float x[8];
 };
 
+// Where a lane's elements lie: two quads. A turned head in halves: the low and the high elements of four pairs; else eight
+// in a row.
+struct Quads {
+  int a, b;
+};
+template <bool kInter>
+__device__ __forceinline__ Quads quads_of(int sl, int rot, bool turned) {
+  const int lanes = rot >> 3;
+  if (!kInter && turned && sl < lanes) return {4 * sl, 4 * sl + (rot >> 1)};
+  return {8 * sl, 8 * sl + 4};   // (the lanes before have 8 elements each as well, whatever their order)
+}
+
+// (cos, sin) of a lane's four pairs.
+struct Turn {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Turn load_turn(const float2* cs, int sl, int rot) {
+  Turn t;
+  if (sl < (rot >> 3)) {
+    const float4* c4 = reinterpret_cast<const float4*>(cs + 4 * sl);
+    const float4 a = c4[0], b = c4[1];
+    t.c[0] = a.x, t.s[0] = a.y, t.c[1] = a.z, t.s[1] = a.w, t.c[2] = b.x, t.s[2] = b.y, t.c[3] = b.z, t.s[3] = b.w;
+  } else {   // (not used: products by 1 and 0 would make NaN of infinities)
+    t.c[0] = t.c[1] = t.c[2] = t.c[3] = 1.f;
+    t.s[0] = t.s[1] = t.s[2] = t.s[3] = 0.f;
+  }
+  return t;
+}
+
+// The lane's elements of a row.
 template <bool kFast>
-__device__ __forceinline__ Row4 load4(const __nv_bfloat16* p, int e) {
-  Row4 r;
+__device__ __forceinline__ Eight load_eight(const __nv_bfloat16* p, const Quads& at) {
+  Eight r;
   if constexpr (kFast) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + e));
-    r.x[0] = bf16_lo(w.x), r.x[1] = bf16_hi(w.x), r.x[2] = bf16_lo(w.y), r.x[3] = bf16_hi(w.y);
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + at.a)), w = __ldg(reinterpret_cast<const uint2*>(p + at.b));
+    r.x[0] = bf16_lo(u.x), r.x[1] = bf16_hi(u.x), r.x[2] = bf16_lo(u.y), r.x[3] = bf16_hi(u.y);
+    r.x[4] = bf16_lo(w.x), r.x[5] = bf16_hi(w.x), r.x[6] = bf16_lo(w.y), r.x[7] = bf16_hi(w.y);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.x[i] = __bfloat162float(p[e + i]);
+    for (int k = 0; k < 8; ++k) r.x[k] = __bfloat162float(p[(k < 4 ? at.a : at.b - 4) + k]);
   }
   return r;
 }
-
-// The lane's four elements e .. e + 3 of a row turned by the row's (cos, sin) table.
+// Turned; cs: the row's table (element by element where pairs may split a lane's elements).
 template <bool kFast, bool kInter>
-__device__ __forceinline__ void turn4(Row4& r, const __nv_bfloat16* p, int e, int rot, const float2* cs, int lane) {
-  const int half = rot >> 1;
-  if constexpr (kInter) {
+__device__ __forceinline__ void turn_eight(Eight& r, const Turn& t, const __nv_bfloat16* p, int sl, int rot, const float2* cs) {
+  if constexpr (kFast) {
+    if (sl >= (rot >> 3)) return;
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      if (e + i >= rot) break;       // (rot is even: pairs are whole)
-      const float2 w = cs[(e + i) >> 1];
-      const float a = r.x[i], b = r.x[i + 1];
-      r.x[i] = a * w.x - b * w.y;
-      r.x[i + 1] = b * w.x + a * w.y;
-    }
-  } else if constexpr (kFast) {
-    const bool low = e < half;
-    const int other = lane + (low ? half : -half) / 4;
-    float o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, r.x[i], other & 31);
-    if (e < rot) {
-      const float4* c4 = reinterpret_cast<const float4*>(cs + (low ? e : e - half));
-      const float4 w0 = c4[0], w1 = c4[1];
-      const float c[4] = {w0.x, w0.z, w1.x, w1.z}, s[4] = {w0.y, w0.w, w1.y, w1.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.x[i] = low ? r.x[i] * c[i] - o[i] * s[i] : r.x[i] * c[i] + o[i] * s[i];
+    for (int k = 0; k < 4; ++k) {
+      float& lo = kInter ? r.x[2 * k] : r.x[k];
+      float& hi = kInter ? r.x[2 * k + 1] : r.x[4 + k];
+      const float a = lo, b = hi;
+      lo = a * t.c[k] - b * t.s[k];
+      hi = b * t.c[k] + a * t.s[k];
     }
   } else {
+    const int half = rot >> 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (e + i >= rot) break;
-      const bool low = e + i < half;
-      const float2 w = cs[low ? e + i : e + i - half];
-      const float o = __bfloat162float(p[low ? e + i + half : e + i - half]);
-      r.x[i] = low ? r.x[i] * w.x - o * w.y : r.x[i] * w.x + o * w.y;
+    for (int k = 0; k < 8; ++k) {
+      const int e = 8 * sl + k;
+      if (e >= rot) break;
+      const bool low = kInter ? !(e & 1) : e < half;
+      const float2 w = cs[kInter ? e >> 1 : low ? e : e - half];
+      const float o = __bfloat162float(p[kInter ? e ^ 1 : low ? e + half : e - half]);
+      r.x[k] = low ? r.x[k] * w.x - o * w.y : r.x[k] * w.x + o * w.y;
     }
   }
 }
 
-__device__ __forceinline__ float magnitude(float x) {   // infinities and NaN do not decide a scale
-  const float a = fabsf(x);
-  return a <= 3.4028235e38f ? a : 0.f;
+constexpr float kMaxFloat = 3.4028235e38f;
+// The largest finite magnitude (infinities and NaN do not decide a scale); `inf`: there is an infinity.
+__device__ __forceinline__ float magnitude(const Eight& r, bool& inf) {
+  float a = fmax3(fmax3(fabsf(r.x[0]), fabsf(r.x[1]), fabsf(r.x[2])), fmax3(fabsf(r.x[3]), fabsf(r.x[4]), fabsf(r.x[5])),
+                  fmaxf(fabsf(r.x[6]), fabsf(r.x[7])));   // (a maximum leaves NaN out)
+  if (a > kMaxFloat) {
+    inf = true;
+    a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = fabsf(r.x[k]) <= kMaxFloat ? fmaxf(a, fabsf(r.x[k])) : a;
+  }
+  return a == a ? a : 0.f;
 }
 
-template <int D, bool kFast, bool kInter>
-__global__ void __launch_bounds__(kThreads) append_fp8_kernel(const AppendFp8Params p) {
-  extern __shared__ __align__(16) float2 s_cs[];      // [rows][rot / 2], padded to whole 16 bytes a row
-  __shared__ uint32_t s_max[2 * kAppendMaxHeads];     // magnitudes (bits) of the block's KV heads: K, then V
-  __shared__ float s_scale[2 * kAppendMaxHeads], s_ratio[2 * kAppendMaxHeads];
-  __shared__ int s_b;
-  constexpr int kLanes = D / 4;                       // lanes of a row
-  constexpr int kPer = 32 / kLanes;                   // rows a warp takes at a time
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = p.page_size;
+// Frequencies as fractions of a turn, 2^-64, by the block's last threads (the first ones look for sequences meanwhile).
+__device__ __forceinline__ void frequencies(const AppendFp8Params& p, unsigned long long* freq) {
+  const int i = kThreads - 1 - (int)threadIdx.x;
+  if (i < p.rot >> 1) {
+    double turns = __ldg(p.inv_freq + i) * 0.15915494309189533577;  // 1 / (2 pi)
+    turns -= floor(turns);
+    freq[i] = (unsigned long long)(turns * 18446744073709551616.0);
+  }
+}
+// The rows' tables: pos_of(r) is row r's position.
+template <typename Pos>
+__device__ __forceinline__ void angles(const AppendFp8Params& p, float2* cs, const unsigned long long* freq, int rows, Pos pos_of) {
+  const int half = p.rot >> 1, pitch = (half + 1) & ~1;
+  for (int x = threadIdx.x; x < rows * half; x += kThreads) {
+    const int r = (int)(((unsigned long long)(unsigned)x * p.by_half) >> 42), i = x - r * half;
+    cs[r * pitch + i] = turn_of((long long)(freq[i] * (unsigned long long)pos_of(r)), p.amplitude);
+  }
+}
 
-  // the block's sequence: sequence b has the blocks from cu[b] / P + 2 b on (it touches at most Lq / P + 2 pages)
-  if (threadIdx.x == 0) s_b = -1;
+struct AppendShared {
+  unsigned long long freq[64];
+  uint32_t max[2 * kAppendMaxHeads];     // magnitudes (bits) of the block's KV heads: K, then V
+  float scale[2 * kAppendMaxHeads], ratio[2 * kAppendMaxHeads];
+  int inf[2 * kAppendMaxHeads];
+  int b[kAppendRows], t[kAppendRows];    // of q's rows: sequence and token, -1: none
+};
+
+// q's rows [row0, row0 + n) with all heads.
+template <int D, bool kFast, bool kInter>
+__device__ __forceinline__ void append_q(const AppendFp8Params& p, float2* cs, AppendShared& sh, int row0, int n) {
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes of a row, rows of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes, sl = lane % kLanes;
+  if (threadIdx.x < kAppendRows) sh.b[threadIdx.x] = -1;
+  frequencies(p, sh.freq);
   __syncthreads();
-  const int id = blockIdx.x;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) {
+    const int c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+    if (c0 < 0 || c1 < c0 || c1 > p.rows) continue;   // (recorded by the pages' blocks)
+    for (int r = 0; r < n; ++r)
+      if (row0 + r >= c0 && row0 + r < c1) sh.b[r] = b;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    int t = -1;
+    const int b = sh.b[threadIdx.x];
+    if (b >= 0) {
+      const long long y = (long long)__ldg(p.seqlens_k + b) - __ldg(p.cu_seqlens + b + 1) + row0 + threadIdx.x;
+      if (y >= 0 && y < (long long)p.max_pages << p.page_shift) {
+        const int page = __ldg(p.block_table + (size_t)b * p.max_pages + (y >> p.page_shift));
+        if (page >= 0 && page < p.num_pages) t = (int)y;
+      }
+    }
+    sh.t[threadIdx.x] = t;
+  }
+  __syncthreads();
+  const int half = p.rot >> 1, pitch = (half + 1) & ~1;
+  angles(p, cs, sh.freq, n, [&](int r) -> long long {
+    return p.positions ? (long long)__ldg(p.positions + row0 + r) : (long long)max(sh.t[r], 0);
+  });
+  __syncthreads();
+  // a warp: kPer rows and a share of the heads
+  const int trips = (n + kPer - 1) / kPer, parts = max(1, kWarps / trips);
+  const Quads at = quads_of<kInter>(sl, kFast ? p.rot : 0, true);
+  for (int it = warp; it < trips * parts; it += kWarps) {
+    const int part = it / trips, r = (it - part * trips) * kPer + sub;
+    if (r >= n || sh.t[r] < 0) continue;
+    const Turn turn = kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{};
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q.in) + (long long)(row0 + r) * p.q.in_row;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q.out) + (long long)(row0 + r) * p.q.out_row;
+#pragma unroll 4
+    for (int h = part; h < p.q.heads; h += parts) {
+      Eight x = load_eight<kFast>(src + h * p.q.in_head, at);
+      turn_eight<kFast, kInter>(x, turn, src + h * p.q.in_head, sl, p.rot, cs + r * pitch);
+      __nv_bfloat16* out = dst + h * p.q.out_head;
+      if constexpr (kFast) {
+        *reinterpret_cast<uint2*>(out + at.a) = make_uint2(pack_bf16x2(x.x[0], x.x[1]), pack_bf16x2(x.x[2], x.x[3]));
+        *reinterpret_cast<uint2*>(out + at.b) = make_uint2(pack_bf16x2(x.x[4], x.x[5]), pack_bf16x2(x.x[6], x.x[7]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[8 * sl + e] = __float2bfloat16_rn(x.x[e]);
+      }
+    }
+  }
+}
+
+// K and V of page `id` (of the sequence that it belongs to), share y of ny of the KV heads.
+template <int D, bool kFast, bool kInter>
+__device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, AppendShared& sh, int id, int y, int ny) {
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes, sl = lane % kLanes;
+  const int shift = p.page_shift, P = 1 << shift;
+  // sequence b has the blocks from cu[b] / P + 2 b on (it touches at most Lq / P + 2 pages)
+  if (threadIdx.x == 0) sh.b[0] = -1;
+  frequencies(p, sh.freq);
+  __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kThreads) {
     const int c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
     if (c0 < 0 || c1 < c0 || c1 > p.rows) {
       if (id == 0) record_status(p.status, kStatusDeviceCheck);
-    } else if (id >= c0 / P + 2 * b && id < c1 / P + 2 * (b + 1)) {
-      s_b = b;
+    } else if (id >= (c0 >> shift) + 2 * b && id < (c1 >> shift) + 2 * (b + 1)) {
+      sh.b[0] = b;
     }
   }
   __syncthreads();
-  const int b = s_b;
+  const int b = sh.b[0];
   if (b < 0) return;
   const int c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
   const int end = __ldg(p.seqlens_k + b);             // tokens [start, end) are new
-  const long long start = (long long)end - (c1 - c0), cap = (long long)p.max_pages * P;
-  const int local = id - (c0 / P + 2 * b);
-  if (local == 0 && blockIdx.y == 0 && threadIdx.x == 0 && c1 > c0 && (start < 0 || end > cap))
+  const long long start = (long long)end - (c1 - c0), cap = (long long)p.max_pages << shift;
+  const int local = id - ((c0 >> shift) + 2 * b);
+  if (local == 0 && y == 0 && threadIdx.x == 0 && c1 > c0 && (start < 0 || end > cap))
     record_status(p.status, kStatusDeviceCheck);      // rows outside the table are skipped
   const long long first = max(start, 0ll);
-  const long long pi = first / P + local;
-  const long long t0 = max(first, pi * P), t1 = min(min((long long)end, cap), (pi + 1) * P);
+  const long long pi = (first >> shift) + local;
+  const long long t0 = max(first, pi << shift), t1 = min(min((long long)end, cap), (pi + 1) << shift);
   if (t0 >= t1) return;
   const int page = __ldg(p.block_table + (size_t)b * p.max_pages + pi);
   if (page < 0 || page >= p.num_pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
+    if (y == 0 && threadIdx.x == 0) record_status(p.status, kStatusDeviceCheck);
     return;
   }
-  const int n = (int)(t1 - t0), slot0 = (int)(t0 - pi * P);
+  const int n = (int)(t1 - t0), slot0 = (int)(t0 - (pi << shift));
   const int row0 = c0 + (int)(t0 - start);            // packed row of token t0
-  const int half = p.rot >> 1, pitch = (half + 1) & ~1;
-  // the block's heads
-  const int kv0 = (int)((long long)p.k.heads * blockIdx.y / gridDim.y), kv1 = (int)((long long)p.k.heads * (blockIdx.y + 1) / gridDim.y);
-  const int q0 = (int)((long long)p.q.heads * blockIdx.y / gridDim.y), q1 = (int)((long long)p.q.heads * (blockIdx.y + 1) / gridDim.y);
-  const int nkv = kv1 - kv0, nq = q1 - q0;
-  float old_scale = 0.f;                              // of thread u < 2 nkv's unit
-  if ((int)threadIdx.x < 2 * nkv) {
-    s_max[threadIdx.x] = 0;
+  const int kv0 = p.k.heads * y / ny, nkv = p.k.heads * (y + 1) / ny - kv0, units = 2 * nkv;
+  float old_scale = 0.f;                              // of thread u's unit
+  if ((int)threadIdx.x < units) {
+    sh.max[threadIdx.x] = 0;
+    sh.inf[threadIdx.x] = 0;
     const int h = kv0 + ((int)threadIdx.x < nkv ? threadIdx.x : threadIdx.x - nkv);
     if (slot0 > 0) old_scale = ((int)threadIdx.x < nkv ? p.kscale : p.vscale)[(size_t)page * p.k.heads + h];
   }
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    double turns = __ldg(p.inv_freq + i) * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= floor(turns);
-    const unsigned long long f = (unsigned long long)(turns * 18446744073709551616.0);
-    for (int r = 0; r < n; ++r) {
-      const long long pos = p.positions ? (long long)__ldg(p.positions + row0 + r) : t0 + r;
-      s_cs[r * pitch + i] = turn_of((long long)(f * (unsigned long long)pos), p.amplitude);
-    }
-  }
+  angles(p, cs, sh.freq, n, [&](int r) -> long long {
+    return p.positions ? (long long)__ldg(p.positions + row0 + r) : t0 + r;
+  });
   __syncthreads();
 
-  const int sub = lane / kLanes, e = (lane % kLanes) * 4;
-  const int units = 2 * nkv * n;                      // (head of K or V, row), rows innermost
-  auto unit = [&](int idx, int& u, int& r) -> const __nv_bfloat16* {
-    u = idx / n;
-    r = idx - u * n;
+  // Units: a head of K (u < nkv) or V; an item is a unit and a share of the page's rows, kPer at a time.
+  const int half = p.rot >> 1, pitch = (half + 1) & ~1;
+  const int trips = (n + kPer - 1) / kPer, shares = min(trips, (2 * kWarps + units - 1) / units);
+  const Quads plain_at = {8 * sl, 8 * sl + 4}, turned_at = quads_of<kInter>(sl, kFast ? p.rot : 0, true);
+  auto source = [&](int u) -> const __nv_bfloat16* {
     const RopeTensor& t = u < nkv ? p.k : p.v;
-    const int h = kv0 + (u < nkv ? u : u - nkv);
-    return static_cast<const __nv_bfloat16*>(t.in) + (long long)(row0 + r) * t.in_row + h * t.in_head;
+    return static_cast<const __nv_bfloat16*>(t.in) + (long long)row0 * t.in_row + (kv0 + (u < nkv ? u : u - nkv)) * t.in_head;
   };
-  // the four elements of unit idx that the lane has, rotated (K) or as they are (V); all lanes of the warp call it
-  auto value = [&](int idx, int& u, int& r) -> Row4 {
-    const __nv_bfloat16* src = unit(idx, u, r);
-    Row4 x = load4<kFast>(src, e);
-    const bool key = u < nkv;
-    if (__any_sync(0xffffffffu, key)) {
-      Row4 y = x;
-      turn4<kFast, kInter>(y, src, e, p.rot, s_cs + r * pitch, lane);
-      if (key) x = y;
-    }
+  auto value = [&](int u, const __nv_bfloat16* src, int r) -> Eight {
+    if (u >= nkv) return load_eight<kFast>(src + (long long)r * p.v.in_row, plain_at);
+    src += (long long)r * p.k.in_row;
+    Eight x = load_eight<kFast>(src, turned_at);
+    turn_eight<kFast, kInter>(x, kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{}, src, sl, p.rot, cs + r * pitch);
     return x;
   };
-  for (int i = warp * kPer + sub; i - sub < units; i += kWarps * kPer) {
-    int u, r;
-    const bool live = i < units;
-    const Row4 x = value(live ? i : units - 1, u, r);
-    float a = fmaxf(fmaxf(magnitude(x.x[0]), magnitude(x.x[1])), fmaxf(magnitude(x.x[2]), magnitude(x.x[3])));
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-    if (live && e == 0) atomicMax(&s_max[u], __float_as_uint(a));
-  }
-  // q meanwhile, heads innermost
-  for (int i = warp * kPer + sub; i - sub < nq * n; i += kWarps * kPer) {
-    const bool live = i < nq * n;
-    const int j = live ? i : 0, r = j / nq, h = q0 + (j - r * nq);
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q.in) + (long long)(row0 + r) * p.q.in_row + h * p.q.in_head;
-    Row4 x = load4<kFast>(src, e);
-    turn4<kFast, kInter>(x, src, e, p.rot, s_cs + r * pitch, lane);
-    if (live) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q.out) + (long long)(row0 + r) * p.q.out_row + h * p.q.out_head + e;
-      if constexpr (kFast) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x.x[0], x.x[1]), pack_bf16x2(x.x[2], x.x[3]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dst[k] = __float2bfloat16_rn(x.x[k]);
-      }
+  Eight kept;    // the values of a warp's only trip
+  const bool once = units * shares <= kWarps && shares == trips;
+  for (int it = warp; it < units * shares; it += kWarps) {
+    const int share = it / units, u = it - share * units;
+    const __nv_bfloat16* src = source(u);
+    const int to = trips * (share + 1) / shares;
+    float a = 0.f;
+    bool inf = false;
+#pragma unroll 4
+    for (int k = trips * share / shares; k < to; ++k) {
+      kept = value(u, src, min(k * kPer + sub, n - 1));
+      a = fmaxf(a, magnitude(kept, inf));
     }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(a));   // (not negative: ordered as integers)
+    if (lane == 0) atomicMax(&sh.max[u], top);
+    if (inf) sh.inf[u] = 1;
   }
   __syncthreads();
-  if ((int)threadIdx.x < 2 * nkv) {
-    const float need = pow2_scale(__uint_as_float(s_max[threadIdx.x]));
+  if ((int)threadIdx.x < units) {
+    const float need = pow2_scale(__uint_as_float(sh.max[threadIdx.x]));
     const float s = slot0 > 0 ? fmaxf(old_scale, need) : need;
-    s_scale[threadIdx.x] = s;
-    s_ratio[threadIdx.x] = slot0 > 0 && s > old_scale ? old_scale / s : 1.f;
+    sh.scale[threadIdx.x] = s;
+    sh.ratio[threadIdx.x] = slot0 > 0 && s > old_scale ? old_scale / s : 1.f;
     const int h = kv0 + ((int)threadIdx.x < nkv ? threadIdx.x : threadIdx.x - nkv);
     ((int)threadIdx.x < nkv ? p.kscale : p.vscale)[(size_t)page * p.k.heads + h] = s;
   }
   __syncthreads();
-  auto slot = [&](int u, int s) -> uint32_t* {        // four codes of slot s
+  auto slot = [&](int u, int s) -> uint8_t* {         // the head's codes of slot s
     const int h = kv0 + (u < nkv ? u : u - nkv);
-    uint8_t* base = static_cast<uint8_t*>(u < nkv ? p.k.out : p.v.out);
-    return reinterpret_cast<uint32_t*>(base + (((size_t)page * P + s) * p.k.heads + h) * D + e);
+    return static_cast<uint8_t*>(u < nkv ? p.k.out : p.v.out) + ((((size_t)page << shift) + s) * p.k.heads + h) * D;
   };
   // the other slots of pages that outgrew their scale: RN(code * old / new)
-  for (int u = 0; u < 2 * nkv && slot0 > 0; ++u) {
-    const float ratio = s_ratio[u];
+  for (int u = 0; u < units && slot0 > 0; ++u) {
+    const float ratio = sh.ratio[u];
     if (ratio == 1.f) continue;
     for (int s = warp * kPer + sub; s < P; s += kWarps * kPer) {
       if (s >= slot0 && s < slot0 + n) continue;
-      uint32_t* c = slot(u, s);
-      const uint32_t w = *c;
-      const float2 a = values2(w), z = values2(w >> 16);
-      *c = codes4({a.x * ratio, a.y * ratio, z.x * ratio, z.y * ratio});
+      uint2* c = reinterpret_cast<uint2*>(slot(u, s) + 8 * sl);
+      uint2 w = *c;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t& x = k ? w.y : w.x;
+        const float2 a = values2(x), z = values2(x >> 16);
+        x = codes4({a.x * ratio, a.y * ratio, z.x * ratio, z.y * ratio});
+      }
+      *c = w;
     }
   }
-  for (int i = warp * kPer + sub; i - sub < units; i += kWarps * kPer) {
-    int u, r;
-    const bool live = i < units;
-    const Row4 x = value(live ? i : units - 1, u, r);
-    const float s = s_scale[u];
-    float y[4];
+  for (int it = warp; it < units * shares; it += kWarps) {
+    const int share = it / units, u = it - share * units;
+    const __nv_bfloat16* src = source(u);
+    const Quads at = u < nkv ? turned_at : plain_at;
+    const float s = sh.scale[u];
+    const uint32_t bits = __float_as_uint(s);
+    const bool pow2 = (bits & 0x7fffffu) == 0, inf = sh.inf[u] != 0;   // (old scales may be others)
+    const float inv = __uint_as_float((254u << 23) - bits);            // 1 / s
+    const int to = trips * (share + 1) / shares;
+#pragma unroll 4
+    for (int k = trips * share / shares; k < to; ++k) {
+      const int r = k * kPer + sub;
+      const Eight x = once ? kept : value(u, src, min(r, n - 1));
+      float y[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = fabsf(x.x[k]) <= 3.4028235e38f ? x.x[k] / s : __int_as_float(0x7fffffff);
-    if (live) *slot(u, slot0 + r) = codes4(y);
+      for (int e = 0; e < 8; ++e) {
+        y[e] = pow2 ? x.x[e] * inv : x.x[e] / s;
+        if (inf && fabsf(x.x[e]) > kMaxFloat) y[e] = __int_as_float(0x7fffffff);   // (the conversion would take 448)
+      }
+      if (r < n) {
+        uint8_t* dst = slot(u, slot0 + r);
+        *reinterpret_cast<uint32_t*>(dst + at.a) = codes4({y[0], y[1], y[2], y[3]});
+        *reinterpret_cast<uint32_t*>(dst + at.b) = codes4({y[4], y[5], y[6], y[7]});
+      }
+    }
+  }
+}
+
+template <int D, bool kFast, bool kInter>
+__global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(const AppendFp8Params p) {
+  extern __shared__ __align__(16) float2 cs[];        // [rows][rot / 2], padded to whole 16 bytes a row
+  __shared__ AppendShared sh;
+  const int kv_blocks = p.pages * p.head_shares;
+  if ((int)blockIdx.x < kv_blocks) {
+    const int id = blockIdx.x / p.head_shares;
+    append_kv<D, kFast, kInter>(p, cs, sh, id, blockIdx.x - id * p.head_shares, p.head_shares);
+  } else {
+    const int row0 = ((int)blockIdx.x - kv_blocks) * p.q_rows;
+    append_q<D, kFast, kInter>(p, cs, sh, row0, min(p.q_rows, p.rows - row0));
   }
 }
 
 template <int D, bool kFast>
-cudaError_t launch_append_t(const AppendFp8Params& p, dim3 grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch_append_t(const AppendFp8Params& p, unsigned grid, size_t smem, cudaStream_t stream) {
   auto kern = p.interleaved ? append_fp8_kernel<D, kFast, true> : append_fp8_kernel<D, kFast, false>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -327,19 +447,25 @@ __global__ void __launch_bounds__(kThreads) expand_fp8_kernel(const ExpandFp8Par
 
 }  // namespace
 
-cudaError_t launch_append_fp8(const AppendFp8Params& p, int num_sms, cudaStream_t stream) {
-  const int ids = p.rows / p.page_size + 2 * p.B;      // blocks of all sequences (some have nothing to do)
-  // heads shared out over blocks where pages alone are fewer than four blocks an SM, one KV head a block at least, and never
-  // more KV heads a block than it has room for
-  const int pages = std::max(1, std::min(ids, p.rows));
-  int ny = std::min(p.k.heads, (4 * num_sms + pages - 1) / pages);
-  ny = std::max(ny, (p.k.heads + kAppendMaxHeads - 1) / kAppendMaxHeads);
+cudaError_t launch_append_fp8(const AppendFp8Params& p0, int num_sms, cudaStream_t stream) {
+  AppendFp8Params p = p0;
+  p.page_shift = p.page_size == 16 ? 4 : p.page_size == 32 ? 5 : p.page_size == 64 ? 6 : 7;
+  p.pages = p.rows / p.page_size + 2 * p.B;            // blocks of all sequences (some have nothing to do)
+  // KV heads shared out over blocks where the pages are fewer than four blocks an SM, one a block at least, and never more
+  // than a block has room for; q: as many rows a block as leave four blocks an SM
+  const int pages = std::max(1, std::min(p.pages, p.rows));
+  p.head_shares = std::min(p.k.heads, (4 * num_sms + pages - 1) / pages);
+  p.head_shares = std::max(p.head_shares, (p.k.heads + kAppendMaxHeads - 1) / kAppendMaxHeads);
+  p.q_rows = std::max(1, std::min(kAppendRows, p.rows / (4 * num_sms)));
   const int half = p.rot / 2, pitch = (half + 1) & ~1;
-  const size_t smem = (size_t)std::min(p.page_size, p.rows) * pitch * sizeof(float2);
-  const bool fast = quads(p.q, true) && quads(p.k, false) && quads(p.v, false) && p.rot % (p.interleaved ? 4 : 8) == 0;
-  const dim3 grid(ids, ny);
-  if (p.d == 128) return fast ? launch_append_t<128, true>(p, grid, smem, stream) : launch_append_t<128, false>(p, grid, smem, stream);
-  return fast ? launch_append_t<64, true>(p, grid, smem, stream) : launch_append_t<64, false>(p, grid, smem, stream);
+  p.by_half = half ? ((1ull << 42) + half - 1) / half : 0;
+  const size_t smem = (size_t)std::max(std::min(p.page_size, p.rows), p.q_rows) * pitch * sizeof(float2);
+  const bool fast = quads(p.q, true) && quads(p.k, false) && quads(p.v, false) && p.rot % 8 == 0;
+  const long long grid = (long long)p.pages * p.head_shares + (p.q.heads ? (p.rows + p.q_rows - 1) / p.q_rows : 0);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.d == 128)
+    return fast ? launch_append_t<128, true>(p, (unsigned)grid, smem, stream) : launch_append_t<128, false>(p, (unsigned)grid, smem, stream);
+  return fast ? launch_append_t<64, true>(p, (unsigned)grid, smem, stream) : launch_append_t<64, false>(p, (unsigned)grid, smem, stream);
 }
 
 cudaError_t launch_expand_fp8(const ExpandFp8Params& p, cudaStream_t stream) {

@@ -85,6 +85,7 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
 
 // 8-bit paged cache: E4M3 codes [num_pages, page_size, Hkv, d], scales [num_pages, Hkv].
 constexpr int kAppendMaxHeads = 64;   // KV heads that a block of the append has room for
+constexpr int kAppendRows = 8;        // rows of q that one takes at most
 
 struct AppendFp8Params {
   RopeTensor q, k, v;         // bf16; out of k and v = the code caches
@@ -98,6 +99,9 @@ struct AppendFp8Params {
   int rows, B, d, rot, interleaved, page_size, max_pages, num_pages;
   float amplitude;
   int* status;
+  // set by the launch: blocks of pages, shares of the KV heads, rows of a block of q, log2 of the page size, 2^42 / (rot / 2)
+  int pages, head_shares, q_rows, page_shift;
+  unsigned long long by_half;
 };
 
 cudaError_t launch_append_fp8(const AppendFp8Params& p, int num_sms, cudaStream_t stream);
