@@ -99,9 +99,12 @@ bool encode_u8_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
 }
 
 int num_sms_current() {  // declared in fattn_internal.h
+  static std::atomic<int> known[128];   // a property of the machine, asked for once per device
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 128 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 128) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

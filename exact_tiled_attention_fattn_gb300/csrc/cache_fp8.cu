@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;            // rows that a lane has in flight
 constexpr int kMinScaleExp = -100;   // the scale of a page of zeros
 
 // The least power of two s with a <= 448 s (448 = 1.75 * 2^8), a >= 0 finite.
@@ -80,19 +81,23 @@ __device__ __forceinline__ Turn load_turn(const float2* cs, int sl, int rot) {
   return t;
 }
 
-// The lane's elements of a row.
+// The lane's elements of a row, as they lie in memory (kFast) and as numbers.
+struct Raw {
+  uint2 a, b;
+};
 template <bool kFast>
-__device__ __forceinline__ Eight load_eight(const __nv_bfloat16* p, const Quads& at) {
-  Eight r;
-  if constexpr (kFast) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + at.a)), w = __ldg(reinterpret_cast<const uint2*>(p + at.b));
-    r.x[0] = bf16_lo(u.x), r.x[1] = bf16_hi(u.x), r.x[2] = bf16_lo(u.y), r.x[3] = bf16_hi(u.y);
-    r.x[4] = bf16_lo(w.x), r.x[5] = bf16_hi(w.x), r.x[6] = bf16_lo(w.y), r.x[7] = bf16_hi(w.y);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r.x[k] = __bfloat162float(p[(k < 4 ? at.a : at.b - 4) + k]);
-  }
+__device__ __forceinline__ Raw load_raw(const __nv_bfloat16* p, const Quads& at) {
+  if constexpr (kFast) return {__ldg(reinterpret_cast<const uint2*>(p + at.a)), __ldg(reinterpret_cast<const uint2*>(p + at.b))};
+  Raw r;
+  const __nv_bfloat16* q = p + at.a;                  // (eight in a row)
+  auto two = [&](int k) -> uint32_t { return (uint32_t)__bfloat16_as_ushort(q[k]) | (uint32_t)__bfloat16_as_ushort(q[k + 1]) << 16; };
+  r.a = make_uint2(two(0), two(2));
+  r.b = make_uint2(two(4), two(6));
   return r;
+}
+__device__ __forceinline__ Eight numbers(const Raw& w) {
+  return {{bf16_lo(w.a.x), bf16_hi(w.a.x), bf16_lo(w.a.y), bf16_hi(w.a.y), bf16_lo(w.b.x), bf16_hi(w.b.x), bf16_lo(w.b.y),
+           bf16_hi(w.b.y)}};
 }
 // Turned; cs: the row's table (element by element where pairs may split a lane's elements).
 template <bool kFast, bool kInter>
@@ -204,17 +209,25 @@ __device__ __forceinline__ void append_q(const AppendFp8Params& p, float2* cs, A
     const Turn turn = kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{};
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q.in) + (long long)(row0 + r) * p.q.in_row;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q.out) + (long long)(row0 + r) * p.q.out_row;
-#pragma unroll 4
-    for (int h = part; h < p.q.heads; h += parts) {
-      Eight x = load_eight<kFast>(src + h * p.q.in_head, at);
-      turn_eight<kFast, kInter>(x, turn, src + h * p.q.in_head, sl, p.rot, cs + r * pitch);
-      __nv_bfloat16* out = dst + h * p.q.out_head;
-      if constexpr (kFast) {
-        *reinterpret_cast<uint2*>(out + at.a) = make_uint2(pack_bf16x2(x.x[0], x.x[1]), pack_bf16x2(x.x[2], x.x[3]));
-        *reinterpret_cast<uint2*>(out + at.b) = make_uint2(pack_bf16x2(x.x[4], x.x[5]), pack_bf16x2(x.x[6], x.x[7]));
-      } else {
+    for (int h0 = part; h0 < p.q.heads; h0 += kBatch * parts) {
+      Raw w[kBatch];                                  // in flight together
 #pragma unroll
-        for (int e = 0; e < 8; ++e) out[8 * sl + e] = __float2bfloat16_rn(x.x[e]);
+      for (int i = 0; i < kBatch; ++i)
+        if (h0 + i * parts < p.q.heads) w[i] = load_raw<kFast>(src + (h0 + i * parts) * p.q.in_head, at);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * parts;
+        if (h >= p.q.heads) break;
+        Eight x = numbers(w[i]);
+        turn_eight<kFast, kInter>(x, turn, src + h * p.q.in_head, sl, p.rot, cs + r * pitch);
+        __nv_bfloat16* out = dst + h * p.q.out_head;
+        if constexpr (kFast) {
+          *reinterpret_cast<uint2*>(out + at.a) = make_uint2(pack_bf16x2(x.x[0], x.x[1]), pack_bf16x2(x.x[2], x.x[3]));
+          *reinterpret_cast<uint2*>(out + at.b) = make_uint2(pack_bf16x2(x.x[4], x.x[5]), pack_bf16x2(x.x[6], x.x[7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[8 * sl + e] = __float2bfloat16_rn(x.x[e]);
+        }
       }
     }
   }
@@ -279,26 +292,33 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
     const RopeTensor& t = u < nkv ? p.k : p.v;
     return static_cast<const __nv_bfloat16*>(t.in) + (long long)row0 * t.in_row + (kv0 + (u < nkv ? u : u - nkv)) * t.in_head;
   };
-  auto value = [&](int u, const __nv_bfloat16* src, int r) -> Eight {
-    if (u >= nkv) return load_eight<kFast>(src + (long long)r * p.v.in_row, plain_at);
-    src += (long long)r * p.k.in_row;
-    Eight x = load_eight<kFast>(src, turned_at);
-    turn_eight<kFast, kInter>(x, kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{}, src, sl, p.rot, cs + r * pitch);
-    return x;
+  // trips [k0, k1) of unit u, kBatch of them in flight together; use(row, values) for each
+  auto walk = [&](int u, int k0, int k1, auto use) {
+    const bool key = u < nkv;
+    const __nv_bfloat16* src = source(u);
+    const long long row = key ? p.k.in_row : p.v.in_row;
+    const Quads at = key ? turned_at : plain_at;
+    for (int k = k0; k < k1; k += kBatch) {
+      Raw w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (k + i < k1) w[i] = load_raw<kFast>(src + min((k + i) * kPer + sub, n - 1) * row, at);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (k + i >= k1) break;
+        const int r = min((k + i) * kPer + sub, n - 1);
+        Eight x = numbers(w[i]);
+        if (key)
+          turn_eight<kFast, kInter>(x, kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{}, src + r * row, sl, p.rot, cs + r * pitch);
+        use((k + i) * kPer + sub, x);
+      }
+    }
   };
-  Eight kept;    // the values of a warp's only trip
-  const bool once = units * shares <= kWarps && shares == trips;
   for (int it = warp; it < units * shares; it += kWarps) {
     const int share = it / units, u = it - share * units;
-    const __nv_bfloat16* src = source(u);
-    const int to = trips * (share + 1) / shares;
     float a = 0.f;
     bool inf = false;
-#pragma unroll 4
-    for (int k = trips * share / shares; k < to; ++k) {
-      kept = value(u, src, min(k * kPer + sub, n - 1));
-      a = fmaxf(a, magnitude(kept, inf));
-    }
+    walk(u, trips * share / shares, trips * (share + 1) / shares, [&](int, const Eight& x) { a = fmaxf(a, magnitude(x, inf)); });
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(a));   // (not negative: ordered as integers)
     if (lane == 0) atomicMax(&sh.max[u], top);
     if (inf) sh.inf[u] = 1;
@@ -336,17 +356,12 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
   }
   for (int it = warp; it < units * shares; it += kWarps) {
     const int share = it / units, u = it - share * units;
-    const __nv_bfloat16* src = source(u);
     const Quads at = u < nkv ? turned_at : plain_at;
     const float s = sh.scale[u];
     const uint32_t bits = __float_as_uint(s);
     const bool pow2 = (bits & 0x7fffffu) == 0, inf = sh.inf[u] != 0;   // (old scales may be others)
     const float inv = __uint_as_float((254u << 23) - bits);            // 1 / s
-    const int to = trips * (share + 1) / shares;
-#pragma unroll 4
-    for (int k = trips * share / shares; k < to; ++k) {
-      const int r = k * kPer + sub;
-      const Eight x = once ? kept : value(u, src, min(r, n - 1));
+    walk(u, trips * share / shares, trips * (share + 1) / shares, [&](int r, const Eight& x) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -358,7 +373,7 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
         *reinterpret_cast<uint32_t*>(dst + at.a) = codes4({y[0], y[1], y[2], y[3]});
         *reinterpret_cast<uint32_t*>(dst + at.b) = codes4({y[4], y[5], y[6], y[7]});
       }
-    }
+    });
   }
 }
 
@@ -451,10 +466,10 @@ cudaError_t launch_append_fp8(const AppendFp8Params& p0, int num_sms, cudaStream
   AppendFp8Params p = p0;
   p.page_shift = p.page_size == 16 ? 4 : p.page_size == 32 ? 5 : p.page_size == 64 ? 6 : 7;
   p.pages = p.rows / p.page_size + 2 * p.B;            // blocks of all sequences (some have nothing to do)
-  // KV heads shared out over blocks where the pages are fewer than four blocks an SM, one a block at least, and never more
+  // KV heads shared out over blocks where the pages are fewer than two blocks an SM, one a block at least, and never more
   // than a block has room for; q: as many rows a block as leave four blocks an SM
   const int pages = std::max(1, std::min(p.pages, p.rows));
-  p.head_shares = std::min(p.k.heads, (4 * num_sms + pages - 1) / pages);
+  p.head_shares = std::min(p.k.heads, (2 * num_sms + pages - 1) / pages);
   p.head_shares = std::max(p.head_shares, (p.k.heads + kAppendMaxHeads - 1) / kAppendMaxHeads);
   p.q_rows = std::max(1, std::min(kAppendRows, p.rows / (4 * num_sms)));
   const int half = p.rot / 2, pitch = (half + 1) & ~1;
