@@ -379,7 +379,9 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   const long long npad = ((long long)N + 127) / 128 * 128;
   if (rows > 0x7fffffffLL || (long long)B * Hq * npad > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
   const size_t vectors = fattn_bwd_workspace_size(B, Hq, N);
-  const size_t need = shape ? fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d) : vectors;
+  const size_t base = shape ? fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d) : vectors;
+  const size_t need =
+      shape && shape->sinks ? fattn_bwd_sinks_workspace_size(B, Hq, Hkv, N, d, causal, shape->window, shape->sinks) : base;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FATTN_ERR_WORKSPACE;
 
@@ -397,6 +399,11 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
     p.shaped = 1;
     p.shape = *shape;
     p.ws_keys = reinterpret_cast<int2*>(static_cast<char*>(workspace) + vectors);
+    p.sink_tiles = sink_blocks(shape->sinks, 128);
+    p.sink_pieces = bwd_sink_pieces(N, causal, shape->window, shape->sinks);
+    p.ws_sink = reinterpret_cast<float*>(static_cast<char*>(workspace) + base);
+    // items of the dK/dV pass are counted in an int
+    if ((long long)B * Hq * (npad / 128 + (long long)p.sink_tiles * p.sink_pieces) > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     if (bwd_per_head(p, sms))
       p.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + vectors + align256((size_t)B * npad * sizeof(int2)));
   }

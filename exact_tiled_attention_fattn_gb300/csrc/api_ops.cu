@@ -252,6 +252,16 @@ extern "C" fattn_status fattn_bwd_shaped(const void* q, const void* k, const voi
                   workspace_bytes, stream);
 }
 
+extern "C" size_t fattn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal, int window, int sinks) {
+  const size_t base = fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d);
+  // (what check_shape makes of a window that hides nothing)
+  if (base == 0 || window <= 0 || sinks <= 0 || window >= N || sinks >= (causal ? N - window : N)) return base;
+  const int pieces = bwd_sink_pieces(N, causal, window, sinks);
+  if (pieces == 1) return base;
+  const size_t rows = (size_t)B * sink_blocks(sinks, 128) * 128 * (bwd_shares(B, Hq, Hkv, N) ? Hq : Hkv);
+  return base + (2 * pieces * rows * d * sizeof(float) + 255) / 256 * 256;
+}
+
 extern "C" fattn_status fattn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                         const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
                                         int d, int causal, float scale, float softcap, const float* slopes, int window,
@@ -506,7 +516,7 @@ static ChunkWorkspace chunk_workspace(int B, int Hq, int Hkv, int d, int page_si
                                       int num_splits) {
   ChunkWorkspace w{};
   const long long rows = (long long)max_q * (Hq / Hkv);
-  w.stream = rows <= kStreamFp8Rows;
+  w.stream = streams_fp8(max_q, Hq / Hkv);
   if (w.stream) {
     w.s = stream_workspace(total_q, Hq, d, num_splits, stream_fp8_groups(B, Hkv, rows));
     w.bytes = w.s.bytes;
@@ -553,7 +563,7 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
       ((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || B > 65535 ||
       stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits)
     return FATTN_ERR_UNSUPPORTED;
-  if (rows <= kStreamFp8Rows && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size)) return FATTN_ERR_UNSUPPORTED;
+  if (streams_fp8(max_seqlen_q, Hq / Hkv) && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size)) return FATTN_ERR_UNSUPPORTED;
   const ChunkWorkspace w =
       chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits);
   if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;

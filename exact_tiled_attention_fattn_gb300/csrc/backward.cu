@@ -625,18 +625,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int nt = (p.N + BT - 1) / BT;
   const int G = kPerHead ? 1 : p.Hq / p.Hkv;
-  const BwdSchedule sch = make_bwd_schedule(p.B * (kPerHead ? p.Hq : p.Hkv), nt, 1);
-  // item: (sequence, KV head, or query head with kPerHead, key tile j); rank 0 = j 0, the most query tiles under the causal rule
-  auto item = [&](int it, int& b, int& hkv, int& j) {
+  const int cut = kShaped ? p.sink_tiles * (p.sink_pieces - 1) : 0;   // items that the sinks' tiles add
+  const BwdSchedule sch = make_bwd_schedule(p.B * (kPerHead ? p.Hq : p.Hkv), nt + cut, 1);
+  // item: (sequence, KV head, or query head with kPerHead, key tile j, piece of its queries); rank 0 = j 0, the most query
+  // tiles under the causal rule
+  auto item = [&](int it, int& b, int& hkv, int& j, int& piece) {
     int head;
     bwd_decode(sch, it, head, j);
     b = head / (kPerHead ? p.Hq : p.Hkv);
     hkv = head - b * (kPerHead ? p.Hq : p.Hkv);
+    piece = 0;
+    if constexpr (kShaped) {
+      if (cut > 0) {
+        if (j < p.sink_tiles + cut) {
+          piece = j / p.sink_tiles;
+          j -= piece * p.sink_tiles;
+        } else {
+          j -= cut;
+        }
+      }
+    }
   };
   // query tiles [i0, i0 + ni) of an item
-  auto tiles = [&](int b, int j, int& i0, int& ni) {
+  auto tiles = [&](int b, int j, int piece, int& i0, int& ni) {
     if constexpr (kShaped) {
       shaped_query_tiles(p, b, j, nt, i0, ni);
+      if (cut > 0 && j < p.sink_tiles) {   // (all query tiles from the first on: at least one a piece)
+        const int from = ni * piece / p.sink_pieces, to = ni * (piece + 1) / p.sink_pieces;
+        i0 += from;
+        ni = max(to - from, 1);
+      }
     } else {
       i0 = p.causal ? j : 0;
       ni = nt - i0;
@@ -650,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_kv = policy_evict_first(), pol_q = policy_evict_last();
       bool ok = true;
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
-        int b, hkv, j;
-        item(it, b, hkv, j);
+        int b, hkv, j, piece;
+        item(it, b, hkv, j, piece);
         if (!mbar_wait(bar(kKvEmpty), (nkv & 1) ^ 1, abort, p.status, p.wait_ns)) break;
         mbar_arrive_expect_tx(bar(kKvFull), 2 * Lay::kTile);
         const int kv_head = kPerHead ? hkv / (p.Hq / p.Hkv) : hkv;
@@ -659,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tile<D>(sb + Lay::kOffV, &tv, bar(kKvFull), kv_head, b * p.N + j * BT, pol_kv);
         ++nkv;
         int i0, ni;
-        tiles(b, j, i0, ni);
+        tiles(b, j, piece, i0, ni);
         for (int t = 0; t < G * ni; ++t) {
           const int h = hkv * G + t / ni, i = i0 + t % ni;
           const uint32_t st = nqd & 1, base = sb + Lay::kOffRing + st * Lay::kStage;
@@ -691,10 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDV = tmem + kColAcc, tDK = tmem + kColAcc + D;
       bool ok = true;
       for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
-        int b, hkv, j;
-        item(it, b, hkv, j);
+        int b, hkv, j, piece;
+        item(it, b, hkv, j, piece);
         int i0, ni;
-        tiles(b, j, i0, ni);
+        tiles(b, j, piece, i0, ni);
         const int steps = G * ni;
         if (!mbar_wait(bar(kKvFull), nkv & 1, abort, p.status, p.wait_ns)) break;
         ++nkv;
@@ -809,10 +827,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every role stops, drains and frees TMEM; the outputs stay unwritten
     if (p.debug_stall && !warp_wait(bar(Lay::kBarStall), 0, abort, p.status, p.wait_ns)) ok = false;
     for (int kk = 0, it; ok && (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
-      int b, hkv, j;
-      item(it, b, hkv, j);
+      int b, hkv, j, piece;
+      item(it, b, hkv, j, piece);
       int i0, ni;
-      tiles(b, j, i0, ni);
+      tiles(b, j, piece, i0, ni);
       // shaped: the queries [qa, qb) that see this thread's key (none for a key past the sequence)
       int qa = 0, qb = 0;
       if constexpr (kShaped) {
@@ -903,7 +921,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t off = (((size_t)b * p.N + (live ? key : 0)) * (kPerHead ? p.Hq : p.Hkv) + hkv) * D + wg * (D / 2);
       const int wkey0 = j * BT + q4 * 32;  // the warp's first key row
       const bool staged = Lay::kStoreTma && wkey0 + 32 <= p.N;
-      if constexpr (kPerHead)
+      // a piece of a sinks' tile: its shares in fp32
+      const bool shared = kShaped && cut > 0 && j < p.sink_tiles;
+      const size_t srow = (size_t)p.B * p.sink_tiles * BT;
+      float* share = nullptr;
+      if (kShaped && shared)
+        share = p.ws_sink + ((2 * piece * srow + (size_t)b * p.sink_tiles * BT + key) * (kPerHead ? p.Hq : p.Hkv) + hkv) * D + wg * (D / 2);
+      if (kShaped && shared)
+        store_row_f32<D / 2>(acc_col + wg * (D / 2), 1.f, share, live);
+      else if constexpr (kPerHead)
         store_row_f32<D / 2>(acc_col + wg * (D / 2), 1.f, p.ws_part + off, live);
       else if (staged)
         stage_out(acc_col + wg * (D / 2), 1.f, &tdv, wg * (D / 2), hkv, b * p.N + wkey0);
@@ -912,7 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(bar(kAccFull), nacc & 1, abort, p.status, p.wait_ns)) break;
       ++nacc;
       tc_fence_after();
-      if constexpr (kPerHead)
+      if (kShaped && shared)
+        store_row_f32<D / 2>(acc_col + D + wg * (D / 2), p.scale, share + srow * (kPerHead ? p.Hq : p.Hkv) * D, live);
+      else if constexpr (kPerHead)
         store_row_f32<D / 2>(acc_col + D + wg * (D / 2), p.scale, p.ws_part + (size_t)p.B * p.N * p.Hq * D + off, live);
       else if (staged)
         stage_out(acc_col + D + wg * (D / 2), p.scale, &tdk, wg * (D / 2), hkv, b * p.N + wkey0);
@@ -1326,6 +1354,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_heads_kernel(const BwdParams 
   const int lanes = p.d / 4, G = p.Hq / p.Hkv;
   const long long at = (long long)blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;  // row * Hkv + KV head
   if (at >= (long long)p.B * p.N * p.Hkv) return;
+  if (p.sink_pieces > 1 && at / p.Hkv % p.N < p.sink_tiles * BT) return;   // (sum_sinks_kernel's)
   const int c = (threadIdx.x % lanes) * 4;
   const float4* src = reinterpret_cast<const float4*>(p.ws_part + (blockIdx.y ? (size_t)p.B * p.N * p.Hq * p.d : 0) +
                                                       (size_t)at * G * p.d + c);
@@ -1344,6 +1373,33 @@ __global__ void __launch_bounds__(kSumThreads) sum_heads_kernel(const BwdParams 
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(blockIdx.y ? p.dk : p.dv) + (size_t)at * p.d + c) = o;
 }
 
+// dV (blockIdx.y 0) and dK (1) of the sinks' key tiles: the sums, in order, of their pieces' fp32 shares, and of the query
+// heads' where those have their own. A thread takes 4 columns of a (row, KV head).
+__global__ void __launch_bounds__(kSumThreads) sum_sinks_kernel(const BwdParams p, int heads) {
+  const int lanes = p.d / 4, G = heads / p.Hkv, rows = p.sink_tiles * BT;
+  const long long at = (long long)blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;  // (sequence, row) * Hkv + KV head
+  if (at >= (long long)p.B * rows * p.Hkv) return;
+  const int row = (int)(at / p.Hkv % rows), b = (int)(at / p.Hkv / rows), c = (threadIdx.x % lanes) * 4;
+  if (row >= p.N) return;
+  const size_t pass = (size_t)p.B * rows * heads * p.d / 4;   // float4s of a piece's dV or dK
+  const float4* src = reinterpret_cast<const float4*>(p.ws_sink + (size_t)at * G * p.d + c) + blockIdx.y * pass;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < p.sink_pieces; ++i)
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+      const float4 v = __ldg(src + 2 * i * pass + (size_t)g * lanes);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+  uint2 o;
+  o.x = pack_bf16x2(sum.x, sum.y);
+  o.y = pack_bf16x2(sum.z, sum.w);
+  const size_t out = (((size_t)b * p.N + row) * p.Hkv + at % p.Hkv) * p.d + c;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(blockIdx.y ? p.dk : p.dv) + out) = o;
+}
+
 template <int D, int kShape, bool kPerHead>
 cudaError_t launch_dkdv(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv, int num_sms,
@@ -1352,12 +1408,19 @@ cudaError_t launch_dkdv(const BwdParams& p, const CUtensorMap& tq, const CUtenso
   auto kern = bwd_dkdv_kernel<D, kShape, kPerHead>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.B * (kPerHead ? p.Hq : p.Hkv) * nt;
+  const long long items =
+      (long long)p.B * (kPerHead ? p.Hq : p.Hkv) * (nt + (kShape != kPlain ? p.sink_tiles * (p.sink_pieces - 1) : 0));
   const int grid = (int)std::min<long long>(items, num_sms);
   kern<<<grid, kThreads, DkdvLayout<D>::kBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
   e = cudaGetLastError();
-  if (!kPerHead || e != cudaSuccess) return e;
+  if (e != cudaSuccess) return e;
   const int rows = kSumThreads / (D / 4);
+  if (kShape != kPlain && p.sink_pieces > 1) {
+    const long long n = (long long)p.B * p.sink_tiles * BT * p.Hkv;
+    sum_sinks_kernel<<<dim3((unsigned)((n + rows - 1) / rows), 2), kSumThreads, 0, stream>>>(p, kPerHead ? p.Hq : p.Hkv);
+    e = cudaGetLastError();
+  }
+  if (!kPerHead || e != cudaSuccess) return e;
   sum_heads_kernel<<<dim3((unsigned)(((long long)p.B * p.N * p.Hkv + rows - 1) / rows), 2), kSumThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -150,6 +150,11 @@ struct BwdParams {
   float* ws_d;                // [B * Hq, Npad]: rowsum(dO o O), 0 past N
   int2* ws_keys;              // shaped: [B, Npad], the query rows [x, y) that see each key
   float* ws_part;             // shaped, per query head: dV, then dK, [B * N, Hq, d] fp32; else nullptr
+  // windows with sinks: the first sink_tiles key tiles, seen from all queries, are cut along them into sink_pieces items
+  // (1: not cut), whose shares of dV, then dK, are [sink_pieces, 2, B, sink_tiles * 128, H, d] fp32, H = Hq per query head,
+  // else Hkv
+  int sink_tiles, sink_pieces;
+  float* ws_sink;
   int B, Hq, Hkv, N, d, Npad; // Npad = N rounded up to 128
   int causal;
   float scale;
@@ -172,6 +177,18 @@ struct BwdParams {
 // Whole calls, causal, per KV head and per query head, d = 128 unless said: 997 rows, 8 heads over 2, d = 64 87 and 51 us; 2048
 // rows, 32 over 8 188 and 159 us (a window of 512: 97 and 119 us); 8192 rows, 32 over 1, d = 64 4059 and 1533 us; 4096
 // rows, 32 over 8 (256 items) 437 and 484 us.
+// Pieces that the key tiles of the sinks are cut into: of about as many query tiles as see any other key tile (for the
+// dK/dV pass one item of them all is the longest by far: N = 32768, window 1024, 32 heads over 8, d = 128 2916 us
+// against 974 without sinks), at least one query tile each; their shares are kept to 128 tiles.
+inline int bwd_sink_pieces(int N, int causal, int window, int sinks) {
+  if (window <= 0 || sinks <= 0) return 1;
+  const int nt = (N - 1) / 128 + 1, S = sink_blocks(sinks, 128), seen = (causal ? 1 : 2) * (window / 128) + 2;
+  int P = (nt + seen - 1) / seen;
+  if (P > 32) P = 32;
+  if (P > 128 / S) P = 128 / S;
+  if (P > nt - S) P = nt - S;
+  return P > 1 ? P : 1;
+}
 constexpr long long kPerHeadItems = 152;
 inline bool bwd_shares(int B, int Hq, int Hkv, int N) {
   return Hq > Hkv && (long long)B * Hkv * (((long long)N + 127) / 128) <= kPerHeadItems;
@@ -182,8 +199,7 @@ inline bool bwd_per_head(const BwdParams& p, int num_sms) {
   double most = nt, mean = p.causal ? (nt + 1) / 2 : nt;
   if (p.shape.window > 0) {
     const double seen = (p.causal ? 1.0 : 2.0) * p.shape.window / 128 + 1;
-    if (seen < mean) mean = seen;
-    if (seen < most && !p.shape.sinks) most = seen;   // (the sinks' tile is seen from all query tiles)
+    if (seen < most) most = seen;   // (the sinks' tiles, seen from all query tiles, are cut into pieces of about that)
   }
   if ((p.shape.key_begin || p.shape.key_end) && most > nt / 4) most = nt / 4 > 1 ? nt / 4 : 1;
   if (mean > most) mean = most;

@@ -160,8 +160,10 @@ inline long long stream_fp8_groups(int B, int Hkv, long long max_rows) {
   const int r = stream_fp8_rows(max_rows);
   return (long long)B * Hkv * ((max_rows + r - 1) / r);
 }
-// Query rows of a KV head up to which a chunk goes to the streaming kernel.
-constexpr int kStreamFp8Rows = FATTN_FP8_STREAM_ROWS;
+// Whether a chunk goes to the streaming kernel. Its time grows with the rows (2 x 30000 tokens, 8 KV heads of 128: 1.0 us a
+// row), the other way's with the query heads, whose tiles have room for 256 queries (44 us for each of a KV head), and the
+// copy of the cache (51 us): with 4 heads a KV head 128 rows take 137 and 234 us, 256 rows 258 and 235.
+inline bool streams_fp8(long long max_q, int group) { return max_q * group <= FATTN_FP8_STREAM_ROWS((long long)group); }
 cudaError_t launch_stream_fp8(const StreamFp8Params& p, cudaStream_t stream);
 
 // From api.cu: the device status word of the current device (nullptr and *err != 0 on

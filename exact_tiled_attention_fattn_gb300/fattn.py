@@ -73,6 +73,7 @@ SIGNATURES_OPS = {
     "fattn_fwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i, _vp]),
     "fattn_bwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i,
                              _vp, _sz, _vp]),
+    "fattn_bwd_sinks_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "fattn_fwd_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                    _f, _vp, _i, _i, _i, _vp, _sz, _vp]),
     "fattn_decode_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
@@ -929,11 +930,16 @@ def bwd_shaped_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
     return int(load_library().fattn_bwd_shaped_workspace_size(B, Hq, Hkv, N, d))
 
 
+def bwd_sinks_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int, causal: bool, window: int, sinks: int) -> int:
+    return int(load_library().fattn_bwd_sinks_workspace_size(B, Hq, Hkv, N, d, 1 if causal else 0,
+                                                             _int(min(window, _INT_MAX), "window"), _sinks(sinks)))
+
+
 def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
                slopes=None, window: int = 0, key_begin=None, key_end=None, dq=None, dk=None, dv=None, workspace=None,
                stream=None, sinks: int = 0):
     """Gradients of ``fwd_shaped`` (same arguments; o and lse are its outputs) with respect to q, k and v;
-    the slopes are constants. Returns (dq, dk, dv), bf16 in the input layouts."""
+    the slopes are constants. ``workspace``: bwd_shaped_workspace_size bytes, with sinks bwd_sinks_workspace_size. Returns (dq, dk, dv), bf16 in the input layouts."""
     lib = load_library()
     _need_cuda(q, k, v, o, lse, dout, dq, dk, dv, workspace)
     if not (q.dtype == k.dtype == v.dtype == o.dtype == dout.dtype == torch.bfloat16):
@@ -956,12 +962,14 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
+    sinks = sinks and _sinks(sinks, key_begin, key_end)
     if workspace is None:
-        workspace = _scratch(bwd_shaped_workspace_size(B, Hq, Hkv, N, d), q.device, stream)
+        need = (bwd_sinks_workspace_size(B, Hq, Hkv, N, d, causal, window, sinks) if sinks else
+                bwd_shaped_workspace_size(B, Hq, Hkv, N, d))
+        workspace = _scratch(need, q.device, stream)
     head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
             1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    sinks = sinks and _sinks(sinks, key_begin, key_end)
     if sinks:
         _check("fattn_bwd_sinks", lib.fattn_bwd_sinks(*head, sinks, *tail))
     else:
@@ -1015,7 +1023,9 @@ def decode_paged_shaped(q, kcache, vcache, block_table, seqlens, num_splits: int
 
 
 # ------------------------------------------------------------------ a cache in 8 bits
-FP8_STREAM_ROWS = 256  # FATTN_FP8_STREAM_ROWS: query rows of a KV head up to which chunks stream the codes
+def fp8_stream_rows(group: int) -> int:
+    """Query rows of a KV head, max_seqlen_q times its ``group`` of query heads, up to which chunks stream the codes."""
+    return 48 * (group + 1)  # FATTN_FP8_STREAM_ROWS
 
 
 def _check_fp8_cache(kcache, vcache, kscale, vscale, block_table, B):
@@ -1125,8 +1135,13 @@ def choose_fp8_splits(batch: int, Hq: int, Hkv: int, d: int, page_size: int, max
     share of the steps: enough for sequences twice as long as the mean. Else ``choose_chunk_splits``."""
     if num_sms is None:
         num_sms = _num_sms(torch.cuda.current_device())
-    rows = max_seqlen_q * (Hq // max(Hkv, 1))
-    if rows > FP8_STREAM_ROWS:
+    group = Hq // max(Hkv, 1)
+    rows = max_seqlen_q * group
+    if rows > fp8_stream_rows(group):
+        # (from two rounds of query tiles on the joining costs more than the last round's balance gives: 2 x 2048 queries over
+        # 16384 keys, 32 heads over 8: 775 us in one piece, 766 and 51 for the joining in two)
+        if batch * Hq * -(-max_seqlen_q // 256) >= 2 * num_sms:
+            return 1
         return choose_chunk_splits(batch, Hq, d, max_seqlen_q, max_context, num_sms)
     groups = max(1, batch * Hkv * -(-rows // 32))
     return max(1, min(-(-max_context // 64), 2 * -(-2 * num_sms // groups) + 1))
@@ -1138,7 +1153,7 @@ def fwd_paged_fp8(q, kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_
                   stream=None):
     """``fwd_paged_shaped`` (cap, distance bias, window, sinks) over a cache in 8 bits: query chunks q [Tq,Hq,d] bf16
     packed by ``cu_seqlens_q`` against kcache, vcache [pages, page_size, Hkv, d] E4M3 codes with kscale, vscale fp32
-    [pages, Hkv]. Up to FP8_STREAM_ROWS query rows per KV head stream the codes; more read a bf16 copy of the pages in the
+    [pages, Hkv]. Up to ``fp8_stream_rows`` query rows per KV head stream the codes; more read a bf16 copy of the pages in the
     ``workspace`` (fwd_paged_fp8_workspace_size bytes, allocated when None). ``num_splits`` None: ``choose_fp8_splits``.
     Returns (O [Tq,Hq,d], lse [Hq,Tq])."""
     lib = load_library()

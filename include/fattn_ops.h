@@ -204,10 +204,12 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
  * sinks and the window are neither read nor computed, so memory may have been reclaimed there: their table
  * entries are not read either (chunks: from the first 128-key tile past the sinks to the window of the first
  * of 256 consecutive rows, rounded down to a multiple of 128).
- * Arguments, layouts, workspaces and errors are those of the shaped calls, with INVALID_ARG for sinks < 0.
+ * Arguments, layouts, workspaces (but the gradient's) and errors are those of the shaped calls, with INVALID_ARG for sinks < 0.
  *
  * fattn_fwd_sinks         — dense prefill (fattn_fwd_shaped).
- * fattn_bwd_sinks         — its gradient (fattn_bwd_shaped, and its workspace). A sink's dK and dV sum over every later row.
+ * fattn_bwd_sinks         — its gradient (fattn_bwd_shaped). A sink's dK and dV sum over every later row, in a fixed
+ *   order. workspace: fattn_bwd_sinks_workspace_size bytes, fattn_bwd_shaped's and room for fp32 shares of the sinks' key
+ *   tiles, which are worked on in pieces: at most 128 tiles of 2 * 128 * d for every sequence and head.
  * fattn_fwd_paged_sinks   — query chunks over the paged cache (fattn_fwd_paged_shaped, and its workspace).
  * fattn_decode_paged_sinks — single tokens (fattn_decode_paged_shaped). The splits share the pages of the sinks and of
  *   the window: n = min(max_pages_per_seq, (window + page_size - 2) / page_size + 1 + ceil(sinks / page_size)).
@@ -215,6 +217,7 @@ fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const 
 fattn_status fattn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                              int N, int d, int causal, float scale, float softcap, const float* slopes, int window,
                              int sinks, cudaStream_t stream);
+size_t fattn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal, int window, int sinks);
 fattn_status fattn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
                              const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
                              int causal, float scale, float softcap, const float* slopes, int window, int sinks,
@@ -274,11 +277,11 @@ fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache, const voi
 
 /*
  * fattn_fwd_paged_fp8_workspace_size — bytes of scratch fattn_fwd_paged_fp8 needs. Few query rows
- * (max_seqlen_q * Hq / Hkv <= FATTN_FP8_STREAM_ROWS): the splits' partials, as for single tokens. More: a bf16 copy of the
+ * (max_seqlen_q * Hq / Hkv <= FATTN_FP8_STREAM_ROWS(Hq / Hkv)): the splits' partials, as for single tokens. More: a bf16 copy of the
  * sequences' pages, 4 Hkv d page_size bytes for each of B * max_pages_per_seq, their table, and the partials of
  * fattn_fwd_paged_shaped_workspace_size. Returns 0 for non-positive arguments.
  */
-#define FATTN_FP8_STREAM_ROWS 256
+#define FATTN_FP8_STREAM_ROWS(group) (48 * ((group) + 1))
 size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq, int total_q,
                                           int max_seqlen_q, int num_splits);
 

@@ -91,7 +91,8 @@ def test_splits():
     for case, S in (((1, 8, 8, 128, 16, 1, 32768), 77), ((4, 32, 8, 128, 64, 6, 12032), 21), ((64, 32, 8, 128, 16, 8, 9000), 3),
                     ((1, 8, 8, 128, 16, 1, 200), 4), ((1, 1, 1, 64, 16, 1, 1), 1), ((0, 8, 8, 64, 16, 1, 100), 2)):
         assert F.choose_fp8_splits(*case, 152) == S, case
-    assert F.choose_fp8_splits(2, 32, 8, 128, 16, 2048, 16384, 152) == F.choose_chunk_splits(2, 32, 128, 2048, 16384, 152)
+    assert F.choose_fp8_splits(2, 32, 8, 128, 16, 2048, 16384, 152) == 1
+    assert F.choose_fp8_splits(1, 32, 8, 128, 16, 256, 32768, 152) == F.choose_chunk_splits(1, 32, 128, 256, 32768, 152) > 1
 
 
 def test_binding_refuses(monkeypatch):

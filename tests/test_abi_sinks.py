@@ -40,6 +40,19 @@ def test_limits_empty_and_workspaces(lib):
     assert list(_calls(lib, ws=None))[1] == list(_calls(lib, ws=None))[3] == F.FATTN_ERR_WORKSPACE
 
 
+def test_gradient_workspace(lib):
+    base, size = lib.fattn_bwd_shaped_workspace_size, lib.fattn_bwd_sinks_workspace_size
+    args = (1, 32, 8, 8192, 128)
+    assert size(*args, 1, 0, 4) == size(*args, 1, 512, 0) == size(*args, 1, 9000, 4) == size(*args, 1, 100, 8100) == base(*args)
+    assert size(*args, 1, 512, 4) == base(*args) + 11 * 2 * 128 * 8 * 128 * 4             # 64 query tiles, 6 a piece
+    assert size(*args, 0, 512, 8100) == base(*args) + 0                                   # nearly all keys are sinks
+    assert size(1, 8, 2, 997, 64, 0, 100, 17) == base(1, 8, 2, 997, 64) + 4 * 2 * 128 * 8 * 64 * 4   # per query head
+    need = size(*args, 1, 512, 4)
+    call = lambda ws, n: lib.fattn_bwd_sinks(A, A, A, A, A, A, A, A, A, 1, 32, 8, 8192, 128, 1, 0.1, 0.0, None, 512, 4, ws, n, None)
+    assert call(A, need - 1) == call(None, need) == call(A + 16, need) == F.FATTN_ERR_WORKSPACE
+    assert F.bwd_sinks_workspace_size(*args, True, 512, 4) == need
+
+
 def test_sinks_exclude_key_ranges_and_fit_32_bits():
     t = torch.zeros(1, 4, dtype=torch.int32)
     assert F._sinks(0, t, t) == 0 and F._sinks(3) == 3 and F._sinks(2 ** 40) == 2 ** 31 - 1

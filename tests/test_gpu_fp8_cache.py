@@ -264,7 +264,7 @@ def test_chunks(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window, sinks, any_scale
     cu = np.concatenate([[0], np.cumsum(lq)])
     slopes = alibi(Hq) if sl else None
     sn = None if slopes is None else f64(slopes)
-    streamed = max(lq) * (Hq // Hkv) <= fa.FP8_STREAM_ROWS
+    streamed = max(lq) * (Hq // Hkv) <= fa.fp8_stream_rows(Hq // Hkv)
     want = []
     for b in range(len(lk)):
         off, x = lk[b] - lq[b], f64(q[cu[b]:cu[b + 1]])
