@@ -373,10 +373,14 @@ __device__ __forceinline__ void write_ds(uint32_t dp_col, const float (&pv)[64],
 // Variants of both kernels: kPlain, or what the shaped scores get (key ranges and the window always).
 // kShapeFar: a cap above 128, under which cap (1 - 2 r), off by 2^-22 of the cap, is not as good as the fp32 sum of
 // a small product next to a large one. (A kernel of its own: under a run-time switch the others lose 2 to 3 %.)
-enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2, kShapeFar = 4 };
+// kShapeSinks: a window with sinks (of its own as well: 1 to 2 % for the others under a run-time switch; with a cap it takes
+// the far form).
+enum : int { kPlain = -1, kShapeCap = 1, kShapeBias = 2, kShapeFar = 4, kShapeSinks = 8 };
+__host__ __device__ constexpr bool shape_with_sinks(int shape) { return shape != kPlain && (shape & kShapeSinks); }
 // Key tiles [top - n, top) that the rows of query tile i see, n >= 1: a tile whose rows see no
 // key visits one tile with everything masked (its dQ is the zero that this gives).
 // With sinks the walk down goes on below the window: step tile t < cut is key tile t - gap.
+template <bool kSinks>
 __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int i, int nt, int& top, int& n, int& cut,
                                                  int& gap) {
   const int first = i * BT, last = min(first + BT, p.N) - 1;
@@ -385,12 +389,12 @@ __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int 
   const int t0 = min(lo / BT, nt - 1);
   top = lo < hi ? (hi + BT - 1) / BT : t0 + 1;
   cut = gap = 0;
-  if (p.shape.sinks > 0) {
+  if constexpr (kSinks) {
     top = max(top, (shape_sinks(p.shape, last, p.N, p.causal) + BT - 1) / BT);
     cut = t0;
     gap = max(t0 - sink_blocks(p.shape.sinks, BT), 0);
   }
-  n = max(top - (p.shape.sinks > 0 ? gap : t0), 1);
+  n = max(top - (kSinks ? gap : t0), 1);
 }
 // The ranges seen from the keys: the queries that see key j are [qa_j, qb_j), as the bounds are
 // monotone: qa_j the first row whose end is above j, qb_j the first whose begin is. The dQ pass's
@@ -398,6 +402,7 @@ __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int 
 // [end_{i-1}, end_i) and qb of the keys [begin_{i-1}, begin_i), row N that of the rest, and the
 // whole warp writes each row's keys. (Searching them per key and item in the dK/dV pass took 2 to 3 us
 // at the start of every item: packed documents, B=4 H=32 N=4096, 966 us for the whole call.)
+template <bool kSinks>
 __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker, int workers, int lane) {
   const int blocks = (p.N + 1 + 31) / 32;  // rows 0 .. N of a sequence
   for (int w = worker; w < p.B * blocks; w += workers) {
@@ -421,17 +426,19 @@ __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker,
       const int r = (w - b * blocks) * 32 + l;
       const int x0 = __shfl_sync(0xffffffffu, a0, l), x1 = __shfl_sync(0xffffffffu, a1, l);
       const int y0 = __shfl_sync(0xffffffffu, b0, l), y1 = __shfl_sync(0xffffffffu, b1, l);
-      for (int k = x0 + lane; k < x1; k += 32) out[k].x = k < p.shape.sinks && !p.causal ? 0 : r;
-      for (int k = y0 + lane; k < y1; k += 32) out[k].y = k < p.shape.sinks ? p.N : r;
+      for (int k = x0 + lane; k < x1; k += 32) out[k].x = kSinks && k < p.shape.sinks && !p.causal ? 0 : r;
+      for (int k = y0 + lane; k < y1; k += 32) out[k].y = kSinks && k < p.shape.sinks ? p.N : r;
     }
   }
 }
 // Query tiles [i0, i0 + n) that see a key of key tile j, n >= 1 (a key tile that no row sees
 // visits one with everything masked: its dK and dV are the zeros that this gives).
+template <bool kSinks>
 __device__ __forceinline__ void shaped_query_tiles(const BwdParams& p, int b, int j, int nt, int& i0, int& n) {
   const int2* keys = p.ws_keys + (size_t)b * p.Npad;
   const int first = __ldg(&keys[j * BT].x);
-  const int last = max(__ldg(&keys[j * BT].y), __ldg(&keys[min((j + 1) * BT, p.N) - 1].y));  // (the first key: a sink's end)
+  int last = __ldg(&keys[min((j + 1) * BT, p.N) - 1].y);
+  if constexpr (kSinks) last = max(last, __ldg(&keys[j * BT].y));   // (the first key: a sink's end)
   // (clamped, so that even a workspace the dQ pass did not finish keeps the tiles inside the sequence)
   i0 = max(min(first / BT, nt - 1), 0);
   n = max(min(last / BT + (last % BT != 0), nt) - i0, 1);
@@ -451,6 +458,7 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
     vis = (vb <= 0 || va >= 32 || va >= vb ? 0u : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)))) |
           low_bits(vs);
   constexpr bool cap = kShape & kShapeCap, bias = kShape & kShapeBias;
+  static_assert(kShape != kPlain, "shaped scores");
   float y[32], f[32];
   if constexpr (cap) {
     if (edge) {  // hidden keys must not decide between the two forms of the cap
@@ -625,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int nt = (p.N + BT - 1) / BT;
   const int G = kPerHead ? 1 : p.Hq / p.Hkv;
-  const int cut = kShaped ? p.sink_tiles * (p.sink_pieces - 1) : 0;   // items that the sinks' tiles add
+  constexpr bool kSinks = shape_with_sinks(kShape);
+  const int cut = kSinks ? p.sink_tiles * (p.sink_pieces - 1) : 0;   // items that the sinks' tiles add
   const BwdSchedule sch = make_bwd_schedule(p.B * (kPerHead ? p.Hq : p.Hkv), nt + cut, 1);
   // item: (sequence, KV head, or query head with kPerHead, key tile j, piece of its queries); rank 0 = j 0, the most query
   // tiles under the causal rule
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = head / (kPerHead ? p.Hq : p.Hkv);
     hkv = head - b * (kPerHead ? p.Hq : p.Hkv);
     piece = 0;
-    if constexpr (kShaped) {
+    if constexpr (kSinks) {
       if (cut > 0) {
         if (j < p.sink_tiles + cut) {
           piece = j / p.sink_tiles;
@@ -649,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // query tiles [i0, i0 + ni) of an item
   auto tiles = [&](int b, int j, int piece, int& i0, int& ni) {
     if constexpr (kShaped) {
-      shaped_query_tiles(p, b, j, nt, i0, ni);
-      if (cut > 0 && j < p.sink_tiles) {   // (all query tiles from the first on: at least one a piece)
+      shaped_query_tiles<kSinks>(p, b, j, nt, i0, ni);
+      if (kSinks && cut > 0 && j < p.sink_tiles) {   // (all query tiles from the first on: at least one a piece)
         const int from = ni * piece / p.sink_pieces, to = ni * (piece + 1) / p.sink_pieces;
         i0 += from;
         ni = max(to - from, 1);
@@ -922,12 +931,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int wkey0 = j * BT + q4 * 32;  // the warp's first key row
       const bool staged = Lay::kStoreTma && wkey0 + 32 <= p.N;
       // a piece of a sinks' tile: its shares in fp32
-      const bool shared = kShaped && cut > 0 && j < p.sink_tiles;
+      const bool shared = kSinks && cut > 0 && j < p.sink_tiles;
       const size_t srow = (size_t)p.B * p.sink_tiles * BT;
       float* share = nullptr;
-      if (kShaped && shared)
+      if (kSinks && shared)
         share = p.ws_sink + ((2 * piece * srow + (size_t)b * p.sink_tiles * BT + key) * (kPerHead ? p.Hq : p.Hkv) + hkv) * D + wg * (D / 2);
-      if (kShaped && shared)
+      if (kSinks && shared)
         store_row_f32<D / 2>(acc_col + wg * (D / 2), 1.f, share, live);
       else if constexpr (kPerHead)
         store_row_f32<D / 2>(acc_col + wg * (D / 2), 1.f, p.ws_part + off, live);
@@ -938,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(bar(kAccFull), nacc & 1, abort, p.status, p.wait_ns)) break;
       ++nacc;
       tc_fence_after();
-      if (kShaped && shared)
+      if (kSinks && shared)
         store_row_f32<D / 2>(acc_col + D + wg * (D / 2), p.scale, share + srow * (kPerHead ? p.Hq : p.Hkv) * D, live);
       else if constexpr (kPerHead)
         store_row_f32<D / 2>(acc_col + D + wg * (D / 2), p.scale, p.ws_part + (size_t)p.B * p.N * p.Hq * D + off, live);
@@ -1002,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const BwdParams p) {
   using Lay = DqLayout<D>;
-  constexpr bool kShaped = kShape != kPlain;
+  constexpr bool kShaped = kShape != kPlain, kSinks = shape_with_sinks(kShape);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -1052,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // key tiles [top - jn, top) of an item, from the highest down; with sinks tile t < cut stands for t - gap
   auto tiles = [&](int b, int i, int& top, int& jn, int& cut, int& gap) {
     if constexpr (kShaped) {
-      shaped_key_tiles(p, b, i, nt, top, jn, cut, gap);
+      shaped_key_tiles<kSinks>(p, b, i, nt, top, jn, cut, gap);
     } else {
       top = jn = p.causal ? i + 1 : nt;
       cut = gap = 0;
@@ -1084,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(bar(kQKvFull + vs), 2 * Lay::kTile);
           int kt = top - 1 - j;  // key tiles from the diagonal down
-          if (kShaped && kt < cut) kt -= gap;
+          if (kSinks && kt < cut) kt -= gap;
           load_tile<D>(sb + Lay::kOffK + ks * Lay::kTile, &tk, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           load_tile<D>(sb + Lay::kOffV + vs * Lay::kTile, &tv, bar(kQKvFull + vs), hkv, b * p.N + kt * BT, pol_kv);
           ++nk;
@@ -1194,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // element-wise warps; they read the vectors back once the warp's count shows them
     // written, and the dK/dV pass (launched after this one) reads them all.
     if constexpr (kShaped) {
-      if (warp == 3) write_key_ranges(p, blockIdx.x, gridDim.x, lane);
+      if (warp == 3) write_key_ranges<kSinks>(p, blockIdx.x, gridDim.x, lane);
     }
     for (int kk = 0, it; (it = bwd_item_index(sch, kk)) >= 0; ++kk) {
       if (!count_wait(items_started, kk - 2, abort, p.status, p.wait_ns)) break;
@@ -1255,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int klo = 0, khi = 0, ksink = 0;
       if constexpr (kShaped) {
         if (qrow < p.N) {
-          ksink = shape_sinks(p.shape, qrow, p.N, p.causal);
+          if constexpr (kSinks) ksink = shape_sinks(p.shape, qrow, p.N, p.causal);
           klo = shape_lo(p.shape, (long long)b * p.N + qrow, qrow);
           khi = shape_hi(p.shape, (long long)b * p.N + qrow, qrow, p.N, p.causal);
         }
@@ -1282,9 +1291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t u[32];
             tmem_ld32(s_col + 32 * q, u);
             const int vt = top - 1 - j;
-            const int kb = (vt - (vt < cut ? gap : 0)) * BT + cb + 32 * q;  // key of the first column
-            shaped_p32<kShape, false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, ksink - kb, nullptr, nl2,
-                                             pv + 32 * q, nullptr);
+            const int kb = (kSinks && vt < cut ? vt - gap : vt) * BT + cb + 32 * q;  // key of the first column
+            shaped_p32<kShape, false, false>(p, slope2, u, (float)(qrow - kb), -1.f, klo - kb, khi - kb, kSinks ? ksink - kb : 0,
+                                             nullptr, nl2, pv + 32 * q, nullptr);
           }
         } else {
           uint32_t u[64];
@@ -1409,13 +1418,13 @@ cudaError_t launch_dkdv(const BwdParams& p, const CUtensorMap& tq, const CUtenso
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvLayout<D>::kBytes);
   if (e != cudaSuccess) return e;
   const long long items =
-      (long long)p.B * (kPerHead ? p.Hq : p.Hkv) * (nt + (kShape != kPlain ? p.sink_tiles * (p.sink_pieces - 1) : 0));
+      (long long)p.B * (kPerHead ? p.Hq : p.Hkv) * (nt + (shape_with_sinks(kShape) ? p.sink_tiles * (p.sink_pieces - 1) : 0));
   const int grid = (int)std::min<long long>(items, num_sms);
   kern<<<grid, kThreads, DkdvLayout<D>::kBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = kSumThreads / (D / 4);
-  if (kShape != kPlain && p.sink_pieces > 1) {
+  if (shape_with_sinks(kShape) && p.sink_pieces > 1) {
     const long long n = (long long)p.B * p.sink_tiles * BT * p.Hkv;
     sum_sinks_kernel<<<dim3((unsigned)((n + rows - 1) / rows), 2), kSumThreads, 0, stream>>>(p, kPerHead ? p.Hq : p.Hkv);
     e = cudaGetLastError();
@@ -1453,6 +1462,13 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq, const CUtens
                          cudaStream_t stream) {
   if (!p.shaped) return launch_bwd_t<D, kPlain>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
   const bool cap = p.shape.cap > 0.f, bias = p.shape.slopes != nullptr;
+  if (p.shape.sinks > 0) {
+    constexpr int kCapped = kShapeSinks + kShapeCap + kShapeFar;
+    if (cap && bias) return launch_bwd_t<D, kCapped + kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+    if (cap) return launch_bwd_t<D, kCapped>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+    if (bias) return launch_bwd_t<D, kShapeSinks + kShapeBias>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+    return launch_bwd_t<D, kShapeSinks>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);
+  }
   if (p.shape.cap > 128.f)
     return bias ? launch_bwd_t<D, kShapeCap + kShapeBias + kShapeFar>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream)
                 : launch_bwd_t<D, kShapeCap + kShapeFar>(p, tq, tk, tv, tdo, tdk, tdv, num_sms, stream);

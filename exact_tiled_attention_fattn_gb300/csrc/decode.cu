@@ -84,7 +84,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // Shaped: the scores get p.shape's cap and distance bias; the query sits at position `qpos`. With sinks [t0, t1) counts
 // tokens without the ones between sinks and window: from `cut` on token t is t + gap, and tokens below `lo` that are no
 // sinks are hidden.
-template <int D, bool kPage16, bool kShaped>
+template <int D, bool kPage16, bool kShaped, bool kSinks>
 __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* smem, int split, int b, int hkv, int h0,
                                              int rows_valid, int t0, int t1, int qpos, int cut, int gap, int lo) {
   using Lay = DecodeLayout<D>;
@@ -128,12 +128,12 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
     int page = 0;
     bool ok = false;
     if (lane < 16 && t < t1) {
-      if (kShaped && t >= cut) t += gap;
+      if (kSinks && t >= cut) t += gap;
       const int pi = kPage16 ? (t >> 4) : t / p.page_size;
       page = table[pi];
       ok = (unsigned)page < (unsigned)p.num_pages;
       if (!ok) record_status(p.status, kStatusDeviceCheck);
-      if (kShaped && t < lo && t >= p.shape.sinks) ok = false;
+      if (kSinks && t < lo && t >= p.shape.sinks) ok = false;
     }
     const uint32_t vmask = __ballot_sync(0xffffffffu, ok);
     const uint32_t kdst = wbase + st * Lay::kStageUnits * 16;
@@ -145,7 +145,7 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
       const int pg = __shfl_sync(0xffffffffu, page, rr);
       const bool okr = (vmask >> rr) & 1u;
       int tt = tb + rr;
-      if (kShaped && tt >= cut) tt += gap;
+      if (kSinks && tt >= cut) tt += gap;
       const int slot = kPage16 ? (tt & 15) : (tt % p.page_size);
       const size_t off = okr ? ((((size_t)pg * p.page_size + slot) * p.Hkv + hkv) * D + u * 8) : 0;
       const int nbytes = okr ? 16 : 0;
@@ -234,7 +234,7 @@ __device__ __forceinline__ void decode_split(const DecodeParams& p, uint8_t* sme
           y = p.shape.cap > 0.f ? s[nt][j] : s[nt][j] * sl2;
           if (p.shape.slopes) {
             float away = dist - (float)(nt * 8 + (j & 1));
-            if (tok0 + nt * 8 + (j & 1) >= cut) away -= (float)gap;
+            if (kSinks && tok0 + nt * 8 + (j & 1) >= cut) away -= (float)gap;
             y = fmaf(j < 2 ? slope0 : slope1, away, y);
           }
         } else {
@@ -376,7 +376,8 @@ __device__ __forceinline__ void merge_group(const DecodeParams& p, int b, int h0
 // three CTAs 118). The shaped one, whose chunks take longer, is held to the registers of three, what shared memory
 // admits at d = 128: capped, 199k context tokens of 8 KV heads take 150 us in 8 splits and 155 in 16 (two CTAs 195
 // and 162), one of 131k tokens 110 in 38 splits (109).
-template <int D, bool kPage16, bool kShaped>
+// kSinks: the shaped one with sinks (a kernel of its own: 1 % for the other under a run-time switch).
+template <int D, bool kPage16, bool kShaped, bool kSinks>
 __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_item, s_last;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(co
     }
     // with sinks the tokens between them and the window's first page are left out of the count
     int cut = 0x7fffffff, gap = 0;
-    if (kShaped && p.shape.sinks > 0 && first > 0) {
+    if (kSinks && first > 0) {
       cut = min(sink_blocks(p.shape.sinks, p.page_size), first / p.page_size) * p.page_size;
       gap = first - cut;
       L -= gap;
@@ -434,8 +435,8 @@ __global__ void __launch_bounds__(kWarps * 32, kShaped ? 3 : 1) decode_kernel(co
       if (split == 0) merge_group<D>(p, b, h0, rows_valid, 0);
       continue;
     }
-    const int from = kShaped && p.shape.sinks > 0 ? (int)t0 : max((int)t0, lo);
-    decode_split<D, kPage16, kShaped>(p, smem, split, b, hkv, h0, rows_valid, from, (int)min((long long)L, t0 + span),
+    const int from = kSinks ? (int)t0 : max((int)t0, lo);
+    decode_split<D, kPage16, kShaped, kSinks>(p, smem, split, b, hkv, h0, rows_valid, from, (int)min((long long)L, t0 + span),
                                       L + gap - 1, cut, gap, lo);
     // publish the partial, count it, and let the last split of the group merge
     __threadfence();
@@ -523,10 +524,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
   }
 }
 
-template <int D, bool kPage16, bool kShaped>
+template <int D, bool kPage16, bool kShaped, bool kSinks>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   using Lay = DecodeLayout<D>;
-  auto kern = decode_kernel<D, kPage16, kShaped>;
+  auto kern = decode_kernel<D, kPage16, kShaped, kSinks>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kBytes);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
@@ -547,14 +548,17 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-template <int D, bool kShaped>
+template <int D, bool kShaped, bool kSinks>
 static cudaError_t launch_decode_d(const DecodeParams& p, cudaStream_t stream) {
-  return p.page_size == 16 ? launch_decode_t<D, true, kShaped>(p, stream) : launch_decode_t<D, false, kShaped>(p, stream);
+  return p.page_size == 16 ? launch_decode_t<D, true, kShaped, kSinks>(p, stream)
+                           : launch_decode_t<D, false, kShaped, kSinks>(p, stream);
 }
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-  if (p.shaped) return p.d == 128 ? launch_decode_d<128, true>(p, stream) : launch_decode_d<64, true>(p, stream);
-  return p.d == 128 ? launch_decode_d<128, false>(p, stream) : launch_decode_d<64, false>(p, stream);
+  if (p.shaped && p.shape.sinks > 0)
+    return p.d == 128 ? launch_decode_d<128, true, true>(p, stream) : launch_decode_d<64, true, true>(p, stream);
+  if (p.shaped) return p.d == 128 ? launch_decode_d<128, true, false>(p, stream) : launch_decode_d<64, true, false>(p, stream);
+  return p.d == 128 ? launch_decode_d<128, false, false>(p, stream) : launch_decode_d<64, false, false>(p, stream);
 }
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {

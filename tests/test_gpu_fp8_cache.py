@@ -247,7 +247,7 @@ CHUNKS = [  # P, Hq, Hkv, d, lk, lq, causal, cap, slopes, window, sinks, any sca
     (64, 8, 2, 128, [1200, 129, 60], [6, 5, 6], True, 30.0, False, 0, 0, False),                  # 24 rows
     (16, 8, 1, 64, [800, 90], [4, 3], True, 0.0, True, 150, 20, True),                            # 32 rows
     (32, 12, 2, 64, [500, 77, 1000], [7, 6, 2], False, 0.0, False, 0, 0, False),                  # 42 rows, groups of 24
-    (16, 8, 2, 128, [3000, 64], [64, 64], True, 0.0, False, 0, 0, False),                         # 256 rows
+    (16, 8, 2, 128, [3000, 64], [60, 60], True, 0.0, False, 0, 0, False),                         # 240 rows, the most in groups of 4
     (16, 4, 2, 128, [900, 257, 1, 130], [300, 257, 1, 1], True, 0.0, False, 0, 0, False),         # through the prefill from here
     (32, 8, 1, 64, [1513, 40, 900], [130, 40, 256], True, 0.0, True, 200, 40, False),
     (64, 8, 2, 128, [1000, 429], [129, 128], False, 20.0, False, 100, 129, False),
