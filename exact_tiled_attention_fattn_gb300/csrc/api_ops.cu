@@ -589,7 +589,8 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
   e.B = B; e.Hkv = Hkv; e.d = d; e.page_size = page_size; e.max_pages = max_pages_per_seq; e.num_pages = num_pages;
   e.total_q = total_q; e.window = p.shape.window; e.sinks = p.shape.sinks; e.status = status;
   if (launch_expand_fp8(e, stream) != cudaSuccess) return FATTN_ERR_CUDA;
+  const bool plain = p.shape.cap == 0.f && !p.shape.slopes && p.shape.window == 0 && num_splits == 1;
   return fwd_paged_impl(q, e.kout, e.vout, e.table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
-                        max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale, &p.shape, num_splits,
+                        max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale, plain ? nullptr : &p.shape, num_splits,
                         num_splits > 1 ? ws + w.splits : nullptr, num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
 }

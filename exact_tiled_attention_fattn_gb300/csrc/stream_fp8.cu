@@ -36,6 +36,9 @@ template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
 // What going from one group to the next costs a CTA, in chunks: it counts in the shares.
 constexpr int kTurn = 16;
+// Pieces of a group at most: one CTA joins them, a round of loads for about ten of them (one context of 199k tokens, one KV
+// head: 45 us in 304 pieces).
+constexpr int kPieces = 96;
 constexpr int kChunk = 16;       // tokens of a step
 constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
 constexpr float kLazy = 8.f;     // log2 units that scores may exceed the running maximum by
@@ -218,6 +221,14 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
       }
     }
   };
+  // V's rows of step i on their way to the L2 cache, a row a lane: its loads, for which registers are free only later, then
+  // wait for the cache and not for memory (8 contexts to 32k: 80 -> 77.5 us; two and more steps ahead, or K as well, is
+  // slower: 80 to 84)
+  const uint8_t* line = static_cast<const uint8_t*>(p.vcache) + (size_t)(lane & 15) * token_bytes + (size_t)hkv * D;
+  auto prefetch_v = [&](const int (&row)[Y]) {
+    if (Y == 2 || lane < 16)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(line + (size_t)(lane < 16 ? row[0] : row[Y - 1]) * token_bytes));
+  };
   // the first step's codes are on their way while Q is brought to fp16 (a chunk without a page reads the pool's first)
   Meta meta, ahead{-1, 0, 1.f, 1.f};
   look(meta, 0);
@@ -335,6 +346,7 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
       next[y] = __shfl_sync(0xffffffffu, wrap ? ahead.row : meta.row, ((i + 1) % kBatch) * Y + y);
       if (!last) load_k(kw[y], next[y]);
     }
+    if (!last) prefetch_v(next);
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
       const int from = (i % kBatch) * Y + y;
@@ -488,7 +500,7 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
 // thread's rows are loaded together (they cost a trip to the L2 cache each otherwise).
 template <int D, int NT>
 __device__ __forceinline__ void join_pieces(const StreamFp8Params& p, const Group& x, int hkv, int pieces) {
-  constexpr int C4 = D / 4, kPer = kWarps<NT> * 32 / C4, kRows = (8 * NT + kPer - 1) / kPer, kRound = 12 / kRows;
+  constexpr int C4 = D / 4, kPer = kWarps<NT> * 32 / C4, kRows = (8 * NT + kPer - 1) / kPer, kRound = 24 / kRows;
   const int col = threadIdx.x % C4 * 4;
   size_t prow[kRows];
   int query[kRows], head[kRows];
@@ -587,10 +599,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   }
   // equal shares in whole rounds of the warps; one piece a group: the groups that begin in the share, whole
   const bool whole = p.num_splits == 1;
+  const unsigned splits = min(p.num_splits, kPieces);
   const unsigned block = blockIdx.x / p.Hkv, blocks = gridDim.x / p.Hkv;
   const int hkv = blockIdx.x - block * p.Hkv;
   unsigned share = ((unsigned)total + blocks - 1) / blocks;
-  if (!whole) share = max(share, ((unsigned)most + p.num_splits - 2) / (p.num_splits - 1));
+  if (!whole) share = max(share, ((unsigned)most + splits - 2) / (splits - 1));
   share = max(share, (unsigned)(Y * W));               // (a step for every warp)
   if ((unsigned long long)share * block >= total) return;
   int at = (int)(share * block);                       // in steps
