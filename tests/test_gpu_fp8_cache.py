@@ -390,3 +390,95 @@ def test_serving_steps_together():
         lens = [a + 1 for a in lens]
         assert n.tolist() == lens
         check(qr, o, lse.t(), lens, [1, 1])
+
+
+def test_pool_past_2_31_bytes():
+    """Pages whose first byte lies past 2^31 of both caches, and rows of the bf16 copy's tables with them."""
+    fa = need_gpu()
+    P, Hq, Hkv, d = 128, 16, 8, 128
+    pages = 2 ** 31 // (P * Hkv * d) + 40
+    kc, vc = (torch.empty(pages, P, Hkv, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(pages, Hkv, device="cuda") for _ in range(2))
+    table = torch.arange(pages - 12, pages, dtype=torch.int32, device="cuda").view(2, 6).flip(1).contiguous()
+    g = torch.Generator().manual_seed(6)
+    lens = [700, 650]
+    T = sum(lens)
+    x = torch.randn(T, Hq + 2 * Hkv, d, generator=g).to(torch.bfloat16).cuda()
+    cu, n = i32([0, 700, T]).cuda(), i32(lens).cuda()
+    inv_freq, _ = fa.rope_frequencies(d, device="cuda")
+    q = fa.rope_append_paged_fp8(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], kc, vc, ks, vs, table, n, cu, inv_freq)
+    o, lse = fa.fwd_paged_fp8(q, kc, vc, ks, vs, table, n, cu, 700, scale=0.1)
+    last = torch.stack([q[699], q[T - 1]])
+    od, ld = fa.decode_paged_fp8(last, kc, vc, ks, vs, table, n, 3, scale=0.1)
+    assert fa.debug_read_status() == 0
+    for b, n in enumerate(lens):
+        pg = table[b, :-(-n // P)].long()
+        full = [held(kc[pg], ks[pg], torch.arange(len(pg)), n), held(vc[pg], vs[pg], torch.arange(len(pg)), n)]
+        rows = [0, 1, 127, 300, n - 1]
+        vis = np.tril(np.ones((n, n), bool))[rows]
+        at = torch.tensor(rows) + (0 if b == 0 else 700)
+        ref = R.forward(f64(q[at.cuda()]), *full, 0.1, 0.0, None, vis)
+        check_fwd(o[at.cuda()], lse[:, at.cuda()], ref, f"sequence {b}")
+        check_fwd(od[b:b + 1], ld[b][:, None], tuple(z[-1:] if z.ndim == 3 else z[:, -1:] for z in ref), f"token of sequence {b}")
+
+
+def test_same_results_on_another_stream_and_again():
+    """A call on another stream than the current one, its workspace its own; and every call gives the same bits again."""
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(3)
+    lens = [3000, 77, 1500]
+    kc, vc, ks, vs, table, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in pool(g, lens, 16, 2, 128))
+    n = i32(lens).cuda()
+    q1 = torch.randn(3, 8, 128, generator=g).to(torch.bfloat16).cuda()
+    qs = torch.randn(90, 8, 128, generator=g).to(torch.bfloat16).cuda()
+    few, many = i32([0, 5, 9, 15]).cuda(), i32([0, 60, 70, 90]).cuda()
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        return [*fa.decode_paged_fp8(q1, kc, vc, ks, vs, table, n, 5, stream=stream),
+                *fa.fwd_paged_fp8(qs[:15], kc, vc, ks, vs, table, n, few, 6, stream=stream),
+                *fa.fwd_paged_fp8(qs, kc, vc, ks, vs, table, n, many, 60, stream=stream, num_splits=2)]
+
+    here = calls(None)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    there = calls(side)
+    again = calls(None)                                   # at the same time
+    torch.cuda.synchronize()
+    assert fa.debug_read_status() == 0
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(here, there, again))
+
+
+def test_empty_problems_and_graphs_that_share_a_workspace():
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(8)
+    kc, vc, ks, vs, table, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in pool(g, [900, 0], 32, 2, 64))
+    e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device="cuda")
+    none = table[:0].contiguous()
+    zero = i32([0]).cuda()
+    o, lse = fa.decode_paged_fp8(e(0, 4, 64), kc, vc, ks, vs, none, e(0, dt=torch.int32), 2)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    fa.fwd_paged_fp8(e(0, 4, 64), kc, vc, ks, vs, none, e(0, dt=torch.int32), zero, 0)
+    fa.rope_append_paged_fp8(e(0, 4, 64), e(0, 2, 64), e(0, 2, 64), kc, vc, ks, vs, none, e(0, dt=torch.int32), zero,
+                             torch.zeros(32, dtype=torch.float64, device="cuda"))
+    # two graphs over one workspace, replayed in turn, each with a row count of its own
+    n, cu = i32([900, 0]).cuda(), (i32([0, 1, 1]).cuda(), i32([0, 40, 40]).cuda())
+    q = torch.randn(40, 4, 64, generator=g).to(torch.bfloat16).cuda()
+    sizes = [fa.fwd_paged_fp8_workspace_size(2, 4, 2, 64, 32, table.shape[1], t, t, 3) for t in (1, 40)]
+    ws = e(max(sizes), dt=torch.uint8)
+    run = lambda i: fa.fwd_paged_fp8(q[:(1, 40)[i]], kc, vc, ks, vs, table, n, cu[i], (1, 40)[i], num_splits=3, workspace=ws)
+    want = [run(0), run(1)]
+    torch.cuda.synchronize()
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    for i in (0, 1):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=side):
+            outs.append(run(i))
+        graphs.append(gr)
+    ws.fill_(255)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    assert fa.debug_read_status() == 0
+    assert all(torch.equal(a, b) for x, y in zip(want, outs) for a, b in zip(x, y))

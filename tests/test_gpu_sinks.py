@@ -182,3 +182,47 @@ def test_decode(P, Hq, Hkv, d, lens, cap, sl, window, sinks):
         assert fa.debug_read_status() == 0
         for b in range(len(lens)):
             check_fwd(o[b:b + 1], lse[b][:, None], want[b], f"splits {S} sequence {b}")
+
+
+def test_gradient_again_and_in_a_graph():
+    """The sinks' tiles are worked on in pieces that are added in a fixed order: the same bits on every run, in a captured
+    graph as well, with a workspace full of anything."""
+    fa = need_gpu()
+    for Hkv, N in ((2, 3000), (8, 1500)):                  # (per query head, and a group's heads together)
+        q, k, v, do = (t.cuda() for t in make(N, 4, N, 8, Hkv, 128))
+        kw = dict(causal=True, window=200, sinks=5)
+        o, lse = fa.fwd_shaped(q, k, v, **kw)
+        want = fa.bwd_shaped(q, k, v, o, lse, do, **kw)
+        ws = torch.full((fa.bwd_sinks_workspace_size(4, 8, Hkv, N, 128, True, 200, 5),), 255, dtype=torch.uint8, device="cuda")
+        grads = [torch.empty_like(t) for t in want]
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            fa.bwd_shaped(q, k, v, o, lse, do, dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws, **kw)
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert fa.debug_read_status() == 0
+            assert all(torch.equal(a, b) for a, b in zip(want, grads))
+            ws.fill_(127)
+
+
+def test_long_sequences_at_their_edges():
+    """Rows and keys at the edges of what the sinks and the window make visible, in a sequence of many tiles."""
+    fa = need_gpu()
+    N, W, S = 6000, 700, 130
+    q, k, v, do = make(2, 1, N, 2, 1, 64)
+    kw = dict(causal=True, scale=0.125, window=W, sinks=S)
+    dev = [t.cuda() for t in (q, k, v)]
+    o, lse = fa.fwd_shaped(*dev, **kw)
+    g = dict(zip(("dq", "dk", "dv"), fa.bwd_shaped(*dev, o, lse, do.cuda(), **kw)))
+    assert fa.debug_read_status() == 0
+    vis = R.window_with_sinks(N, N, 0, True, W, S)
+    x = [f64(t[0]) for t in (q, k, v)]
+    ref = R.forward(*x, 0.125, 0.0, None, vis)
+    check_fwd(o[0], lse[0], ref)
+    want, a, e = R.backward(*x, f64(o[0]), f64(lse[0]), f64(do[0]), 0.125, 0.0, None, vis)
+    es = 2 * score_err(ref[3].max())
+    for n in g:
+        tol = H * 1.02 * (a[n] + np.abs(want[n])) + es * e[n] + 1e-30
+        assert (np.abs(f64(g[n][0]) - want[n]) <= tol).all(), n
