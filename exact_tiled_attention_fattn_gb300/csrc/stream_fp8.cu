@@ -1,11 +1,16 @@
 // Attention of few query rows over the 8-bit paged cache (single tokens, and chunks of a few queries), split along the
 // keys, the splits joined in the same launch.
 //
-// Bound by the cache's bytes. A warp streams tokens 16 at a time straight from global memory into registers: the codes are
-// laid out as the tensor-core fragments want them, so that shared memory, shuffles of the cache and transposes are not
-// needed, and the registers of the next 16 tokens are in flight while these are worked on. Both products are taken
-// transposed, with tokens (K) and head elements (V) as the 16 rows of mma.sync m16n8k16 and up to 8 query rows as its columns, which is
-// what a group of heads gives:
+// Bound by the cache's bytes where a KV head has few rows: 8 contexts to 32k tokens, 32 heads over 8 of 128, 409 MB, in 77 us
+// (5.3 TB/s; 6.4 in the stream itself, the rest is launch, first lookups and the joining), four times the tokens in 262 us
+// (6.2 TB/s). By the latency of a step with more (24 rows, 4 contexts to 12k, capped: 78 MB in 41 us, 8 warps an SM): the
+// registers hold a warp's O^T, 32 a tile of 8 rows.
+// A warp streams tokens 16 at a time straight from global memory into registers: the codes are laid out as the tensor-core
+// fragments want them, so that shared memory, shuffles of the cache and transposes are not needed. The next step's K is
+// loaded while this one's softmax and V are worked on, its V brought to the L2 cache. (Through shared memory by
+// cp.async, three stages, 16 warps an SM: 91 us for the first case above.) Both products are taken transposed, with tokens (K) and head
+// elements (V) as the 16 rows of mma.sync m16n8k16 and up to 8 query rows as its columns, which is what a group of heads
+// gives, where a tile of tcgen05.mma would have 128 rows for them and its operands in shared memory:
 //   S^T = K Q^T   lane (g, c) holds tokens g and g + 8: 16 consecutive codes of each are the A fragments of four steps, if
 //                 the head's elements are taken in the order in which they lie there (Q^T is permuted alike);
 //   O^T = V^T P^T lane (g, c) holds the codes 16 g .. 16 g + 15 of tokens 2c, 2c + 1, 2c + 8 and 2c + 9: pairs of tokens
@@ -139,7 +144,7 @@ struct Sight {
   int lo, hi, sk, pos;
   __device__ __forceinline__ bool sees(int t) const { return (t >= lo && t < hi) || t < sk; }
 };
-// A piece's rows, kept out of registers: they are looked at where a chunk holds tokens that not every row sees.
+// A group's rows, kept out of registers: they are looked at where a chunk holds tokens that not every row sees.
 template <int D, int R>
 struct Shared {
   uint2 q[R / 8][D / 16][32];   // Q^T's fragments

@@ -265,9 +265,11 @@ fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, const void*
 
 /*
  * fattn_decode_paged_fp8 — one query token per sequence over the 8-bit cache: fattn_decode_paged_sinks with its
- * arguments, splits, outputs and workspace (fattn_decode_workspace_size). q bf16. Products of q with codes are exact in
- * fp32 sums, weights are rounded to fp16 (11 bits) for the product with V. B == 0 is an empty problem. A table entry outside the
- * pool hides its tokens and records FATTN_ERR_DEVICE_CHECK, as do lengths outside the table.
+ * arguments, outputs and workspace (fattn_decode_workspace_size). The thread blocks take equal shares of all sequences' visible tokens;
+ * num_splits bounds the pieces that one sequence's tokens of a KV head are cut into (1: none, and no more than 96 are made).
+ * q bf16. Products of q with codes are exact in fp32 sums, weights are rounded to fp16 (11 bits) for the product with V.
+ * Equal calls give equal bits. B == 0 is an empty problem. A table entry outside the pool hides its tokens and records
+ * FATTN_ERR_DEVICE_CHECK, as do lengths outside the table.
  */
 fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
                                     const float* vscale, const int32_t* block_table, const int32_t* seqlens,
@@ -277,8 +279,8 @@ fattn_status fattn_decode_paged_fp8(const void* q, const void* kcache, const voi
 
 /*
  * fattn_fwd_paged_fp8_workspace_size — bytes of scratch fattn_fwd_paged_fp8 needs. Few query rows
- * (max_seqlen_q * Hq / Hkv <= FATTN_FP8_STREAM_ROWS(Hq / Hkv)): the splits' partials, as for single tokens. More: a bf16 copy of the
- * sequences' pages, 4 Hkv d page_size bytes for each of B * max_pages_per_seq, their table, and the partials of
+ * (max_seqlen_q * Hq / Hkv <= FATTN_FP8_STREAM_ROWS(Hq / Hkv)): the pieces' partials, as for single tokens. More: a bf16
+ * copy of the sequences' pages, 4 Hkv d page_size bytes for each of B * max_pages_per_seq, their table, and the partials of
  * fattn_fwd_paged_shaped_workspace_size. Returns 0 for non-positive arguments.
  */
 #define FATTN_FP8_STREAM_ROWS(group) (48 * ((group) + 1))
@@ -289,7 +291,8 @@ size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int pag
  * fattn_fwd_paged_fp8 — query chunks over the 8-bit cache: fattn_fwd_paged_sinks with its arguments and outputs.
  * Few query rows stream the codes as single tokens do; with more, the pages that any of them sees are expanded to
  * bf16 (exact for scales that are powers of two, else one rounding) in the workspace and read by the tensor-core prefill.
- * num_splits >= 1 cuts the keys in both. workspace: 256-byte aligned, contents ignored, always needed.
+ * num_splits >= 1: the pieces at most of a group of up to 32 streamed rows, or the prefill's splits. workspace: 256-byte
+ * aligned, contents ignored, always needed.
  * Errors: those of fattn_fwd_paged_sinks and of the cache; UNSUPPORTED also for (B * max_pages_per_seq + 1) * page_size
  *   >= 2^31.
  */

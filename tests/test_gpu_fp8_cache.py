@@ -206,7 +206,7 @@ def peaks(q, k, vscale, scale, cap, slopes, vis, off, lse):
     (32, 4, 4, 64, [2049, 64, 65], 0.0, False, 0, 0, True),
     (64, 16, 2, 128, [700, 129], 0.0, False, 0, 0, True),
     (128, 16, 1, 128, [1500, 129], 20.0, False, 0, 0, False),           # 16 rows
-    (16, 20, 1, 64, [900, 40], 0.0, True, 0, 0, False),                 # 16 and 4 rows
+    (16, 20, 1, 64, [900, 40], 0.0, True, 0, 0, False),                 # 20 rows, three tiles of 8
     (16, 10, 2, 128, [3000, 41], 30.0, True, 100, 0, False),
     (32, 8, 2, 128, [2500, 300, 64], 0.0, False, 64, 4, False),
     (16, 5, 5, 64, [1900, 640, 641], 0.0, True, 128, 64, True),
