@@ -147,6 +147,7 @@ struct StreamFp8Params {
   int* status;
   // set by the launch: heads of a KV head, groups of rows of a sequence, their reciprocals, log2 of the page size
   int group, subs, page_shift;
+  int cluster;                // CTAs of a cluster that share a group of rows; 1: the groups' line is shared
   unsigned long long by_group, by_subs;
 };
 

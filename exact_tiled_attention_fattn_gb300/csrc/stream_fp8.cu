@@ -29,6 +29,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace fattn {
 namespace {
@@ -41,9 +42,10 @@ template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
 // What going from one group to the next costs a CTA, in chunks: it counts in the shares.
 constexpr int kTurn = 16;
-// Pieces of a group at most: one CTA joins them, a round of loads for about ten of them (one context of 199k tokens, one KV
+// Pieces of a group in the line at most: one CTA joins them, a round of loads for about ten of them (one context of 199k tokens, one KV
 // head: 45 us in 304 pieces).
 constexpr int kPieces = 96;
+constexpr int kMostCluster = 16;  // CTAs of a cluster
 constexpr int kChunk = 16;       // tokens of a step
 constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
 constexpr float kLazy = 8.f;     // log2 units that scores may exceed the running maximum by
@@ -80,6 +82,32 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// This CTA's rank in its cluster; a float4 and a float of the CTA of rank r, at the shared-memory address that `p` has here.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(const void* p, int r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(r));
+  return a;
+}
+__device__ __forceinline__ float4 peer_float4(const float* p, int r) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_address(p, r)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float peer_float(const float* p, int r) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_address(p, r)) : "memory");
+  return v;
 }
 
 // u / d by a multiplication with m = ceil(2^42 / d), for u d < 2^42 (a division by a run-time number takes some 40 cycles
@@ -150,6 +178,7 @@ struct Shared {
   uint2 q[R / 8][D / 16][32];   // Q^T's fragments
   Sight rows[R], all, any;      // of each row, what all of them see, and what at least one does
   float slope[R], fac[R];
+  float lse[R];                 // of a cluster's piece
 };
 
 // Raw codes of 16 tokens: K of tokens g, g + 8 and V of tokens 2c, 2c + 1, 2c + 8, 2c + 9.
@@ -494,6 +523,9 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
     const size_t out = (size_t)(x.q0 + query) * p.Hq + head;
     if (alone) {
       store_row(p, x.q0 + query, head, D, col, acc, lse);
+    } else if (p.cluster > 1) {                        // (in place of the first warp's, which this thread alone has read)
+      *reinterpret_cast<float4*>(scratch + 2 * R + r * D + col) = acc;
+      if (col == 0) sh.lse[r] = lse;
     } else {
       *reinterpret_cast<float4*>(p.o_part + (out * p.num_splits + piece) * D + col) = acc;
       if (col == 0) p.lse_part[out * p.num_splits + piece] = lse;
@@ -561,7 +593,45 @@ __device__ __forceinline__ void join_pieces(const StreamFp8Params& p, const Grou
   }
 }
 
-// The groups' steps in one line, group of rows after group of rows, cut into equal shares, one for Hkv CTAs, which take a KV
+// The group's rows from the pieces of its cluster's CTAs, which share the rows out. A CTA leaves when all have read.
+template <int D, int NT>
+__device__ __forceinline__ void join_cluster(const StreamFp8Params& p, float* scratch, const Shared<D, 8 * NT>& sh, const Group& x,
+                                             int hkv, int rank) {
+  constexpr int C4 = D / 4, T = kWarps<NT> * 32, R = 8 * NT;
+  cluster_sync();
+  for (int idx = rank * T + threadIdx.x; idx < x.rows * C4; idx += p.cluster * T) {
+    const int r = idx / C4, col = (idx - r * C4) * 4;
+    float ls[kMostCluster];
+    float4 a[kMostCluster];
+    float top = kNone;
+#pragma unroll
+    for (int s = 0; s < kMostCluster; ++s)
+      if (s < p.cluster) {
+        ls[s] = peer_float(sh.lse + r, s) * kLog2e;
+        a[s] = peer_float4(scratch + 2 * R + r * D + col, s);
+        top = fmaxf(top, ls[s]);
+      }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMostCluster; ++s)
+      if (s < p.cluster) {
+        const float f = ex2(ls[s] - top);
+        acc.x = fmaf(f, a[s].x, acc.x), acc.y = fmaf(f, a[s].y, acc.y);
+        acc.z = fmaf(f, a[s].z, acc.z), acc.w = fmaf(f, a[s].w, acc.w);
+        sum += f;
+      }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    const int query = quotient(x.r0 + r, p.by_group), head = hkv * p.group + x.r0 + r - query * p.group;
+    store_row(p, x.q0 + query, head, D, col, acc, sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2);
+  }
+  cluster_sync();
+}
+
+// Where the groups are few and not long a cluster of CTAs takes each (cluster_of), their pieces joined through its shared
+// memory, with neither counters to clear nor partials in global memory. Else:
+// the groups' steps in one line, group of rows after group of rows, cut into equal shares, one for Hkv CTAs, which take a KV
 // head each: every SM streams the same number of bytes whatever the sequences' lengths are, and the heads of a page, side
 // by side in memory, are read at about the same time (reading the pages of 8 heads of 128 alone: 58.5 us for 393 MB so,
 // 64 to 66 with head after head). A share is long enough that no group is cut into more than num_splits pieces. A group that lies
@@ -574,6 +644,15 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   __shared__ Group s_x;
   __shared__ int s_sum[W], s_most[W], s_begin, s_v, s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.cluster > 1) {
+    const int rank = cluster_rank(), at = blockIdx.x / p.cluster, v = at / p.Hkv, hkv = at - v * p.Hkv;
+    const Group x = describe<R>(p, v, hkv == 0 && rank == 0 && threadIdx.x == 0);
+    if (x.chunks == 0) return;                         // (as all of the cluster)
+    const int share = (x.chunks + p.cluster - 1) / p.cluster, from = min(rank * share, x.chunks);
+    stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from, min(share, x.chunks - from), 0, false);
+    join_cluster<D, NT>(p, scratch, sh, x, hkv, rank);
+    return;
+  }
   const int V = p.B * p.subs;                          // groups of rows
   // a thread's groups of rows, and the steps before them (the host has made sure that all of them are an int)
   const int per = (V + T - 1) / T;
@@ -660,21 +739,67 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
 template <int D, int NT>
 constexpr int kScratch = kWarps<NT> * 8 * NT * (D + 2) * 4;
 
+// CTAs of a cluster for a group of rows; 1: the line of steps for all of them, joined through global memory. With M the
+// steps that a group may have, a cluster of c takes ceil(M / c) of them per warp, and as many again for every further round
+// of CTAs (two an SM; clusters of 16 find less room); the line takes equal shares (three quarters of M for the mean of several
+// sequences), about four steps for the counters and the joining, and a tenth for every piece. Line and clusters of 2, 4, 8, 16, d = 128:
+// one context of 2000, 4 KV heads 10.9, 11.9, 8.3, 7.1 and 6.2 us, of 30000 22.6, 110, 59, 32.7 and 19.6; four contexts to 6000
+// 15.3, 25.8, 15.4, 11.4 and 15.2; 8 contexts, 8 heads, to 3000 21.0, 16.5 and 13.0, to 32768 77.5, 125, 81.9 and 80.6.
+template <int NT>
+int cluster_of(const StreamFp8Params& p, int sms) {
+  constexpr int kStep = kWarps<NT> * kTogether<NT>;    // chunks that a CTA's warps take at a time
+  const long long groups = (long long)p.B * p.subs * p.Hkv, seqs = (long long)p.B * p.subs;
+  long long pages = p.max_pages;
+  if (p.shape.window > 0)
+    pages = std::min<long long>(pages, ((long long)p.shape.window + p.max_q + p.page_size - 3) / p.page_size + 1 +
+                                           sink_blocks(p.shape.sinks, p.page_size));
+  const double M = (double)(pages * p.page_size / kChunk), line_blocks = std::max(2 * sms / p.Hkv, 1);
+  const double share = std::max((p.B > 1 ? 0.75 : 1.0) * (double)seqs * (M + kTurn) / line_blocks, (double)kStep);
+  double best = share / kStep + 4.0 + 0.1 * std::min(M / share, (double)std::min(p.num_splits, kPieces));
+  int cluster = 1;
+  for (int c = 2; c <= std::min(kMostCluster, p.num_splits); c *= 2) {
+    if (groups * c > 0x3fffffff) break;
+    const int room = c > 8 ? sms : 2 * sms;
+    const double steps = (double)((groups * c + room - 1) / room) * std::ceil(M / (c * kStep));
+    if (steps < best) best = steps, cluster = c;
+  }
+  return cluster;
+}
+
 template <int D, int NT, bool kScores>
-cudaError_t launch_t(const StreamFp8Params& p, cudaStream_t stream) {
+cudaError_t launch_t(const StreamFp8Params& p0, cudaStream_t stream) {
   const int sms = num_sms_current();
   if (sms <= 0) return cudaErrorInvalidValue;
-  const long long groups = (long long)p.B * p.subs * p.Hkv;
-  if (p.num_splits > 1) {
-    const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
-    if (e != cudaSuccess) return e;
-  }
-  const long long blocks = std::min<long long>((long long)p.B * p.subs * p.num_splits, std::max(2 * sms / p.Hkv, 1));
+  StreamFp8Params p = p0;
+  p.cluster = cluster_of<NT>(p, sms);
   auto kern = stream_fp8_kernel<D, NT, kScores>;
   if (kScratch<D, NT> > 40 * 1024) {   // (without asking, 48 KB with the static part)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScratch<D, NT>);
     if (e != cudaSuccess) return e;
   }
+  const long long groups = (long long)p.B * p.subs * p.Hkv;
+  if (p.cluster > 1) {
+    if (p.cluster > 8) {               // (8 is what every launch may have)
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(groups * p.cluster));
+    c.blockDim = dim3(kWarps<NT> * 32);
+    c.dynamicSmemBytes = kScratch<D, NT>;
+    c.stream = stream;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim = {(unsigned)p.cluster, 1, 1};
+    c.attrs = &a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kern, p);
+  }
+  if (p.num_splits > 1) {
+    const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
+    if (e != cudaSuccess) return e;
+  }
+  const long long blocks = std::min<long long>((long long)p.B * p.subs * p.num_splits, std::max(2 * sms / p.Hkv, 1));
   kern<<<(int)(blocks * p.Hkv), kWarps<NT> * 32, kScratch<D, NT>, stream>>>(p);
   return cudaGetLastError();
 }

@@ -265,8 +265,10 @@ fattn_status fattn_rope_append_paged_fp8(const void* q, void* q_out, const void*
 
 /*
  * fattn_decode_paged_fp8 — one query token per sequence over the 8-bit cache: fattn_decode_paged_sinks with its
- * arguments, outputs and workspace (fattn_decode_workspace_size). The thread blocks take equal shares of all sequences' visible tokens;
- * num_splits bounds the pieces that one sequence's tokens of a KV head are cut into (1: none, and no more than 96 are made).
+ * arguments, outputs and workspace (fattn_decode_workspace_size). num_splits bounds the pieces that one sequence's visible
+ * tokens of a KV head are cut into (1: none): up to 16 of equal length where max_pages_per_seq and the window leave little
+ * work, else, up to 96, what makes the thread blocks' shares of all sequences' tokens equal. A table much wider than the
+ * sequences need costs time for short ones.
  * q bf16. Products of q with codes are exact in fp32 sums, weights are rounded to fp16 (11 bits) for the product with V.
  * Equal calls give equal bits. B == 0 is an empty problem. A table entry outside the pool hides its tokens and records
  * FATTN_ERR_DEVICE_CHECK, as do lengths outside the table.

@@ -227,7 +227,9 @@ def test_decode(P, Hq, Hkv, d, lens, cap, sl, window, sinks, any_scale):
         want.append((ref, peaks(f64(q[b:b + 1]), full[b][0], vt, 0.15, cap, sn, vis, n - 1, ref[1])))
         if window:
             table[b, -(-sinks // P):max(n - window, 0) // P] = -5        # what neither touches is not read
-    for S in (1, 2, 7):
+    # (a table with room for long contexts: the sequences' steps shared in one line, else by clusters)
+    wide = torch.nn.functional.pad(table, (0, 8000), value=-1)
+    for S, table in ((1, table), (2, table), (7, table), (16, table), (2, wide), (7, wide), (200, wide)):
         o = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
         lse = torch.full((len(lens), Hq), float("nan"), device="cuda")
         fa.decode_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), table.cuda(), i32(lens).cuda(), S, scale=0.15,
@@ -274,7 +276,8 @@ def test_chunks(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window, sinks, any_scale
         want.append((ref, peaks(x, full[b][0], vt, 0.15, cap, sn, vis, off, ref[1])))
         if window:
             table[b, -(-sinks // 128) * 128 // P:max(off - window + 1, 0) // 128 * 128 // P] = -5
-    for S in (1, 3):
+    wide = [torch.nn.functional.pad(table, (0, 8000), value=-1)] if streamed else []
+    for S, table in ((1, table), (3, table), (9, table), *((S, t) for S in (3, 64) for t in wide)):
         o = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
         lse = torch.full((Hq, T + pad), float("nan"), device="cuda")
         fa.fwd_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), table.cuda(), i32(lk).cuda(), i32(cu).cuda(), max(lq),
@@ -288,6 +291,7 @@ def test_chunks(P, Hq, Hkv, d, lk, lq, causal, cap, sl, window, sinks, any_scale
             else:
                 check_fwd(*mine, want[b][0], f"splits {S} sequence {b}")
         assert torch.isnan(o[T:].float()).all() and torch.isnan(lse[:, T:]).all()
+    table = table[:, :table.shape[1] - 8000 * len(wide)].contiguous()
     again = fa.fwd_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), table.cuda(), i32(lk).cuda(), i32(cu).cuda(),
                              max(lq), causal=causal, scale=0.15, softcap=cap, slopes=None if slopes is None else slopes.cuda(),
                              window=window, sinks=sinks)
@@ -432,10 +436,13 @@ def test_same_results_on_another_stream_and_again():
     q1 = torch.randn(3, 8, 128, generator=g).to(torch.bfloat16).cuda()
     qs = torch.randn(90, 8, 128, generator=g).to(torch.bfloat16).cuda()
     few, many = i32([0, 5, 9, 15]).cuda(), i32([0, 60, 70, 90]).cuda()
+    wide = torch.nn.functional.pad(table, (0, 8000), value=-1)
     side = torch.cuda.Stream()
 
     def calls(stream):
         return [*fa.decode_paged_fp8(q1, kc, vc, ks, vs, table, n, 5, stream=stream),
+                *fa.decode_paged_fp8(q1, kc, vc, ks, vs, wide, n, 50, stream=stream),
+                *fa.fwd_paged_fp8(qs[:15], kc, vc, ks, vs, wide, n, few, 6, stream=stream, num_splits=9),
                 *fa.fwd_paged_fp8(qs[:15], kc, vc, ks, vs, table, n, few, 6, stream=stream),
                 *fa.fwd_paged_fp8(qs, kc, vc, ks, vs, table, n, many, 60, stream=stream, num_splits=2)]
 
@@ -482,3 +489,41 @@ def test_empty_problems_and_graphs_that_share_a_workspace():
     torch.cuda.synchronize()
     assert fa.debug_read_status() == 0
     assert all(torch.equal(a, b) for x, y in zip(want, outs) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("B,window,sinks,extra,lq", [(1000, 64, 4, 0, 1), (1000, 0, 0, 4000, 1), (1000, 0, 0, 0, 3), (700, 0, 0, 4000, 2),
+                                                     (40, 30, 17, 0, 1)])
+def test_many_sequences(B, window, sinks, extra, lq):
+    """More groups of rows than a block has threads, many to a share."""
+    fa = need_gpu()
+    g = torch.Generator().manual_seed(B)
+    P, Hq, Hkv, d = 16, 4, 2, 64
+    lens = [int(n) for n in torch.randint(lq - 1 if lq == 1 else lq, 200, (B,), generator=g)]
+    kc, vc, ks, vs, table, full = pool(g, lens, P, Hkv, d)
+    table = torch.nn.functional.pad(table, (0, extra), value=-1)
+    q = torch.randn(B * lq, Hq, d, generator=g).to(torch.bfloat16)
+    kw = dict(scale=0.15, window=window, sinks=sinks)
+    dev = [t.cuda() for t in (q, kc, vc, ks, vs, table, i32(lens))]
+    for S in (1, 3):
+        if lq == 1:
+            o, lse = fa.decode_paged_fp8(*dev, S, **kw)
+            lse = lse.t()
+        else:
+            o, lse = fa.fwd_paged_fp8(*dev, i32([lq * b for b in range(B + 1)]).cuda(), lq, num_splits=S, **kw)
+        assert fa.debug_read_status() == 0
+        for b in list(range(0, B, 37)) + [B - 1]:
+            n, rows = lens[b], slice(b * lq, (b + 1) * lq)
+            vis = R.window_with_sinks(lq, n, n - lq, True, window, sinks)
+            ref = R.forward(f64(q[rows]), *full[b], 0.15, 0.0, None, vis, n - lq)
+            vt = np.repeat(f64(vs[table[b, :-(-n // P)].long()]), P, 0)[:n]
+            pk = peaks(f64(q[rows]), full[b][0], vt, 0.15, 0.0, None, vis, n - lq, ref[1])
+            check_codes(o[rows], lse[:, rows], ref, pk, n, f"splits {S} sequence {b}")
+        # and all of them against single calls' bits, a sequence at a time
+        for b in range(5, B, 101):
+            one = [q[b * lq:(b + 1) * lq].cuda(), *dev[1:5], table[b:b + 1].cuda(), i32(lens[b:b + 1]).cuda()]
+            if lq == 1:
+                o1, _ = fa.decode_paged_fp8(*one, 1, **kw)
+            else:
+                o1, _ = fa.fwd_paged_fp8(*one, i32([0, lq]).cuda(), lq, num_splits=1, **kw)
+            if S == 1:
+                assert torch.equal(o1, o[b * lq:(b + 1) * lq])
