@@ -46,7 +46,7 @@ __device__ __forceinline__ float2 values2(uint32_t codes) {   // of the low two 
 // point): with q's heads shared out over the pages' blocks, angles were half of the work. A lane has eight elements of a
 // row, both halves of its four pairs among them, so that D / 8 lanes take a row and a warp two or four rows at a time.
 // Bound by the chain lookup - load - maximum - load - store of a block for prompts (6.7k tokens, 32 + 8 heads of 128, 150 MB
-// by the formula: 36 us, 22 at the copy rate; q in the pages' blocks: 85), as for single tokens (64 of them: 7 us).
+// by the formula: 34 us, 22 at the copy rate; q in the pages' blocks: 85), as for single tokens (64 of them: 6.4 us).
 //
 // kFast: 8-byte aligned rows and heads, and pairs that never split a lane's elements; else element by element.
 struct Eight {
@@ -208,20 +208,21 @@ __device__ __forceinline__ void append_q(const AppendFp8Params& p, float2* cs, A
     const int part = it / trips, r = (it - part * trips) * kPer + sub;
     if (r >= n || sh.t[r] < 0) continue;
     const Turn turn = kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{};
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q.in) + (long long)(row0 + r) * p.q.in_row;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q.out) + (long long)(row0 + r) * p.q.out_row;
+    // (pointers that step: a 64-bit product a head is half of what a head costs beside its numbers)
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q.in) + (long long)(row0 + r) * p.q.in_row + part * p.q.in_head;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q.out) + (long long)(row0 + r) * p.q.out_row + part * p.q.out_head;
+    const long long in_step = parts * p.q.in_head, out_step = parts * p.q.out_head;
     for (int h0 = part; h0 < p.q.heads; h0 += kBatch * parts) {
       Raw w[kBatch];                                  // in flight together
+      const __nv_bfloat16* from = src;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (h0 + i * parts < p.q.heads) w[i] = load_raw<kFast>(src + (h0 + i * parts) * p.q.in_head, at);
+      for (int i = 0; i < kBatch; ++i, src += in_step)
+        if (h0 + i * parts < p.q.heads) w[i] = load_raw<kFast>(src, at);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * parts;
-        if (h >= p.q.heads) break;
+      for (int i = 0; i < kBatch; ++i, out += out_step, from += in_step) {
+        if (h0 + i * parts >= p.q.heads) break;
         Eight x = numbers(w[i]);
-        turn_eight<kFast, kInter>(x, turn, src + h * p.q.in_head, sl, p.rot, cs + r * pitch);
-        __nv_bfloat16* out = dst + h * p.q.out_head;
+        turn_eight<kFast, kInter>(x, turn, from, sl, p.rot, cs + r * pitch);
         if constexpr (kFast) {
           *reinterpret_cast<uint2*>(out + at.a) = make_uint2(pack_bf16x2(x.x[0], x.x[1]), pack_bf16x2(x.x[2], x.x[3]));
           *reinterpret_cast<uint2*>(out + at.b) = make_uint2(pack_bf16x2(x.x[4], x.x[5]), pack_bf16x2(x.x[6], x.x[7]));
@@ -299,18 +300,22 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
     const __nv_bfloat16* src = source(u);
     const long long row = key ? p.k.in_row : p.v.in_row;
     const Quads at = key ? turned_at : plain_at;
+    const __nv_bfloat16 *last = src + (n - 1) * row, *next = src + (k0 * kPer + sub) * row;   // (stepping: see the rows of q)
+    const long long step = kPer * row;
     for (int k = k0; k < k1; k += kBatch) {
       Raw w[kBatch];
+      const __nv_bfloat16* from = next;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (k + i < k1) w[i] = load_raw<kFast>(src + min((k + i) * kPer + sub, n - 1) * row, at);
+      for (int i = 0; i < kBatch; ++i, next += step)
+        if (k + i < k1) w[i] = load_raw<kFast>((k + i) * kPer + sub < n ? next : last, at);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
+      for (int i = 0; i < kBatch; ++i, from += step) {
         if (k + i >= k1) break;
         const int r = min((k + i) * kPer + sub, n - 1);
         Eight x = numbers(w[i]);
         if (key)
-          turn_eight<kFast, kInter>(x, kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{}, src + r * row, sl, p.rot, cs + r * pitch);
+          turn_eight<kFast, kInter>(x, kFast ? load_turn(cs + r * pitch, sl, p.rot) : Turn{}, (k + i) * kPer + sub < n ? from : last, sl,
+                                    p.rot, cs + r * pitch);
         use((k + i) * kPer + sub, x);
       }
     }
@@ -362,15 +367,23 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
     const uint32_t bits = __float_as_uint(s);
     const bool pow2 = (bits & 0x7fffffu) == 0, inf = sh.inf[u] != 0;   // (old scales may be others)
     const float inv = __uint_as_float((254u << 23) - bits);            // 1 / s
+    uint8_t* base = slot(u, slot0);
     walk(u, trips * share / shares, trips * (share + 1) / shares, [&](int r, const Eight& x) {
       float y[8];
+      if (pow2) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = pow2 ? x.x[e] * inv : x.x[e] / s;
-        if (inf && fabsf(x.x[e]) > kMaxFloat) y[e] = __int_as_float(0x7fffffff);   // (the conversion would take 448)
+        for (int e = 0; e < 8; ++e) y[e] = x.x[e] * inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x.x[e] / s;
+      }
+      if (inf) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (fabsf(x.x[e]) > kMaxFloat) y[e] = __int_as_float(0x7fffffff);   // (the conversion would take 448)
       }
       if (r < n) {
-        uint8_t* dst = slot(u, slot0 + r);
+        uint8_t* dst = base + (unsigned)r * (unsigned)(p.k.heads * D);   // (a page's bytes are an int)
         *reinterpret_cast<uint32_t*>(dst + at.a) = codes4({y[0], y[1], y[2], y[3]});
         *reinterpret_cast<uint32_t*>(dst + at.b) = codes4({y[4], y[5], y[6], y[7]});
       }
@@ -467,10 +480,11 @@ cudaError_t launch_append_fp8(const AppendFp8Params& p0, int num_sms, cudaStream
   AppendFp8Params p = p0;
   p.page_shift = p.page_size == 16 ? 4 : p.page_size == 32 ? 5 : p.page_size == 64 ? 6 : 7;
   p.pages = p.rows / p.page_size + 2 * p.B;            // blocks of all sequences (some have nothing to do)
-  // KV heads shared out over blocks where the pages are fewer than two blocks an SM, one a block at least, and never more
-  // than a block has room for; q: as many rows a block as leave four blocks an SM
+  // KV heads shared out over blocks where the pages are fewer than two blocks an SM (one where a page gets a token or two:
+  // 64 single tokens 6.4 us, 7.2 with two; prompts 34 with two, 38 with one and with three), one a block at least, and
+  // never more than a block has room for; q: as many rows a block as leave four blocks an SM
   const int pages = std::max(1, std::min(p.pages, p.rows));
-  p.head_shares = std::min(p.k.heads, (2 * num_sms + pages - 1) / pages);
+  p.head_shares = std::min(p.k.heads, ((p.rows > 2 * pages ? 2 : 1) * num_sms + pages - 1) / pages);
   p.head_shares = std::max(p.head_shares, (p.k.heads + kAppendMaxHeads - 1) / kAppendMaxHeads);
   p.q_rows = std::max(1, std::min(kAppendRows, p.rows / (4 * num_sms)));
   const int half = p.rot / 2, pitch = (half + 1) & ~1;
