@@ -211,7 +211,9 @@ def peaks(q, k, vscale, scale, cap, slopes, vis, off, lse):
     (32, 8, 2, 128, [2500, 300, 64], 0.0, False, 64, 4, False),
     (16, 5, 5, 64, [1900, 640, 641], 0.0, True, 128, 64, True),
     (128, 9, 1, 128, [2000, 1], 0.0, False, 1, 1, False),
-    (64, 2, 2, 64, [3001], 5.0, False, 700, 200, False)])
+    (64, 2, 2, 64, [3001], 5.0, False, 700, 200, False),
+    (16, 72, 1, 128, [500, 0, 33], 0.0, False, 0, 0, False),            # groups of 24 rows of one query
+    (32, 80, 2, 64, [1200, 31], 25.0, True, 90, 10, True)])
 def test_decode(P, Hq, Hkv, d, lens, cap, sl, window, sinks, any_scale):
     fa = need_gpu()
     g = torch.Generator().manual_seed(P + Hq)
