@@ -731,8 +731,10 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
     }
     begin = zero + x.chunks;
     if (begin >= stop) break;
-    do x = describe<R>(p, ++v, false);
-    while (x.chunks == 0);
+    do {
+      if (++v >= V) return;                            // (only if the lengths change under the kernel)
+      x = describe<R>(p, v, false);
+    } while (x.chunks == 0);
   }
 }
 
