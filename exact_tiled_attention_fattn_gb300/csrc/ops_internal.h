@@ -139,7 +139,7 @@ struct StreamFp8Params {
   long long lse_head, lse_row;
   float* lse_part;            // [rows, Hq, S]
   float* o_part;              // [rows, Hq, S, d]
-  int* counters;              // work counter, then one arrival counter per group of rows
+  int* counters;              // arrivals, one counter per group of rows and KV head
   int B, Hq, Hkv, d, page_size, max_pages, num_pages, num_splits;
   int rows, max_q, causal;
   float scale;
@@ -147,7 +147,7 @@ struct StreamFp8Params {
   int* status;
   // set by the launch: heads of a KV head, groups of rows of a sequence, their reciprocals, log2 of the page size
   int group, subs, page_shift;
-  int cluster;                // CTAs of a cluster that share a group of rows; 1: the groups' line is shared
+  int cluster;                // CTAs of a cluster that share a group of rows; 0: the groups' line is shared
   unsigned long long by_group, by_subs;
 };
 

@@ -629,8 +629,8 @@ __device__ __forceinline__ void join_cluster(const StreamFp8Params& p, float* sc
   cluster_sync();
 }
 
-// Where the groups are few and not long a cluster of CTAs takes each (cluster_of), their pieces joined through its shared
-// memory, with neither counters to clear nor partials in global memory. Else:
+// Where the groups are short, or few and not long, a cluster of CTAs (or one) takes each (cluster_of), their pieces joined
+// through its shared memory, with neither counters to clear nor partials in global memory. Else:
 // the groups' steps in one line, group of rows after group of rows, cut into equal shares, one for Hkv CTAs, which take a KV
 // head each: every SM streams the same number of bytes whatever the sequences' lengths are, and the heads of a page, side
 // by side in memory, are read at about the same time (reading the pages of 8 heads of 128 alone: 58.5 us for 393 MB so,
@@ -644,13 +644,13 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   __shared__ Group s_x;
   __shared__ int s_sum[W], s_most[W], s_begin, s_v, s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (p.cluster > 1) {
-    const int rank = cluster_rank(), at = blockIdx.x / p.cluster, v = at / p.Hkv, hkv = at - v * p.Hkv;
+  if (p.cluster > 0) {
+    const int rank = p.cluster > 1 ? cluster_rank() : 0, at = blockIdx.x / p.cluster, v = at / p.Hkv, hkv = at - v * p.Hkv;
     const Group x = describe<R>(p, v, hkv == 0 && rank == 0 && threadIdx.x == 0);
     if (x.chunks == 0) return;                         // (as all of the cluster)
     const int share = (x.chunks + p.cluster - 1) / p.cluster, from = min(rank * share, x.chunks);
-    stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from, min(share, x.chunks - from), 0, false);
-    join_cluster<D, NT>(p, scratch, sh, x, hkv, rank);
+    stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from, min(share, x.chunks - from), 0, p.cluster == 1);
+    if (p.cluster > 1) join_cluster<D, NT>(p, scratch, sh, x, hkv, rank);
     return;
   }
   const int V = p.B * p.subs;                          // groups of rows
@@ -681,18 +681,15 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
     total += s_sum[w];
     most = max(most, s_most[w]);
   }
-  // equal shares in whole rounds of the warps; one piece a group: the groups that begin in the share, whole
-  const bool whole = p.num_splits == 1;
   const unsigned splits = min(p.num_splits, kPieces);
   const unsigned block = blockIdx.x / p.Hkv, blocks = gridDim.x / p.Hkv;
   const int hkv = blockIdx.x - block * p.Hkv;
   unsigned share = ((unsigned)total + blocks - 1) / blocks;
-  if (!whole) share = max(share, ((unsigned)most + splits - 2) / (splits - 1));
+  share = max(share, ((unsigned)most + splits - 2) / (splits - 1));
   share = max(share, (unsigned)(Y * W));               // (a step for every warp)
   if ((unsigned long long)share * block >= total) return;
   int at = (int)(share * block);                       // in steps
   const int stop = (int)min((unsigned long long)share * (block + 1ull), (unsigned long long)total);
-  const int end = whole ? total : stop;
   if (at >= before && at < before + sum) {
     int y = before;
     for (int v = mine0; v < mine1; ++v) {
@@ -712,10 +709,10 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   x = s_x;
   for (;;) {
     const int zero = begin + kTurn;                    // of its first chunk
-    const int from = whole ? (at <= begin ? zero : zero + x.chunks) : max(at, zero), to = min(end, zero + x.chunks);
+    const int from = max(at, zero), to = min(stop, zero + x.chunks);
     if (from < to) {
       const int c0 = (unsigned)zero / share, c1 = (unsigned)(zero + x.chunks - 1) / share;
-      const int pieces = whole ? 1 : c1 - c0 + 1;
+      const int pieces = c1 - c0 + 1;
       stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from - zero, to - from, (int)block - c0, pieces == 1);
       if (pieces > 1) {
         __syncthreads();                               // the partial is written
@@ -741,14 +738,16 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
 template <int D, int NT>
 constexpr int kScratch = kWarps<NT> * 8 * NT * (D + 2) * 4;
 
-// CTAs of a cluster for a group of rows; 1: the line of steps for all of them, joined through global memory. With M the
-// steps that a group may have, a cluster of c takes ceil(M / c) of them per warp, and as many again for every further round
-// of CTAs (two an SM; clusters of 16 find less room); the line takes equal shares (three quarters of M for the mean of several
-// sequences), about four steps for the counters and the joining, and a tenth for every piece. Line and clusters of 2, 4, 8, 16, d = 128:
-// one context of 2000, 4 KV heads 10.9, 11.9, 8.3, 7.1 and 6.2 us, of 30000 22.6, 110, 59, 32.7 and 19.6; four contexts to 6000
-// 15.3, 25.8, 15.4, 11.4 and 15.2; 8 contexts, 8 heads, to 3000 21.0, 16.5 and 13.0, to 32768 77.5, 125, 81.9 and 80.6.
+// CTAs of a cluster for a group of rows; 0: the line of steps for all of them, joined through global memory. With M the steps
+// that a group may have, a cluster of c takes ceil(M / c) of them per warp, two to begin with and one to join, and about as many
+// again for every further round of CTAs (two an SM; clusters of 16 find less room); the line takes equal shares (0.85 M for the
+// mean of several sequences), about eight steps for the counters and the joining, and a tenth for every piece.
+// The line and clusters of 1, 2, 4, 8, 16, d = 128: one context of 2000, 4 KV heads 12.3, 17.5, 12.3, 8.4, 7.2 and 6.3 us, of
+// 30000 22.7, 216, 113, 62, 34.6 and 20.4; 8 contexts, 8 heads, to 3000 21.4, 27.2, 17.2 and 13.2, to 32768 77.3, 240, 126, 81.9
+// and 81.0; 64 contexts of 1000, 8 heads 39.0, 30.5, 41.7 and 59.5.
 template <int NT>
 int cluster_of(const StreamFp8Params& p, int sms) {
+  if (p.num_splits == 1) return 1;
   constexpr int kStep = kWarps<NT> * kTogether<NT>;    // chunks that a CTA's warps take at a time
   const long long groups = (long long)p.B * p.subs * p.Hkv, seqs = (long long)p.B * p.subs;
   long long pages = p.max_pages;
@@ -756,14 +755,15 @@ int cluster_of(const StreamFp8Params& p, int sms) {
     pages = std::min<long long>(pages, ((long long)p.shape.window + p.max_q + p.page_size - 3) / p.page_size + 1 +
                                            sink_blocks(p.shape.sinks, p.page_size));
   const double M = (double)(pages * p.page_size / kChunk), line_blocks = std::max(2 * sms / p.Hkv, 1);
-  const double share = std::max((p.B > 1 ? 0.75 : 1.0) * (double)seqs * (M + kTurn) / line_blocks, (double)kStep);
-  double best = share / kStep + 4.0 + 0.1 * std::min(M / share, (double)std::min(p.num_splits, kPieces));
-  int cluster = 1;
-  for (int c = 2; c <= std::min(kMostCluster, p.num_splits); c *= 2) {
-    if (groups * c > 0x3fffffff) break;
+  const int splits = std::min(p.num_splits, kPieces);
+  const double share = std::max({(p.B > 1 ? 0.85 : 1.0) * (double)seqs * (M + kTurn) / line_blocks, M / (splits - 1), (double)kStep});
+  double best = share / kStep + 8.0 + 0.1 * M / share;
+  int cluster = 0;
+  for (int c = 1; c <= std::min(kMostCluster, p.num_splits); c *= 2) {
     const int room = c > 8 ? sms : 2 * sms;
-    const double steps = (double)((groups * c + room - 1) / room) * std::ceil(M / (c * kStep));
-    if (steps < best) best = steps, cluster = c;
+    const long long rounds = (groups * c + room - 1) / room;
+    const double steps = (rounds == 1 ? 1.0 : 0.95 * (double)rounds) * (std::ceil(M / (c * kStep)) + 2) + (c > 1 ? 1 : 0);
+    if (groups * c <= 0x3fffffff && steps < best) best = steps, cluster = c;
   }
   return cluster;
 }
@@ -780,7 +780,7 @@ cudaError_t launch_t(const StreamFp8Params& p0, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const long long groups = (long long)p.B * p.subs * p.Hkv;
-  if (p.cluster > 1) {
+  if (p.cluster > 0) {
     if (p.cluster > 8) {               // (8 is what every launch may have)
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
@@ -797,10 +797,8 @@ cudaError_t launch_t(const StreamFp8Params& p0, cudaStream_t stream) {
     c.numAttrs = 1;
     return cudaLaunchKernelEx(&c, kern, p);
   }
-  if (p.num_splits > 1) {
-    const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = cudaMemsetAsync(p.counters, 0, (size_t)groups * sizeof(int), stream);
+  if (e != cudaSuccess) return e;
   const long long blocks = std::min<long long>((long long)p.B * p.subs * p.num_splits, std::max(2 * sms / p.Hkv, 1));
   kern<<<(int)(blocks * p.Hkv), kWarps<NT> * 32, kScratch<D, NT>, stream>>>(p);
   return cudaGetLastError();
