@@ -563,7 +563,8 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
       ((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || B > 65535 ||
       stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits)
     return FATTN_ERR_UNSUPPORTED;
-  if (streams_fp8(max_seqlen_q, Hq / Hkv) && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size)) return FATTN_ERR_UNSUPPORTED;
+  if (streams_fp8(max_seqlen_q, Hq / Hkv) && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size))
+    return FATTN_ERR_UNSUPPORTED;
   const ChunkWorkspace w =
       chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits);
   if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;
@@ -591,6 +592,6 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
   if (launch_expand_fp8(e, stream) != cudaSuccess) return FATTN_ERR_CUDA;
   const bool plain = p.shape.cap == 0.f && !p.shape.slopes && p.shape.window == 0 && num_splits == 1;
   return fwd_paged_impl(q, e.kout, e.vout, e.table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
-                        max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale, plain ? nullptr : &p.shape, num_splits,
-                        num_splits > 1 ? ws + w.splits : nullptr, num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
+                        max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale,
+                        plain ? nullptr : &p.shape, num_splits, num_splits > 1 ? ws + w.splits : nullptr, num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
 }

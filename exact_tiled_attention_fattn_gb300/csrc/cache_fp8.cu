@@ -91,7 +91,9 @@ __device__ __forceinline__ Raw load_raw(const __nv_bfloat16* p, const Quads& at)
   if constexpr (kFast) return {__ldg(reinterpret_cast<const uint2*>(p + at.a)), __ldg(reinterpret_cast<const uint2*>(p + at.b))};
   Raw r;
   const __nv_bfloat16* q = p + at.a;                  // (eight in a row)
-  auto two = [&](int k) -> uint32_t { return (uint32_t)__bfloat16_as_ushort(q[k]) | (uint32_t)__bfloat16_as_ushort(q[k + 1]) << 16; };
+  auto two = [&](int k) -> uint32_t {
+    return (uint32_t)__bfloat16_as_ushort(q[k]) | (uint32_t)__bfloat16_as_ushort(q[k + 1]) << 16;
+  };
   r.a = make_uint2(two(0), two(2));
   r.b = make_uint2(two(4), two(6));
   return r;

@@ -8,9 +8,9 @@
 // A warp streams tokens 16 at a time straight from global memory into registers: the codes are laid out as the tensor-core
 // fragments want them, so that shared memory, shuffles of the cache and transposes are not needed. The next step's K is
 // loaded while this one's softmax and V are worked on, its V brought to the L2 cache. (Through shared memory by
-// cp.async, three stages, 16 warps an SM: 91 us for the first case above.) Both products are taken transposed, with tokens (K) and head
-// elements (V) as the 16 rows of mma.sync m16n8k16 and up to 8 query rows as its columns, which is what a group of heads
-// gives, where a tile of tcgen05.mma would have 128 rows for them and its operands in shared memory:
+// cp.async, three stages, 16 warps an SM: 91 us for the first case above.) Both products are taken transposed, with tokens
+// (K) and head elements (V) as the 16 rows of mma.sync m16n8k16 and up to 8 query rows as its columns, which is what a group
+// of heads gives, where a tile of tcgen05.mma would have 128 rows for them and its operands in shared memory:
 //   S^T = K Q^T   lane (g, c) holds tokens g and g + 8: 16 consecutive codes of each are the A fragments of four steps, if
 //                 the head's elements are taken in the order in which they lie there (Q^T is permuted alike);
 //   O^T = V^T P^T lane (g, c) holds the codes 16 g .. 16 g + 15 of tokens 2c, 2c + 1, 2c + 8 and 2c + 9: pairs of tokens
@@ -42,8 +42,8 @@ template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
 // What going from one group to the next costs a CTA, in chunks: it counts in the shares.
 constexpr int kTurn = 16;
-// Pieces of a group in the line at most: one CTA joins them, a round of loads for about ten of them (one context of 199k tokens, one KV
-// head: 45 us in 304 pieces).
+// Pieces of a group in the line at most: one CTA joins them, a round of loads for some of them (one context of 199k tokens,
+// one KV head: 34.9 us, 36.3 in 160 pieces, 41.2 in 304).
 constexpr int kPieces = 96;
 constexpr int kMostCluster = 16;  // CTAs of a cluster
 constexpr int kChunk = 16;       // tokens of a step
@@ -756,7 +756,8 @@ int cluster_of(const StreamFp8Params& p, int sms) {
                                            sink_blocks(p.shape.sinks, p.page_size));
   const double M = (double)(pages * p.page_size / kChunk), line_blocks = std::max(2 * sms / p.Hkv, 1);
   const int splits = std::min(p.num_splits, kPieces);
-  const double share = std::max({(p.B > 1 ? 0.85 : 1.0) * (double)seqs * (M + kTurn) / line_blocks, M / (splits - 1), (double)kStep});
+  const double mean = p.B > 1 ? 0.85 : 1.0;
+  const double share = std::max({mean * (double)seqs * (M + kTurn) / line_blocks, M / (splits - 1), (double)kStep});
   double best = share / kStep + 8.0 + 0.1 * M / share;
   int cluster = 0;
   for (int c = 1; c <= std::min(kMostCluster, p.num_splits); c *= 2) {
