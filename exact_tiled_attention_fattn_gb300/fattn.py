@@ -144,6 +144,17 @@ def _scratch(need: int, device, stream):
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
 
 
+def _packed(t, stream):
+    """t, or where its strides leave gaps or another order a contiguous copy, made on the stream that the call runs on
+    and in that stream's memory (as ``_scratch``)."""
+    if t.is_contiguous():
+        return t
+    if stream is None:
+        return t.contiguous()
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
 def _ptr(t):
     """Address for a c_void_p argument (an int: ctypes converts it without an object of its own)."""
     return None if t is None else t.data_ptr()
@@ -387,9 +398,11 @@ def bwd_workspace_size(B: int, Hq: int, N: int) -> int:
 def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, dq=None, dk=None, dv=None,
         workspace=None, stream=None):
     """Attention backward. q, o, dout [B,N,Hq,d], k, v [B,N,Hkv,d] bf16; lse [B,Hq,N] fp32 from
-    ``fwd`` on the same inputs. Returns (dq, dk, dv) in the input layouts (bf16)."""
+    ``fwd`` on the same inputs. o and dout may be any views (transposed heads, an expanded gradient): one that is not
+    contiguous is copied within the call. Returns (dq, dk, dv) in the input layouts (bf16)."""
     lib = load_library()
-    _need_cuda(q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    _need_cuda(q, k, v, lse, dq, dk, dv, workspace)
+    _need_cuda(o, dout, contiguous=False)
     if not (q.dtype == k.dtype == v.dtype == o.dtype == dout.dtype == torch.bfloat16):
         raise TypeError("backward takes bf16 q, k, v, o and dout")
     if q.dim() != 4 or k.dim() != 4:
@@ -412,6 +425,7 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     need = bwd_workspace_size(B, Hq, N)
     if workspace is None:
         workspace = _scratch(need, q.device, stream)
+    o, dout = _packed(o, stream), _packed(dout, stream)
     st = lib.fattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                        B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), _ptr(workspace),
                        workspace.numel() * workspace.element_size(), _stream_handle(stream))
@@ -939,9 +953,11 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
                slopes=None, window: int = 0, key_begin=None, key_end=None, dq=None, dk=None, dv=None, workspace=None,
                stream=None, sinks: int = 0):
     """Gradients of ``fwd_shaped`` (same arguments; o and lse are its outputs) with respect to q, k and v;
-    the slopes are constants. ``workspace``: bwd_shaped_workspace_size bytes, with sinks bwd_sinks_workspace_size. Returns (dq, dk, dv), bf16 in the input layouts."""
+    the slopes are constants. o and dout may be any views, as in ``bwd``. ``workspace``: bwd_shaped_workspace_size bytes, with
+    sinks bwd_sinks_workspace_size. Returns (dq, dk, dv), bf16 in the input layouts."""
     lib = load_library()
-    _need_cuda(q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    _need_cuda(q, k, v, lse, dq, dk, dv, workspace)
+    _need_cuda(o, dout, contiguous=False)
     if not (q.dtype == k.dtype == v.dtype == o.dtype == dout.dtype == torch.bfloat16):
         raise TypeError("backward takes bf16 q, k, v, o and dout")
     if q.dim() != 4 or k.dim() != 4:
@@ -967,6 +983,7 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
         need = (bwd_sinks_workspace_size(B, Hq, Hkv, N, d, causal, window, sinks) if sinks else
                 bwd_shaped_workspace_size(B, Hq, Hkv, N, d))
         workspace = _scratch(need, q.device, stream)
+    o, dout = _packed(o, stream), _packed(dout, stream)
     head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
             1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
