@@ -47,6 +47,7 @@ constexpr int kTurn = 16;
 constexpr int kPieces = 96;
 constexpr int kMostCluster = 16;  // CTAs of a cluster
 constexpr int kChunk = 16;       // tokens of a step
+constexpr int kZeros = -2;       // page of tokens whose K and V are zeros
 constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
 constexpr float kLazy = 8.f;     // log2 units that scores may exceed the running maximum by
 
@@ -190,7 +191,8 @@ template <int D>
 struct VCodes {
   uint32_t w[4][D / 32];
 };
-// What a warp knows of 32 chunks, one per lane: the chunk's page (-1: none) and first row in the pool, and its page's
+// What a warp knows of 32 chunks, one per lane: the chunk's page (-1: none, its tokens are hidden; kZeros: a chunk of queries
+// met a table entry outside the pool, whose tokens are zeros, as for the prefill) and first row in the pool, and its page's
 // scales. It is asked for in two trips, each many steps before it is used: the table's entry, then the scales.
 struct Meta {
   int page, row;
@@ -223,8 +225,9 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
   auto scales = [&](Meta& m, int i0) {
     const int i = i0 + lane / Y, y = lane % Y, t = token(i, y);
     if (m.page < 0 || m.page >= p.num_pages) {
-      if (i < n_mine && number(i, y) < nchunks && t < x.L) record_status(p.status, kStatusDeviceCheck);
-      m.page = -1;
+      const bool mine = i < n_mine && number(i, y) < nchunks && t < x.L;
+      if (mine) record_status(p.status, kStatusDeviceCheck);
+      m.page = mine && p.cu_seqlens ? kZeros : -1;
     }
     const size_t at = (size_t)max(m.page, 0) * p.Hkv + hkv;
     m.row = m.page < 0 ? 0 : (m.page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
@@ -384,7 +387,8 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
       const int from = (i % kBatch) * Y + y;
-      const bool none = __shfl_sync(0xffffffffu, meta.page, from) < 0;
+      const int page = __shfl_sync(0xffffffffu, meta.page, from);
+      const bool none = page < 0;
       const float ks = __shfl_sync(0xffffffffu, meta.ks, from), lv = __shfl_sync(0xffffffffu, lv_of, from);
       ivs[y] = __shfl_sync(0xffffffffu, iv_of, from);
       const int t0 = token(i, y);
@@ -416,8 +420,11 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (none || !sh.rows[8 * n + 2 * c + (k & 1)].sees(t0 + g + 8 * (k >> 1))) s[y][n][k] = -CUDART_INF_F;
+          for (int k = 0; k < 4; ++k) {
+            const int r = 8 * n + 2 * c + (k & 1), t = t0 + g + 8 * (k >> 1);
+            if (page == kZeros) s[y][n][k] = sh.slope[r] * fabsf((float)(sh.rows[r].pos - t));   // (a score of 0, biased)
+            if (page == -1 || !sh.rows[r].sees(t)) s[y][n][k] = -CUDART_INF_F;
+          }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (none || !sh.any.sees(t0 + 2 * c + (k & 1) + 8 * (k >> 1))) {

@@ -295,6 +295,8 @@ size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int pag
  * bf16 (exact for scales that are powers of two, else one rounding) in the workspace and read by the tensor-core prefill.
  * num_splits >= 1: the pieces at most of a group of up to 32 streamed rows, or the prefill's splits. workspace: 256-byte
  * aligned, contents ignored, always needed.
+ * A table entry outside the pool is recorded as FATTN_ERR_DEVICE_CHECK and, as in fattn_fwd_paged, its tokens read as zeros
+ * (K and V, so a score of 0 before the distance bias), whichever way the rows take; single tokens do not see them.
  * Errors: those of fattn_fwd_paged_sinks and of the cache; UNSUPPORTED also for (B * max_pages_per_seq + 1) * page_size
  *   >= 2^31.
  */
