@@ -168,15 +168,6 @@ struct BwdParams {
   int debug_stall;
 };
 
-// The shaped backward's dK/dV pass per query head, its fp32 shares added up afterwards, or per KV head, the group's heads
-// one after the other in an item. Room for the shares is asked for (bwd_shares) where there are no more (key tile, KV
-// head) items than the whole chip has SMs, a constant, as the workspace's size knows no device; bwd_per_head then weighs,
-// for the SMs that there are and in steps of 128 queries (about 1.2 us), the longest item or the SMs' mean against the same with single heads, the shares' way through memory and the
-// launch that adds them. A key tile is seen from all query tiles, at a mean half of them with causal, from a window's, and
-// with key ranges, which the host does not know, from a quarter.
-// Whole calls, causal, per KV head and per query head, d = 128 unless said: 997 rows, 8 heads over 2, d = 64 87 and 51 us; 2048
-// rows, 32 over 8 188 and 159 us (a window of 512: 97 and 119 us); 8192 rows, 32 over 1, d = 64 4059 and 1533 us; 4096
-// rows, 32 over 8 (256 items) 437 and 484 us.
 // Pieces that the key tiles of the sinks are cut into: of about as many query tiles as see any other key tile (for the
 // dK/dV pass one item of them all is the longest by far: N = 32768, window 1024, 32 heads over 8, d = 128 2916 us
 // against 974 without sinks), at least one query tile each; their shares are kept to 128 tiles.
@@ -189,6 +180,17 @@ inline int bwd_sink_pieces(int N, int causal, int window, int sinks) {
   if (P > nt - S) P = nt - S;
   return P > 1 ? P : 1;
 }
+
+// The shaped backward's dK/dV pass per query head, its fp32 shares added up afterwards, or per KV head, the group's heads
+// one after the other in an item. Room for the shares is asked for (bwd_shares) where there are no more (key tile, KV
+// head) items than the whole chip has SMs, a constant, as the workspace's size knows no device; bwd_per_head then weighs,
+// for the SMs that there are and in steps of 128 queries (about 1.2 us), the longest item or the SMs' mean against the same with single heads, the shares' way through memory and the
+// launch that adds them. A key tile is seen from all query tiles, at a mean half of them with causal, from a window's, and
+// with key ranges, which the host does not know, from a quarter. The sinks' tiles beside a window are seen from all and cut into
+// pieces, which may be far longer than the other items: there are at most 32 of a tile, and fewer the more tiles the sinks have.
+// Whole calls, causal, per KV head and per query head, d = 128 unless said: 997 rows, 8 heads over 2, d = 64 87 and 51 us; 2048
+// rows, 32 over 8 188 and 159 us (a window of 512: 97 and 119 us); 8192 rows, 32 over 1, d = 64 4059 and 1533 us; 4096
+// rows, 32 over 8 (256 items) 437 and 484 us.
 constexpr long long kPerHeadItems = 152;
 inline bool bwd_shares(int B, int Hq, int Hkv, int N) {
   return Hq > Hkv && (long long)B * Hkv * (((long long)N + 127) / 128) <= kPerHeadItems;
@@ -199,11 +201,16 @@ inline bool bwd_per_head(const BwdParams& p, int num_sms) {
   double most = nt, mean = p.causal ? (nt + 1) / 2 : nt;
   if (p.shape.window > 0) {
     const double seen = (p.causal ? 1.0 : 2.0) * p.shape.window / 128 + 1;
-    if (seen < most) most = seen;   // (the sinks' tiles, seen from all query tiles, are cut into pieces of about that)
+    if (seen < most) most = seen;
   }
   if ((p.shape.key_begin || p.shape.key_end) && most > nt / 4) most = nt / 4 > 1 ? nt / 4 : 1;
   if (mean > most) mean = most;
-  const double all = items * G * mean / num_sms;
+  double all = items * G * mean / num_sms;
+  if (p.shape.window > 0 && p.sink_tiles > 0) {
+    const double piece = nt / p.sink_pieces;
+    if (piece > most) most = piece;
+    all += p.B * p.Hq * (p.sink_tiles * (p.causal ? nt - 0.5 * p.sink_tiles : nt)) / num_sms;
+  }
   const double join = 2 + 2.0 * p.B * p.N * p.Hq * p.d * 1.3e-6;   // 8 bytes an element, 5 TB/s
   return (most > all ? most : all) + join < (G * most > all ? G * most : all);
 }
