@@ -5,6 +5,9 @@
 #include "fattn_ops.h"
 #include "fattn_internal.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace fattn {
 
 // One tensor that rotary positions read and write: heads of `heads` x d elements per
@@ -160,6 +163,42 @@ inline int stream_fp8_rows(long long max_rows) {
 inline long long stream_fp8_groups(int B, int Hkv, long long max_rows) {
   const int r = stream_fp8_rows(max_rows);
   return (long long)B * Hkv * ((max_rows + r - 1) / r);
+}
+// What going from one group to the next costs a CTA, in chunks of 16 tokens: it counts in the shares.
+constexpr int kStreamTurn = 16;
+// Pieces of a group in the line at most: one CTA joins them, a round of loads for some of them (one context of 199k tokens,
+// one KV head: 34.9 us, 36.3 in 160 pieces, 41.2 in 304).
+constexpr int kStreamPieces = 96;
+constexpr int kStreamMostCluster = 16;   // CTAs of a cluster
+// CTAs of a cluster for a group of rows, at most `most`; 0: the line of steps for all of them, joined through global memory.
+// With M the steps that a group may have, a cluster of c takes ceil(M / c) of them per warp (`step`: chunks that a CTA's warps
+// take at a time), two to begin with and one to join, and about as many again for every further round of CTAs (two an SM;
+// clusters of 16 find less room); the line takes equal shares (0.85 M for the mean of several sequences), about eight steps for
+// the counters and the joining, and a tenth for every piece.
+// The line and clusters of 1, 2, 4, 8, 16, d = 128: one context of 2000, 4 KV heads 12.3, 17.5, 12.3, 8.4, 7.2 and 6.3 us, of
+// 30000 22.7, 216, 113, 62, 34.6 and 20.4; 8 contexts, 8 heads, to 3000 21.4, 27.2, 17.2 and 13.2, to 32768 77.3, 240, 126, 81.9
+// and 81.0; 64 contexts of 1000, 8 heads 39.0, 30.5, 41.7 and 59.5.
+inline int stream_fp8_cluster(const StreamFp8Params& p, int step, int sms, int most) {
+  if (p.num_splits == 1) return 1;
+  const long long groups = (long long)p.B * p.subs * p.Hkv, seqs = (long long)p.B * p.subs;
+  long long pages = p.max_pages;
+  if (p.shape.window > 0) {   // (without causal on both sides of the queries)
+    const long long tokens = (p.causal ? 1ll : 2ll) * p.shape.window + p.max_q;
+    pages = std::min<long long>(pages, (tokens + p.page_size - 3) / p.page_size + 1 + sink_blocks(p.shape.sinks, p.page_size));
+  }
+  const double M = (double)(pages * p.page_size / 16), line_blocks = std::max(2 * sms / p.Hkv, 1);
+  const int splits = std::min(p.num_splits, kStreamPieces);
+  const double mean = p.B > 1 ? 0.85 : 1.0;
+  const double share = std::max({mean * (double)seqs * (M + kStreamTurn) / line_blocks, M / (splits - 1), (double)step});
+  double best = share / step + 8.0 + 0.1 * M / share;
+  int cluster = 0;
+  for (int c = 1; c <= std::min(most, p.num_splits); c *= 2) {
+    const int room = c > 8 ? sms : 2 * sms;
+    const long long rounds = (groups * c + room - 1) / room;
+    const double steps = (rounds == 1 ? 1.0 : 0.95 * (double)rounds) * (std::ceil(M / ((double)c * step)) + 2) + (c > 1 ? 1 : 0);
+    if (groups * c <= 0x3fffffff && steps < best) best = steps, cluster = c;
+  }
+  return cluster;
 }
 // Whether a chunk goes to the streaming kernel. Its time grows with the rows (2 x 30000 tokens, 8 KV heads of 128: 1.0 us a
 // row), the other way's with the query heads, whose tiles have room for 256 queries (44 us for each of a KV head), and the

@@ -29,7 +29,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
-#include <cmath>
+#include <atomic>
 
 namespace fattn {
 namespace {
@@ -40,12 +40,8 @@ constexpr int kWarps = NT <= 2 ? 6 : 4;
 // Chunks of 16 tokens that a warp works on together.
 template <int NT>
 constexpr int kTogether = NT == 1 ? 2 : 1;
-// What going from one group to the next costs a CTA, in chunks: it counts in the shares.
-constexpr int kTurn = 16;
-// Pieces of a group in the line at most: one CTA joins them, a round of loads for some of them (one context of 199k tokens,
-// one KV head: 34.9 us, 36.3 in 160 pieces, 41.2 in 304).
-constexpr int kPieces = 96;
-constexpr int kMostCluster = 16;  // CTAs of a cluster
+constexpr int kTurn = kStreamTurn, kPieces = kStreamPieces;
+constexpr int kMostCluster = kStreamMostCluster;   // CTAs of a cluster
 constexpr int kChunk = 16;       // tokens of a step
 constexpr int kZeros = -2;       // page of tokens whose K and V are zeros
 constexpr float kNone = -3.0e38f;  // no maximum yet: finite, so that hidden scores give 2^(-inf) = 0 against it
@@ -636,7 +632,7 @@ __device__ __forceinline__ void join_cluster(const StreamFp8Params& p, float* sc
   cluster_sync();
 }
 
-// Where the groups are short, or few and not long, a cluster of CTAs (or one) takes each (cluster_of), their pieces joined
+// Where the groups are short, or few and not long, a cluster of CTAs (or one) takes each (stream_fp8_cluster), their pieces joined
 // through its shared memory, with neither counters to clear nor partials in global memory. Else:
 // the groups' steps in one line, group of rows after group of rows, cut into equal shares, one for Hkv CTAs, which take a KV
 // head each: every SM streams the same number of bytes whatever the sequences' lengths are, and the heads of a page, side
@@ -745,35 +741,32 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
 template <int D, int NT>
 constexpr int kScratch = kWarps<NT> * 8 * NT * (D + 2) * 4;
 
-// CTAs of a cluster for a group of rows; 0: the line of steps for all of them, joined through global memory. With M the steps
-// that a group may have, a cluster of c takes ceil(M / c) of them per warp, two to begin with and one to join, and about as many
-// again for every further round of CTAs (two an SM; clusters of 16 find less room); the line takes equal shares (0.85 M for the
-// mean of several sequences), about eight steps for the counters and the joining, and a tenth for every piece.
-// The line and clusters of 1, 2, 4, 8, 16, d = 128: one context of 2000, 4 KV heads 12.3, 17.5, 12.3, 8.4, 7.2 and 6.3 us, of
-// 30000 22.7, 216, 113, 62, 34.6 and 20.4; 8 contexts, 8 heads, to 3000 21.4, 27.2, 17.2 and 13.2, to 32768 77.3, 240, 126, 81.9
-// and 81.0; 64 contexts of 1000, 8 heads 39.0, 30.5, 41.7 and 59.5.
-template <int NT>
-int cluster_of(const StreamFp8Params& p, int sms) {
-  if (p.num_splits == 1) return 1;
-  constexpr int kStep = kWarps<NT> * kTogether<NT>;    // chunks that a CTA's warps take at a time
-  const long long groups = (long long)p.B * p.subs * p.Hkv, seqs = (long long)p.B * p.subs;
-  long long pages = p.max_pages;
-  if (p.shape.window > 0)
-    pages = std::min<long long>(pages, ((long long)p.shape.window + p.max_q + p.page_size - 3) / p.page_size + 1 +
-                                           sink_blocks(p.shape.sinks, p.page_size));
-  const double M = (double)(pages * p.page_size / kChunk), line_blocks = std::max(2 * sms / p.Hkv, 1);
-  const int splits = std::min(p.num_splits, kPieces);
-  const double mean = p.B > 1 ? 0.85 : 1.0;
-  const double share = std::max({mean * (double)seqs * (M + kTurn) / line_blocks, M / (splits - 1), (double)kStep});
-  double best = share / kStep + 8.0 + 0.1 * M / share;
-  int cluster = 0;
-  for (int c = 1; c <= std::min(kMostCluster, p.num_splits); c *= 2) {
-    const int room = c > 8 ? sms : 2 * sms;
-    const long long rounds = (groups * c + room - 1) / room;
-    const double steps = (rounds == 1 ? 1.0 : 0.95 * (double)rounds) * (std::ceil(M / (c * kStep)) + 2) + (c > 1 ? 1 : 0);
-    if (groups * c <= 0x3fffffff && steps < best) best = steps, cluster = c;
+// CTAs that a cluster of this kernel may have on the current device: 16 where the GPU has room for one (8 is what every
+// launch may have; a part of a GPU, or a context held to a few SMs, may have room for fewer). Asked for once per device.
+template <int D, int NT, bool kScores>
+int most_cluster() {
+  static std::atomic<int> known[128];
+  int dev = 0, most = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev >= 0 && dev < 128 && (most = known[dev].load(std::memory_order_relaxed)) > 0) return most;
+  auto kern = stream_fp8_kernel<D, NT, kScores>;
+  const bool wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  for (most = wide ? kStreamMostCluster : 8; most > 1; most /= 2) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(most);
+    c.blockDim = dim3(kWarps<NT> * 32);
+    c.dynamicSmemBytes = kScratch<D, NT>;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim = {(unsigned)most, 1, 1};
+    c.attrs = &a;
+    c.numAttrs = 1;
+    int room = 0;
+    if (cudaOccupancyMaxActiveClusters(&room, kern, &c) == cudaSuccess && room > 0) break;
   }
-  return cluster;
+  cudaGetLastError();   // (a size that has no room is no error of this call)
+  if (dev >= 0 && dev < 128) known[dev].store(most, std::memory_order_relaxed);
+  return most;
 }
 
 template <int D, int NT, bool kScores>
@@ -781,12 +774,12 @@ cudaError_t launch_t(const StreamFp8Params& p0, cudaStream_t stream) {
   const int sms = num_sms_current();
   if (sms <= 0) return cudaErrorInvalidValue;
   StreamFp8Params p = p0;
-  p.cluster = cluster_of<NT>(p, sms);
   auto kern = stream_fp8_kernel<D, NT, kScores>;
   if (kScratch<D, NT> > 40 * 1024) {   // (without asking, 48 KB with the static part)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScratch<D, NT>);
     if (e != cudaSuccess) return e;
   }
+  p.cluster = stream_fp8_cluster(p, kWarps<NT> * kTogether<NT>, sms, most_cluster<D, NT, kScores>());
   const long long groups = (long long)p.B * p.subs * p.Hkv;
   if (p.cluster > 0) {
     if (p.cluster > 8) {               // (8 is what every launch may have)

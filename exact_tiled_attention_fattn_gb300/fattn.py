@@ -1201,7 +1201,7 @@ def fwd_paged_fp8(q, kcache, vcache, kscale, vscale, block_table, seqlens_k, cu_
     if num_splits is None:
         context = maxp * page_size
         if window > 0:
-            context = min(context, int(window) + max_seqlen_q + int(sinks))
+            context = min(context, (1 if causal else 2) * int(window) + max_seqlen_q + int(sinks))
         num_splits = choose_fp8_splits(B, Hq, Hkv, d, page_size, max_seqlen_q, context)
     num_splits = _int(num_splits, "num_splits")
     if workspace is None:
