@@ -559,12 +559,17 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
   st = check_cache_fp8(kcache, vcache, kscale, vscale, block_table, seqlens_k, d, page_size, max_pages_per_seq, num_pages);
   if (st != FATTN_OK) return st;
   const long long rows = (long long)max_seqlen_q * (Hq / Hkv);
-  if (rows > 0x7fffffffLL || (long long)total_q * Hq > 0x7fffffffLL / num_splits ||
-      ((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || B > 65535 ||
-      stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits)
-    return FATTN_ERR_UNSUPPORTED;
-  if (streams_fp8(max_seqlen_q, Hq / Hkv) && !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size))
-    return FATTN_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffffLL || (long long)total_q * Hq > 0x7fffffffLL / num_splits) return FATTN_ERR_UNSUPPORTED;
+  if (streams_fp8(max_seqlen_q, Hq / Hkv)) {
+    if (stream_fp8_groups(B, Hkv, rows) > 0x3fffffffLL / num_splits ||
+        !countable_steps(B, Hkv, rows, max_pages_per_seq, page_size))
+      return FATTN_ERR_UNSUPPORTED;
+  } else {   // the copy's slots, and what the prefill and its joining refuse, before the copy is launched
+    const long long pairs = ((long long)max_seqlen_q + 255) / 256;
+    if (((long long)B * max_pages_per_seq + 1) * page_size > 0x7fffffffLL || (long long)B * Hq > 0x7fffffffLL / pairs / num_splits ||
+        (num_splits > 1 && (B > 65535 || (long long)max_seqlen_q * Hq > 0x7fffffffLL)))
+      return FATTN_ERR_UNSUPPORTED;
+  }
   const ChunkWorkspace w =
       chunk_workspace(B, Hq, Hkv, d, page_size, max_pages_per_seq, total_q, max_seqlen_q, num_splits);
   if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 256)) return FATTN_ERR_WORKSPACE;

@@ -432,7 +432,7 @@ bool quads(const RopeTensor& t, bool out) {
 // two written a value): 28k tokens of 8 heads of 128, K and V, 172 MB, in 32 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads) expand_fp8_kernel(const ExpandFp8Params p) {
-  const int b = blockIdx.y, pi = blockIdx.x, P = p.page_size;
+  const int b = blockIdx.x / p.max_pages, pi = blockIdx.x - b * p.max_pages, P = p.page_size;
   const int c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1), L = __ldg(p.seqlens_k + b);
   // (the prefill skips sequences with inconsistent lengths and records them)
   if (c0 < 0 || c1 <= c0 || c1 > p.total_q || L < c1 - c0 || L > (long long)p.max_pages * P) return;
@@ -501,7 +501,7 @@ cudaError_t launch_append_fp8(const AppendFp8Params& p0, int num_sms, cudaStream
 }
 
 cudaError_t launch_expand_fp8(const ExpandFp8Params& p, cudaStream_t stream) {
-  const dim3 grid(p.max_pages, p.B);
+  const unsigned grid = (unsigned)p.B * p.max_pages;   // (slots of the copy are an int)
   if (p.d == 128)
     expand_fp8_kernel<128><<<grid, kThreads, 0, stream>>>(p);
   else

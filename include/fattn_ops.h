@@ -297,8 +297,9 @@ size_t fattn_fwd_paged_fp8_workspace_size(int B, int Hq, int Hkv, int d, int pag
  * aligned, contents ignored, always needed.
  * A table entry outside the pool is recorded as FATTN_ERR_DEVICE_CHECK and, as in fattn_fwd_paged, its tokens read as zeros
  * (K and V, so a score of 0 before the distance bias), whichever way the rows take; single tokens do not see them.
- * Errors: those of fattn_fwd_paged_sinks and of the cache; UNSUPPORTED also for (B * max_pages_per_seq + 1) * page_size
- *   >= 2^31.
+ * Errors: those of fattn_fwd_paged_sinks and of the cache; UNSUPPORTED also for total_q * Hq * num_splits >= 2^31, with few
+ *   rows for more tokens than an int counts (B * Hkv * ceil(rows / 32) * max_pages_per_seq * page_size / 16 about 2^31), with more
+ *   for (B * max_pages_per_seq + 1) * page_size >= 2^31, and for B > 65535 in splits.
  */
 fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, const void* vcache, const float* kscale,
                                  const float* vscale, const int32_t* block_table, const int32_t* seqlens_k,
