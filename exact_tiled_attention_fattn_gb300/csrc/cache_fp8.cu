@@ -367,7 +367,8 @@ __device__ __forceinline__ void append_kv(const AppendFp8Params& p, float2* cs, 
     const Quads at = u < nkv ? turned_at : plain_at;
     const float s = sh.scale[u];
     const uint32_t bits = __float_as_uint(s);
-    const bool pow2 = (bits & 0x7fffffu) == 0, inf = sh.inf[u] != 0;   // (old scales may be others)
+    // (old scales may be others, or 2^127, whose reciprocal has no such form)
+    const bool pow2 = (bits & 0x7fffffu) == 0 && bits < 254u << 23, inf = sh.inf[u] != 0;
     const float inv = __uint_as_float((254u << 23) - bits);            // 1 / s
     uint8_t* base = slot(u, slot0);
     walk(u, trips * share / shares, trips * (share + 1) / shares, [&](int r, const Eight& x) {

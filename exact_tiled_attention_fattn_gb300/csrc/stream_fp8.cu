@@ -345,11 +345,11 @@ __device__ __forceinline__ void stream_piece(const StreamFp8Params& p, float* sc
         meta = ahead;
         look(ahead, i + kBatch);
       }
-      // log2 and the reciprocal of V's scale; a power of two has both exactly
+      // log2 and the reciprocal of V's scale; a power of two has both exactly (2^127 by the division)
       const uint32_t b = __float_as_uint(meta.vs);
       if (meta.page < 0) meta.ks = 1.f;
       lv_of = meta.page < 0 ? 0.f : (b & 0x7fffffu) == 0 ? (float)((int)(b >> 23) - 127) : log2f(meta.vs);
-      iv_of = meta.page < 0 ? 1.f : (b & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - b) : 1.f / meta.vs;
+      iv_of = meta.page < 0 ? 1.f : (b & 0x7fffffu) == 0 && b < 254u << 23 ? __uint_as_float((254u << 23) - b) : 1.f / meta.vs;
     } else if (i % kBatch == kBatch / 2) {
       scales(ahead, i + kBatch / 2);
     }

@@ -238,8 +238,10 @@ fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const v
  * The 8-bit cache: kcache, vcache [num_pages, page_size, Hkv, d] E4M3 codes ('fn' variant: no
  * infinities), kscale, vscale fp32 [num_pages, Hkv]; token t of a sequence is slot t % page_size of page
  * block_table[b * max_pages_per_seq + t / page_size], its k in head h is kscale[page, h] * code, its v
- * likewise. Scales of pages in use are positive and finite; the append writes powers of two. d in {64, 128},
- * page_size in {16, 32, 64, 128}.
+ * likewise. Scales of pages in use are finite and at least 2^-100; the append writes powers of two. d in {64, 128},
+ * page_size in {16, 32, 64, 128}. Where rows are streamed a key counts, in O and in lse, while its weight times its page's V
+ * scale is at least 2^-118 of the largest such product that the row sees: any key whose weight matters if V's scales lie within
+ * 2^90 of each other.
  *
  * fattn_rope_append_paged_fp8 — fattn_rope_append_paged into the 8-bit cache: q and k of new tokens
  * rotated, q written to q_out (bf16), k and v as codes, in one launch. Per page, head and cache, with a the
