@@ -251,6 +251,9 @@ fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const v
  *   old one the codes of its other slots become RN(code * old / new); any other page has scale need (its old one is not
  *   read) and its other slots mean nothing;
  *   new codes = RN(value / scale); infinities and NaN become NaN codes.
+ * A token with NaN codes is not finite for the attention calls: hidden keys have weight 0, as with shaped scores, and 0 times NaN is
+ * NaN, so its V may reach rows of its own sequence that do not see it (drafted tokens before it). Rows of other sequences, and
+ * what lies in a page past its sequence's end, are not concerned.
  * Which slots hold context follows from seqlens_k alone. A page that is appended to must not be shared with another sequence, and
  * no two tokens of a call share a slot. Everything else (chunks, positions, padding rows, strides, skipped rows) is as in
  * fattn_rope_append_paged. Errors: as there; UNSUPPORTED also for other d or page sizes, or
