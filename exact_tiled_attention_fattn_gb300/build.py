@@ -83,7 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and r.stderr:
             print(r.stderr, file=sys.stderr)
-        if os.path.basename(src) == "prefill_tc.cu":
+        if os.path.basename(src) in ("prefill_tc.cu", "prefill_tc_sinks.cu"):
             _check_launch_registers(r.stderr)
         return obj
 

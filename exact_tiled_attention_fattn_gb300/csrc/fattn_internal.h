@@ -94,6 +94,9 @@ constexpr int kSparseMaxBlocks = 2048;
 // boxes) and of o (bf16, 32-row boxes: the epilogue's stores).
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& to, int num_sms, cudaStream_t stream);
+// A window with sinks (prefill_tc_sinks.cu; called by launch_prefill_tc).
+cudaError_t launch_prefill_sinks(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const CUtensorMap& to, int num_sms, cudaStream_t stream);
 
 // Joins the partials of a split paged prefill into p.o and p.lse.
 cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream);

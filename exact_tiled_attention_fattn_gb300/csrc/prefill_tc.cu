@@ -132,10 +132,11 @@ enum : int {
 enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, kModeFp8 = 4 };
 // Shaped variants: kModeShaped plus what the scores get (key ranges and the window always),
 // whether K/V come through a block table, and then whether key tiles are cut into runs (the
-// epilogue's second form costs the others up to 25 %, in registers). One kernel for each, as the softmax loop of the one
+// epilogue's second form costs the others up to 25 %, in registers), and whether a window has sinks (at run time the others
+// lose up to 4 %: 32 heads over 8, 2 x 8192 tokens, capped, window 128 160 -> 165 us). One kernel for each, as the softmax loop of the one
 // with everything under run-time switches is 6 % slower without a cap or bias: its unrolled
 // forms no longer stay in the instruction cache.
-enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4, kShapeSplit = 16 };
+enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4, kShapeSplit = 16, kShapeSinks = 32 };
 __host__ __device__ constexpr bool mode_shaped(int m) { return m >= kModeShaped; }
 
 template <int D, int kMode>
@@ -237,7 +238,7 @@ __device__ __forceinline__ int item_index(const Schedule& s, int k) {
   return idx < s.total ? idx : -1;
 }
 
-template <bool kShaped, bool kSplits>
+template <bool kShaped, bool kSplits, bool kSinks>
 __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedule& s, int it) {
   Item x;
   x.top[0] = x.top[1] = x.jtop = x.jbot = x.cut = x.gap = 0;
@@ -284,8 +285,7 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
     x.n[0] = x.n[1] = 0;
     x.jbot = 1 << 30;
     if (x.valid) {
-      const bool sinks = p.shape.sinks > 0;
-      if (sinks) {
+      if constexpr (kSinks) {
         x.cut = shape_lo(p.shape, (long long)x.row0 + x.base, x.base + x.off) / BN;
         x.gap = max(x.cut - sink_blocks(p.shape.sinks, BN), 0);
       }
@@ -295,9 +295,9 @@ __device__ __forceinline__ Item decode_item(const PrefillParams& p, const Schedu
         const int first = x.base + t * BM, last = min(first + BM, x.L) - 1;
         const int lo = shape_lo(p.shape, (long long)x.row0 + first, first + x.off);
         int hi = shape_hi(p.shape, (long long)x.row0 + last, last + x.off, x.Lk, p.causal);
-        if (sinks) hi = max(hi, shape_sinks(p.shape, last + x.off, x.Lk, p.causal));
+        if constexpr (kSinks) hi = max(hi, shape_sinks(p.shape, last + x.off, x.Lk, p.causal));
         if (lo < hi) {
-          const int t0 = sinks ? x.gap : lo / BN, n = (hi + BN - 1) / BN - t0;
+          const int t0 = kSinks ? x.gap : lo / BN, n = (hi + BN - 1) / BN - t0;
           int from = t0;
           x.top[t] = t0 + n;
           if constexpr (kSplits) {
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kPaged = kMode == kModePaged || (mode_shaped(kMode) && (kMode & kShapePaged));  // K/V through a block table
   constexpr bool kShaped = mode_shaped(kMode);    // window and key ranges
   constexpr bool kSplits = kShaped && (kMode & kShapeSplit);  // a query tile's key tiles are cut into runs
+  constexpr bool kSinks = kShaped && (kMode & kShapeSinks);   // a window's sinks
   constexpr bool kCap = kShaped && (kMode & kShapeCap);    // and the scores' tanh cap
   constexpr bool kBias = kShaped && (kMode & kShapeBias);  // and distance bias
   constexpr bool kMasked = kMode == kModeMasked;  // additive bf16 mask M on the scores
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0;; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item<kShaped, kSplits>(p, sch, it);
+        const Item x = decode_item<kShaped, kSplits, kSinks>(p, sch, it);
         if (!x.valid) continue;
         const int hkv = x.h / G;
         const int n = kShaped ? x.jtop - x.jbot : max(x.n[0], x.n[1]);
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // same swizzled layout as one 128-row box (page_size is a multiple of 8 rows).
         auto issue_kv = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, int j, bool is_v) {
           (void)is_v;
-          if constexpr (kShaped) j -= j < x.cut ? x.gap : 0;
+          if constexpr (kSinks) j -= j < x.cut ? x.gap : 0;
           if constexpr (kPaged) {
             const int P = p.page_size, per = BN / P;  // per <= 8 (page_size >= 16)
             const int i = lane;                       // this lane's page of the tile
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int it = item_index(sch, k);
         if (it < 0) break;
-        const Item x = decode_item<kShaped, kSplits>(p, sch, it);
+        const Item x = decode_item<kShaped, kSplits, kSinks>(p, sch, it);
         if (!x.valid) continue;
         if constexpr (kSparse) {
           // walk the blocks either tile keeps: per block j, O_t += P_t(prev) V_prev for each tile
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0;; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item<kShaped, kSplits>(p, sch, it);
+      const Item x = decode_item<kShaped, kSplits, kSinks>(p, sch, it);
       if (!x.valid) continue;
       if (!warp_wait(bar(kBarMaskEmpty + nm % kMaskSlots), ((nm / kMaskSlots) & 1) ^ 1, abort, p.status, p.wait_ns)) break;
       uint32_t* w = reinterpret_cast<uint32_t*>(smem + Lay::kOffMask + (nm % kMaskSlots) * kMaskSlotBytes);
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       const int it = item_index(sch, k);
       if (it < 0) break;
-      const Item x = decode_item<kShaped, kSplits>(p, sch, it);
+      const Item x = decode_item<kShaped, kSplits, kSinks>(p, sch, it);
       if (!x.valid) continue;
       const uint32_t* mw = nullptr;
       // this tile's K/V tile count, selected rather than indexed (a run-time index into the
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int e = shape_hi(p.shape, (long long)x.row0 + r1, r1 + x.off, x.Lk, p.causal);
           out = a >= e || lo < a / BN * BN || hi > (e + BN - 1) / BN * BN;
         }
-        if (lo < hi && out && p.shape.sinks == 0) record_status(p.status, kStatusDeviceCheck);
+        if (!kSinks && lo < hi && out) record_status(p.status, kStatusDeviceCheck);
       };
       if (nt == 0) {
         release_mask();
@@ -1013,12 +1014,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++ns;
         tc_fence_after();
-        const int kbase = (kShaped ? (j < x.cut ? j - x.gap : j) : j) * BN;  // first key of the tile
+        const int kbase = (kSinks && j < x.cut ? j - x.gap : j) * BN;  // first key of the tile
         // columns [32 c, 32 c + 32) that are visible, as bits: keys [lo, lim) and the sinks
         auto visible = [&](int c) -> uint32_t {
           const int first = kbase + 32 * c, a = max(lo - first, 0), e = min(lim - first, 32);
-          return (a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u) |
-                 low_bits(shape_sinks(p.shape, pos, x.Lk, p.causal) - first);
+          uint32_t seen = a < e ? (0xffffffffu << a) & (0xffffffffu >> (32 - e)) : 0u;
+          if constexpr (kSinks) seen |= low_bits(shape_sinks(p.shape, pos, x.Lk, p.causal) - first);
+          return seen;
         };
         if constexpr (kCap) {
           // ---- capped scores: two rolled walks over the tile's 128 columns, 32 at a time from TMEM. The
@@ -1287,12 +1289,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (kShaped) {
           if (edge) {
+            if constexpr (!kSinks && kBias && kPaged) {  // (129 us against 133 by bits; the other variants are 2 to 10 % slower so)
+              const uint32_t span = (uint32_t)max(lim - lo, 0), first_key = (uint32_t)(lo - kbase);
 #pragma unroll
-            for (int w = 0; w < BN / 32; ++w) {
-              const uint32_t vis = visible(w);
+              for (int c = 0; c < BN; ++c)
+                if ((uint32_t)c - first_key >= span) s[c] = -CUDART_INF_F;
+            } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!((vis >> c) & 1u)) s[32 * w + c] = !kBias && neg ? CUDART_INF_F : -CUDART_INF_F;
+              for (int w = 0; w < BN / 32; ++w) {
+                const uint32_t vis = visible(w);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((vis >> c) & 1u)) s[32 * w + c] = !kBias && neg ? CUDART_INF_F : -CUDART_INF_F;
+              }
             }
           }
           masked = false;
@@ -1543,17 +1552,19 @@ cudaError_t launch_shaped_t(const PrefillParams& p, const CUtensorMap& tq, const
                       : launch_t<D, kModeShaped + kShape + kShapePaged>(p, tq, tk, tv, to, num_sms, stream);
 }
 
-template <int D>
+// kSinks: 0 or kShapeSinks.
+template <int D, int kSinks>
 cudaError_t launch_shaped(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& to, int num_sms, cudaStream_t stream) {
   // (a scale of 0 goes with the bias: -inf marks hidden keys, and raw products would carry it to 0 * inf)
   const bool cap = p.shape.cap > 0.f, bias = p.shape.slopes != nullptr || p.scale == 0.f;
-  if (cap && bias) return launch_shaped_t<D, kShapeCap + kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
-  if (cap) return launch_shaped_t<D, kShapeCap>(p, tq, tk, tv, to, num_sms, stream);
-  if (bias) return launch_shaped_t<D, kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
-  return launch_shaped_t<D, 0>(p, tq, tk, tv, to, num_sms, stream);
+  if (cap && bias) return launch_shaped_t<D, kSinks + kShapeCap + kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
+  if (cap) return launch_shaped_t<D, kSinks + kShapeCap>(p, tq, tk, tv, to, num_sms, stream);
+  if (bias) return launch_shaped_t<D, kSinks + kShapeBias>(p, tq, tk, tv, to, num_sms, stream);
+  return launch_shaped_t<D, kSinks>(p, tq, tk, tv, to, num_sms, stream);
 }
 
+#ifndef FATTN_PREFILL_SINKS
 // Partials joined with the rescaling rule: lse = ln sum_s e^{lse_s}, O = sum_s e^{lse_s - lse} O_s. A thread
 // takes 4 columns of a (query, head) row; grid (rows of the longest chunk, sequences). Bound by the partials'
 // bytes; chunks that the attention kernel skipped (inconsistent lengths) are skipped here too.
@@ -1597,8 +1608,16 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
   }
 }
 
+#endif
 }  // namespace
 
+#ifdef FATTN_PREFILL_SINKS   // prefill_tc_sinks.cu: the kernels with sinks alone
+cudaError_t launch_prefill_sinks(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const CUtensorMap& to, int num_sms, cudaStream_t stream) {
+  return p.d == 128 ? launch_shaped<128, kShapeSinks>(p, tq, tk, tv, to, num_sms, stream)
+                    : launch_shaped<64, kShapeSinks>(p, tq, tk, tv, to, num_sms, stream);
+}
+#else
 cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream) {
   const int rows = kMergeThreads / (p.d / 4);
   const dim3 grid((unsigned)(((long long)p.N * p.Hq + rows - 1) / rows), p.B);
@@ -1612,9 +1631,10 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, con
     if (p.d == 128) return launch_t<128, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
     return launch_t<64, kModeSparse>(p, tq, tk, tv, to, num_sms, stream);
   }
+  if (p.shaped && p.shape.sinks > 0) return launch_prefill_sinks(p, tq, tk, tv, to, num_sms, stream);
   if (p.shaped)
-    return p.d == 128 ? launch_shaped<128>(p, tq, tk, tv, to, num_sms, stream)
-                      : launch_shaped<64>(p, tq, tk, tv, to, num_sms, stream);
+    return p.d == 128 ? launch_shaped<128, 0>(p, tq, tk, tv, to, num_sms, stream)
+                      : launch_shaped<64, 0>(p, tq, tk, tv, to, num_sms, stream);
   if (p.block_table) {
     if (p.d == 128) return launch_t<128, kModePaged>(p, tq, tk, tv, to, num_sms, stream);
     return launch_t<64, kModePaged>(p, tq, tk, tv, to, num_sms, stream);
@@ -1627,5 +1647,6 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tq, con
   if (p.d == 128) return launch_t<128, kModeDense>(p, tq, tk, tv, to, num_sms, stream);
   return launch_t<64, kModeDense>(p, tq, tk, tv, to, num_sms, stream);
 }
+#endif
 
 }  // namespace fattn
