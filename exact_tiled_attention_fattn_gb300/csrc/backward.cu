@@ -453,10 +453,8 @@ __device__ __forceinline__ void shaped_p32(const BwdParams& p, float slope2, uin
                                            int va, int vb, int vs, const float* nlv, float nl, float* pv, uint32_t* pk) {
   const ScoreShape& sh = p.shape;
   const bool edge = !__all_sync(0xffffffffu, va <= 0 && vb >= 32);
-  uint32_t vis = 0xffffffffu;
-  if (edge)
-    vis = (vb <= 0 || va >= 32 || va >= vb ? 0u : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)))) |
-          low_bits(vs);
+  uint32_t vis = vb <= 0 || va >= 32 || va >= vb ? 0u : (0xffffffffu << max(va, 0)) & (0xffffffffu >> (32 - min(vb, 32)));
+  if constexpr (shape_with_sinks(kShape)) vis |= low_bits(vs);
   constexpr bool cap = kShape & kShapeCap, bias = kShape & kShapeBias;
   static_assert(kShape != kPlain, "shaped scores");
   float y[32], f[32];
