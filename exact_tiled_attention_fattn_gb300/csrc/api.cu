@@ -362,12 +362,14 @@ extern "C" size_t fattn_bwd_workspace_size(int B, int Hq, int N) {
   return 2 * align256((size_t)B * Hq * npad * sizeof(float));
 }
 
-// fattn_bwd, and with a shape fattn_bwd_shaped.
+// fattn_bwd, with a shape fattn_bwd_shaped and fattn_bwd_sinks, with strides fattn_bwd_strided.
 fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const void* o, const float* lse,
                              const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
                              int causal, float scale, const ScoreShape* shape, void* workspace, size_t workspace_bytes,
-                             cudaStream_t stream) {
+                             cudaStream_t stream, const long long* o_strides) {
   if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FATTN_ERR_INVALID_ARG;
+  for (int i = 0; o_strides && i < 3; ++i)   // (rows of o are read 16 bytes at a time)
+    if (o_strides[i] < 0 || o_strides[i] % 8 != 0) return FATTN_ERR_INVALID_ARG;
   if (B == 0 || N == 0) return FATTN_OK;
   if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FATTN_ERR_INVALID_ARG;
   if (Hq % Hkv != 0 || !std::isfinite(scale)) return FATTN_ERR_INVALID_ARG;
@@ -390,6 +392,9 @@ fattn_status fattn::bwd_impl(const void* q, const void* k, const void* v, const 
   int err = 0;
   BwdParams p{};
   p.q = q; p.k = k; p.v = v; p.o = o; p.dout = dout; p.lse = lse;
+  p.o_batch = o_strides ? o_strides[0] : (long long)N * Hq * d;
+  p.o_row = o_strides ? o_strides[1] : (long long)Hq * d;
+  p.o_head = o_strides ? o_strides[2] : d;
   p.dq = dq; p.dk = dk; p.dv = dv;
   p.ws_nl2 = static_cast<float*>(workspace);
   p.ws_d = reinterpret_cast<float*>(static_cast<char*>(workspace) + vectors / 2);

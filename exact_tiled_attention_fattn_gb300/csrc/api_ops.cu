@@ -274,6 +274,25 @@ extern "C" fattn_status fattn_bwd_sinks(const void* q, const void* k, const void
                   workspace_bytes, stream);
 }
 
+extern "C" fattn_status fattn_bwd_strided(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                          const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N,
+                                          int d, int causal, float scale, int shaped, float softcap, const float* slopes,
+                                          int window, int sinks, const int32_t* key_begin, const int32_t* key_end,
+                                          long long o_batch, long long o_row, long long o_head, void* workspace,
+                                          size_t workspace_bytes, cudaStream_t stream) {
+  const long long strides[3] = {o_batch, o_row, o_head};
+  ScoreShape shape{};
+  if (shaped) {
+    const fattn_status st =
+        check_shape(scale, softcap, slopes, window, sinks, causal != 0, key_begin, key_end, N, &shape);
+    if (st != FATTN_OK) return st;
+  } else if (softcap != 0.f || slopes || window != 0 || sinks != 0 || key_begin || key_end) {
+    return FATTN_ERR_INVALID_ARG;
+  }
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, shaped ? &shape : nullptr, workspace,
+                  workspace_bytes, stream, strides);
+}
+
 extern "C" fattn_status fattn_decode_paged_shaped(const void* q, const void* kcache, const void* vcache,
                                                   const int32_t* block_table, const int32_t* seqlens, int num_splits,
                                                   void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,

@@ -107,8 +107,9 @@ template <int D>
 __device__ __forceinline__ void row_vectors(const BwdParams& p, int b, int h, int i0, int lane) {
   constexpr int E = D / 32;  // elements per lane: 4 (8 bytes) or 2 (4 bytes)
   using Vec = typename std::conditional<E == 4, uint2, uint32_t>::type;
-  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o);
-  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout);
+  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.o_batch + h * p.o_head + i0 * p.o_row + lane * E;
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout) + (((size_t)b * p.N + i0) * p.Hq + h) * D + lane * E;
+  const int g_row = p.Hq * D;
   const int bh = b * p.Hq + h;
   const int i = i0 + lane;                        // this lane's row of the block
   const float lse = i < p.N ? __ldg(p.lse + (size_t)bh * p.N + i) : -CUDART_INF_F;
@@ -119,10 +120,11 @@ __device__ __forceinline__ void row_vectors(const BwdParams& p, int b, int h, in
 #pragma unroll
     for (int u = 0; u < kRowsPerWarp; ++u) {
       if (u0 + u < nrows) {
-        const size_t off = (((size_t)b * p.N + i0 + u0 + u) * p.Hq + h) * D + lane * E;
-        a[u] = __ldg(reinterpret_cast<const Vec*>(o + off));
-        d[u] = __ldg(reinterpret_cast<const Vec*>(g + off));
+        a[u] = __ldg(reinterpret_cast<const Vec*>(o));
+        d[u] = __ldg(reinterpret_cast<const Vec*>(g));
       }
+      o += p.o_row;
+      g += g_row;
     }
 #pragma unroll
     for (int u = 0; u < kRowsPerWarp; ++u) {
@@ -152,8 +154,12 @@ __device__ __forceinline__ void row_vectors(const BwdParams& p, int b, int h, in
 template <int D>
 __device__ __forceinline__ void row_vectors_wide(const BwdParams& p, int b, int h, int i0, int lane) {
   constexpr int L = D / 8, R = 32 / L;            // lanes per row, rows per load; L loads cover the block
-  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o);
-  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout);
+  const int first = i0 + lane / L;                  // this lane's row of the first load; R rows on each time
+  const __nv_bfloat16* o =
+      static_cast<const __nv_bfloat16*>(p.o) + b * p.o_batch + h * p.o_head + first * p.o_row + (lane % L) * 8;
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout) + (((size_t)b * p.N + first) * p.Hq + h) * D + (lane % L) * 8;
+  const long long o_step = R * p.o_row;
+  const int g_step = R * p.Hq * D;
   const int bh = b * p.Hq + h;
   const int mine = i0 + (lane % L) * R + lane / L;  // the row whose sum this lane ends with
   const float lse = mine < p.N ? __ldg(p.lse + (size_t)bh * p.N + mine) : -CUDART_INF_F;
@@ -163,13 +169,13 @@ __device__ __forceinline__ void row_vectors_wide(const BwdParams& p, int b, int 
     uint4 a[L / 2], d[L / 2];
 #pragma unroll
     for (int t = 0; t < L / 2; ++t) {
-      const int i = i0 + (half * (L / 2) + t) * R + lane / L;
       a[t] = d[t] = make_uint4(0, 0, 0, 0);
-      if (i < p.N) {
-        const size_t off = (((size_t)b * p.N + i) * p.Hq + h) * D + (lane % L) * 8;
-        a[t] = __ldg(reinterpret_cast<const uint4*>(o + off));
-        d[t] = __ldg(reinterpret_cast<const uint4*>(g + off));
+      if (first + (half * (L / 2) + t) * R < p.N) {
+        a[t] = __ldg(reinterpret_cast<const uint4*>(o));
+        d[t] = __ldg(reinterpret_cast<const uint4*>(g));
       }
+      o += o_step;
+      g += g_step;
     }
 #pragma unroll
     for (int t = 0; t < L / 2; ++t) {

@@ -143,7 +143,8 @@ struct BwdParams {
   const void* q;
   const void* k;
   const void* v;
-  const void* o;
+  const void* o;              // element (b, i, h, c) at b o_batch + i o_row + h o_head + c; the others are packed
+  long long o_batch, o_row, o_head;
   const void* dout;
   const float* lse;
   void* dq;

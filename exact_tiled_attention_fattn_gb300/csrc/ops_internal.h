@@ -219,7 +219,8 @@ fattn_status fwd_paged_impl(const void* q, const void* kcache, const void* vcach
                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
 fattn_status bwd_impl(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                       void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d, int causal, float scale,
-                      const ScoreShape* shape, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+                      const ScoreShape* shape, void* workspace, size_t workspace_bytes, cudaStream_t stream,
+                      const long long* o_strides = nullptr);   // batch, row, head; nullptr: packed
 fattn_status decode_paged_impl(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
                                const int32_t* seqlens, int num_splits, void* o, float* lse, int B, int Hq, int Hkv,
                                int d, int page_size, int max_pages_per_seq, int num_pages, float scale,

@@ -73,6 +73,8 @@ SIGNATURES_OPS = {
     "fattn_fwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i, _vp]),
     "fattn_bwd_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i,
                              _vp, _sz, _vp]),
+    "fattn_bwd_strided": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _f, _vp, _i,
+                               _i, _vp, _vp, _ll, _ll, _ll, _vp, _sz, _vp]),
     "fattn_bwd_sinks_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "fattn_fwd_paged_sinks": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                    _f, _vp, _i, _i, _i, _vp, _sz, _vp]),
@@ -153,6 +155,14 @@ def _packed(t, stream):
         return t.contiguous()
     with torch.cuda.stream(stream):
         return t.contiguous()
+
+
+def _view_strides(o):
+    """The strides (batch, row, head) by which the gradient can read o where it lies, or None: packed, or to be copied."""
+    b, n, h, e = o.stride()
+    if o.is_contiguous() or e != 1 or (b | n | h | o.data_ptr() // 2) & 7:
+        return None
+    return b, n, h
 
 
 def _ptr(t):
@@ -398,8 +408,8 @@ def bwd_workspace_size(B: int, Hq: int, N: int) -> int:
 def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None, dq=None, dk=None, dv=None,
         workspace=None, stream=None):
     """Attention backward. q, o, dout [B,N,Hq,d], k, v [B,N,Hkv,d] bf16; lse [B,Hq,N] fp32 from
-    ``fwd`` on the same inputs. o and dout may be any views (transposed heads, an expanded gradient): one that is not
-    contiguous is copied within the call. Returns (dq, dk, dv) in the input layouts (bf16)."""
+    ``fwd`` on the same inputs. o and dout may be any views: o is read where it lies if its elements of a head do (heads
+    first in memory, a slice), and what else is not contiguous is copied within the call. Returns (dq, dk, dv) in the input layouts (bf16)."""
     lib = load_library()
     _need_cuda(q, k, v, lse, dq, dk, dv, workspace)
     _need_cuda(o, dout, contiguous=False)
@@ -425,11 +435,15 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     need = bwd_workspace_size(B, Hq, N)
     if workspace is None:
         workspace = _scratch(need, q.device, stream)
-    o, dout = _packed(o, stream), _packed(dout, stream)
-    st = lib.fattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
-                       B, Hq, Hkv, N, d, 1 if causal else 0, float(scale), _ptr(workspace),
-                       workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check("fattn_bwd", st)
+    strides, dout = _view_strides(o), _packed(dout, stream)
+    o = o if strides else _packed(o, stream)
+    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
+            1 if causal else 0, float(scale))
+    tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if strides:
+        _check("fattn_bwd_strided", lib.fattn_bwd_strided(*head, 0, 0.0, None, 0, 0, None, None, *strides, *tail))
+    else:
+        _check("fattn_bwd", lib.fattn_bwd(*head, *tail))
     return dq, dk, dv
 
 
@@ -983,11 +997,16 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
         need = (bwd_sinks_workspace_size(B, Hq, Hkv, N, d, causal, window, sinks) if sinks else
                 bwd_shaped_workspace_size(B, Hq, Hkv, N, d))
         workspace = _scratch(need, q.device, stream)
-    o, dout = _packed(o, stream), _packed(dout, stream)
-    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
-            1 if causal else 0, float(scale), float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
+    strides, dout = _view_strides(o), _packed(dout, stream)
+    o = o if strides else _packed(o, stream)
+    base = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, N, d,
+            1 if causal else 0, float(scale))
+    shape = (float(softcap), _ptr(slopes), _int(min(window, _INT_MAX), "window"))
+    head = base + shape
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    if sinks:
+    if strides:
+        _check("fattn_bwd_strided", lib.fattn_bwd_strided(*base, 1, *shape, sinks or 0, _ptr(key_begin), _ptr(key_end), *strides, *tail))
+    elif sinks:
         _check("fattn_bwd_sinks", lib.fattn_bwd_sinks(*head, sinks, *tail))
     else:
         _check("fattn_bwd_shaped", lib.fattn_bwd_shaped(*head, _ptr(key_begin), _ptr(key_end), *tail))

@@ -235,6 +235,19 @@ fattn_status fattn_decode_paged_sinks(const void* q, const void* kcache, const v
                                       size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * fattn_bwd_strided — the gradients above for an o that is a view: element (b, i, h, c) is o[b * o_batch + i * o_row +
+ * h * o_head + c] (heads first in memory, a slice of a wider tensor, a broadcast), strides >= 0 and multiples of 8 elements.
+ * shaped == 0: fattn_bwd (softcap, window and sinks 0, no slopes and key ranges); else fattn_bwd_sinks, with key ranges where
+ * sinks == 0. Everything else, bits included, is theirs for the packed o. Errors: theirs, and INVALID_ARG for other strides.
+ */
+fattn_status fattn_bwd_strided(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                               const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
+                               int causal, float scale, int shaped, float softcap, const float* slopes, int window,
+                               int sinks, const int32_t* key_begin, const int32_t* key_end, long long o_batch,
+                               long long o_row, long long o_head, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
  * The 8-bit cache: kcache, vcache [num_pages, page_size, Hkv, d] E4M3 codes ('fn' variant: no
  * infinities), kscale, vscale fp32 [num_pages, Hkv]; token t of a sequence is slot t % page_size of page
  * block_table[b * max_pages_per_seq + t / page_size], its k in head h is kscale[page, h] * code, its v

@@ -21,10 +21,13 @@ def test_views(kw):
     o, lse = fwd(q, k, v, **kw)
     want = bwd(q, k, v, o, lse, do, **kw)
     heads_first = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)
-    wide = torch.cat([o, do], -1)
-    for ov, gv in ((heads_first(o), do), (o, heads_first(do)), (wide[..., :d], wide[..., d:])):
+    wide, odd = torch.cat([o, do], -1), torch.cat([o[..., :1], o], -1)[..., 1:]
+    for ov, gv in ((heads_first(o), do), (o, heads_first(do)), (wide[..., :d], wide[..., d:]), (odd, do)):
         assert not (ov.is_contiguous() and gv.is_contiguous())
         assert all(torch.equal(a, b) for a, b in zip(want, bwd(q, k, v, ov, lse, gv, **kw)))
+    # a row of o for all
+    row = o[:1, :1, :1].expand(B, N, Hq, d)
+    assert all(torch.equal(a, b) for a, b in zip(bwd(q, k, v, row.contiguous(), lse, do, **kw), bwd(q, k, v, row, lse, do, **kw)))
     one = torch.ones(1, 1, 1, 1, dtype=torch.bfloat16, device="cuda").expand(B, N, Hq, d)
     assert all(torch.equal(a, b) for a, b in zip(bwd(q, k, v, o, lse, one.contiguous(), **kw), bwd(q, k, v, o, lse, one, **kw)))
     # on another stream: the copies are that stream's, and what the current one allocates meanwhile is not theirs
