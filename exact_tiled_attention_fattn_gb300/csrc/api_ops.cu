@@ -617,5 +617,6 @@ extern "C" fattn_status fattn_fwd_paged_fp8(const void* q, const void* kcache, c
   const bool plain = p.shape.cap == 0.f && !p.shape.slopes && p.shape.window == 0 && num_splits == 1;
   return fwd_paged_impl(q, e.kout, e.vout, e.table, seqlens_k, cu_seqlens_q, o, lse, B, Hq, Hkv, d, page_size,
                         max_pages_per_seq, B * max_pages_per_seq, total_q, max_seqlen_q, causal, scale,
-                        plain ? nullptr : &p.shape, num_splits, num_splits > 1 ? ws + w.splits : nullptr, num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
+                        plain ? nullptr : &p.shape, num_splits, num_splits > 1 ? ws + w.splits : nullptr,
+                        num_splits > 1 ? workspace_bytes - w.splits : 0, stream);
 }

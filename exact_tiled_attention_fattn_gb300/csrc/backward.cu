@@ -97,7 +97,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // One warp forms D = rowsum(dO o O) and -lse * log2(e) for 32 consecutive query rows
 // i0 .. i0 + 31 of one (sequence, head) and writes both into the workspace: lane u
 // reads row u's lse (one 128-byte read per warp), the warp walks the 32 rows of O and
-// dO (each a contiguous d-long row; kRowsPerWarp rows with their loads in flight
+// dO (each a contiguous d-long row, O's at its strides; pointers that step, as the offsets' 64-bit products cost the
+// shaped calls 1 to 3 % and short plain ones up to 5; kRowsPerWarp rows with their loads in flight
 // together, each lane d / 32 elements of both), reduces each row's dot product with
 // shuffles and keeps row u's in lane u, and writes the two vectors with one 128-byte
 // store each. Rows past N (the padding up to Npad) get -inf and 0, so their P is 0.
@@ -404,9 +405,10 @@ __device__ __forceinline__ void shaped_key_tiles(const BwdParams& p, int b, int 
 }
 // The ranges seen from the keys: the queries that see key j are [qa_j, qb_j), as the bounds are
 // monotone: qa_j the first row whose end is above j, qb_j the first whose begin is. The dQ pass's
-// warps 2-3 write them (a sink is seen to the last row, from its own on or, without causal, from the first) for the dK/dV pass, 32 rows a warp at a time: row i is qa of the keys
+// warps 2-3 write them for the dK/dV pass, 32 rows a warp at a time: row i is qa of the keys
 // [end_{i-1}, end_i) and qb of the keys [begin_{i-1}, begin_i), row N that of the rest, and the
-// whole warp writes each row's keys. (Searching them per key and item in the dK/dV pass took 2 to 3 us
+// whole warp writes each row's keys. A sink is seen to the last row, from its own on or, without causal,
+// from the first. (Searching them per key and item in the dK/dV pass took 2 to 3 us
 // at the start of every item: packed documents, B=4 H=32 N=4096, 966 us for the whole call.)
 template <bool kSinks>
 __device__ __forceinline__ void write_key_ranges(const BwdParams& p, int worker, int workers, int lane) {

@@ -202,7 +202,8 @@ inline int stream_fp8_cluster(const StreamFp8Params& p, int step, int sms, int m
 }
 // Whether a chunk goes to the streaming kernel. Its time grows with the rows (2 x 30000 tokens, 8 KV heads of 128: 1.0 us a
 // row), the other way's with the query heads, whose tiles have room for 256 queries (44 us for each of a KV head), and the
-// copy of the cache (51 us): with 4 heads a KV head 128 rows take 137 and 234 us, 256 rows 258 and 235.
+// copy of the cache (51 us): with 4 heads a KV head 128 rows take 137 and 234 us, 256 rows 258 and 235. A fit to that shape: the
+// other way's copy and rounds depend on contexts, sequences and KV heads too, which are not weighed.
 inline bool streams_fp8(long long max_q, int group) { return max_q * group <= FATTN_FP8_STREAM_ROWS((long long)group); }
 cudaError_t launch_stream_fp8(const StreamFp8Params& p, cudaStream_t stream);
 

@@ -133,8 +133,8 @@ enum : int { kModeDense = 0, kModeSparse = 1, kModePaged = 2, kModeMasked = 3, k
 // Shaped variants: kModeShaped plus what the scores get (key ranges and the window always),
 // whether K/V come through a block table, and then whether key tiles are cut into runs (the
 // epilogue's second form costs the others up to 25 %, in registers), and whether a window has sinks (at run time the others
-// lose up to 4 %: 32 heads over 8, 2 x 8192 tokens, capped, window 128 160 -> 165 us). One kernel for each, as the softmax loop of the one
-// with everything under run-time switches is 6 % slower without a cap or bias: its unrolled
+// lose up to 4 %: 32 heads over 8, 2 x 8192 tokens, capped, window 128 160 -> 167 us). One kernel for each, as the softmax loop of
+// the one with everything under run-time switches is 6 % slower without a cap or bias: its unrolled
 // forms no longer stay in the instruction cache.
 enum : int { kModeShaped = 8, kShapeCap = 1, kShapeBias = 2, kShapePaged = 4, kShapeSplit = 16, kShapeSinks = 32 };
 __host__ __device__ constexpr bool mode_shaped(int m) { return m >= kModeShaped; }

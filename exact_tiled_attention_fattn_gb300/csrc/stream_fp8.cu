@@ -10,7 +10,9 @@
 // loaded while this one's softmax and V are worked on, its V brought to the L2 cache. (Through shared memory by
 // cp.async, three stages, 16 warps an SM: 91 us for the first case above.) Both products are taken transposed, with tokens
 // (K) and head elements (V) as the 16 rows of mma.sync m16n8k16 and up to 8 query rows as its columns, which is what a group
-// of heads gives, where a tile of tcgen05.mma would have 128 rows for them and its operands in shared memory:
+// of heads gives. (tcgen05.mma takes the same transposed products, tokens or head elements as M = 128 and N = 16 or more query
+// rows, with O^T in tensor memory; its operands come from shared memory, where the codes would have to be written as fp16
+// first. That way is not tried.)
 //   S^T = K Q^T   lane (g, c) holds tokens g and g + 8: 16 consecutive codes of each are the A fragments of four steps, if
 //                 the head's elements are taken in the order in which they lie there (Q^T is permuted alike);
 //   O^T = V^T P^T lane (g, c) holds the codes 16 g .. 16 g + 15 of tokens 2c, 2c + 1, 2c + 8 and 2c + 9: pairs of tokens

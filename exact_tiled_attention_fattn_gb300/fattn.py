@@ -1005,7 +1005,8 @@ def bwd_shaped(q, k, v, o, lse, dout, causal: bool = False, scale: float | None 
     head = base + shape
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
     if strides:
-        _check("fattn_bwd_strided", lib.fattn_bwd_strided(*base, 1, *shape, sinks or 0, _ptr(key_begin), _ptr(key_end), *strides, *tail))
+        _check("fattn_bwd_strided", lib.fattn_bwd_strided(*base, 1, *shape, sinks or 0, _ptr(key_begin), _ptr(key_end),
+                                                          *strides, *tail))
     elif sinks:
         _check("fattn_bwd_sinks", lib.fattn_bwd_sinks(*head, sinks, *tail))
     else:
@@ -1168,7 +1169,8 @@ def choose_fp8_splits(batch: int, Hq: int, Hkv: int, d: int, page_size: int, max
                       num_sms: int | None = None) -> int:
     """Split count of ``fwd_paged_fp8`` for contexts of ``max_context`` visible tokens. Where the codes are streamed the
     splits only bound the pieces that a group of up to 32 query rows may be cut into, so that every CTA (two an SM) takes an equal
-    share of the steps: enough for sequences twice as long as the mean. Else ``choose_chunk_splits``."""
+    share of the steps: enough for sequences twice as long as the mean. Else ``choose_chunk_splits``. ``page_size`` is of no
+    weight."""
     if num_sms is None:
         num_sms = _num_sms(torch.cuda.current_device())
     group = Hq // max(Hkv, 1)
