@@ -652,7 +652,10 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) stream_fp8_kernel(const St
   if (p.cluster > 0) {
     const int rank = p.cluster > 1 ? cluster_rank() : 0, at = blockIdx.x / p.cluster, v = at / p.Hkv, hkv = at - v * p.Hkv;
     const Group x = describe<R>(p, v, hkv == 0 && rank == 0 && threadIdx.x == 0);
-    if (x.chunks == 0) return;                         // (as all of the cluster)
+    if (x.chunks == 0) {   // (as all of the cluster; it stays for the others should the lengths change under the kernel)
+      if (p.cluster > 1) cluster_sync(), cluster_sync();
+      return;
+    }
     const int share = (x.chunks + p.cluster - 1) / p.cluster, from = min(rank * share, x.chunks);
     stream_piece<D, NT, kScores>(p, scratch, sh, x, hkv, from, min(share, x.chunks - from), 0, p.cluster == 1);
     if (p.cluster > 1) join_cluster<D, NT>(p, scratch, sh, x, hkv, rank);
