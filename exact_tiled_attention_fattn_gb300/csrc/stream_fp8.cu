@@ -755,7 +755,9 @@ int most_cluster() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   if (dev >= 0 && dev < 128 && (most = known[dev].load(std::memory_order_relaxed)) > 0) return most;
   auto kern = stream_fp8_kernel<D, NT, kScores>;
-  const bool wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  // (an answer of no, which is no error of this call, does not stay behind; what was there before does)
+  auto yes = [](cudaError_t e) -> bool { return e == cudaSuccess || (cudaGetLastError(), false); };
+  const bool wide = yes(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   for (most = wide ? kStreamMostCluster : 8; most > 1; most /= 2) {
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(most);
@@ -767,9 +769,8 @@ int most_cluster() {
     c.attrs = &a;
     c.numAttrs = 1;
     int room = 0;
-    if (cudaOccupancyMaxActiveClusters(&room, kern, &c) == cudaSuccess && room > 0) break;
+    if (yes(cudaOccupancyMaxActiveClusters(&room, kern, &c)) && room > 0) break;
   }
-  cudaGetLastError();   // (a size that has no room is no error of this call)
   if (dev >= 0 && dev < 128) known[dev].store(most, std::memory_order_relaxed);
   return most;
 }

@@ -409,7 +409,8 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
         workspace=None, stream=None):
     """Attention backward. q, o, dout [B,N,Hq,d], k, v [B,N,Hkv,d] bf16; lse [B,Hq,N] fp32 from
     ``fwd`` on the same inputs. o and dout may be any views: o is read where it lies if its elements of a head do (heads
-    first in memory, a slice), and what else is not contiguous is copied within the call. Returns (dq, dk, dv) in the input layouts (bf16)."""
+    first in memory, a slice), and what else is not contiguous is copied within the call. Returns (dq, dk, dv) in the
+    input layouts (bf16)."""
     lib = load_library()
     _need_cuda(q, k, v, lse, dq, dk, dv, workspace)
     _need_cuda(o, dout, contiguous=False)
